@@ -19,15 +19,27 @@ Entry points (same names as the C ABI):
                        partials use a scratch array the library holds on each GPU
   conv1d_fwd_cf / conv1d_bwd_cf  the channels-first layout [B, D, T] (T contiguous, one sequence
                        per (b, d) row, zero history)
+
+What follows the convolution in a mixer block (C ABI in include/ssm.h, binding in ``ssm.py``):
+  ssm_scan_fwd / ssm_scan_bwd   selective state space scan over packed rows, with a slot pool of
+                       states or initial / final state arrays, and its training backward
+  ssm_state_update     one decode step per sequence against its state slot
+  gated_norm_fwd / gated_norm_bwd        RMS norm with its gate, by groups of channels
+  residual_norm_fwd / residual_norm_bwd  residual addition with a scale and the next RMS norm
 """
 import ctypes
 
 from . import _lib
+from .ssm import (SsmGrads, gated_norm_bwd, gated_norm_fwd, norm_bwd_workspace_bytes, residual_norm_bwd,
+                  residual_norm_fwd, ssm_scan_bwd, ssm_scan_bwd_workspace_bytes, ssm_scan_fwd,
+                  ssm_scan_fwd_workspace_bytes, ssm_state_update)
 
 __all__ = ["conv1d_fwd", "conv1d_state_update", "conv1d_state_update_spec", "conv1d_bwd", "conv1d_bwd_combine",
            "conv1d_bwd_noalloc", "conv1d_fwd_cf",
            "conv1d_bwd_cf", "conv1d_bwd_cf_workspace_bytes", "conv1d_fwd_workspace_bytes",
-           "conv1d_bwd_workspace_bytes", "library_path"]
+           "conv1d_bwd_workspace_bytes", "library_path", "ssm_scan_fwd", "ssm_scan_bwd", "SsmGrads",
+           "ssm_state_update", "ssm_scan_fwd_workspace_bytes", "ssm_scan_bwd_workspace_bytes", "gated_norm_fwd",
+           "gated_norm_bwd", "residual_norm_fwd", "residual_norm_bwd", "norm_bwd_workspace_bytes"]
 
 library_path = _lib.LIB_PATH
 

@@ -53,7 +53,39 @@ SIGNATURES = {
     "conv1d_status_str": (ctypes.c_char_p, [c_int]),
 }
 
+class SsmShape(ctypes.Structure):
+    _fields_ = [("H", c_i64), ("P", c_i64), ("G", c_i64), ("N", c_i64), ("dt_dtype", c_int), ("dt_softplus", c_int)]
+
+
+class SsmStates(ctypes.Structure):
+    _fields_ = [("initial", c_p), ("final", c_p), ("slots", c_i64), ("s_slot", c_i64), ("cache_indices", c_p),
+                ("has_initial_state", c_p)]
+
+
+_SHAPE, _STATES, _SEQ = ctypes.POINTER(SsmShape), ctypes.POINTER(SsmStates), ctypes.POINTER(Seq)
+_ROWS = [c_p, c_i64]  # an array of rows and its row stride
+
+# name -> (restype, argtypes); must match include/ssm.h
+SSM_SIGNATURES = {
+    "ssm_scan_fwd": (c_int, [_SHAPE, c_i64, *_ROWS, *_ROWS, c_p, *_ROWS, *_ROWS, c_p, c_p, _SEQ, _STATES, *_ROWS, c_p,
+                             c_size, c_p]),
+    "ssm_scan_fwd_workspace_bytes": (c_size, [_SHAPE, c_i64, c_i64]),
+    "ssm_scan_bwd": (c_int, [_SHAPE, c_i64, *_ROWS, *_ROWS, *_ROWS, c_p, *_ROWS, *_ROWS, c_p, c_p, _SEQ, c_p, c_p, *_ROWS,
+                             *_ROWS, c_p, *_ROWS, *_ROWS, c_p, c_p, c_p, c_p, c_size, c_p]),
+    "ssm_scan_bwd_workspace_bytes": (c_size, [_SHAPE, c_i64, c_i64]),
+    "ssm_state_update": (c_int, [_SHAPE, c_i64, *_ROWS, *_ROWS, c_p, *_ROWS, *_ROWS, c_p, c_p, _STATES, *_ROWS, c_p]),
+    "gated_norm_fwd": (c_int, [c_i64, c_i64, c_i64, *_ROWS, *_ROWS, c_p, c_int, c_int, ctypes.c_float, *_ROWS, c_p]),
+    "gated_norm_bwd": (c_int, [c_i64, c_i64, c_i64, *_ROWS, *_ROWS, *_ROWS, c_p, c_int, c_int, ctypes.c_float, *_ROWS,
+                               *_ROWS, c_p, c_p, c_size, c_p]),
+    "residual_norm_fwd": (c_int, [c_i64, c_i64, *_ROWS, *_ROWS, c_int, ctypes.c_float, c_p, c_int, ctypes.c_float, *_ROWS,
+                                  *_ROWS, c_p]),
+    "residual_norm_bwd": (c_int, [c_i64, c_i64, *_ROWS, *_ROWS, *_ROWS, c_int, ctypes.c_float, c_p, c_int,
+                                  ctypes.c_float, *_ROWS, *_ROWS, c_p, c_p, c_size, c_p]),
+    "norm_bwd_workspace_bytes": (c_size, [c_i64, c_i64, c_i64]),
+}
+
 _LIB = None
+_SSM = None
 
 
 def load(path=LIB_PATH):
@@ -74,6 +106,19 @@ def load(path=LIB_PATH):
     if path == LIB_PATH:
         _LIB = lib
     return lib
+
+
+def load_ssm():
+    """The same library with the entry points of include/ssm.h."""
+    global _SSM
+    if _SSM is None:
+        lib = load()
+        for name, (res, args) in SSM_SIGNATURES.items():
+            fn = getattr(lib, name)
+            fn.restype = res
+            fn.argtypes = args
+        _SSM = lib
+    return _SSM
 
 
 class Conv1dError(RuntimeError):

@@ -14,6 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libcausal_conv1d.so")
 SOURCES = ["conv1d_fwd.hip", "conv1d_bwd.hip", "conv1d_cf.hip", "conv1d_api.cpp"]
+# the scan, step and norm operators (include/ssm.h); the kernels tile through LDS, unlike SOURCES
+SSM_SOURCES = ["ssm_scan.hip", "ssm_scan_bwd.hip", "ssm_step.hip", "norm.hip", "ssm_api.cpp"]
 ARCH = "gfx950"
 
 
@@ -40,7 +42,7 @@ def build(out=LIB, jobs=4, verbose=False, defines=()):
     objdir = os.path.join(PKG, "_build", os.path.basename(out))
     os.makedirs(objdir, exist_ok=True)
     objs, procs = [], []
-    for src in SOURCES:
+    for src in SOURCES + SSM_SOURCES:
         obj = os.path.join(objdir, src + ".o")
         lang = ["-x", "hip"] if src.endswith(".hip") else []
         cmd = ["hipcc", *hipcc_flags(), *[f"-D{d}" for d in defines], *lang, "-c", os.path.join(CSRC, src), "-o", obj]

@@ -1,0 +1,284 @@
+// ssm_device.h -- device-side building blocks of the scan, step and norm kernels (library-internal).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ssm_launch.h"
+
+namespace cssm {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// 16- and 8-byte accesses at 2-byte aligned addresses: one instruction each in the unaligned access
+// mode the HSA runtime sets, so odd row strides and views into wider rows need no separate path.
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ float bf_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+// two FP32 -> two bf16, round to nearest even
+__device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
+  f32x2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+__device__ __forceinline__ uint16_t to_bf16(float a) { return (uint16_t)pk_bf16(a, 0.f); }
+
+// 2^x by the hardware instruction (about 1 ulp)
+__device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + ex2(-kLog2e * z)); }
+
+// the step size: v, or log(1 + e^v) (v itself above 20, where the two agree to FP32)
+__device__ __forceinline__ float step_size(float v, int softplus) {
+  if (!softplus) return v;
+  return v > 20.f ? v : log1pf(expf(v));
+}
+
+__device__ __forceinline__ float load_num(const void* p, int64_t i, int f32) {
+  return f32 ? static_cast<const float*>(p)[i] : bf_f32(static_cast<const uint16_t*>(p)[i]);
+}
+
+// ------------------------------------------------------------------ wave reductions and scans
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float dpp0(float v) {  // 0 where the source lane is masked or out of its row
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, ROW_MASK, 0xf, true));
+}
+// inclusive prefix sum over the wave: shifts inside rows of 16 lanes, then the rows' last lanes broadcast
+__device__ __forceinline__ float wave_prefix(float v) {
+  v += dpp0<0x111, 0xf>(v);
+  v += dpp0<0x112, 0xf>(v);
+  v += dpp0<0x114, 0xf>(v);
+  v += dpp0<0x118, 0xf>(v);
+  v += dpp0<0x142, 0xa>(v);
+  v += dpp0<0x143, 0xc>(v);
+  return v;
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp0(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROW_MASK, 0xf, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROW_MASK, 0xf, true);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_prefix(double v) {
+  v += dpp0<0x111, 0xf>(v);
+  v += dpp0<0x112, 0xf>(v);
+  v += dpp0<0x114, 0xf>(v);
+  v += dpp0<0x118, 0xf>(v);
+  v += dpp0<0x142, 0xa>(v);
+  v += dpp0<0x143, 0xc>(v);
+  return v;
+}
+// sum over the 16 lanes of each row; valid in lane 15 of the row
+__device__ __forceinline__ float row16_sum(float v) {
+  v += dpp0<0x111, 0xf>(v);
+  v += dpp0<0x112, 0xf>(v);
+  v += dpp0<0x114, 0xf>(v);
+  v += dpp0<0x118, 0xf>(v);
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) { return lane_value(wave_prefix(v), 63); }
+
+// ------------------------------------------------------------------ sequences, pieces, chunks
+struct Piece {
+  int64_t seq, s, e;  // the sequence's rows [s, e)
+  int64_t r0, r1;     // this piece's rows
+  bool ok;            // the item is a piece (false: nothing to do)
+};
+
+__device__ __forceinline__ int64_t cu_at(const Seqs& q, int64_t k) {
+  const int64_t v = q.cu[k];
+  return v < 0 ? 0 : (v > q.rows ? q.rows : v);
+}
+__device__ __forceinline__ void seq_bounds(const Seqs& q, int64_t i, int64_t& s, int64_t& e) {
+  if (q.cu) {
+    s = cu_at(q, i);
+    e = cu_at(q, i + 1);
+  } else {
+    s = i * q.seqlen;
+    e = s + q.seqlen;
+  }
+}
+
+// The sequence holding `row` (-1: none): a 64-ary search over the offsets, one probe a lane.
+__device__ __forceinline__ int64_t seq_of_row(const Seqs& q, int64_t row) {
+  if (!q.cu) return row / q.seqlen;
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, len = q.nseq + 1;  // offsets before lo are <= row, offsets from lo + len on are > row
+  while (len > 64) {
+    const int64_t step = (len + 63) / 64;
+    const int64_t k = (lane + 1) * step;
+    const bool le = q.cu[lo + (k < len ? k : len) - 1] <= row;
+    const int64_t skip = (int64_t)__popcll(__ballot(le)) * step;
+    if (skip >= len) {
+      lo += len;
+      len = 0;
+    } else {
+      lo += skip;
+      len = len - skip < step ? len - skip : step;
+    }
+  }
+  const bool le = lane < len && q.cu[lo + (lane < len ? lane : 0)] <= row;
+  return lo + __popcll(__ballot(le)) - 1;
+}
+
+// Item `it` of a cut of the packed rows at sequence starts and multiples of seg: items below n_slots
+// are the pieces that begin at row it * seg inside a sequence, item n_slots + i is sequence i's first.
+__device__ __forceinline__ Piece find_piece(const Seqs& q, int64_t it, int64_t seg, int64_t n_slots) {
+  Piece p;
+  p.ok = false;
+  if (it >= n_slots) {
+    p.seq = it - n_slots;
+    seq_bounds(q, p.seq, p.s, p.e);
+    p.r0 = p.s;
+    p.ok = p.e > p.s;
+  } else {
+    p.r0 = it * seg;
+    p.seq = seq_of_row(q, p.r0);
+    if (p.seq < 0 || p.seq >= q.nseq) return p;
+    seq_bounds(q, p.seq, p.s, p.e);
+    p.ok = p.r0 > p.s && p.r0 < p.e;
+  }
+  p.r1 = p.e;
+  if (seg > 0) {
+    const int64_t cut = (p.r0 / seg + 1) * seg;
+    if (cut < p.r1) p.r1 = cut;
+  }
+  return p;
+}
+
+__device__ __forceinline__ int64_t chunk_end(int64_t r, int64_t r1) {
+  const int64_t c = (r / kChunk + 1) * kChunk;
+  return c < r1 ? c : r1;
+}
+
+// ------------------------------------------------------------------ tiles of 64 rows in shared memory
+// [64][W] bf16, row-major, 16-byte pieces of a row permuted by the row number so that 16 rows' same
+// piece, and the transposing reads of 4 rows by 16 columns, fall on different banks (64 banks of 4
+// bytes: two 128-byte rows or one longer row a turn).
+template <int W>
+__device__ __forceinline__ int swz(int row, int piece) {
+  return row * W + ((piece ^ (W == 64 ? (row >> 1) & 7 : row & 15)) << 3);
+}
+template <int W>
+__device__ __forceinline__ int swz4(int row, int col) {  // col a multiple of 4
+  return swz<W>(row, col >> 3) + (col & 4);
+}
+
+template <int W>
+struct TileRegs {
+  u32x4 v[W / 32];
+};
+
+// Rows [0, nrows) x columns [0, ncols) of a global array into registers, 256 threads, zeros outside.
+// Addresses outside are replaced by the first element's, so the loads need no branches.  VEC: ncols
+// is a multiple of 8.
+template <int W, bool VEC>
+__device__ __forceinline__ void load_tile(TileRegs<W>& t, const uint16_t* __restrict__ base, int64_t ld, int nrows,
+                                          int ncols) {
+#pragma unroll
+  for (int k = 0; k < W / 32; ++k) {
+    const int q = threadIdx.x + 256 * k, row = q / (W / 8), c = (q % (W / 8)) * 8;
+    const bool ok = row < nrows && c < ncols;
+    const uint16_t* p = base + (ok ? row * ld + c : 0);
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if constexpr (VEC) {
+      v = *reinterpret_cast<const u32x4_a2*>(p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u = p[c + e < ncols && ok ? e : 0];
+        v[e >> 1] |= (c + e < ncols ? u : 0u) << (16 * (e & 1));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t.v[k][e] = ok ? v[e] : 0u;
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void store_tile(uint16_t* lds, const TileRegs<W>& t) {
+#pragma unroll
+  for (int k = 0; k < W / 32; ++k) {
+    const int q = threadIdx.x + 256 * k;
+    *reinterpret_cast<u32x4*>(lds + swz<W>(q / (W / 8), q % (W / 8))) = t.v[k];
+  }
+}
+
+// ------------------------------------------------------------------ matrix operands
+// 16x16x32 bf16: lane l holds index l % 16 of its operand and 8 of the 32 contracted positions; the
+// result has the first operand's index in the registers (4 * (l / 16) + r) and the second's in the
+// lanes.  The contracted positions may be taken in any order that both operands share.  Two orders
+// are used: "straight", positions 8 * (l / 16) + e, and "split", positions 4 * (l / 16) + e and
+// 16 + 4 * (l / 16) + e, which is how results and transposing reads come.
+__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+// index = rows of the tile, contracted = columns k0 .. k0 + 31, straight
+template <int W>
+__device__ __forceinline__ bf16x8 op_straight(const uint16_t* lds, int row0, int k0) {
+  const int l = threadIdx.x & 63;
+  return *reinterpret_cast<const bf16x8*>(lds + swz<W>(row0 + (l & 15), (k0 >> 3) + (l >> 4)));
+}
+// the same, split
+template <int W>
+__device__ __forceinline__ bf16x8 op_split(const uint16_t* lds, int row0, int k0) {
+  const int l = threadIdx.x & 63, row = row0 + (l & 15), c = k0 + (l >> 4) * 4;
+  const u32x2 a = *reinterpret_cast<const u32x2*>(lds + swz4<W>(row, c));
+  const u32x2 b = *reinterpret_cast<const u32x2*>(lds + swz4<W>(row, c + 16));
+  const u32x4 v = {a.x, a.y, b.x, b.y};
+  return __builtin_bit_cast(bf16x8, v);
+}
+// index = columns c0 .. c0 + 15, contracted = rows k0 .. k0 + 31, split (the transposing read gives
+// lane i of 16 column i of the 4 rows x 16 columns that the 16 lanes address)
+template <int W>
+__device__ __forceinline__ bf16x8 op_cols(const uint16_t* lds, int k0, int c0) {
+  const int l = threadIdx.x & 63, row = k0 + (l >> 4) * 4 + ((l & 15) >> 2), c = c0 + (l & 3) * 4;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + swz4<W>(row, c)));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + swz4<W>(row + 16, c)));
+  const u32x2 ua = __builtin_bit_cast(u32x2, a), ub = __builtin_bit_cast(u32x2, b);
+  const u32x4 v = {ua.x, ua.y, ub.x, ub.y};
+  return __builtin_bit_cast(bf16x8, v);
+}
+// results of two neighbouring blocks (registers = contracted) as an operand, split
+__device__ __forceinline__ bf16x8 op_result(f32x4 a, f32x4 b) {
+  const u32x4 v = {pk_bf16(a[0], a[1]), pk_bf16(a[2], a[3]), pk_bf16(b[0], b[1]), pk_bf16(b[2], b[3])};
+  return __builtin_bit_cast(bf16x8, v);
+}
+// w[e] * v[e] in FP32 as the sum of two bf16 operands: the remainder is at most 2^-16 of the product
+__device__ __forceinline__ void split_scaled(bf16x8 v, f32x4 wa, f32x4 wb, bf16x8& hi, bf16x8& lo) {
+  const u32x4 u = __builtin_bit_cast(u32x4, v);
+  u32x4 h, l;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float a = bf_lo(u[e]) * (e < 2 ? wa[2 * e] : wb[2 * e - 4]);
+    const float b = bf_hi(u[e]) * (e < 2 ? wa[2 * e + 1] : wb[2 * e - 3]);
+    h[e] = pk_bf16(a, b);
+    l[e] = pk_bf16(a - bf_lo(h[e]), b - bf_hi(h[e]));
+  }
+  hi = __builtin_bit_cast(bf16x8, h);
+  lo = __builtin_bit_cast(bf16x8, l);
+}
+
+// ------------------------------------------------------------------ XCD-aware block order
+// Workgroups are dealt to the 8 XCDs in turn, each with its own L2.  Every XCD takes one contiguous
+// range of logical blocks, so the heads that share a group's B and C rows meet in one L2.
+__device__ __forceinline__ uint32_t xcd_block(uint32_t b, uint32_t nb) {
+  const uint32_t q = nb / 8, r = nb % 8, x = b % 8, i = b / 8;
+  return x < r ? x * (q + 1) + i : r * (q + 1) + (x - r) * q + i;
+}
+
+}  // namespace cssm

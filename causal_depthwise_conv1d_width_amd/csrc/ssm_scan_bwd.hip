@@ -1,0 +1,457 @@
+// ssm_scan_bwd.hip -- backward of the selective state space scan.
+//
+// For a chunk of 64 rows of one sequence and one head, with S the state before the chunk, T the adjoint
+// of the state after it, L the prefix sums of l_t = dt_t A, M_ij = e^{L_i - L_j} (i >= j), and
+//   G = C B^T,  W = dY X^T,  Z_ij = M_ij dt_j W_ij,  K_ij = G_ij M_ij W_ij:
+//   dC_i = sum over heads of  e^{L_i} S^T dy_i + sum_j Z_ij B_j
+//   dB_j = sum over heads of  dt_j e^{L_Q - L_j} T^T x_j + sum_i Z_ij C_i
+//   dx_j = dt_j (e^{L_Q - L_j} T B_j + sum_i G_ij M_ij dy_i) + D dy_j
+//   dl_t = e^{L_Q} <T, S> + sum_{i >= t} e^{L_i} dy_i . S C_i + sum_{j < t} dt_j e^{L_Q - L_j} x_j . T B_j
+//          + sum_{i >= t > j} dt_j K_ij
+//   d(dt_t) = A dl_t + e^{L_Q - L_t} x_t . T B_t + sum_i K_it
+// The first kernel walks the states forward and the adjoints in reverse and stores both at every chunk;
+// then every chunk is independent: a block takes one chunk and the heads of one group (or a part of
+// them), keeps dB and dC in registers over its heads, and sums nothing through memory.  S and T are
+// stored as a high and a low bf16 part, already in matrix-operand order: with both parts the row
+// sums that feed d(dt) and dA keep FP32's weight (dC and dB share those products); dx, rounded to
+// bf16 in the end, takes the high part of T.  Z and G M are rounded to bf16 once, as operands.
+#include "ssm_state.h"
+
+namespace cssm {
+
+template <int NT, bool VEC, bool STORE>
+__global__ __launch_bounds__(256, 2) void ssm_states_kernel(StateArgs f, StateArgs r) {
+  __shared__ StateShared<NT> sh;
+  if (blockIdx.y == 0) state_walk<NT, VEC, false, STORE>(f, sh);
+  else state_walk<NT, VEC, true, STORE>(r, sh);
+}
+
+__device__ __forceinline__ float across16(float v) {  // sum over the four rows of 16 lanes
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+template <int NT, bool VEC>
+__global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(ScanBwdArgs b) {
+  constexpr int NBW = NT / 64;                                  // 16-column blocks n of a wave
+  constexpr int R = 64 * NT > 2 * 64 * 64 ? 64 * NT : 2 * 64 * 64;
+  __shared__ __align__(16) uint16_t sx[64 * 64];
+  __shared__ __align__(16) uint16_t sy[64 * 64];
+  __shared__ __align__(16) uint16_t sB[64 * NT];
+  __shared__ __align__(16) uint16_t sC[64 * NT];
+  __shared__ __align__(16) uint16_t sR[R];  // T^T [n][p], then Z and G M [i][j]
+  __shared__ __align__(16) double sL[64];  // differences of FP32 sums would lose a fast decay's weights
+  __shared__ __align__(16) float sd[64], se[64], sr[64];
+  __shared__ float s_row[64], s_diag[64], s_rint[4][64], s_u[4][64], s_col[4][64], s_dot[4], s_trace[4];
+  uint16_t *sZ = sR, *sG = sR + 64 * 64;
+  const ScanArgs& a = b.s;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, i = lane & 15;
+  const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
+  const int part = blk % b.hsplit, grp = blk / b.hsplit % a.G;
+  const int64_t id = blk / b.hsplit / a.G;
+  const int hg = a.H / a.G, per = (hg + b.hsplit - 1) / b.hsplit;
+  const int h_lo = grp * hg + part * per, h_hi = h_lo + per < (grp + 1) * hg ? h_lo + per : (grp + 1) * hg;
+  const Piece pc = find_piece(a.q, id, kChunk, b.n_chunk_slots);
+  if (!pc.ok) {
+    for (int e = threadIdx.x; e < (h_hi - h_lo) * 3; e += 256) b.head_part[(id * a.H + h_lo) * 3 + e] = 0.f;
+    return;
+  }
+  const int rows = (int)(pc.r1 - pc.r0);
+  const int hp = a.H * a.ptiles;
+  const int tiles = (h_hi - h_lo) * a.ptiles;
+  const int64_t gn = (int64_t)grp * a.N;
+  const int nw = 16 * NBW * w;  // this wave's first column n
+
+  f32x4 dC[NBW][4], dB[NBW][4];
+#pragma unroll
+  for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dC[nb][k] = dB[nb][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  TileRegs<64> tx, ty;
+  u32x4 Sh[NBW][2], Sl[NBW][2], Th[NBW][2], Tl[NBW][2];
+  auto load_rows = [&](int t) {
+    const int h = h_lo + t / a.ptiles, p_first = t % a.ptiles * kPTile;
+    const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
+    const int64_t o = (int64_t)h * a.P + p_first;
+    load_tile<64, VEC>(tx, a.x + pc.r0 * a.x_ld + o, a.x_ld, rows, pn);
+    load_tile<64, VEC>(ty, b.dy + pc.r0 * b.dy_ld + o, b.dy_ld, rows, pn);
+  };
+  auto load_states = [&](int t) {
+    const int64_t o = (id * hp + h_lo * a.ptiles + t) * (2 * 64 * NT);
+    const u32x4 *cs = reinterpret_cast<const u32x4*>(b.cs + o), *ct = reinterpret_cast<const u32x4*>(b.ct + o);
+#pragma unroll
+    for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int at = ((w * NBW + nb) * 2 + ks) * 64 + lane;
+        Th[nb][ks] = ct[at];
+        Sh[nb][ks] = cs[at];
+        Sl[nb][ks] = cs[8 * NT + at];
+        Tl[nb][ks] = ct[8 * NT + at];
+      }
+  };
+  load_rows(0);
+  load_states(0);
+  {
+    TileRegs<NT> t;
+    load_tile<NT, VEC>(t, a.B + pc.r0 * a.B_ld + gn, a.B_ld, rows, a.N);
+    store_tile<NT>(sB, t);
+    load_tile<NT, VEC>(t, a.C + pc.r0 * a.C_ld + gn, a.C_ld, rows, a.N);
+    store_tile<NT>(sC, t);
+  }
+  __syncthreads();
+  f32x4 G[4];  // G^T: rows i = 16 w + lane, columns j in the registers; blocks past the diagonal stay 0
+#pragma unroll
+  for (int jb = 0; jb < 4; ++jb) {
+    G[jb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (jb <= w) {
+#pragma unroll
+      for (int ks = 0; ks < NT / 32; ++ks)
+        G[jb] = mma(op_straight<NT>(sB, 16 * jb, 32 * ks), op_straight<NT>(sC, 16 * w, 32 * ks), G[jb]);
+    }
+  }
+
+  float dl_sum = 0.f, q_sum = 0.f, trace_sum = 0.f;  // wave 0: over a head's column tiles
+  for (int t = 0; t < tiles; ++t) {
+    const int h = h_lo + t / a.ptiles, ptile = t % a.ptiles, p_first = ptile * kPTile;
+    const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
+    const float A2 = a.A[h] * kLog2e, bias = a.bias ? a.bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
+    store_tile<64>(sx, tx);
+    store_tile<64>(sy, ty);
+    if (w == 0) {
+      float d;
+      const bool in = lane < rows;
+      const double L = wave_prefix((double)row_decay(a, pc.r0 + (in ? lane : 0), in, h, A2, bias, d));
+      sL[lane] = L;
+      sd[lane] = d;
+      se[lane] = ex2((float)L);
+    } else if (w == 1) {
+      float d;
+      const bool in = 63 - lane < rows;
+      const float Rv = wave_prefix(row_decay(a, pc.r0 + (in ? 63 - lane : 0), in, h, A2, bias, d));
+      sr[63 - lane] = ex2(dpp0<0x138, 0xf>(Rv));
+    }
+#pragma unroll
+    for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int n = nw + 16 * nb + i;
+        *reinterpret_cast<u32x2*>(sR + swz4<64>(n, 32 * ks + 4 * g)) = u32x2{Th[nb][ks].x, Th[nb][ks].y};
+        *reinterpret_cast<u32x2*>(sR + swz4<64>(n, 32 * ks + 16 + 4 * g)) = u32x2{Th[nb][ks].z, Th[nb][ks].w};
+      }
+    __syncthreads();
+    if (t + 1 < tiles) load_rows(t + 1);
+
+    f32x4 dX[4];  // registers p = 16 w + 4 g + r, lanes j
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) dX[jb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < NT / 32; ++ks) {
+      const bf16x8 tt = op_cols<64>(sR, 32 * ks, 16 * w);
+#pragma unroll
+      for (int jb = 0; jb < 4; ++jb) dX[jb] = mma(tt, op_split<NT>(sB, 16 * jb, 32 * ks), dX[jb]);
+    }
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) dX[jb] *= sr[16 * jb + i];
+    __syncthreads();
+
+    {  // rows i = 16 w + lane against columns j in the registers
+      bf16x8 yv[2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) yv[ks] = op_straight<64>(sy, 16 * w, 32 * ks);
+      const double Li = sL[16 * w + i];
+      float row = 0.f, trace = 0.f;
+#pragma unroll
+      for (int jb = 0; jb < 4; ++jb) {
+        float col[4] = {0.f, 0.f, 0.f, 0.f};
+        if (jb <= (w | 1)) {
+          f32x4 z = {0.f, 0.f, 0.f, 0.f}, gm = {0.f, 0.f, 0.f, 0.f};
+          if (jb <= w) {
+            f32x4 W = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) W = mma(op_straight<64>(sx, 16 * jb, 32 * ks), yv[ks], W);
+            const double* Lj = sL + 16 * jb + 4 * g;
+            const f32x4 dj = *reinterpret_cast<const f32x4*>(sd + 16 * jb + 4 * g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int j = 16 * jb + 4 * g + r;
+              const float m = j <= 16 * w + i ? ex2((float)(Li - Lj[r])) : 0.f;
+              gm[r] = G[jb][r] * m;
+              z[r] = W[r] * (m * dj[r]);
+              const float K = gm[r] * W[r];
+              if (j == 16 * w + i) {  // in the row's and the column's sum alike: kept out of their difference
+                s_diag[j] = K;
+                trace += W[r];
+              } else {
+                col[r] = K;
+                row = __builtin_fmaf(dj[r], K, row);
+              }
+            }
+          }
+          *reinterpret_cast<u32x2*>(sZ + swz4<64>(16 * w + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(z[0], z[1]), pk_bf16(z[2], z[3])};
+          *reinterpret_cast<u32x2*>(sG + swz4<64>(16 * w + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(gm[0], gm[1]), pk_bf16(gm[2], gm[3])};
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float c = row16_sum(col[r]);
+          if (i == 15) s_col[w][16 * jb + 4 * g + r] = c;
+        }
+      }
+      row = across16(row);
+      if (g == 0) s_row[16 * w + i] = row;
+      trace = wave_sum(trace);
+      if (lane == 0) s_trace[w] = trace;
+    }
+    __syncthreads();
+
+    {  // dC and the rows' sums with S
+      float rint[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+        for (int ib = 0; ib < 4; ++ib) {
+          f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            const bf16x8 y = op_split<64>(sy, 16 * ib, 32 * ks);
+            v = mma(__builtin_bit_cast(bf16x8, Sh[nb][ks]), y, v);
+            v = mma(__builtin_bit_cast(bf16x8, Sl[nb][ks]), y, v);
+          }
+          v *= se[16 * ib + i];
+          const u32x2 c = *reinterpret_cast<const u32x2*>(sC + swz4<NT>(16 * ib + i, nw + 16 * nb + 4 * g));
+          rint[ib] += v[0] * bf_lo(c.x) + v[1] * bf_hi(c.x) + v[2] * bf_lo(c.y) + v[3] * bf_hi(c.y);
+          f32x4 acc = dC[nb][ib] + v;
+#pragma unroll
+          for (int ks = 0; ks <= ib / 2; ++ks)
+            acc = mma(op_cols<NT>(sB, 32 * ks, nw + 16 * nb), op_split<64>(sZ, 16 * ib, 32 * ks), acc);
+          dC[nb][ib] = acc;
+        }
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) {
+        const float v = across16(rint[ib]);
+        if (g == 0) s_rint[w][16 * ib + i] = v;
+      }
+    }
+    {  // dB and the rows' sums with T
+      float u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb) {
+          f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            const bf16x8 x = op_split<64>(sx, 16 * jb, 32 * ks);
+            v = mma(__builtin_bit_cast(bf16x8, Th[nb][ks]), x, v);
+            v = mma(__builtin_bit_cast(bf16x8, Tl[nb][ks]), x, v);
+          }
+          v *= sr[16 * jb + i];
+          const u32x2 c = *reinterpret_cast<const u32x2*>(sB + swz4<NT>(16 * jb + i, nw + 16 * nb + 4 * g));
+          u[jb] += v[0] * bf_lo(c.x) + v[1] * bf_hi(c.x) + v[2] * bf_lo(c.y) + v[3] * bf_hi(c.y);
+          f32x4 acc = dB[nb][jb] + v * sd[16 * jb + i];
+#pragma unroll
+          for (int ks = jb / 2; ks < 2; ++ks)
+            acc = mma(op_cols<NT>(sC, 32 * ks, nw + 16 * nb), op_cols<64>(sZ, 32 * ks, 16 * jb), acc);
+          dB[nb][jb] = acc;
+        }
+#pragma unroll
+      for (int jb = 0; jb < 4; ++jb) {
+        const float v = across16(u[jb]);
+        if (g == 0) s_u[w][16 * jb + i] = v;
+      }
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float s0 = bf_lo(Sh[nb][ks][e]) + bf_lo(Sl[nb][ks][e]), t0 = bf_lo(Th[nb][ks][e]) + bf_lo(Tl[nb][ks][e]);
+          const float s1 = bf_hi(Sh[nb][ks][e]) + bf_hi(Sl[nb][ks][e]), t1 = bf_hi(Th[nb][ks][e]) + bf_hi(Tl[nb][ks][e]);
+          dot = __builtin_fmaf(s0, t0, __builtin_fmaf(s1, t1, dot));
+        }
+    dot = wave_sum(dot);
+    if (lane == 0) s_dot[w] = dot;
+    if (t + 1 < tiles) load_states(t + 1);
+
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const bf16x8 y = op_cols<64>(sy, 32 * ks, 16 * w);
+#pragma unroll
+      for (int jb = 0; jb < 2 * ks + 2; ++jb) dX[jb] = mma(y, op_cols<64>(sG, 32 * ks, 16 * jb), dX[jb]);
+    }
+    const int p_out = 16 * w + 4 * g;
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) {
+      const int row = 16 * jb + i;
+      const float d = sd[row];
+      const u32x2 yv = *reinterpret_cast<const u32x2*>(sy + swz4<64>(row, p_out));
+      const u32x2 o = {pk_bf16(d * dX[jb][0] + Dh * bf_lo(yv.x), d * dX[jb][1] + Dh * bf_hi(yv.x)),
+                       pk_bf16(d * dX[jb][2] + Dh * bf_lo(yv.y), d * dX[jb][3] + Dh * bf_hi(yv.y))};
+      if (row < rows) {
+        uint16_t* dst = b.dx + (pc.r0 + row) * b.dx_ld + (int64_t)h * a.P + p_first + p_out;
+        if (VEC || p_out + 3 < pn) {
+          if (p_out < pn) *reinterpret_cast<u32x2_a2*>(dst) = o;
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (p_out + r < pn) dst[r] = (uint16_t)(o[r >> 1] >> (16 * (r & 1)));
+        }
+      }
+    }
+    __syncthreads();
+
+    if (w == 0) {  // lane = row: the gradients of the decays and steps
+      const float d = sd[lane];
+      float rint = 0.f, u = 0.f, col = 0.f, dots = 0.f, trace = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        rint += s_rint[k][lane];
+        u += s_u[k][lane];
+        col += s_col[k][lane];
+        dots += s_dot[k];
+        trace += s_trace[k];
+      }
+      const float from_later = rint + (s_row[lane] - d * col);
+      const float suffix = __shfl(wave_prefix(__shfl(from_later, 63 - lane)), 63 - lane);  // rows >= this one
+      const float before = dpp0<0x138, 0xf>(wave_prefix(d * u));                            // rows < this one
+      dl_sum += se[63] * dots + suffix + before;
+      q_sum += col + s_diag[lane] + u;
+      trace_sum += trace;
+      if (ptile + 1 == a.ptiles) {
+        const float step = a.A[h] * dl_sum + q_sum;
+        const float raw = a.softplus ? step * -expm1f(-d) : step;  // softplus' = 1 - e^{-softplus}
+        if (lane < rows) {
+          const int64_t o = (pc.r0 + lane) * b.ddt_ld + h;
+          if (a.dt_f32) static_cast<float*>(b.ddt)[o] = raw;
+          else static_cast<uint16_t*>(b.ddt)[o] = to_bf16(raw);
+        }
+        const float sum_A = wave_sum(lane < rows ? d * dl_sum : 0.f), sum_b = wave_sum(lane < rows ? raw : 0.f);
+        if (lane == 0) {
+          float* dst = b.head_part + (id * a.H + h) * 3;
+          dst[0] = sum_A;
+          dst[1] = sum_b;
+          dst[2] = trace_sum;
+        }
+        dl_sum = q_sum = trace_sum = 0.f;
+      }
+    }
+  }
+
+#pragma unroll
+  for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = 16 * k + i, n = nw + 16 * nb + 4 * g;
+      if (row >= rows || n >= a.N) continue;
+      const int64_t r = pc.r0 + row;
+      if (b.hsplit > 1) {
+        const int64_t width = (int64_t)a.G * a.N;
+        float* dst = b.bc_part + ((int64_t)part * a.q.rows + r) * width + gn + n;
+        const int64_t other = (int64_t)b.hsplit * a.q.rows * width;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < a.N) {
+            dst[e] = dB[nb][k][e];
+            dst[other + e] = dC[nb][k][e];
+          }
+      } else {
+        uint16_t *pB = b.dB + r * b.dB_ld + gn + n, *pC = b.dC + r * b.dC_ld + gn + n;
+        const u32x2 vB = {pk_bf16(dB[nb][k][0], dB[nb][k][1]), pk_bf16(dB[nb][k][2], dB[nb][k][3])};
+        const u32x2 vC = {pk_bf16(dC[nb][k][0], dC[nb][k][1]), pk_bf16(dC[nb][k][2], dC[nb][k][3])};
+        if (VEC || n + 3 < a.N) {
+          *reinterpret_cast<u32x2_a2*>(pB) = vB;
+          *reinterpret_cast<u32x2_a2*>(pC) = vC;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < a.N) {
+              pB[e] = (uint16_t)(vB[e >> 1] >> (16 * (e & 1)));
+              pC[e] = (uint16_t)(vC[e >> 1] >> (16 * (e & 1)));
+            }
+        }
+      }
+    }
+}
+
+// dB, dC from the head parts, in ascending order of the parts
+__global__ __launch_bounds__(256) void ssm_bc_reduce_kernel(ScanBwdArgs b) {
+  const int64_t width = (int64_t)b.s.G * b.s.N, rows = b.s.q.rows;
+  const int64_t end = b.s.q.cu ? cu_at(b.s.q, b.s.q.nseq) : rows;
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= end * width) return;
+  const float* src = b.bc_part + (blockIdx.y ? (int64_t)b.hsplit * rows * width : 0) + e;
+  float s = src[0];
+  for (int k = 1; k < b.hsplit; ++k) s += src[(int64_t)k * rows * width];
+  const int64_t row = e / width, c = e % width;
+  if (blockIdx.y) b.dC[row * b.dC_ld + c] = to_bf16(s);
+  else b.dB[row * b.dB_ld + c] = to_bf16(s);
+}
+
+// dA, d(dt_bias), dD of one head: the chunks' sums, 256 strided subsets and then a fixed tree
+__global__ __launch_bounds__(256) void ssm_head_reduce_kernel(ScanBwdArgs b, int64_t ids) {
+  __shared__ float lds[4][3];
+  const int h = blockIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  float s[3] = {0.f, 0.f, 0.f};
+  for (int64_t id = threadIdx.x; id < ids; id += 256) {
+    const float* src = b.head_part + (id * b.s.H + h) * 3;
+#pragma unroll
+    for (int e = 0; e < 3; ++e) s[e] += src[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+    const float v = wave_sum(s[e]);
+    if (lane == 0) lds[w][e] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    const int e = threadIdx.x;
+    const float v = lds[0][e] + lds[1][e] + lds[2][e] + lds[3][e];
+    float* dst = e == 0 ? b.dA : (e == 1 ? b.dbias : b.dD);
+    if (dst) dst[h] = v;
+  }
+}
+
+template <int NT, bool VEC>
+static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
+  const ScanArgs& a = b.s;
+  const int64_t hp = (int64_t)a.H * a.ptiles, items = a.n_slots + a.q.nseq, ids = b.n_chunk_slots + a.q.nseq;
+  StateArgs f{}, r{};
+  f.s = r.s = a;
+  f.u = a.x, f.u_ld = a.x_ld, f.v = a.B, f.v_ld = a.B_ld;
+  r.u = b.dy, r.u_ld = b.dy_ld, r.v = a.C, r.v_ld = a.C_ld;
+  f.start = a.init, f.piece = a.piece, f.store = b.cs;
+  r.start = b.dfin, r.piece = b.piece_t, r.store = b.ct, r.end = b.dinit;
+  f.n_chunk_slots = r.n_chunk_slots = b.n_chunk_slots;
+  if (a.q.nseq == 0) {  // no sequences: the parameters' gradients are zero
+    ssm_head_reduce_kernel<<<dim3((uint32_t)a.H), 256, 0, s>>>(b, 0);
+    return hipGetLastError();
+  }
+  const dim3 walk((uint32_t)(items * hp), 2);
+  if (a.seg > 0) {
+    const dim3 join((uint32_t)(a.q.nseq * hp * (64 * NT / 1024)));
+    ssm_states_kernel<NT, VEC, false><<<walk, 256, 0, s>>>(f, r);
+    ssm_join_kernel<NT, false><<<join, 256, 0, s>>>(f);
+    ssm_join_kernel<NT, true><<<join, 256, 0, s>>>(r);
+  }
+  ssm_states_kernel<NT, VEC, true><<<walk, 256, 0, s>>>(f, r);
+  ssm_scan_bwd_kernel<NT, VEC><<<dim3((uint32_t)(ids * a.G * b.hsplit)), 256, 0, s>>>(b);
+  if (b.hsplit > 1 && a.q.rows > 0) {
+    const int64_t n = a.q.rows * a.G * a.N;
+    ssm_bc_reduce_kernel<<<dim3((uint32_t)((n + 255) / 256), 2), 256, 0, s>>>(b);
+  }
+  ssm_head_reduce_kernel<<<dim3((uint32_t)a.H), 256, 0, s>>>(b, ids);
+  return hipGetLastError();
+}
+
+hipError_t launch_scan_bwd(const ScanBwdArgs& b, bool vec, hipStream_t s) {
+  switch (state_tile(b.s.N)) {
+    case 64: return vec ? launch<64, true>(b, s) : launch<64, false>(b, s);
+    case 128: return vec ? launch<128, true>(b, s) : launch<128, false>(b, s);
+    default: return vec ? launch<256, true>(b, s) : launch<256, false>(b, s);
+  }
+}
+
+}  // namespace cssm

@@ -1,0 +1,262 @@
+// ssm_state.h -- the walk of the state alone, over the chunks of a piece, forward or in reverse.
+//
+//   forward  S' = e^{L_Q} S + sum_j e^{L_Q - L_j} dt_j x_j B_j^T        (u = x, v = B)
+//   reverse  T' = e^{L_Q} T + sum_i e^{L_i} dy_i C_i^T                   (u = dy, v = C)
+//
+// with L the inclusive prefix sums of l_t = dt_t A over the chunk.  States are FP32 results held in
+// registers over the whole walk; the weights multiply u in FP32, and the product enters the matrix
+// instructions as a high and a low bf16 part, so a state is right to about 2^-16 of its terms (one bf16
+// part would leave 2^-8).  Decays to the chunk's end are summed from the end, so that the last tokens of
+// a fast-decaying chunk keep exact weights.
+#pragma once
+
+#include "ssm_device.h"
+
+namespace cssm {
+
+struct StateArgs {
+  ScanArgs s;              // sequences, pieces, decays, head counts, slot mapping
+  const uint16_t* u;       // [rows, H, P]
+  const uint16_t* v;       // [rows, G, N]
+  int64_t u_ld, v_ld;
+  const float* start;      // state before the walk [slot or seq, H, P, N], nullptr: zeros
+  float* end;              // reverse: state after the walk at the sequence's start, or nullptr
+  float* piece;            // [item, H * ptiles, 64, NT]
+  uint16_t* store;         // chunk states (STORE), planes of `plane` elements
+  int64_t n_chunk_slots, plane;
+};
+
+// log2 decay of row r0 + lane (0 past the chunk's rows) and its step size
+__device__ __forceinline__ float row_decay(const ScanArgs& a, int64_t row, bool in, int h, float A2, float bias, float& d) {
+  const float raw = load_num(a.dt, row * a.dt_ld + h, a.dt_f32) + bias;
+  d = in ? step_size(raw, a.softplus) : 0.f;
+  return d * A2;
+}
+
+// slot of a sequence's state, and whether it has one
+__device__ __forceinline__ bool state_slot(const ScanArgs& a, int64_t seq, int64_t& slot) {
+  slot = a.ci ? a.ci[seq] : seq;
+  if (!a.ci) return true;
+  return slot >= 0 && slot < a.slots;
+}
+__device__ __forceinline__ bool starts_from_state(const ScanArgs& a, int64_t seq) {
+  return a.init && (!a.has_init || a.has_init[seq]);
+}
+
+// LOCAL: from zeros, the end state goes to the piece's place (pieces whose end nobody needs do nothing).
+// STORE: from the piece's start state (or the sequence's), every chunk's start state goes to `store`.
+template <int NT>
+struct StateShared {
+  __align__(16) uint16_t u[64 * 64];
+  __align__(16) uint16_t v[64 * NT];
+  __align__(16) float w[64];
+  float total;
+};
+template <int NT, bool VEC, bool REV, bool STORE>
+__device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& sh) {
+  constexpr int NB = NT / 32;  // 16-column blocks a wave holds: a wave has 32 rows p and NT / 2 columns n
+  uint16_t *su = sh.u, *sv = sh.v;
+  float* sw = sh.w;
+  const ScanArgs& a = k.s;
+  const int hp = a.H * a.ptiles;
+  const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
+  const int64_t item = blk / hp;
+  const int head_tile = blk % hp, h = head_tile / a.ptiles, p_first = head_tile % a.ptiles * kPTile;
+  const Piece pc = find_piece(a.q, item, a.seg, a.n_slots);
+  const bool first = pc.r0 == pc.s, last = pc.r1 == pc.e;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, i = lane & 15;
+  const int p0 = (w & 1) * 32, n0 = (w >> 1) * (NT / 2);
+  const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
+  if (!pc.ok) {
+    // an empty sequence's adjoint passes through
+    if (REV && STORE && k.end && item >= a.n_slots) {
+      for (int e = threadIdx.x; e < pn * a.N; e += 256) {
+        const int64_t o = ((pc.seq * a.H + h) * a.P + p_first) * a.N + e;
+        k.end[o] = k.start ? k.start[o] : 0.f;
+      }
+    }
+    return;
+  }
+  if (!STORE && (REV ? first : last)) return;
+
+  f32x4 S[2][NB];
+#pragma unroll
+  for (int pb = 0; pb < 2; ++pb)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) S[pb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if constexpr (STORE) {
+    if (a.seg > 0) {
+      const float* src = k.piece + (item * hp + head_tile) * (64 * NT);
+#pragma unroll
+      for (int pb = 0; pb < 2; ++pb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[pb][nb][r] = src[(p0 + 16 * pb + 4 * g + r) * NT + n0 + 16 * nb + i];
+    } else if (k.start) {
+      const float* src = k.start + ((pc.seq * a.H + h) * a.P + p_first) * a.N;
+#pragma unroll
+      for (int pb = 0; pb < 2; ++pb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int p = p0 + 16 * pb + 4 * g + r, n = n0 + 16 * nb + i;
+            if (p < pn && n < a.N) S[pb][nb][r] = src[(int64_t)p * a.N + n];
+          }
+    }
+  }
+
+  const float A2 = a.A[h] * kLog2e, bias = a.bias ? a.bias[h] : 0.f;
+  const uint16_t* ub = k.u + (int64_t)h * a.P + p_first;
+  const uint16_t* vb = k.v + (int64_t)(h / (a.H / a.G)) * a.N;
+  float log_total = 0.f;
+  TileRegs<64> tu;
+  TileRegs<NT> tv;
+  int64_t c0 = REV ? (pc.r1 - 1) / kChunk * kChunk : pc.r0;
+  if (REV && c0 < pc.r0) c0 = pc.r0;
+  int64_t c1 = chunk_end(c0, pc.r1);
+  load_tile<64, VEC>(tu, ub + c0 * k.u_ld, k.u_ld, (int)(c1 - c0), pn);
+  load_tile<NT, VEC>(tv, vb + c0 * k.v_ld, k.v_ld, (int)(c1 - c0), a.N);
+  while (true) {
+    store_tile<64>(su, tu);
+    store_tile<NT>(sv, tv);
+    if (w == 0) {
+      float d;
+      if constexpr (REV) {
+        const bool in = c0 + lane < c1;
+        const float L = wave_prefix(row_decay(a, in ? c0 + lane : c0, in, h, A2, bias, d));
+        sw[lane] = ex2(L);
+        if (lane == 63) sh.total = L;
+      } else {
+        const int64_t row = c0 + 63 - lane;  // lanes from the chunk's end
+        const bool in = row < c1;
+        const float R = wave_prefix(row_decay(a, in ? row : c0, in, h, A2, bias, d));
+        sw[63 - lane] = ex2(dpp0<0x138, 0xf>(R)) * d;  // the rows after this one: the previous lane's sum
+        if (lane == 63) sh.total = R;
+      }
+    }
+    __syncthreads();
+    const int64_t here = c0;
+    const bool more = REV ? c0 > pc.r0 : c1 < pc.r1;
+    if (more) {
+      c0 = REV ? (c0 - 1) / kChunk * kChunk : c1;
+      if (REV && c0 < pc.r0) c0 = pc.r0;
+      c1 = chunk_end(c0, pc.r1);
+      load_tile<64, VEC>(tu, ub + c0 * k.u_ld, k.u_ld, (int)(c1 - c0), pn);
+      load_tile<NT, VEC>(tv, vb + c0 * k.v_ld, k.v_ld, (int)(c1 - c0), a.N);
+    }
+    if constexpr (STORE) {  // operand order: [n block of 16][p step of 32][lane] 16 bytes, high plane then low
+      const int64_t id = here == pc.s ? k.n_chunk_slots + pc.seq : here / kChunk;
+      uint16_t* dst = k.store + (id * hp + head_tile) * (2 * 64 * NT);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        u32x4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = S[e >> 1][nb][2 * (e & 1)], y = S[e >> 1][nb][2 * (e & 1) + 1];
+          hi[e] = pk_bf16(x, y);
+          lo[e] = pk_bf16(x - bf_lo(hi[e]), y - bf_hi(hi[e]));
+        }
+        const int64_t o = (((n0 >> 4) + nb) * 2 + (w & 1)) * 64 + lane;
+        reinterpret_cast<u32x4*>(dst)[o] = hi;
+        reinterpret_cast<u32x4*>(dst + 64 * NT)[o] = lo;
+      }
+    }
+    const float total = sh.total;
+    log_total += total;
+    const float et = ex2(total);
+#pragma unroll
+    for (int pb = 0; pb < 2; ++pb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) S[pb][nb] *= et;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const f32x4 wa = *reinterpret_cast<const f32x4*>(sw + 32 * ks + 4 * g);
+      const f32x4 wb = *reinterpret_cast<const f32x4*>(sw + 32 * ks + 16 + 4 * g);
+      bf16x8 hi[2], lo[2];
+#pragma unroll
+      for (int pb = 0; pb < 2; ++pb) split_scaled(op_cols<64>(su, 32 * ks, p0 + 16 * pb), wa, wb, hi[pb], lo[pb]);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const bf16x8 b = op_cols<NT>(sv, 32 * ks, n0 + 16 * nb);
+#pragma unroll
+        for (int pb = 0; pb < 2; ++pb) {
+          S[pb][nb] = mma(hi[pb], b, S[pb][nb]);
+          S[pb][nb] = mma(lo[pb], b, S[pb][nb]);
+        }
+      }
+    }
+    if (!more) break;
+    __syncthreads();
+  }
+
+  if constexpr (!STORE) {
+    float* dst = k.piece + (item * hp + head_tile) * (64 * NT);
+#pragma unroll
+    for (int pb = 0; pb < 2; ++pb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) dst[(p0 + 16 * pb + 4 * g + r) * NT + n0 + 16 * nb + i] = S[pb][nb][r];
+    if (threadIdx.x == 0 && head_tile % a.ptiles == 0) a.piece_decay[item * a.H + h] = log_total;
+  } else if (REV && first && k.end) {
+    float* dst = k.end + ((pc.seq * a.H + h) * a.P + p_first) * a.N;
+#pragma unroll
+    for (int pb = 0; pb < 2; ++pb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int p = p0 + 16 * pb + 4 * g + r, n = n0 + 16 * nb + i;
+          if (p < pn && n < a.N) dst[(int64_t)p * a.N + n] = S[pb][nb][r];
+        }
+  }
+}
+
+template <int NT, bool VEC>
+__global__ __launch_bounds__(256, 2) void ssm_state_local_kernel(StateArgs k) {
+  __shared__ StateShared<NT> sh;
+  state_walk<NT, VEC, false, false>(k, sh);
+}
+
+// Local end states of a sequence's pieces -> start states, in place, in the order of the walk:
+// start[m + 1] = decay[m] start[m] + local[m].  One thread per four columns of a state.
+template <int NT, bool REV>
+__global__ __launch_bounds__(256) void ssm_join_kernel(StateArgs k) {
+  const ScanArgs& a = k.s;
+  constexpr int kPer = 64 * NT / 4 / 256;  // blocks a tile
+  const int hp = a.H * a.ptiles;
+  const int64_t seq = blockIdx.x / ((int64_t)hp * kPer);
+  const int rest = blockIdx.x % (hp * kPer), head_tile = rest / kPer, h = head_tile / a.ptiles;
+  const int at = (rest % kPer * 256 + threadIdx.x) * 4, p = at / NT, n = at % NT;
+  const int p_abs = head_tile % a.ptiles * kPTile + p;
+  int64_t s, e;
+  seq_bounds(a.q, seq, s, e);
+  if (e <= s) return;
+  int64_t slot = seq;
+  const bool live = state_slot(a, seq, slot);
+  const bool from = REV ? k.start != nullptr : live && starts_from_state(a, seq);
+  f32x4 S = {0.f, 0.f, 0.f, 0.f};
+  if (from && p_abs < a.P) {
+    const float* src = k.start + (REV ? seq * (int64_t)a.H * a.P * a.N : slot * a.s_slot) + ((int64_t)h * a.P + p_abs) * a.N;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (n + r < a.N) S[r] = src[n + r];
+  }
+  const int64_t slot0 = s / a.seg + 1, pieces = (e - 1) / a.seg - s / a.seg + 1;
+  for (int64_t m = 0; m < pieces; ++m) {
+    const int64_t j = REV ? pieces - 1 - m : m;
+    const int64_t item = j == 0 ? a.n_slots + seq : slot0 + j - 1;
+    f32x4* place = reinterpret_cast<f32x4*>(k.piece + (item * hp + head_tile) * (64 * NT) + at);
+    if (m + 1 == pieces) {
+      *place = S;
+    } else {
+      const f32x4 local = *place;
+      *place = S;
+      S = S * ex2(a.piece_decay[item * a.H + h]) + local;
+    }
+  }
+}
+
+}  // namespace cssm
