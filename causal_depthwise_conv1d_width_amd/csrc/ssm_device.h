@@ -166,16 +166,15 @@ __device__ __forceinline__ int64_t chunk_end(int64_t r, int64_t r1) {
 }
 
 // ------------------------------------------------------------------ tiles of 64 rows in shared memory
-// [64][W] bf16, row-major, 16-byte pieces of a row permuted by the row number so that 16 rows' same
-// piece, and the transposing reads of 4 rows by 16 columns, fall on different banks (64 banks of 4
-// bytes: two 128-byte rows or one longer row a turn).
+// [64][W] bf16, row-major, rows 16 bytes further apart than their length: 16 rows' same 16-byte piece,
+// and the transposing reads of 4 rows by 16 columns a quarter wave, then fall on different banks (64
+// of 4 bytes), and every address is one lane's base plus a constant.  (A permutation of each row's pieces
+// has no such constants: its addresses took over a hundred registers.)
 template <int W>
-__device__ __forceinline__ int swz(int row, int piece) {
-  return row * W + ((piece ^ (W == 64 ? (row >> 1) & 7 : row & 15)) << 3);
-}
+constexpr int kLd = W + 8;
 template <int W>
-__device__ __forceinline__ int swz4(int row, int col) {  // col a multiple of 4
-  return swz<W>(row, col >> 3) + (col & 4);
+__device__ __forceinline__ int at(int row, int col) {
+  return row * kLd<W> + col;
 }
 
 template <int W>
@@ -214,7 +213,7 @@ __device__ __forceinline__ void store_tile(uint16_t* lds, const TileRegs<W>& t) 
 #pragma unroll
   for (int k = 0; k < W / 32; ++k) {
     const int q = threadIdx.x + 256 * k;
-    *reinterpret_cast<u32x4*>(lds + swz<W>(q / (W / 8), q % (W / 8))) = t.v[k];
+    *reinterpret_cast<u32x4*>(lds + at<W>(q / (W / 8), q % (W / 8) * 8)) = t.v[k];
   }
 }
 
@@ -231,14 +230,14 @@ __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
 template <int W>
 __device__ __forceinline__ bf16x8 op_straight(const uint16_t* lds, int row0, int k0) {
   const int l = threadIdx.x & 63;
-  return *reinterpret_cast<const bf16x8*>(lds + swz<W>(row0 + (l & 15), (k0 >> 3) + (l >> 4)));
+  return *reinterpret_cast<const bf16x8*>(lds + at<W>(row0 + (l & 15), k0 + (l >> 4) * 8));
 }
 // the same, split
 template <int W>
 __device__ __forceinline__ bf16x8 op_split(const uint16_t* lds, int row0, int k0) {
   const int l = threadIdx.x & 63, row = row0 + (l & 15), c = k0 + (l >> 4) * 4;
-  const u32x2 a = *reinterpret_cast<const u32x2*>(lds + swz4<W>(row, c));
-  const u32x2 b = *reinterpret_cast<const u32x2*>(lds + swz4<W>(row, c + 16));
+  const u32x2 a = *reinterpret_cast<const u32x2*>(lds + at<W>(row, c));
+  const u32x2 b = *reinterpret_cast<const u32x2*>(lds + at<W>(row, c + 16));
   const u32x4 v = {a.x, a.y, b.x, b.y};
   return __builtin_bit_cast(bf16x8, v);
 }
@@ -247,8 +246,8 @@ __device__ __forceinline__ bf16x8 op_split(const uint16_t* lds, int row0, int k0
 template <int W>
 __device__ __forceinline__ bf16x8 op_cols(const uint16_t* lds, int k0, int c0) {
   const int l = threadIdx.x & 63, row = k0 + (l >> 4) * 4 + ((l & 15) >> 2), c = c0 + (l & 3) * 4;
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + swz4<W>(row, c)));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + swz4<W>(row + 16, c)));
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at<W>(row, c)));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at<W>(row + 16, c)));
   const u32x2 ua = __builtin_bit_cast(u32x2, a), ub = __builtin_bit_cast(u32x2, b);
   const u32x4 v = {ua.x, ua.y, ub.x, ub.y};
   return __builtin_bit_cast(bf16x8, v);

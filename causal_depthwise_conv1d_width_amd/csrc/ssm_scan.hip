@@ -12,11 +12,11 @@ namespace cssm {
 template <int NT, bool VEC>
 __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_fwd_kernel(ScanArgs a) {
   constexpr int NB = NT / 16;
-  __shared__ __align__(16) uint16_t sx[64 * 64];
-  __shared__ __align__(16) uint16_t sB[64 * NT];
-  __shared__ __align__(16) uint16_t sC[64 * NT];
-  __shared__ __align__(16) uint16_t sP[64 * 64];
-  __shared__ __align__(16) float sL[64], sd[64], se[64], sw[64];
+  __shared__ __align__(16) uint16_t sx[64 * kLd<64>];
+  __shared__ __align__(16) uint16_t sB[64 * kLd<NT>];
+  __shared__ __align__(16) uint16_t sC[64 * kLd<NT>];
+  __shared__ __align__(16) uint16_t sP[64 * kLd<64>];
+  __shared__ __align__(16) float sdecay[2][4][64];  // this chunk's and the next one's
   const int hp = a.H * a.ptiles;
   const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
   const int64_t item = blk / hp;
@@ -65,44 +65,55 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_fwd_kernel(Sca
     }
   }
 
-  const float A2 = a.A[h] * kLog2e, bias = a.bias ? a.bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
+  const Rate rate(a, h);
+  const float Dh = a.D ? a.D[h] : 0.f;
   const uint16_t* xb = a.x + (int64_t)h * a.P + p_first;
   const int64_t gn = (int64_t)(h / (a.H / a.G)) * a.N;
   const uint16_t *Bb = a.B + gn, *Cb = a.C + gn;
   TileRegs<64> tx;
   TileRegs<NT> tB, tC;
-  int64_t c0 = pc.r0, c1 = chunk_end(c0, pc.r1);
-  load_tile<64, VEC>(tx, xb + c0 * a.x_ld, a.x_ld, (int)(c1 - c0), pn);
-  load_tile<NT, VEC>(tB, Bb + c0 * a.B_ld, a.B_ld, (int)(c1 - c0), a.N);
-  load_tile<NT, VEC>(tC, Cb + c0 * a.C_ld, a.C_ld, (int)(c1 - c0), a.N);
-  while (true) {
+  // a chunk's decays into buffer `at`: wave 0 the prefix sums, steps and their powers, wave 1, whose lanes
+  // count from the chunk's end, the weights of the state update
+  float raw = 0.f;
+  const int my = w == 0 ? lane : 63 - lane;
+  auto decays = [&](const Chunks<false>& c, int at) {
+    const float d = rate.step(raw, my < c.rows());
+    const float L = wave_prefix(d * rate.A2);
+    if (w == 0) {
+      sdecay[at][0][lane] = L;
+      sdecay[at][1][lane] = d;
+      sdecay[at][2][lane] = ex2(L);
+    } else {
+      sdecay[at][3][my] = ex2(dpp0<0x138, 0xf>(L)) * d;
+    }
+  };
+  Chunks<false> c(pc.r0, pc.r1);
+  load_tile<64, VEC>(tx, xb + c.c0 * a.x_ld, a.x_ld, c.rows(), pn);
+  load_tile<NT, VEC>(tB, Bb + c.c0 * a.B_ld, a.B_ld, c.rows(), a.N);
+  load_tile<NT, VEC>(tC, Cb + c.c0 * a.C_ld, a.C_ld, c.rows(), a.N);
+  if (w < 2) {
+    raw = raw_step(a, c.c0 + my, c.c0, c.c1, h);
+    decays(c, 0);
+    if (!c.last()) raw = raw_step(a, c.next().c0 + my, c.next().c0, c.next().c1, h);
+  }
+  for (int buf = 0;; buf ^= 1) {
     store_tile<64>(sx, tx);
     store_tile<NT>(sB, tB);
     store_tile<NT>(sC, tC);
-    if (w == 0) {
-      float d;
-      const bool in = c0 + lane < c1;
-      const float L = wave_prefix(row_decay(a, in ? c0 + lane : c0, in, h, A2, bias, d));
-      sL[lane] = L;
-      sd[lane] = d;
-      se[lane] = ex2(L);
-    } else if (w == 1) {  // from the chunk's end: weights of the state update
-      float d;
-      const int64_t row = c0 + 63 - lane;
-      const bool in = row < c1;
-      const float R = wave_prefix(row_decay(a, in ? row : c0, in, h, A2, bias, d));
-      sw[63 - lane] = ex2(dpp0<0x138, 0xf>(R)) * d;
-    }
     __syncthreads();
-    const int64_t r0 = c0;
-    const int rows = (int)(c1 - c0);
-    const bool more = c1 < pc.r1;
+    const int64_t r0 = c.c0;
+    const int rows = c.rows();
+    const bool more = !c.last();
+    const float *sL = sdecay[buf][0], *sd = sdecay[buf][1], *se = sdecay[buf][2], *sw = sdecay[buf][3];
     if (more) {
-      c0 = c1;
-      c1 = chunk_end(c0, pc.r1);
-      load_tile<64, VEC>(tx, xb + c0 * a.x_ld, a.x_ld, (int)(c1 - c0), pn);
-      load_tile<NT, VEC>(tB, Bb + c0 * a.B_ld, a.B_ld, (int)(c1 - c0), a.N);
-      load_tile<NT, VEC>(tC, Cb + c0 * a.C_ld, a.C_ld, (int)(c1 - c0), a.N);
+      c = c.next();
+      load_tile<64, VEC>(tx, xb + c.c0 * a.x_ld, a.x_ld, c.rows(), pn);
+      load_tile<NT, VEC>(tB, Bb + c.c0 * a.B_ld, a.B_ld, c.rows(), a.N);
+      load_tile<NT, VEC>(tC, Cb + c.c0 * a.C_ld, a.C_ld, c.rows(), a.N);
+      if (w < 2) {  // these waves have the fewer score blocks
+        decays(c, buf ^ 1);
+        if (!c.last()) raw = raw_step(a, c.next().c0 + my, c.next().c0, c.next().c1, h);
+      }
     }
     // scores of rows 16 w .. 16 w + 15 (lanes) against columns j (registers), decayed, times dt_j
     {
@@ -126,7 +137,7 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_fwd_kernel(Sca
           }
         }
         const u32x2 o = {pk_bf16(t[0], t[1]), pk_bf16(t[2], t[3])};
-        *reinterpret_cast<u32x2*>(sP + swz4<64>(16 * w + i, 16 * jb + 4 * g)) = o;
+        *reinterpret_cast<u32x2*>(sP + at<64>(16 * w + i, 16 * jb + 4 * g)) = o;
       }
     }
     // Y^T (registers p, lanes i) from the state before the chunk
@@ -164,7 +175,7 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_fwd_kernel(Sca
 #pragma unroll
     for (int ib = 0; ib < 4; ++ib) {
       const int row = 16 * ib + i;
-      const u32x2 xv = *reinterpret_cast<const u32x2*>(sx + swz4<64>(row, p_out));
+      const u32x2 xv = *reinterpret_cast<const u32x2*>(sx + at<64>(row, p_out));
       const u32x2 o = {pk_bf16(y[ib][0] + Dh * bf_lo(xv.x), y[ib][1] + Dh * bf_hi(xv.x)),
                        pk_bf16(y[ib][2] + Dh * bf_lo(xv.y), y[ib][3] + Dh * bf_hi(xv.y))};
       if (row < rows) {

@@ -15,6 +15,8 @@
 // stored as a high and a low bf16 part, already in matrix-operand order: with both parts the row
 // sums that feed d(dt) and dA keep FP32's weight (dC and dB share those products); dx, rounded to
 // bf16 in the end, takes the high part of T.  Z and G M are rounded to bf16 once, as operands.
+#include <type_traits>
+
 #include "ssm_state.h"
 
 namespace cssm {
@@ -26,24 +28,33 @@ __global__ __launch_bounds__(256, 2) void ssm_states_kernel(StateArgs f, StateAr
   else state_walk<NT, VEC, true, STORE>(r, sh);
 }
 
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {  // two bf16 products in FP32
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
+}
 __device__ __forceinline__ float across16(float v) {  // sum over the four rows of 16 lanes
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
 }
 
+// Keeps the compiler from moving one phase's loads and products into another: with them mixed, the
+// kernel needs more registers than two blocks a CU leave it.
+__device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
+
 template <int NT, bool VEC>
 __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(ScanBwdArgs b) {
   constexpr int NBW = NT / 64;                                  // 16-column blocks n of a wave
-  constexpr int R = 64 * NT > 2 * 64 * 64 ? 64 * NT : 2 * 64 * 64;
-  __shared__ __align__(16) uint16_t sx[64 * 64];
-  __shared__ __align__(16) uint16_t sy[64 * 64];
-  __shared__ __align__(16) uint16_t sB[64 * NT];
-  __shared__ __align__(16) uint16_t sC[64 * NT];
+  constexpr int R = (NT > 128 ? NT : 128) * kLd<64>;
+  __shared__ __align__(16) uint16_t sx[64 * kLd<64>];
+  __shared__ __align__(16) uint16_t sy[64 * kLd<64>];
+  __shared__ __align__(16) uint16_t sB[64 * kLd<NT>];
+  __shared__ __align__(16) uint16_t sC[64 * kLd<NT>];
   __shared__ __align__(16) uint16_t sR[R];  // T^T [n][p], then Z and G M [i][j]
-  __shared__ __align__(16) double sL[64];  // differences of FP32 sums would lose a fast decay's weights
-  __shared__ __align__(16) float sd[64], se[64], sr[64];
-  __shared__ float s_row[64], s_diag[64], s_rint[4][64], s_u[4][64], s_col[4][64], s_dot[4], s_trace[4];
-  uint16_t *sZ = sR, *sG = sR + 64 * 64;
+  // this head's and the next one's (differences of FP32 prefix sums would lose a fast decay's weights)
+  __shared__ __align__(16) double sdecay[2][64];
+  __shared__ __align__(16) float ssteps[2][3][64];
+  __shared__ __align__(16) float s_col[4][64];
+  __shared__ float s_row[64], s_diag[64], s_rint[4][64], s_u[4][64], s_dot[4], s_trace[4];
+  uint16_t *sZ = sR, *sG = sR + 64 * kLd<64>;
   const ScanArgs& a = b.s;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, i = lane & 15;
   const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
@@ -77,6 +88,23 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
     load_tile<64, VEC>(tx, a.x + pc.r0 * a.x_ld + o, a.x_ld, rows, pn);
     load_tile<64, VEC>(ty, b.dy + pc.r0 * b.dy_ld + o, b.dy_ld, rows, pn);
   };
+  // a head's decays into its buffer: wave 0 the prefix sums, steps and powers, wave 1, whose lanes count
+  // from the chunk's end, the decays to the end
+  float raw = 0.f;
+  const int my = w == 0 ? lane : 63 - lane;
+  auto load_raw = [&](int t) { raw = raw_step(a, pc.r0 + my, pc.r0, pc.r1, h_lo + t / a.ptiles); };
+  auto decays = [&](int t) {
+    const Rate rate(a, h_lo + t / a.ptiles);
+    const float d = rate.step(raw, my < rows);
+    const double L = wave_prefix((double)(d * rate.A2));
+    if (w == 0) {
+      sdecay[t & 1][lane] = L;
+      ssteps[t & 1][0][lane] = d;
+      ssteps[t & 1][1][lane] = ex2((float)L);
+    } else {
+      ssteps[t & 1][2][my] = ex2((float)dpp0<0x138, 0xf>(L));
+    }
+  };
   auto load_states = [&](int t) {
     const int64_t o = (id * hp + h_lo * a.ptiles + t) * (2 * 64 * NT);
     const u32x4 *cs = reinterpret_cast<const u32x4*>(b.cs + o), *ct = reinterpret_cast<const u32x4*>(b.ct + o);
@@ -93,6 +121,11 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
   };
   load_rows(0);
   load_states(0);
+  if (w < 2) {
+    load_raw(0);
+    decays(0);
+    if (tiles > 1) load_raw(1);
+  }
   {
     TileRegs<NT> t;
     load_tile<NT, VEC>(t, a.B + pc.r0 * a.B_ld + gn, a.B_ld, rows, a.N);
@@ -116,31 +149,21 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
   for (int t = 0; t < tiles; ++t) {
     const int h = h_lo + t / a.ptiles, ptile = t % a.ptiles, p_first = ptile * kPTile;
     const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
-    const float A2 = a.A[h] * kLog2e, bias = a.bias ? a.bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
+    const float Dh = a.D ? a.D[h] : 0.f;
+    const double* sL = sdecay[t & 1];
+    const float *sd = ssteps[t & 1][0], *se = ssteps[t & 1][1], *sr = ssteps[t & 1][2];
     store_tile<64>(sx, tx);
     store_tile<64>(sy, ty);
-    if (w == 0) {
-      float d;
-      const bool in = lane < rows;
-      const double L = wave_prefix((double)row_decay(a, pc.r0 + (in ? lane : 0), in, h, A2, bias, d));
-      sL[lane] = L;
-      sd[lane] = d;
-      se[lane] = ex2((float)L);
-    } else if (w == 1) {
-      float d;
-      const bool in = 63 - lane < rows;
-      const float Rv = wave_prefix(row_decay(a, pc.r0 + (in ? 63 - lane : 0), in, h, A2, bias, d));
-      sr[63 - lane] = ex2(dpp0<0x138, 0xf>(Rv));
-    }
 #pragma unroll
     for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const int n = nw + 16 * nb + i;
-        *reinterpret_cast<u32x2*>(sR + swz4<64>(n, 32 * ks + 4 * g)) = u32x2{Th[nb][ks].x, Th[nb][ks].y};
-        *reinterpret_cast<u32x2*>(sR + swz4<64>(n, 32 * ks + 16 + 4 * g)) = u32x2{Th[nb][ks].z, Th[nb][ks].w};
+        *reinterpret_cast<u32x2*>(sR + at<64>(n, 32 * ks + 4 * g)) = u32x2{Th[nb][ks].x, Th[nb][ks].y};
+        *reinterpret_cast<u32x2*>(sR + at<64>(n, 32 * ks + 16 + 4 * g)) = u32x2{Th[nb][ks].z, Th[nb][ks].w};
       }
     __syncthreads();
+    phase();
     if (t + 1 < tiles) load_rows(t + 1);
 
     f32x4 dX[4];  // registers p = 16 w + 4 g + r, lanes j
@@ -154,6 +177,7 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
     }
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb) dX[jb] *= sr[16 * jb + i];
+    phase();
     __syncthreads();
 
     {  // rows i = 16 w + lane against columns j in the registers
@@ -162,47 +186,60 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
       for (int ks = 0; ks < 2; ++ks) yv[ks] = op_straight<64>(sy, 16 * w, 32 * ks);
       const double Li = sL[16 * w + i];
       float row = 0.f, trace = 0.f;
+      // one 16 x 16 block; the diagonal's K is in its row's and its column's sum alike and is kept out of both
+      auto block = [&](const int jb, auto diagonal) {
+        f32x4 W = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int jb = 0; jb < 4; ++jb) {
-        float col[4] = {0.f, 0.f, 0.f, 0.f};
-        if (jb <= (w | 1)) {
-          f32x4 z = {0.f, 0.f, 0.f, 0.f}, gm = {0.f, 0.f, 0.f, 0.f};
-          if (jb <= w) {
-            f32x4 W = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) W = mma(op_straight<64>(sx, 16 * jb, 32 * ks), yv[ks], W);
-            const double* Lj = sL + 16 * jb + 4 * g;
-            const f32x4 dj = *reinterpret_cast<const f32x4*>(sd + 16 * jb + 4 * g);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int j = 16 * jb + 4 * g + r;
-              const float m = j <= 16 * w + i ? ex2((float)(Li - Lj[r])) : 0.f;
-              gm[r] = G[jb][r] * m;
-              z[r] = W[r] * (m * dj[r]);
-              const float K = gm[r] * W[r];
-              if (j == 16 * w + i) {  // in the row's and the column's sum alike: kept out of their difference
-                s_diag[j] = K;
-                trace += W[r];
-              } else {
-                col[r] = K;
-                row = __builtin_fmaf(dj[r], K, row);
-              }
-            }
-          }
-          *reinterpret_cast<u32x2*>(sZ + swz4<64>(16 * w + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(z[0], z[1]), pk_bf16(z[2], z[3])};
-          *reinterpret_cast<u32x2*>(sG + swz4<64>(16 * w + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(gm[0], gm[1]), pk_bf16(gm[2], gm[3])};
-        }
+        for (int ks = 0; ks < 2; ++ks) W = mma(op_straight<64>(sx, 16 * jb, 32 * ks), yv[ks], W);
+        const f32x4 dj = *reinterpret_cast<const f32x4*>(sd + 16 * jb + 4 * g);
+        f32x4 z, gm;
+        float on_diagonal = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float c = row16_sum(col[r]);
+          float m = ex2((float)(Li - sL[16 * jb + 4 * g + r]));
+          if (diagonal) m = 4 * g + r <= i ? m : 0.f;
+          gm[r] = G[jb][r] * m;
+          z[r] = W[r] * (m * dj[r]);
+          float K = gm[r] * W[r];
+          if (diagonal) {
+            const bool here = 4 * g + r == i;
+            on_diagonal = here ? K : on_diagonal;
+            trace += here ? W[r] : 0.f;
+            K = here ? 0.f : K;
+          }
+          row = __builtin_fmaf(dj[r], K, row);
+          const float c = row16_sum(K);
           if (i == 15) s_col[w][16 * jb + 4 * g + r] = c;
         }
+        if (diagonal && (i >> 2) == g) s_diag[16 * w + i] = on_diagonal;
+        *reinterpret_cast<u32x2*>(sZ + at<64>(16 * w + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(z[0], z[1]), pk_bf16(z[2], z[3])};
+        *reinterpret_cast<u32x2*>(sG + at<64>(16 * w + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(gm[0], gm[1]), pk_bf16(gm[2], gm[3])};
+      };
+#pragma unroll
+      for (int jb = 0; jb < 4; ++jb) {
+        if (jb < w) {
+          block(jb, std::false_type{});
+        } else if (jb == w) {
+          block(jb, std::true_type{});
+        } else {
+          if (i == 15) *reinterpret_cast<f32x4*>(&s_col[w][16 * jb + 4 * g]) = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (jb == w + 1) {  // read with the diagonal block by products over 32 columns
+            *reinterpret_cast<u32x2*>(sZ + at<64>(16 * w + i, 16 * jb + 4 * g)) = u32x2{0u, 0u};
+            *reinterpret_cast<u32x2*>(sG + at<64>(16 * w + i, 16 * jb + 4 * g)) = u32x2{0u, 0u};
+          }
+        }
+        phase();
+      }
+      if (w < 2 && t + 1 < tiles) {  // these waves have the fewer blocks
+        decays(t + 1);
+        if (t + 2 < tiles) load_raw(t + 2);
       }
       row = across16(row);
       if (g == 0) s_row[16 * w + i] = row;
       trace = wave_sum(trace);
       if (lane == 0) s_trace[w] = trace;
     }
+    phase();
     __syncthreads();
 
     {  // dC and the rows' sums with S
@@ -219,13 +256,14 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
             v = mma(__builtin_bit_cast(bf16x8, Sl[nb][ks]), y, v);
           }
           v *= se[16 * ib + i];
-          const u32x2 c = *reinterpret_cast<const u32x2*>(sC + swz4<NT>(16 * ib + i, nw + 16 * nb + 4 * g));
+          const u32x2 c = *reinterpret_cast<const u32x2*>(sC + at<NT>(16 * ib + i, nw + 16 * nb + 4 * g));
           rint[ib] += v[0] * bf_lo(c.x) + v[1] * bf_hi(c.x) + v[2] * bf_lo(c.y) + v[3] * bf_hi(c.y);
           f32x4 acc = dC[nb][ib] + v;
 #pragma unroll
           for (int ks = 0; ks <= ib / 2; ++ks)
             acc = mma(op_cols<NT>(sB, 32 * ks, nw + 16 * nb), op_split<64>(sZ, 16 * ib, 32 * ks), acc);
           dC[nb][ib] = acc;
+          phase();
         }
 #pragma unroll
       for (int ib = 0; ib < 4; ++ib) {
@@ -247,13 +285,14 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
             v = mma(__builtin_bit_cast(bf16x8, Tl[nb][ks]), x, v);
           }
           v *= sr[16 * jb + i];
-          const u32x2 c = *reinterpret_cast<const u32x2*>(sB + swz4<NT>(16 * jb + i, nw + 16 * nb + 4 * g));
+          const u32x2 c = *reinterpret_cast<const u32x2*>(sB + at<NT>(16 * jb + i, nw + 16 * nb + 4 * g));
           u[jb] += v[0] * bf_lo(c.x) + v[1] * bf_hi(c.x) + v[2] * bf_lo(c.y) + v[3] * bf_hi(c.y);
           f32x4 acc = dB[nb][jb] + v * sd[16 * jb + i];
 #pragma unroll
           for (int ks = jb / 2; ks < 2; ++ks)
             acc = mma(op_cols<NT>(sC, 32 * ks, nw + 16 * nb), op_cols<64>(sZ, 32 * ks, 16 * jb), acc);
           dB[nb][jb] = acc;
+          phase();
         }
 #pragma unroll
       for (int jb = 0; jb < 4; ++jb) {
@@ -268,12 +307,14 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float s0 = bf_lo(Sh[nb][ks][e]) + bf_lo(Sl[nb][ks][e]), t0 = bf_lo(Th[nb][ks][e]) + bf_lo(Tl[nb][ks][e]);
-          const float s1 = bf_hi(Sh[nb][ks][e]) + bf_hi(Sl[nb][ks][e]), t1 = bf_hi(Th[nb][ks][e]) + bf_hi(Tl[nb][ks][e]);
-          dot = __builtin_fmaf(s0, t0, __builtin_fmaf(s1, t1, dot));
+          dot = dot2(Sh[nb][ks][e], Th[nb][ks][e], dot);
+          dot = dot2(Sh[nb][ks][e], Tl[nb][ks][e], dot);
+          dot = dot2(Sl[nb][ks][e], Th[nb][ks][e], dot);
+          dot = dot2(Sl[nb][ks][e], Tl[nb][ks][e], dot);
         }
     dot = wave_sum(dot);
     if (lane == 0) s_dot[w] = dot;
+    phase();
     if (t + 1 < tiles) load_states(t + 1);
 
 #pragma unroll
@@ -287,7 +328,7 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
     for (int jb = 0; jb < 4; ++jb) {
       const int row = 16 * jb + i;
       const float d = sd[row];
-      const u32x2 yv = *reinterpret_cast<const u32x2*>(sy + swz4<64>(row, p_out));
+      const u32x2 yv = *reinterpret_cast<const u32x2*>(sy + at<64>(row, p_out));
       const u32x2 o = {pk_bf16(d * dX[jb][0] + Dh * bf_lo(yv.x), d * dX[jb][1] + Dh * bf_hi(yv.x)),
                        pk_bf16(d * dX[jb][2] + Dh * bf_lo(yv.y), d * dX[jb][3] + Dh * bf_hi(yv.y))};
       if (row < rows) {

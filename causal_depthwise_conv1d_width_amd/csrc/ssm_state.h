@@ -26,12 +26,49 @@ struct StateArgs {
   int64_t n_chunk_slots, plane;
 };
 
-// log2 decay of row r0 + lane (0 past the chunk's rows) and its step size
-__device__ __forceinline__ float row_decay(const ScanArgs& a, int64_t row, bool in, int h, float A2, float bias, float& d) {
-  const float raw = load_num(a.dt, row * a.dt_ld + h, a.dt_f32) + bias;
-  d = in ? step_size(raw, a.softplus) : 0.f;
-  return d * A2;
+// Decays and step sizes of one chunk, computed by one wave with a row a lane from the raw steps, which
+// are loaded a chunk ahead (they would otherwise stand at the head of every chunk, a memory round trip
+// and a scan that all waves wait for).  Rows past the chunk's end have step 0.
+__device__ __forceinline__ float raw_step(const ScanArgs& a, int64_t row, int64_t c0, int64_t c1, int h) {
+  return load_num(a.dt, (row < c1 ? row : c0) * a.dt_ld + h, a.dt_f32);
 }
+struct Rate {
+  float A2, bias;  // A log2 e, and what is added to the raw step
+  int softplus;
+  __device__ __forceinline__ Rate(const ScanArgs& a, int h)
+      : A2(a.A[h] * kLog2e), bias(a.bias ? a.bias[h] : 0.f), softplus(a.softplus) {}
+  __device__ __forceinline__ float step(float raw, bool in) const { return in ? step_size(raw + bias, softplus) : 0.f; }
+};
+
+// The chunks of rows [r0, r1) in the order of the walk.
+template <bool REV>
+struct Chunks {
+  int64_t r0, r1, c0, c1;
+  __device__ __forceinline__ Chunks(int64_t r0_, int64_t r1_) : r0(r0_), r1(r1_) {
+    if (REV) {
+      c0 = (r1 - 1) / kChunk * kChunk;
+      if (c0 < r0) c0 = r0;
+      c1 = r1;
+    } else {
+      c0 = r0;
+      c1 = chunk_end(r0, r1);
+    }
+  }
+  __device__ __forceinline__ bool last() const { return REV ? c0 <= r0 : c1 >= r1; }
+  __device__ __forceinline__ Chunks next() const {
+    Chunks n = *this;
+    if (REV) {
+      n.c1 = c0;
+      n.c0 = (c0 - 1) / kChunk * kChunk;
+      if (n.c0 < r0) n.c0 = r0;
+    } else {
+      n.c0 = c1;
+      n.c1 = chunk_end(c1, r1);
+    }
+    return n;
+  }
+  __device__ __forceinline__ int rows() const { return (int)(c1 - c0); }
+};
 
 // slot of a sequence's state, and whether it has one
 __device__ __forceinline__ bool state_slot(const ScanArgs& a, int64_t seq, int64_t& slot) {
@@ -47,16 +84,15 @@ __device__ __forceinline__ bool starts_from_state(const ScanArgs& a, int64_t seq
 // STORE: from the piece's start state (or the sequence's), every chunk's start state goes to `store`.
 template <int NT>
 struct StateShared {
-  __align__(16) uint16_t u[64 * 64];
-  __align__(16) uint16_t v[64 * NT];
-  __align__(16) float w[64];
-  float total;
+  __align__(16) uint16_t u[64 * kLd<64>];
+  __align__(16) uint16_t v[64 * kLd<NT>];
+  __align__(16) float w[2][64];  // this chunk's weights and the next one's
+  float total[2];
 };
 template <int NT, bool VEC, bool REV, bool STORE>
 __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& sh) {
   constexpr int NB = NT / 32;  // 16-column blocks a wave holds: a wave has 32 rows p and NT / 2 columns n
   uint16_t *su = sh.u, *sv = sh.v;
-  float* sw = sh.w;
   const ScanArgs& a = k.s;
   const int hp = a.H * a.ptiles;
   const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
@@ -107,44 +143,44 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
     }
   }
 
-  const float A2 = a.A[h] * kLog2e, bias = a.bias ? a.bias[h] : 0.f;
+  const Rate rate(a, h);
   const uint16_t* ub = k.u + (int64_t)h * a.P + p_first;
   const uint16_t* vb = k.v + (int64_t)(h / (a.H / a.G)) * a.N;
-  float log_total = 0.f;
+  float log_total = 0.f, raw = 0.f;
   TileRegs<64> tu;
   TileRegs<NT> tv;
-  int64_t c0 = REV ? (pc.r1 - 1) / kChunk * kChunk : pc.r0;
-  if (REV && c0 < pc.r0) c0 = pc.r0;
-  int64_t c1 = chunk_end(c0, pc.r1);
-  load_tile<64, VEC>(tu, ub + c0 * k.u_ld, k.u_ld, (int)(c1 - c0), pn);
-  load_tile<NT, VEC>(tv, vb + c0 * k.v_ld, k.v_ld, (int)(c1 - c0), a.N);
-  while (true) {
+  // a chunk's weights into buffer `at` by wave 0; forward, a lane's row counts from the chunk's end
+  const int my = REV ? lane : 63 - lane;
+  auto weights = [&](const Chunks<REV>& c, int at) {
+    const float d = rate.step(raw, my < c.rows());
+    const float L = wave_prefix(d * rate.A2);
+    // the rows after this one: the previous lane's sum
+    sh.w[at][my] = REV ? ex2(L) : ex2(dpp0<0x138, 0xf>(L)) * d;
+    if (lane == 63) sh.total[at] = L;
+  };
+  Chunks<REV> c(pc.r0, pc.r1);
+  load_tile<64, VEC>(tu, ub + c.c0 * k.u_ld, k.u_ld, c.rows(), pn);
+  load_tile<NT, VEC>(tv, vb + c.c0 * k.v_ld, k.v_ld, c.rows(), a.N);
+  if (w == 0) {
+    raw = raw_step(a, c.c0 + my, c.c0, c.c1, h);
+    weights(c, 0);
+    if (!c.last()) raw = raw_step(a, c.next().c0 + my, c.next().c0, c.next().c1, h);
+  }
+  for (int buf = 0;; buf ^= 1) {
     store_tile<64>(su, tu);
     store_tile<NT>(sv, tv);
-    if (w == 0) {
-      float d;
-      if constexpr (REV) {
-        const bool in = c0 + lane < c1;
-        const float L = wave_prefix(row_decay(a, in ? c0 + lane : c0, in, h, A2, bias, d));
-        sw[lane] = ex2(L);
-        if (lane == 63) sh.total = L;
-      } else {
-        const int64_t row = c0 + 63 - lane;  // lanes from the chunk's end
-        const bool in = row < c1;
-        const float R = wave_prefix(row_decay(a, in ? row : c0, in, h, A2, bias, d));
-        sw[63 - lane] = ex2(dpp0<0x138, 0xf>(R)) * d;  // the rows after this one: the previous lane's sum
-        if (lane == 63) sh.total = R;
-      }
-    }
     __syncthreads();
-    const int64_t here = c0;
-    const bool more = REV ? c0 > pc.r0 : c1 < pc.r1;
+    const int64_t here = c.c0;
+    const bool more = !c.last();
+    const float* sw = sh.w[buf];
     if (more) {
-      c0 = REV ? (c0 - 1) / kChunk * kChunk : c1;
-      if (REV && c0 < pc.r0) c0 = pc.r0;
-      c1 = chunk_end(c0, pc.r1);
-      load_tile<64, VEC>(tu, ub + c0 * k.u_ld, k.u_ld, (int)(c1 - c0), pn);
-      load_tile<NT, VEC>(tv, vb + c0 * k.v_ld, k.v_ld, (int)(c1 - c0), a.N);
+      c = c.next();
+      load_tile<64, VEC>(tu, ub + c.c0 * k.u_ld, k.u_ld, c.rows(), pn);
+      load_tile<NT, VEC>(tv, vb + c.c0 * k.v_ld, k.v_ld, c.rows(), a.N);
+      if (w == 0) {
+        weights(c, buf ^ 1);
+        if (!c.last()) raw = raw_step(a, c.next().c0 + my, c.next().c0, c.next().c1, h);
+      }
     }
     if constexpr (STORE) {  // operand order: [n block of 16][p step of 32][lane] 16 bytes, high plane then low
       const int64_t id = here == pc.s ? k.n_chunk_slots + pc.seq : here / kChunk;
@@ -163,7 +199,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
         reinterpret_cast<u32x4*>(dst + 64 * NT)[o] = lo;
       }
     }
-    const float total = sh.total;
+    const float total = sh.total[buf];
     log_total += total;
     const float et = ex2(total);
 #pragma unroll
