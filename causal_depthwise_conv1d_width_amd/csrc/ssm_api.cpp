@@ -168,6 +168,8 @@ struct Operand {
 bool operand_ok(const Operand& o, int64_t rows) {
   return (rows == 0 || o.p) && o.ld >= o.len && mul_ok(rows, o.ld);
 }
+// The scan addresses the 64 rows of a chunk by 32-bit byte offsets from the first.
+bool scan_operand_ok(const Operand& o, int64_t rows) { return operand_ok(o, rows) && o.ld <= SSM_MAX_ROW_STRIDE; }
 
 void fill(ScanArgs* a, const ssm_shape* s, int64_t rows, const void* x, int64_t x_ld, const void* dt, int64_t dt_ld,
           const float* A, const void* B, int64_t B_ld, const void* C, int64_t C_ld, const float* D,
@@ -236,7 +238,7 @@ int ssm_scan_fwd(const ssm_shape* shape, int64_t rows, const void* x, int64_t x_
   const int64_t H = shape->H, hp = H * shape->P, gn = shape->G * shape->N, dte = dsize(shape->dt_dtype);
   const Operand ops[5] = {{x, x_ld, hp}, {dt, dt_ld, H}, {B, B_ld, gn}, {C, C_ld, gn}, {y, y_ld, hp}};
   for (const Operand& o : ops)
-    if (!operand_ok(o, rows)) return CONV1D_EINVAL;
+    if (!scan_operand_ok(o, rows)) return CONV1D_EINVAL;
   if (!aligned(x, 2) || !aligned(B, 2) || !aligned(C, 2) || !aligned(y, 2) || !aligned(dt, dte)) return CONV1D_EINVAL;
   ScanArgs a{};
   Span si, sf, sci, shi;
@@ -273,7 +275,7 @@ int ssm_scan_bwd(const ssm_shape* shape, int64_t rows, const void* dy, int64_t d
   const Operand ops[9] = {{dy, dy_ld, hp}, {x, x_ld, hp}, {dt, dt_ld, H}, {B, B_ld, gn}, {C, C_ld, gn},
                           {dx, dx_ld, hp}, {ddt, ddt_ld, H}, {dB, dB_ld, gn}, {dC, dC_ld, gn}};
   for (const Operand& o : ops)
-    if (!operand_ok(o, rows) || !aligned(o.p, o.p == dt || o.p == ddt ? dte : 2)) return CONV1D_EINVAL;
+    if (!scan_operand_ok(o, rows) || !aligned(o.p, o.p == dt || o.p == ddt ? dte : 2)) return CONV1D_EINVAL;
   const BwdPlan p = nseq > 0 ? plan_bwd(shape, rows, nseq) : BwdPlan{};
   if ((size_t)p.bytes > ws_bytes || (p.bytes && !ws)) return CONV1D_EWORKSPACE;
   if (p.bytes && !aligned(ws, 16)) return CONV1D_EINVAL;

@@ -93,6 +93,16 @@ __device__ __forceinline__ float row16_sum(float v) {
 __device__ __forceinline__ float wave_sum(float v) { return lane_value(wave_prefix(v), 63); }
 
 // ------------------------------------------------------------------ sequences, pieces, chunks
+// Everything here is the same in all lanes; values that come from memory are moved to scalar registers,
+// so that row numbers and tile bases cost no vector registers or instructions.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ float uniform(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(v)));
+}
 struct Piece {
   int64_t seq, s, e;  // the sequence's rows [s, e)
   int64_t r0, r1;     // this piece's rows
@@ -100,7 +110,7 @@ struct Piece {
 };
 
 __device__ __forceinline__ int64_t cu_at(const Seqs& q, int64_t k) {
-  const int64_t v = q.cu[k];
+  const int64_t v = __builtin_amdgcn_readfirstlane(q.cu[k]);
   return v < 0 ? 0 : (v > q.rows ? q.rows : v);
 }
 __device__ __forceinline__ void seq_bounds(const Seqs& q, int64_t i, int64_t& s, int64_t& e) {
@@ -177,44 +187,113 @@ __device__ __forceinline__ int at(int row, int col) {
   return row * kLd<W> + col;
 }
 
+// Blocks of the scan's kernels have 8 waves.
+constexpr int kThreads = 512;
+// this thread's wave, as a scalar (the compiler takes threadIdx.x / 64 for a value of each lane)
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 template <int W>
 struct TileRegs {
-  u32x4 v[W / 32];
+  u32x4 v[W / 64];
 };
 
-// Rows [0, nrows) x columns [0, ncols) of a global array into registers, 256 threads, zeros outside.
-// Addresses outside are replaced by the first element's, so the loads need no branches.  VEC: ncols
-// is a multiple of 8.
+// The rows of one chunk of a global array, as a buffer: offsets past its end read zeros and write nothing.
+// Every load and store of the chunk loops goes through one, without a test around it: with a store under
+// a branch the compiler can no longer count what is in flight and waits for all of it, the next chunk's
+// loads and the stores' completion, at every chunk.  Offsets are 32-bit bytes from the chunk's first row
+// (the host keeps 63 row strides under 2^32 bytes) and do not change from chunk to chunk.
+struct Rows {
+  __amdgpu_buffer_rsrc_t r;
+  // nrows rows of ncols columns of `size` bytes, ld columns apart; no rows or columns: everything is outside
+  __device__ __forceinline__ Rows(const void* first, int64_t ld, int nrows, int ncols, int size) {
+    const uint32_t bytes = nrows > 0 && ncols > 0 ? (uint32_t)(((nrows - 1) * ld + ncols) * size) : 0u;
+    r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(first), 0, (int)bytes, 0x00020000);
+  }
+};
+constexpr uint32_t kOutside = 0xffffff00u;  // an offset past every buffer's end
+
+// Columns [0, ncols) of a chunk's rows into registers, kThreads threads, zeros outside.  VEC: ncols is a
+// multiple of 8.
 template <int W, bool VEC>
-__device__ __forceinline__ void load_tile(TileRegs<W>& t, const uint16_t* __restrict__ base, int64_t ld, int nrows,
-                                          int ncols) {
+__device__ __forceinline__ void load_tile(TileRegs<W>& t, const Rows& rows, uint32_t ld, int ncols) {
 #pragma unroll
-  for (int k = 0; k < W / 32; ++k) {
-    const int q = threadIdx.x + 256 * k, row = q / (W / 8), c = (q % (W / 8)) * 8;
-    const bool ok = row < nrows && c < ncols;
-    const uint16_t* p = base + (ok ? row * ld + c : 0);
-    u32x4 v = {0u, 0u, 0u, 0u};
+  for (int k = 0; k < W / 64; ++k) {
+    const int q = threadIdx.x + kThreads * k, row = q / (W / 8), c = (q % (W / 8)) * 8;
+    const uint32_t off = (row * ld + c) * 2;
     if constexpr (VEC) {
-      v = *reinterpret_cast<const u32x4_a2*>(p);
+      t.v[k] = __builtin_amdgcn_raw_buffer_load_b128(rows.r, (int)(c < ncols ? off : kOutside), 0, 0);
     } else {
+      u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t u = p[c + e < ncols && ok ? e : 0];
-        v[e >> 1] |= (c + e < ncols ? u : 0u) << (16 * (e & 1));
+        const uint32_t u = __builtin_amdgcn_raw_buffer_load_b16(rows.r, (int)(c + e < ncols ? off + 2 * e : kOutside), 0, 0);
+        v[e >> 1] |= u << (16 * (e & 1));
       }
+      t.v[k] = v;
     }
+  }
+}
+
+// Four bf16 columns c .. c + 3 (those below ncols) of a row
+template <bool VEC>
+__device__ __forceinline__ void store4(const Rows& rows, uint32_t ld, int row, int c, int ncols, u32x2 v) {
+  const uint32_t off = (row * ld + c) * 2;
+  if constexpr (VEC) {
+    __builtin_amdgcn_raw_buffer_store_b64(v, rows.r, (int)(c < ncols ? off : kOutside), 0, 0);
+  } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) t.v[k][e] = ok ? v[e] : 0u;
+    for (int e = 0; e < 4; ++e)
+      __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v[e >> 1] >> (16 * (e & 1))), rows.r,
+                                            (int)(c + e < ncols ? off + 2 * e : kOutside), 0, 0);
   }
 }
 
 template <int W>
 __device__ __forceinline__ void store_tile(uint16_t* lds, const TileRegs<W>& t) {
 #pragma unroll
-  for (int k = 0; k < W / 32; ++k) {
-    const int q = threadIdx.x + 256 * k;
+  for (int k = 0; k < W / 64; ++k) {
+    const int q = threadIdx.x + kThreads * k;
     *reinterpret_cast<u32x4*>(lds + at<W>(q / (W / 8), q % (W / 8) * 8)) = t.v[k];
   }
+}
+
+// What a block of the scan or of the state walk works on: two units (64 columns of one head each) of one
+// group, which share the group's B and C rows; a group with an odd number of units ends with a single one.
+// Workgroups are dealt to the 8 XCDs in turn, each with its own L2: the pairs of one piece and group stay
+// on one XCD, and pieces and groups go to the XCDs in turn, so that long and absent pieces spread over them.
+struct Units {
+  int64_t item;
+  int group, first, count;  // units first .. first + count - 1 of the group
+  bool ok;
+  __device__ __forceinline__ Units(const ScanArgs& a, uint32_t block) {
+    const uint32_t units = a.H / a.G * a.ptiles, pairs = (units + 1) / 2;
+    const uint32_t set = block / 8 / pairs * 8 + block % 8;  // (piece, group)
+    item = set / (uint32_t)a.G;
+    group = set % (uint32_t)a.G;
+    first = block / 8 % pairs * 2;
+    count = (int)units - first < 2 ? 1 : 2;
+    ok = item < a.n_slots + a.q.nseq;
+  }
+};
+struct Unit {
+  int tile, h, p_first, pn;  // head_tile over all heads, head, first column, columns
+  __device__ __forceinline__ Unit(const ScanArgs& a, const Units& u, int k) {
+    tile = u.group * (a.H / a.G) * a.ptiles + u.first + k;
+    h = tile / a.ptiles;
+    p_first = tile % a.ptiles * kPTile;
+    pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
+  }
+};
+
+// Keeps the compiler from moving one phase's loads and products into another: with them mixed, the
+// kernels need more registers than 16 waves a CU leave them.
+__device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
+
+// The ten 16 x 16 blocks (ib, jb) of a 64 x 64 tile up to the diagonal, over 8 waves: (3, 0..3), (2, 0..2),
+// (1, 0) one a wave, then (1, 1) and (0, 0) for waves 0 and 1.
+__device__ __forceinline__ void first_block(int wave, int& ib, int& jb) {
+  ib = wave < 4 ? 3 : (wave < 7 ? 2 : 1);
+  jb = wave < 4 ? wave : (wave < 7 ? wave - 4 : 0);
 }
 
 // ------------------------------------------------------------------ matrix operands

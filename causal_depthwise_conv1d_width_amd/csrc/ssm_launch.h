@@ -110,6 +110,12 @@ hipError_t launch_gated_bwd(const NormArgs& a, hipStream_t s);
 hipError_t launch_residual_fwd(const NormArgs& a, hipStream_t s);
 hipError_t launch_residual_bwd(const NormArgs& a, hipStream_t s);
 
+// blocks of the scan and of the state walk: pairs of 64-column units for every piece and group, these in
+// sets of 8 (one an XCD)
+inline int64_t pair_blocks(int64_t items, int64_t H, int64_t G, int64_t ptiles) {
+  return (items * G + 7) / 8 * 8 * ((H / G * ptiles + 1) / 2);
+}
+
 inline int state_tile(int64_t N) { return N <= 64 ? 64 : (N <= 128 ? 128 : 256); }
 
 // threads that share one (row, group) of a norm

@@ -22,7 +22,7 @@
 namespace cssm {
 
 template <int NT, bool VEC, bool STORE>
-__global__ __launch_bounds__(256, 2) void ssm_states_kernel(StateArgs f, StateArgs r) {
+__global__ __launch_bounds__(kThreads, NT > 128 ? 2 : 4) void ssm_states_kernel(StateArgs f, StateArgs r) {
   __shared__ StateShared<NT> sh;
   if (blockIdx.y == 0) state_walk<NT, VEC, false, STORE>(f, sh);
   else state_walk<NT, VEC, true, STORE>(r, sh);
@@ -36,13 +36,12 @@ __device__ __forceinline__ float across16(float v) {  // sum over the four rows 
   return v + __shfl_xor(v, 32);
 }
 
-// Keeps the compiler from moving one phase's loads and products into another: with them mixed, the
-// kernel needs more registers than two blocks a CU leave it.
-__device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
-
+// A block of 8 waves takes a chunk and walks the 64-column units of its heads.  A wave owns 16 * NBW columns n
+// of dB and dC (with NT = 64: two waves share 16, each with half of the rows) and two 16 x 16 blocks of dX.
 template <int NT, bool VEC>
-__global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(ScanBwdArgs b) {
-  constexpr int NBW = NT / 64;                                  // 16-column blocks n of a wave
+__global__ __launch_bounds__(kThreads, NT > 128 ? 2 : 4) void ssm_scan_bwd_kernel(ScanBwdArgs b) {
+  constexpr int NBW = NT > 128 ? NT / 128 : 1;  // 16-column blocks n of a wave
+  constexpr int KB = NT > 64 ? 4 : 2;           // 16-row blocks of a wave
   constexpr int R = (NT > 128 ? NT : 128) * kLd<64>;
   __shared__ __align__(16) uint16_t sx[64 * kLd<64>];
   __shared__ __align__(16) uint16_t sy[64 * kLd<64>];
@@ -53,10 +52,10 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
   __shared__ __align__(16) double sdecay[2][64];
   __shared__ __align__(16) float ssteps[2][3][64];
   __shared__ __align__(16) float s_col[4][64];
-  __shared__ float s_row[64], s_diag[64], s_rint[4][64], s_u[4][64], s_dot[4], s_trace[4];
+  __shared__ float s_row[4][64], s_diag[64], s_rint[8][64], s_u[8][64], s_dot[8], s_trace[4];
   uint16_t *sZ = sR, *sG = sR + 64 * kLd<64>;
   const ScanArgs& a = b.s;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, i = lane & 15;
+  const int lane = threadIdx.x & 63, w = wave_id(), g = lane >> 4, i = lane & 15;
   const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
   const int part = blk % b.hsplit, grp = blk / b.hsplit % a.G;
   const int64_t id = blk / b.hsplit / a.G;
@@ -64,20 +63,23 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
   const int h_lo = grp * hg + part * per, h_hi = h_lo + per < (grp + 1) * hg ? h_lo + per : (grp + 1) * hg;
   const Piece pc = find_piece(a.q, id, kChunk, b.n_chunk_slots);
   if (!pc.ok) {
-    for (int e = threadIdx.x; e < (h_hi - h_lo) * 3; e += 256) b.head_part[(id * a.H + h_lo) * 3 + e] = 0.f;
+    for (int e = threadIdx.x; e < (h_hi - h_lo) * 3; e += kThreads) b.head_part[(id * a.H + h_lo) * 3 + e] = 0.f;
     return;
   }
   const int rows = (int)(pc.r1 - pc.r0);
   const int hp = a.H * a.ptiles;
   const int tiles = (h_hi - h_lo) * a.ptiles;
   const int64_t gn = (int64_t)grp * a.N;
-  const int nw = 16 * NBW * w;  // this wave's first column n
+  const int nw = NT > 64 ? 16 * NBW * w : 16 * (w & 3);  // this wave's first column n
+  const int kb0 = NT > 64 ? 0 : 2 * (w >> 2);            // and its first block of rows
+  const bool owner = NT > 64 || w < 4;                   // of the columns, where two waves share them
+  const int pw = 16 * (w & 3), jw = 2 * (w >> 2);        // its blocks of dX: columns pw, rows 16 jw, 16 jw + 16
 
-  f32x4 dC[NBW][4], dB[NBW][4];
+  f32x4 dC[NBW][KB], dB[NBW][KB];
 #pragma unroll
   for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) dC[nb][k] = dB[nb][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < KB; ++k) dC[nb][k] = dB[nb][k] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   TileRegs<64> tx, ty;
   u32x4 Sh[NBW][2], Sl[NBW][2], Th[NBW][2], Tl[NBW][2];
@@ -85,19 +87,20 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
     const int h = h_lo + t / a.ptiles, p_first = t % a.ptiles * kPTile;
     const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
     const int64_t o = (int64_t)h * a.P + p_first;
-    load_tile<64, VEC>(tx, a.x + pc.r0 * a.x_ld + o, a.x_ld, rows, pn);
-    load_tile<64, VEC>(ty, b.dy + pc.r0 * b.dy_ld + o, b.dy_ld, rows, pn);
+    const int n = t < tiles ? rows : 0;  // past the last one nothing is read
+    load_tile<64, VEC>(tx, Rows(a.x + pc.r0 * a.x_ld + o, a.x_ld, n, pn, 2), (uint32_t)a.x_ld, pn);
+    load_tile<64, VEC>(ty, Rows(b.dy + pc.r0 * b.dy_ld + o, b.dy_ld, n, pn, 2), (uint32_t)b.dy_ld, pn);
   };
-  // a head's decays into its buffer: wave 0 the prefix sums, steps and powers, wave 1, whose lanes count
-  // from the chunk's end, the decays to the end
-  float raw = 0.f;
-  const int my = w == 0 ? lane : 63 - lane;
-  auto load_raw = [&](int t) { raw = raw_step(a, pc.r0 + my, pc.r0, pc.r1, h_lo + t / a.ptiles); };
+  // a head's decays into its buffer: wave 6 the prefix sums, steps and powers, wave 7, whose lanes count
+  // from the chunk's end, the decays to the end (waves 0 and 1 have two score blocks, these one)
+  RawStep raw{};
+  const int my = w == 6 ? lane : 63 - lane;
+  auto load_raw = [&](int t) { raw = raw_step(a, pc.r0, t < tiles ? rows : 0, my, h_lo + t / a.ptiles); };
   auto decays = [&](int t) {
     const Rate rate(a, h_lo + t / a.ptiles);
     const float d = rate.step(raw, my < rows);
     const double L = wave_prefix((double)(d * rate.A2));
-    if (w == 0) {
+    if (w == 6) {
       sdecay[t & 1][lane] = L;
       ssteps[t & 1][0][lane] = d;
       ssteps[t & 1][1][lane] = ex2((float)L);
@@ -107,198 +110,178 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
   };
   auto load_states = [&](int t) {
     const int64_t o = (id * hp + h_lo * a.ptiles + t) * (2 * 64 * NT);
-    const u32x4 *cs = reinterpret_cast<const u32x4*>(b.cs + o), *ct = reinterpret_cast<const u32x4*>(b.ct + o);
+    const int n = t < tiles ? 2 * 64 * NT : 0;
+    const Rows cs(b.cs + o, n, 1, n, 2), ct(b.ct + o, n, 1, n, 2);
 #pragma unroll
     for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        const int at = ((w * NBW + nb) * 2 + ks) * 64 + lane;
-        Th[nb][ks] = ct[at];
-        Sh[nb][ks] = cs[at];
-        Sl[nb][ks] = cs[8 * NT + at];
-        Tl[nb][ks] = ct[8 * NT + at];
+        const int at = (((nw / 16 + nb) * 2 + ks) * 64 + lane) * 16;
+        Th[nb][ks] = __builtin_amdgcn_raw_buffer_load_b128(ct.r, at, 0, 0);
+        Sh[nb][ks] = __builtin_amdgcn_raw_buffer_load_b128(cs.r, at, 0, 0);
+        Sl[nb][ks] = __builtin_amdgcn_raw_buffer_load_b128(cs.r, at + 64 * NT * 2, 0, 0);
+        Tl[nb][ks] = __builtin_amdgcn_raw_buffer_load_b128(ct.r, at + 64 * NT * 2, 0, 0);
       }
   };
   load_rows(0);
   load_states(0);
-  if (w < 2) {
-    load_raw(0);
-    decays(0);
-    if (tiles > 1) load_raw(1);
-  }
+  load_raw(0);
+  if (w >= 6) decays(0);
+  load_raw(1);
   {
     TileRegs<NT> t;
-    load_tile<NT, VEC>(t, a.B + pc.r0 * a.B_ld + gn, a.B_ld, rows, a.N);
+    load_tile<NT, VEC>(t, Rows(a.B + pc.r0 * a.B_ld + gn, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
     store_tile<NT>(sB, t);
-    load_tile<NT, VEC>(t, a.C + pc.r0 * a.C_ld + gn, a.C_ld, rows, a.N);
+    load_tile<NT, VEC>(t, Rows(a.C + pc.r0 * a.C_ld + gn, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
     store_tile<NT>(sC, t);
   }
   __syncthreads();
-  f32x4 G[4];  // G^T: rows i = 16 w + lane, columns j in the registers; blocks past the diagonal stay 0
+  // G^T blocks of this wave: rows i in the lanes, columns j in the registers
+  int ib0, jb0;
+  first_block(w, ib0, jb0);
+  f32x4 G0 = {0.f, 0.f, 0.f, 0.f}, G1 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int jb = 0; jb < 4; ++jb) {
-    G[jb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (jb <= w) {
-#pragma unroll
-      for (int ks = 0; ks < NT / 32; ++ks)
-        G[jb] = mma(op_straight<NT>(sB, 16 * jb, 32 * ks), op_straight<NT>(sC, 16 * w, 32 * ks), G[jb]);
-    }
+  for (int ks = 0; ks < NT / 32; ++ks) {
+    G0 = mma(op_straight<NT>(sB, 16 * jb0, 32 * ks), op_straight<NT>(sC, 16 * ib0, 32 * ks), G0);
+    if (w < 2) G1 = mma(op_straight<NT>(sB, 16 * (1 - w), 32 * ks), op_straight<NT>(sC, 16 * (1 - w), 32 * ks), G1);
   }
 
   float dl_sum = 0.f, q_sum = 0.f, trace_sum = 0.f;  // wave 0: over a head's column tiles
   for (int t = 0; t < tiles; ++t) {
     const int h = h_lo + t / a.ptiles, ptile = t % a.ptiles, p_first = ptile * kPTile;
     const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
-    const float Dh = a.D ? a.D[h] : 0.f;
     const double* sL = sdecay[t & 1];
     const float *sd = ssteps[t & 1][0], *se = ssteps[t & 1][1], *sr = ssteps[t & 1][2];
     store_tile<64>(sx, tx);
     store_tile<64>(sy, ty);
+    if (owner) {
 #pragma unroll
-    for (int nb = 0; nb < NBW; ++nb)
+      for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const int n = nw + 16 * nb + i;
-        *reinterpret_cast<u32x2*>(sR + at<64>(n, 32 * ks + 4 * g)) = u32x2{Th[nb][ks].x, Th[nb][ks].y};
-        *reinterpret_cast<u32x2*>(sR + at<64>(n, 32 * ks + 16 + 4 * g)) = u32x2{Th[nb][ks].z, Th[nb][ks].w};
-      }
-    __syncthreads();
+        for (int ks = 0; ks < 2; ++ks) {
+          const int n = nw + 16 * nb + i;
+          *reinterpret_cast<u32x2*>(sR + at<64>(n, 32 * ks + 4 * g)) = u32x2{Th[nb][ks].x, Th[nb][ks].y};
+          *reinterpret_cast<u32x2*>(sR + at<64>(n, 32 * ks + 16 + 4 * g)) = u32x2{Th[nb][ks].z, Th[nb][ks].w};
+        }
+    }
     phase();
-    if (t + 1 < tiles) load_rows(t + 1);
+    __syncthreads();
+    load_rows(t + 1);
+    phase();
 
-    f32x4 dX[4];  // registers p = 16 w + 4 g + r, lanes j
-#pragma unroll
-    for (int jb = 0; jb < 4; ++jb) dX[jb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 dX[2];  // registers p = pw + 4 g + r, lanes j
+    dX[0] = dX[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < NT / 32; ++ks) {
-      const bf16x8 tt = op_cols<64>(sR, 32 * ks, 16 * w);
+      const bf16x8 tt = op_cols<64>(sR, 32 * ks, pw);
 #pragma unroll
-      for (int jb = 0; jb < 4; ++jb) dX[jb] = mma(tt, op_split<NT>(sB, 16 * jb, 32 * ks), dX[jb]);
+      for (int k = 0; k < 2; ++k) dX[k] = mma(tt, op_split<NT>(sB, 16 * (jw + k), 32 * ks), dX[k]);
     }
 #pragma unroll
-    for (int jb = 0; jb < 4; ++jb) dX[jb] *= sr[16 * jb + i];
+    for (int k = 0; k < 2; ++k) dX[k] *= sr[16 * (jw + k) + i];
     phase();
     __syncthreads();
 
-    {  // rows i = 16 w + lane against columns j in the registers
-      bf16x8 yv[2];
+    // score block (ib, jb), G its C B^T; the diagonal's K is in its row's and its column's sum alike and is
+    // kept out of both
+    auto scores = [&](const int ib, const int jb, const f32x4& G) {
+      f32x4 W = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) yv[ks] = op_straight<64>(sy, 16 * w, 32 * ks);
-      const double Li = sL[16 * w + i];
-      float row = 0.f, trace = 0.f;
-      // one 16 x 16 block; the diagonal's K is in its row's and its column's sum alike and is kept out of both
-      auto block = [&](const int jb, auto diagonal) {
-        f32x4 W = {0.f, 0.f, 0.f, 0.f};
+      for (int ks = 0; ks < 2; ++ks) W = mma(op_straight<64>(sx, 16 * jb, 32 * ks), op_straight<64>(sy, 16 * ib, 32 * ks), W);
+      const double Li = sL[16 * ib + i];
+      const f32x4 dj = *reinterpret_cast<const f32x4*>(sd + 16 * jb + 4 * g);
+      f32x4 z, gm;
+      float row = 0.f, on_diagonal = 0.f, trace = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) W = mma(op_straight<64>(sx, 16 * jb, 32 * ks), yv[ks], W);
-        const f32x4 dj = *reinterpret_cast<const f32x4*>(sd + 16 * jb + 4 * g);
-        f32x4 z, gm;
-        float on_diagonal = 0.f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float m = ex2((float)(Li - sL[16 * jb + 4 * g + r]));
-          if (diagonal) m = 4 * g + r <= i ? m : 0.f;
-          gm[r] = G[jb][r] * m;
-          z[r] = W[r] * (m * dj[r]);
-          float K = gm[r] * W[r];
-          if (diagonal) {
-            const bool here = 4 * g + r == i;
-            on_diagonal = here ? K : on_diagonal;
-            trace += here ? W[r] : 0.f;
-            K = here ? 0.f : K;
-          }
-          row = __builtin_fmaf(dj[r], K, row);
-          const float c = row16_sum(K);
-          if (i == 15) s_col[w][16 * jb + 4 * g + r] = c;
-        }
-        if (diagonal && (i >> 2) == g) s_diag[16 * w + i] = on_diagonal;
-        *reinterpret_cast<u32x2*>(sZ + at<64>(16 * w + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(z[0], z[1]), pk_bf16(z[2], z[3])};
-        *reinterpret_cast<u32x2*>(sG + at<64>(16 * w + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(gm[0], gm[1]), pk_bf16(gm[2], gm[3])};
-      };
-#pragma unroll
-      for (int jb = 0; jb < 4; ++jb) {
-        if (jb < w) {
-          block(jb, std::false_type{});
-        } else if (jb == w) {
-          block(jb, std::true_type{});
-        } else {
-          if (i == 15) *reinterpret_cast<f32x4*>(&s_col[w][16 * jb + 4 * g]) = f32x4{0.f, 0.f, 0.f, 0.f};
-          if (jb == w + 1) {  // read with the diagonal block by products over 32 columns
-            *reinterpret_cast<u32x2*>(sZ + at<64>(16 * w + i, 16 * jb + 4 * g)) = u32x2{0u, 0u};
-            *reinterpret_cast<u32x2*>(sG + at<64>(16 * w + i, 16 * jb + 4 * g)) = u32x2{0u, 0u};
-          }
-        }
-        phase();
+      for (int r = 0; r < 4; ++r) {
+        const float m = 16 * jb + 4 * g + r <= 16 * ib + i ? ex2((float)(Li - sL[16 * jb + 4 * g + r])) : 0.f;
+        gm[r] = G[r] * m;
+        z[r] = W[r] * (m * dj[r]);
+        float K = gm[r] * W[r];
+        const bool here = 16 * jb + 4 * g + r == 16 * ib + i;
+        on_diagonal = here ? K : on_diagonal;
+        trace += here ? W[r] : 0.f;
+        K = here ? 0.f : K;
+        row = __builtin_fmaf(dj[r], K, row);
+        const float c = row16_sum(K);
+        if (i == 15) s_col[ib][16 * jb + 4 * g + r] = c;
       }
-      if (w < 2 && t + 1 < tiles) {  // these waves have the fewer blocks
-        decays(t + 1);
-        if (t + 2 < tiles) load_raw(t + 2);
-      }
+      *reinterpret_cast<u32x2*>(sZ + at<64>(16 * ib + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(z[0], z[1]), pk_bf16(z[2], z[3])};
+      *reinterpret_cast<u32x2*>(sG + at<64>(16 * ib + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(gm[0], gm[1]), pk_bf16(gm[2], gm[3])};
       row = across16(row);
-      if (g == 0) s_row[16 * w + i] = row;
-      trace = wave_sum(trace);
-      if (lane == 0) s_trace[w] = trace;
+      if (g == 0) s_row[jb][16 * ib + i] = row;
+      if (ib == jb) {
+        if ((i >> 2) == g) s_diag[16 * ib + i] = on_diagonal;
+        trace = wave_sum(trace);
+        if (lane == 0) s_trace[ib] = trace;
+      }
+      phase();
+    };
+    scores(ib0, jb0, G0);
+    if (w < 2) scores(1 - w, 1 - w, G1);
+    if (w == 4 || w == 5) {  // blocks (0, 1), (2, 3): products over 32 columns read them
+      const int z = 2 * (w - 4);
+      *reinterpret_cast<u32x2*>(sZ + at<64>(16 * z + i, 16 * z + 16 + 4 * g)) = u32x2{0u, 0u};
+      *reinterpret_cast<u32x2*>(sG + at<64>(16 * z + i, 16 * z + 16 + 4 * g)) = u32x2{0u, 0u};
     }
+    if (w >= 6 && t + 1 < tiles) decays(t + 1);
+    load_raw(t + 2);
     phase();
     __syncthreads();
 
-    {  // dC and the rows' sums with S
-      float rint[4] = {0.f, 0.f, 0.f, 0.f};
+    // dC and the rows' sums with S
 #pragma unroll
-      for (int nb = 0; nb < NBW; ++nb)
+    for (int k = 0; k < KB; ++k) {
+      const int ib = kb0 + k;
+      float rint = 0.f;
 #pragma unroll
-        for (int ib = 0; ib < 4; ++ib) {
-          f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      for (int nb = 0; nb < NBW; ++nb) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            const bf16x8 y = op_split<64>(sy, 16 * ib, 32 * ks);
-            v = mma(__builtin_bit_cast(bf16x8, Sh[nb][ks]), y, v);
-            v = mma(__builtin_bit_cast(bf16x8, Sl[nb][ks]), y, v);
-          }
-          v *= se[16 * ib + i];
-          const u32x2 c = *reinterpret_cast<const u32x2*>(sC + at<NT>(16 * ib + i, nw + 16 * nb + 4 * g));
-          rint[ib] += v[0] * bf_lo(c.x) + v[1] * bf_hi(c.x) + v[2] * bf_lo(c.y) + v[3] * bf_hi(c.y);
-          f32x4 acc = dC[nb][ib] + v;
-#pragma unroll
-          for (int ks = 0; ks <= ib / 2; ++ks)
-            acc = mma(op_cols<NT>(sB, 32 * ks, nw + 16 * nb), op_split<64>(sZ, 16 * ib, 32 * ks), acc);
-          dC[nb][ib] = acc;
-          phase();
+        for (int ks = 0; ks < 2; ++ks) {
+          const bf16x8 y = op_split<64>(sy, 16 * ib, 32 * ks);
+          v = mma(__builtin_bit_cast(bf16x8, Sh[nb][ks]), y, v);
+          v = mma(__builtin_bit_cast(bf16x8, Sl[nb][ks]), y, v);
         }
+        v *= se[16 * ib + i];
+        const u32x2 c = *reinterpret_cast<const u32x2*>(sC + at<NT>(16 * ib + i, nw + 16 * nb + 4 * g));
+        rint += v[0] * bf_lo(c.x) + v[1] * bf_hi(c.x) + v[2] * bf_lo(c.y) + v[3] * bf_hi(c.y);
+        f32x4 acc = dC[nb][k] + v;
 #pragma unroll
-      for (int ib = 0; ib < 4; ++ib) {
-        const float v = across16(rint[ib]);
-        if (g == 0) s_rint[w][16 * ib + i] = v;
+        for (int ks = 0; ks < 2; ++ks)
+          if (ks <= ib / 2) acc = mma(op_cols<NT>(sB, 32 * ks, nw + 16 * nb), op_split<64>(sZ, 16 * ib, 32 * ks), acc);
+        dC[nb][k] = acc;
       }
+      rint = across16(rint);
+      if (g == 0) s_rint[w][16 * ib + i] = rint;
+      phase();
     }
-    {  // dB and the rows' sums with T
-      float u[4] = {0.f, 0.f, 0.f, 0.f};
+    // dB and the rows' sums with T
 #pragma unroll
-      for (int nb = 0; nb < NBW; ++nb)
+    for (int k = 0; k < KB; ++k) {
+      const int jb = kb0 + k;
+      float u = 0.f;
 #pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-          f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      for (int nb = 0; nb < NBW; ++nb) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            const bf16x8 x = op_split<64>(sx, 16 * jb, 32 * ks);
-            v = mma(__builtin_bit_cast(bf16x8, Th[nb][ks]), x, v);
-            v = mma(__builtin_bit_cast(bf16x8, Tl[nb][ks]), x, v);
-          }
-          v *= sr[16 * jb + i];
-          const u32x2 c = *reinterpret_cast<const u32x2*>(sB + at<NT>(16 * jb + i, nw + 16 * nb + 4 * g));
-          u[jb] += v[0] * bf_lo(c.x) + v[1] * bf_hi(c.x) + v[2] * bf_lo(c.y) + v[3] * bf_hi(c.y);
-          f32x4 acc = dB[nb][jb] + v * sd[16 * jb + i];
-#pragma unroll
-          for (int ks = jb / 2; ks < 2; ++ks)
-            acc = mma(op_cols<NT>(sC, 32 * ks, nw + 16 * nb), op_cols<64>(sZ, 32 * ks, 16 * jb), acc);
-          dB[nb][jb] = acc;
-          phase();
+        for (int ks = 0; ks < 2; ++ks) {
+          const bf16x8 x = op_split<64>(sx, 16 * jb, 32 * ks);
+          v = mma(__builtin_bit_cast(bf16x8, Th[nb][ks]), x, v);
+          v = mma(__builtin_bit_cast(bf16x8, Tl[nb][ks]), x, v);
         }
+        v *= sr[16 * jb + i];
+        const u32x2 c = *reinterpret_cast<const u32x2*>(sB + at<NT>(16 * jb + i, nw + 16 * nb + 4 * g));
+        u += v[0] * bf_lo(c.x) + v[1] * bf_hi(c.x) + v[2] * bf_lo(c.y) + v[3] * bf_hi(c.y);
+        f32x4 acc = dB[nb][k] + v * sd[16 * jb + i];
 #pragma unroll
-      for (int jb = 0; jb < 4; ++jb) {
-        const float v = across16(u[jb]);
-        if (g == 0) s_u[w][16 * jb + i] = v;
+        for (int ks = 0; ks < 2; ++ks)
+          if (ks >= jb / 2) acc = mma(op_cols<NT>(sC, 32 * ks, nw + 16 * nb), op_cols<64>(sZ, 32 * ks, 16 * jb), acc);
+        dB[nb][k] = acc;
       }
+      u = across16(u);
+      if (g == 0) s_u[w][16 * jb + i] = u;
+      phase();
     }
     float dot = 0.f;
 #pragma unroll
@@ -313,49 +296,52 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
           dot = dot2(Sl[nb][ks][e], Tl[nb][ks][e], dot);
         }
     dot = wave_sum(dot);
-    if (lane == 0) s_dot[w] = dot;
+    if (lane == 0) s_dot[w] = owner ? dot : 0.f;
     phase();
-    if (t + 1 < tiles) load_states(t + 1);
+    load_states(t + 1);
+    phase();
 
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      const bf16x8 y = op_cols<64>(sy, 32 * ks, 16 * w);
+      if (ks < jw / 2) continue;
+      const bf16x8 y = op_cols<64>(sy, 32 * ks, pw);
 #pragma unroll
-      for (int jb = 0; jb < 2 * ks + 2; ++jb) dX[jb] = mma(y, op_cols<64>(sG, 32 * ks, 16 * jb), dX[jb]);
+      for (int k = 0; k < 2; ++k) dX[k] = mma(y, op_cols<64>(sG, 32 * ks, 16 * (jw + k)), dX[k]);
     }
-    const int p_out = 16 * w + 4 * g;
+    const int p_out = pw + 4 * g;
+    const Rows out(b.dx + pc.r0 * b.dx_ld + (int64_t)h * a.P + p_first, b.dx_ld, rows, pn, 2);
+    const float Dh = a.D ? uniform(a.D[h]) : 0.f;
 #pragma unroll
-    for (int jb = 0; jb < 4; ++jb) {
-      const int row = 16 * jb + i;
+    for (int k = 0; k < 2; ++k) {
+      const int row = 16 * (jw + k) + i;
       const float d = sd[row];
       const u32x2 yv = *reinterpret_cast<const u32x2*>(sy + at<64>(row, p_out));
-      const u32x2 o = {pk_bf16(d * dX[jb][0] + Dh * bf_lo(yv.x), d * dX[jb][1] + Dh * bf_hi(yv.x)),
-                       pk_bf16(d * dX[jb][2] + Dh * bf_lo(yv.y), d * dX[jb][3] + Dh * bf_hi(yv.y))};
-      if (row < rows) {
-        uint16_t* dst = b.dx + (pc.r0 + row) * b.dx_ld + (int64_t)h * a.P + p_first + p_out;
-        if (VEC || p_out + 3 < pn) {
-          if (p_out < pn) *reinterpret_cast<u32x2_a2*>(dst) = o;
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (p_out + r < pn) dst[r] = (uint16_t)(o[r >> 1] >> (16 * (r & 1)));
-        }
-      }
+      const u32x2 o = {pk_bf16(d * dX[k][0] + Dh * bf_lo(yv.x), d * dX[k][1] + Dh * bf_hi(yv.x)),
+                       pk_bf16(d * dX[k][2] + Dh * bf_lo(yv.y), d * dX[k][3] + Dh * bf_hi(yv.y))};
+      store4<VEC>(out, (uint32_t)b.dx_ld, row, p_out, pn, o);
     }
+    phase();
     __syncthreads();
 
     if (w == 0) {  // lane = row: the gradients of the decays and steps
       const float d = sd[lane];
-      float rint = 0.f, u = 0.f, col = 0.f, dots = 0.f, trace = 0.f;
+      float rint = 0.f, u = 0.f, row = 0.f, col = 0.f, dots = 0.f, trace = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        rint += s_rint[k][lane];
-        u += s_u[k][lane];
-        col += s_col[k][lane];
-        dots += s_dot[k];
+      for (int k = 0; k < 8; ++k) dots += s_dot[k];
+#pragma unroll
+      for (int k = 0; k < (NT > 64 ? 8 : 4); ++k) {
+        const int from = NT > 64 ? k : k + 4 * (lane >> 5);
+        rint += s_rint[from][lane];
+        u += s_u[from][lane];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // blocks up to the diagonal
+        const float r = s_row[k][lane], c = s_col[k][lane];
+        row += k <= (lane >> 4) ? r : 0.f;
+        col += k >= (lane >> 4) ? c : 0.f;
         trace += s_trace[k];
       }
-      const float from_later = rint + (s_row[lane] - d * col);
+      const float from_later = rint + (row - d * col);
       const float suffix = __shfl(wave_prefix(__shfl(from_later, 63 - lane)), 63 - lane);  // rows >= this one
       const float before = dpp0<0x138, 0xf>(wave_prefix(d * u));                            // rows < this one
       dl_sum += se[63] * dots + suffix + before;
@@ -363,13 +349,13 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
       trace_sum += trace;
       if (ptile + 1 == a.ptiles) {
         const float step = a.A[h] * dl_sum + q_sum;
-        const float raw = a.softplus ? step * -expm1f(-d) : step;  // softplus' = 1 - e^{-softplus}
-        if (lane < rows) {
-          const int64_t o = (pc.r0 + lane) * b.ddt_ld + h;
-          if (a.dt_f32) static_cast<float*>(b.ddt)[o] = raw;
-          else static_cast<uint16_t*>(b.ddt)[o] = to_bf16(raw);
-        }
-        const float sum_A = wave_sum(lane < rows ? d * dl_sum : 0.f), sum_b = wave_sum(lane < rows ? raw : 0.f);
+        const float grad = a.softplus ? step * -expm1f(-d) : step;  // softplus' = 1 - e^{-softplus}
+        const int size = a.dt_f32 ? 4 : 2;
+        const Rows to(static_cast<char*>(b.ddt) + (pc.r0 * b.ddt_ld + h) * size, b.ddt_ld, rows, 1, size);
+        const int off = (int)((uint32_t)lane * (uint32_t)b.ddt_ld * size);
+        if (a.dt_f32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(grad), to.r, off, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16(to_bf16(grad), to.r, off, 0, 0);
+        const float sum_A = wave_sum(lane < rows ? d * dl_sum : 0.f), sum_b = wave_sum(lane < rows ? grad : 0.f);
         if (lane == 0) {
           float* dst = b.head_part + (id * a.H + h) * 3;
           dst[0] = sum_A;
@@ -384,8 +370,8 @@ __global__ __launch_bounds__(256, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(Sca
 #pragma unroll
   for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int row = 16 * k + i, n = nw + 16 * nb + 4 * g;
+    for (int k = 0; k < KB; ++k) {
+      const int row = 16 * (kb0 + k) + i, n = nw + 16 * nb + 4 * g;
       if (row >= rows || n >= a.N) continue;
       const int64_t r = pc.r0 + row;
       if (b.hsplit > 1) {
@@ -470,15 +456,15 @@ static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
     ssm_head_reduce_kernel<<<dim3((uint32_t)a.H), 256, 0, s>>>(b, 0);
     return hipGetLastError();
   }
-  const dim3 walk((uint32_t)(items * hp), 2);
+  const dim3 walk((uint32_t)(pair_blocks(items, a.H, a.G, a.ptiles)), 2);
   if (a.seg > 0) {
     const dim3 join((uint32_t)(a.q.nseq * hp * (64 * NT / 1024)));
-    ssm_states_kernel<NT, VEC, false><<<walk, 256, 0, s>>>(f, r);
+    ssm_states_kernel<NT, VEC, false><<<walk, kThreads, 0, s>>>(f, r);
     ssm_join_kernel<NT, false><<<join, 256, 0, s>>>(f);
     ssm_join_kernel<NT, true><<<join, 256, 0, s>>>(r);
   }
-  ssm_states_kernel<NT, VEC, true><<<walk, 256, 0, s>>>(f, r);
-  ssm_scan_bwd_kernel<NT, VEC><<<dim3((uint32_t)(ids * a.G * b.hsplit)), 256, 0, s>>>(b);
+  ssm_states_kernel<NT, VEC, true><<<walk, kThreads, 0, s>>>(f, r);
+  ssm_scan_bwd_kernel<NT, VEC><<<dim3((uint32_t)(ids * a.G * b.hsplit)), kThreads, 0, s>>>(b);
   if (b.hsplit > 1 && a.q.rows > 0) {
     const int64_t n = a.q.rows * a.G * a.N;
     ssm_bc_reduce_kernel<<<dim3((uint32_t)((n + 255) / 256), 2), 256, 0, s>>>(b);

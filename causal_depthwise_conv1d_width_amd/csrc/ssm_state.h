@@ -29,15 +29,27 @@ struct StateArgs {
 // Decays and step sizes of one chunk, computed by one wave with a row a lane from the raw steps, which
 // are loaded a chunk ahead (they would otherwise stand at the head of every chunk, a memory round trip
 // and a scan that all waves wait for).  Rows past the chunk's end have step 0.
-__device__ __forceinline__ float raw_step(const ScanArgs& a, int64_t row, int64_t c0, int64_t c1, int h) {
-  return load_num(a.dt, (row < c1 ? row : c0) * a.dt_ld + h, a.dt_f32);
+struct RawStep {  // loaded as two halves and put together at use, so that nothing waits for it before
+  uint16_t hi, lo;
+};
+__device__ __forceinline__ RawStep raw_step(const ScanArgs& a, int64_t c0, int rows, int row, int h) {
+  const int size = a.dt_f32 ? 4 : 2;
+  const Rows r(static_cast<const char*>(a.dt) + (c0 * a.dt_ld + h) * size, a.dt_ld, rows, 1, size);
+  const uint32_t off = (uint32_t)row * (uint32_t)a.dt_ld * size;
+  RawStep s;
+  s.lo = __builtin_amdgcn_raw_buffer_load_b16(r.r, (int)off, 0, 0);
+  s.hi = __builtin_amdgcn_raw_buffer_load_b16(r.r, (int)(off + size - 2), 0, 0);
+  return s;
 }
 struct Rate {
   float A2, bias;  // A log2 e, and what is added to the raw step
-  int softplus;
+  int softplus, f32;
   __device__ __forceinline__ Rate(const ScanArgs& a, int h)
-      : A2(a.A[h] * kLog2e), bias(a.bias ? a.bias[h] : 0.f), softplus(a.softplus) {}
-  __device__ __forceinline__ float step(float raw, bool in) const { return in ? step_size(raw + bias, softplus) : 0.f; }
+      : A2(uniform(a.A[h] * kLog2e)), bias(a.bias ? uniform(a.bias[h]) : 0.f), softplus(a.softplus), f32(a.dt_f32) {}
+  __device__ __forceinline__ float step(RawStep raw, bool in) const {
+    const float v = __uint_as_float(((uint32_t)raw.hi << 16) | (f32 ? raw.lo : 0u));
+    return in ? step_size(v + bias, softplus) : 0.f;
+  }
 };
 
 // The chunks of rows [r0, r1) in the order of the walk.
@@ -69,47 +81,58 @@ struct Chunks {
   }
   __device__ __forceinline__ int rows() const { return (int)(c1 - c0); }
 };
+// The chunk after c and its number of rows, 0 (nothing is read) after the last one.
+template <bool REV>
+__device__ __forceinline__ Chunks<REV> step_chunk(const Chunks<REV>& c, int& rows) {
+  const bool last = rows == 0 || c.last();
+  const Chunks<REV> n = last ? c : c.next();
+  rows = last ? 0 : n.rows();
+  return n;
+}
 
 // slot of a sequence's state, and whether it has one
 __device__ __forceinline__ bool state_slot(const ScanArgs& a, int64_t seq, int64_t& slot) {
-  slot = a.ci ? a.ci[seq] : seq;
+  slot = a.ci ? __builtin_amdgcn_readfirstlane(a.ci[seq]) : seq;
   if (!a.ci) return true;
   return slot >= 0 && slot < a.slots;
 }
 __device__ __forceinline__ bool starts_from_state(const ScanArgs& a, int64_t seq) {
-  return a.init && (!a.has_init || a.has_init[seq]);
+  return a.init && (!a.has_init || __builtin_amdgcn_readfirstlane(a.has_init[seq]));
 }
 
+// A block of 8 waves walks two units of a group (they share v): four waves a unit, each with 32 rows p and
+// NT / 2 columns n of the state.
 // LOCAL: from zeros, the end state goes to the piece's place (pieces whose end nobody needs do nothing).
 // STORE: from the piece's start state (or the sequence's), every chunk's start state goes to `store`.
 template <int NT>
 struct StateShared {
-  __align__(16) uint16_t u[64 * kLd<64>];
+  __align__(16) uint16_t u[2][64 * kLd<64>];
   __align__(16) uint16_t v[64 * kLd<NT>];
-  __align__(16) float w[2][64];  // this chunk's weights and the next one's
-  float total[2];
+  __align__(16) float w[2][2][64];  // weights of this chunk and the next one, by unit
+  float total[2][2];
 };
 template <int NT, bool VEC, bool REV, bool STORE>
 __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& sh) {
-  constexpr int NB = NT / 32;  // 16-column blocks a wave holds: a wave has 32 rows p and NT / 2 columns n
-  uint16_t *su = sh.u, *sv = sh.v;
+  constexpr int NB = NT / 32;  // 16-column blocks a wave holds
   const ScanArgs& a = k.s;
   const int hp = a.H * a.ptiles;
-  const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
-  const int64_t item = blk / hp;
-  const int head_tile = blk % hp, h = head_tile / a.ptiles, p_first = head_tile % a.ptiles * kPTile;
-  const Piece pc = find_piece(a.q, item, a.seg, a.n_slots);
+  const Units us(a, blockIdx.x);
+  if (!us.ok) return;
+  const int wave = wave_id(), un = wave >> 2, w = wave & 3;
+  const bool mine = un < us.count;
+  const Unit me(a, us, mine ? un : 0), u0(a, us, 0), u1(a, us, us.count - 1);
+  const Piece pc = find_piece(a.q, us.item, a.seg, a.n_slots);
   const bool first = pc.r0 == pc.s, last = pc.r1 == pc.e;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, i = lane & 15;
+  const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
   const int p0 = (w & 1) * 32, n0 = (w >> 1) * (NT / 2);
-  const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
+  const int64_t state_at = ((pc.seq * a.H + me.h) * a.P + me.p_first) * a.N;
+  float* place = k.piece + (us.item * hp + me.tile) * (64 * NT);
+  const uint16_t* su = sh.u[un];
+  const uint16_t* sv = sh.v;
   if (!pc.ok) {
     // an empty sequence's adjoint passes through
-    if (REV && STORE && k.end && item >= a.n_slots) {
-      for (int e = threadIdx.x; e < pn * a.N; e += 256) {
-        const int64_t o = ((pc.seq * a.H + h) * a.P + p_first) * a.N + e;
-        k.end[o] = k.start ? k.start[o] : 0.f;
-      }
+    if (REV && STORE && k.end && us.item >= a.n_slots && mine) {
+      for (int e = threadIdx.x & 255; e < me.pn * a.N; e += 256) k.end[state_at + e] = k.start ? k.start[state_at + e] : 0.f;
     }
     return;
   }
@@ -122,15 +145,14 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
     for (int nb = 0; nb < NB; ++nb) S[pb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
   if constexpr (STORE) {
     if (a.seg > 0) {
-      const float* src = k.piece + (item * hp + head_tile) * (64 * NT);
 #pragma unroll
       for (int pb = 0; pb < 2; ++pb)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[pb][nb][r] = src[(p0 + 16 * pb + 4 * g + r) * NT + n0 + 16 * nb + i];
+          for (int r = 0; r < 4; ++r) S[pb][nb][r] = place[(p0 + 16 * pb + 4 * g + r) * NT + n0 + 16 * nb + i];
     } else if (k.start) {
-      const float* src = k.start + ((pc.seq * a.H + h) * a.P + p_first) * a.N;
+      const float* src = k.start + state_at;
 #pragma unroll
       for (int pb = 0; pb < 2; ++pb)
 #pragma unroll
@@ -138,53 +160,58 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int p = p0 + 16 * pb + 4 * g + r, n = n0 + 16 * nb + i;
-            if (p < pn && n < a.N) S[pb][nb][r] = src[(int64_t)p * a.N + n];
+            if (p < me.pn && n < a.N) S[pb][nb][r] = src[(int64_t)p * a.N + n];
           }
     }
   }
 
-  const Rate rate(a, h);
-  const uint16_t* ub = k.u + (int64_t)h * a.P + p_first;
-  const uint16_t* vb = k.v + (int64_t)(h / (a.H / a.G)) * a.N;
-  float log_total = 0.f, raw = 0.f;
-  TileRegs<64> tu;
+  const Rate rate(a, me.h);
+  const uint16_t* ub0 = k.u + (int64_t)u0.h * a.P + u0.p_first;
+  const uint16_t* ub1 = k.u + (int64_t)u1.h * a.P + u1.p_first;
+  const int pn1 = us.count > 1 ? u1.pn : 0;
+  const uint16_t* vb = k.v + (int64_t)us.group * a.N;
+  float log_total = 0.f;
+  RawStep raw{};
+  TileRegs<64> t0, t1;
   TileRegs<NT> tv;
-  // a chunk's weights into buffer `at` by wave 0; forward, a lane's row counts from the chunk's end
+  auto load = [&](const Chunks<REV>& c, int rows) {
+    load_tile<64, VEC>(t0, Rows(ub0 + c.c0 * k.u_ld, k.u_ld, rows, u0.pn, 2), (uint32_t)k.u_ld, u0.pn);
+    load_tile<64, VEC>(t1, Rows(ub1 + c.c0 * k.u_ld, k.u_ld, rows, pn1, 2), (uint32_t)k.u_ld, pn1);
+    load_tile<NT, VEC>(tv, Rows(vb + c.c0 * k.v_ld, k.v_ld, rows, a.N, 2), (uint32_t)k.v_ld, a.N);
+  };
+  // a chunk's weights into buffer `at` by a unit's first wave; forward, a lane's row counts from the end
   const int my = REV ? lane : 63 - lane;
-  auto weights = [&](const Chunks<REV>& c, int at) {
-    const float d = rate.step(raw, my < c.rows());
+  auto weights = [&](int rows, int at) {
+    const float d = rate.step(raw, my < rows);
     const float L = wave_prefix(d * rate.A2);
     // the rows after this one: the previous lane's sum
-    sh.w[at][my] = REV ? ex2(L) : ex2(dpp0<0x138, 0xf>(L)) * d;
-    if (lane == 63) sh.total[at] = L;
+    sh.w[at][un][my] = REV ? ex2(L) : ex2(dpp0<0x138, 0xf>(L)) * d;
+    if (lane == 63) sh.total[at][un] = L;
   };
   Chunks<REV> c(pc.r0, pc.r1);
-  load_tile<64, VEC>(tu, ub + c.c0 * k.u_ld, k.u_ld, c.rows(), pn);
-  load_tile<NT, VEC>(tv, vb + c.c0 * k.v_ld, k.v_ld, c.rows(), a.N);
-  if (w == 0) {
-    raw = raw_step(a, c.c0 + my, c.c0, c.c1, h);
-    weights(c, 0);
-    if (!c.last()) raw = raw_step(a, c.next().c0 + my, c.next().c0, c.next().c1, h);
-  }
+  int rows = c.rows();
+  load(c, rows);
+  raw = raw_step(a, c.c0, rows, my, me.h);
+  if (w == 0) weights(rows, 0);
+  Chunks<REV> after = c;
+  int after_rows = rows;  // the chunk whose raw steps come next
+  after = step_chunk(after, after_rows);
+  raw = raw_step(a, after.c0, after_rows, my, me.h);
   for (int buf = 0;; buf ^= 1) {
-    store_tile<64>(su, tu);
-    store_tile<NT>(sv, tv);
+    store_tile<64>(sh.u[0], t0);
+    store_tile<64>(sh.u[1], t1);
+    store_tile<NT>(sh.v, tv);
     __syncthreads();
     const int64_t here = c.c0;
-    const bool more = !c.last();
-    const float* sw = sh.w[buf];
-    if (more) {
-      c = c.next();
-      load_tile<64, VEC>(tu, ub + c.c0 * k.u_ld, k.u_ld, c.rows(), pn);
-      load_tile<NT, VEC>(tv, vb + c.c0 * k.v_ld, k.v_ld, c.rows(), a.N);
-      if (w == 0) {
-        weights(c, buf ^ 1);
-        if (!c.last()) raw = raw_step(a, c.next().c0 + my, c.next().c0, c.next().c1, h);
-      }
-    }
+    const float* sw = sh.w[buf][un];
+    c = step_chunk(c, rows);  // rows == 0: that was the last one
+    load(c, rows);
+    if (w == 0) weights(rows, buf ^ 1);
+    after = step_chunk(after, after_rows);
+    raw = raw_step(a, after.c0, after_rows, my, me.h);
     if constexpr (STORE) {  // operand order: [n block of 16][p step of 32][lane] 16 bytes, high plane then low
       const int64_t id = here == pc.s ? k.n_chunk_slots + pc.seq : here / kChunk;
-      uint16_t* dst = k.store + (id * hp + head_tile) * (2 * 64 * NT);
+      const Rows dst(k.store + (id * hp + me.tile) * (2 * 64 * NT), 2 * 64 * NT, 1, mine ? 2 * 64 * NT : 0, 2);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         u32x4 hi, lo;
@@ -194,12 +221,12 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
           hi[e] = pk_bf16(x, y);
           lo[e] = pk_bf16(x - bf_lo(hi[e]), y - bf_hi(hi[e]));
         }
-        const int64_t o = (((n0 >> 4) + nb) * 2 + (w & 1)) * 64 + lane;
-        reinterpret_cast<u32x4*>(dst)[o] = hi;
-        reinterpret_cast<u32x4*>(dst + 64 * NT)[o] = lo;
+        const int o = ((((n0 >> 4) + nb) * 2 + (w & 1)) * 64 + lane) * 16;
+        __builtin_amdgcn_raw_buffer_store_b128(hi, dst.r, o, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(lo, dst.r, o + 64 * NT * 2, 0, 0);
       }
     }
-    const float total = sh.total[buf];
+    const float total = sh.total[buf][un];
     log_total += total;
     const float et = ex2(total);
 #pragma unroll
@@ -223,21 +250,21 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
         }
       }
     }
-    if (!more) break;
+    if (rows == 0) break;
     __syncthreads();
   }
 
+  if (!mine) return;
   if constexpr (!STORE) {
-    float* dst = k.piece + (item * hp + head_tile) * (64 * NT);
 #pragma unroll
     for (int pb = 0; pb < 2; ++pb)
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) dst[(p0 + 16 * pb + 4 * g + r) * NT + n0 + 16 * nb + i] = S[pb][nb][r];
-    if (threadIdx.x == 0 && head_tile % a.ptiles == 0) a.piece_decay[item * a.H + h] = log_total;
+        for (int r = 0; r < 4; ++r) place[(p0 + 16 * pb + 4 * g + r) * NT + n0 + 16 * nb + i] = S[pb][nb][r];
+    if (w == 0 && lane == 0 && me.p_first == 0) a.piece_decay[us.item * a.H + me.h] = log_total;
   } else if (REV && first && k.end) {
-    float* dst = k.end + ((pc.seq * a.H + h) * a.P + p_first) * a.N;
+    float* dst = k.end + state_at;
 #pragma unroll
     for (int pb = 0; pb < 2; ++pb)
 #pragma unroll
@@ -245,13 +272,13 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int p = p0 + 16 * pb + 4 * g + r, n = n0 + 16 * nb + i;
-          if (p < pn && n < a.N) dst[(int64_t)p * a.N + n] = S[pb][nb][r];
+          if (p < me.pn && n < a.N) dst[(int64_t)p * a.N + n] = S[pb][nb][r];
         }
   }
 }
 
 template <int NT, bool VEC>
-__global__ __launch_bounds__(256, 2) void ssm_state_local_kernel(StateArgs k) {
+__global__ __launch_bounds__(kThreads, NT > 128 ? 2 : 4) void ssm_state_local_kernel(StateArgs k) {
   __shared__ StateShared<NT> sh;
   state_walk<NT, VEC, false, false>(k, sh);
 }

@@ -35,6 +35,7 @@ extern "C" {
 
 #define SSM_MAX_STATE 256
 #define SSM_MAX_NORM_GROUP 32768
+#define SSM_MAX_ROW_STRIDE (1 << 24) /* elements; the scan's row strides are at most this */
 
 typedef struct {
   int64_t H, P, G, N;
