@@ -59,28 +59,42 @@ bool clash(const Span (&outs)[NO], const Span (&ins)[NI]) {
   return false;
 }
 
-// Rows a piece has at most, 0 for whole sequences.  A block walks a piece chunk by chunk, so fewer
-// blocks than the chip holds leave it idle; cutting sequences costs a first walk for the pieces' states
-// and a join.
-constexpr int64_t kWantBlocks = 512, kMinSeg = 256;
-int64_t piece_rows(const ssm_shape* s, int64_t rows, int64_t nseq) {
-  const int64_t hp = s->H * ceil_div(s->P, kPTile);
-  if (nseq <= 0 || nseq * hp >= kWantBlocks) return 0;
-  int64_t seg = ceil_div(ceil_div(rows * hp, kWantBlocks), kChunk) * kChunk;
+// How the scan's walks are cut.  A block walks a piece chunk by chunk for 4 units (2 where the state tile is 256
+// columns, or where 4 would leave most of the chip idle).  Sequences are cut into pieces where whole ones
+// give too few blocks, or, with offsets (the host does not know the lengths), where one could be long against
+// the rest; the cost is a first walk for the pieces' states and a join.
+constexpr int64_t kWantBlocks = 256, kMinSeg = 256;
+struct Cut {
+  int units;
+  int64_t seg;  // rows a piece has at most, 0 for whole sequences
+};
+Cut cut_rows(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows) {
+  const int64_t per_group = s->H / s->G * ceil_div(s->P, kPTile);
+  Cut c{2, 0};
+  if (nseq <= 0) return c;
+  if (state_tile(s->N) <= 128 && ceil_div(rows, kMinSeg) * s->G * ceil_div(per_group, 4) >= kWantBlocks / 2) c.units = 4;
+  const int64_t sets = s->G * ceil_div(per_group, c.units);
+  const bool enough = nseq * sets >= kWantBlocks;
+  if (batch_rows && enough) return c;
+  int64_t seg = ceil_div(ceil_div(rows * sets, kWantBlocks * (enough ? 2 : 1)), kChunk) * kChunk;
   if (seg < kMinSeg) seg = kMinSeg;
-  return seg * 3 / 2 < rows / nseq ? seg : 0;
+  if (seg < (batch_rows ? rows / nseq : rows - nseq + 1)) c.seg = seg;
+  return c;
 }
 
 int64_t align_up(int64_t v) { return (v + 255) / 256 * 256; }
 
 struct FwdPlan {
+  int units;
   int64_t seg, n_slots, piece, decay, bytes;  // byte offsets into the workspace
 };
-FwdPlan plan_fwd(const ssm_shape* s, int64_t rows, int64_t nseq) {
+FwdPlan plan_fwd(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows) {
   FwdPlan p{};
-  p.seg = piece_rows(s, rows, nseq);
-  p.n_slots = p.seg ? ceil_div(rows, p.seg) : 0;
+  const Cut cut = cut_rows(s, rows, nseq, batch_rows);
+  p.units = cut.units;
+  p.seg = cut.seg;
   if (!p.seg) return p;
+  p.n_slots = batch_rows ? nseq * (ceil_div(rows / nseq, p.seg) - 1) : ceil_div(rows, p.seg);
   const int64_t items = p.n_slots + nseq, hp = s->H * ceil_div(s->P, kPTile);
   p.decay = align_up(items * hp * 64 * state_tile(s->N) * 4);
   p.bytes = p.decay + align_up(items * s->H * 4);
@@ -94,13 +108,14 @@ struct BwdPlan {
 };
 // Blocks of the chunk kernel: one a chunk and group; heads of a group go to several blocks (FP32
 // parts of dB and dC, added by another kernel) only where that many blocks would leave CUs idle.
-BwdPlan plan_bwd(const ssm_shape* s, int64_t rows, int64_t nseq) {
+constexpr int64_t kWantChunkBlocks = 512;
+BwdPlan plan_bwd(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows) {
   BwdPlan p{};
-  p.f = plan_fwd(s, rows, nseq);
+  p.f = plan_fwd(s, rows, nseq, batch_rows);
   p.n_chunk_slots = ceil_div(rows, kChunk);
   p.ids = p.n_chunk_slots + nseq;
   const int64_t hp = s->H * ceil_div(s->P, kPTile), tile = 64 * state_tile(s->N), chunks = ceil_div(rows, kChunk);
-  int64_t split = ceil_div(kWantBlocks, chunks * s->G > 0 ? chunks * s->G : 1);
+  int64_t split = ceil_div(kWantChunkBlocks, chunks * s->G > 0 ? chunks * s->G : 1);
   const int64_t hg = s->H / s->G;
   if (split > hg) split = hg;
   split = ceil_div(hg, ceil_div(hg, split));  // no empty parts
@@ -185,6 +200,7 @@ void fill(ScanArgs* a, const ssm_shape* s, int64_t rows, const void* x, int64_t 
   a->H = (int)s->H, a->P = (int)s->P, a->G = (int)s->G, a->N = (int)s->N;
   a->ptiles = (int)ceil_div(s->P, kPTile);
   a->q = Seqs{seq->cu_seqlens, nseq, seq->cu_seqlens ? 1 : seq->seqlen, rows};
+  a->units = p.units;
   a->seg = p.seg;
   a->n_slots = p.n_slots;
   if (p.seg) {
@@ -215,12 +231,16 @@ extern "C" {
 
 size_t ssm_scan_fwd_workspace_bytes(const ssm_shape* shape, int64_t rows, int64_t nseq) {
   if (!shape_ok(shape) || rows <= 0 || nseq <= 0 || !scan_sizes_ok(shape, rows, nseq)) return 0;
-  return (size_t)plan_fwd(shape, rows, nseq).bytes;
+  const int64_t a = plan_fwd(shape, rows, nseq, false).bytes;
+  const int64_t b = rows % nseq == 0 ? plan_fwd(shape, rows, nseq, true).bytes : 0;
+  return (size_t)(a > b ? a : b);  // offsets or batch rows
 }
 
 size_t ssm_scan_bwd_workspace_bytes(const ssm_shape* shape, int64_t rows, int64_t nseq) {
   if (!shape_ok(shape) || rows < 0 || nseq <= 0 || !scan_sizes_ok(shape, rows, nseq)) return 0;
-  return (size_t)plan_bwd(shape, rows, nseq).bytes;
+  const int64_t a = plan_bwd(shape, rows, nseq, false).bytes;
+  const int64_t b = rows % nseq == 0 ? plan_bwd(shape, rows, nseq, true).bytes : 0;
+  return (size_t)(a > b ? a : b);  // offsets or batch rows
 }
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t d, int64_t group) {
@@ -243,7 +263,7 @@ int ssm_scan_fwd(const ssm_shape* shape, int64_t rows, const void* x, int64_t x_
   ScanArgs a{};
   Span si, sf, sci, shi;
   if (check_states(shape, states, nseq, &a, &si, &sf, &sci, &shi) != CONV1D_OK) return CONV1D_EINVAL;
-  const FwdPlan p = plan_fwd(shape, rows, nseq);
+  const FwdPlan p = plan_fwd(shape, rows, nseq, !seq->cu_seqlens);
   if ((size_t)p.bytes > ws_bytes || (p.bytes && !ws)) return CONV1D_EWORKSPACE;
   if (p.bytes && !aligned(ws, 16)) return CONV1D_EINVAL;
   const Span reads[10] = {span(x, rows, hp, x_ld, 2), span(dt, rows, H, dt_ld, dte), span(B, rows, gn, B_ld, 2),
@@ -276,7 +296,7 @@ int ssm_scan_bwd(const ssm_shape* shape, int64_t rows, const void* dy, int64_t d
                           {dx, dx_ld, hp}, {ddt, ddt_ld, H}, {dB, dB_ld, gn}, {dC, dC_ld, gn}};
   for (const Operand& o : ops)
     if (!scan_operand_ok(o, rows) || !aligned(o.p, o.p == dt || o.p == ddt ? dte : 2)) return CONV1D_EINVAL;
-  const BwdPlan p = nseq > 0 ? plan_bwd(shape, rows, nseq) : BwdPlan{};
+  const BwdPlan p = nseq > 0 ? plan_bwd(shape, rows, nseq, !seq->cu_seqlens) : BwdPlan{};
   if ((size_t)p.bytes > ws_bytes || (p.bytes && !ws)) return CONV1D_EWORKSPACE;
   if (p.bytes && !aligned(ws, 16)) return CONV1D_EINVAL;
   const Span reads[11] = {span(dy, rows, hp, dy_ld, 2), span(x, rows, hp, x_ld, 2), span(dt, rows, H, dt_ld, dte),

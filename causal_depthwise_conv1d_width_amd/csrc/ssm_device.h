@@ -38,10 +38,16 @@ __device__ __forceinline__ uint16_t to_bf16(float a) { return (uint16_t)pk_bf16(
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + ex2(-kLog2e * z)); }
 
-// the step size: v, or log(1 + e^v) (v itself above 20, where the two agree to FP32)
+// The step size: v, or log(1 + e^v) = max(v, 0) + log1p(e^-|v|).  The exponent's argument keeps its low
+// part, and log1p(u) = log(w) u / (w - 1) with w = 1 + u rounded: right to a few ulp at every v.
 __device__ __forceinline__ float step_size(float v, int softplus) {
   if (!softplus) return v;
-  return v > 20.f ? v : log1pf(expf(v));
+  const float a = __builtin_fabsf(v), t = a * kLog2e;
+  const float rest = __builtin_fmaf(a, kLog2e, -t) + a * 1.92596303e-8f;  // log2 e - its FP32 value
+  const float u = ex2(-t) * __builtin_fmaf(rest, -0.693147181f, 1.f);
+  const float w = 1.f + u, m = w - 1.f;
+  const float l = m > 0.f ? __builtin_amdgcn_logf(w) * 0.693147181f * u * __builtin_amdgcn_rcpf(m) : u;
+  return (v > 0.f ? v : 0.f) + (a < 126.f ? l : 0.f);
 }
 
 __device__ __forceinline__ float load_num(const void* p, int64_t i, int f32) {
@@ -145,9 +151,9 @@ __device__ __forceinline__ int64_t seq_of_row(const Seqs& q, int64_t row) {
   return lo + __popcll(__ballot(le)) - 1;
 }
 
-// Item `it` of a cut of the packed rows at sequence starts and multiples of seg: items below n_slots
-// are the pieces that begin at row it * seg inside a sequence, item n_slots + i is sequence i's first.
-__device__ __forceinline__ Piece find_piece(const Seqs& q, int64_t it, int64_t seg, int64_t n_slots) {
+// The cut of the packed rows at sequence starts and at multiples of `step` rows: items below n_slots are the
+// parts that begin at row it * step inside a sequence, item n_slots + i is sequence i's first.
+__device__ __forceinline__ Piece find_part(const Seqs& q, int64_t it, int64_t step, int64_t n_slots) {
   Piece p;
   p.ok = false;
   if (it >= n_slots) {
@@ -156,17 +162,53 @@ __device__ __forceinline__ Piece find_piece(const Seqs& q, int64_t it, int64_t s
     p.r0 = p.s;
     p.ok = p.e > p.s;
   } else {
-    p.r0 = it * seg;
+    p.r0 = it * step;
     p.seq = seq_of_row(q, p.r0);
+    p.s = p.e = p.r1 = 0;
     if (p.seq < 0 || p.seq >= q.nseq) return p;
     seq_bounds(q, p.seq, p.s, p.e);
     p.ok = p.r0 > p.s && p.r0 < p.e;
   }
   p.r1 = p.e;
-  if (seg > 0) {
-    const int64_t cut = (p.r0 / seg + 1) * seg;
+  if (step > 0) {
+    const int64_t cut = (p.r0 / step + 1) * step;
     if (cut < p.r1) p.r1 = cut;
   }
+  return p;
+}
+
+// The pieces of the scan: a sequence is cut every seg rows from its start, rounded down to whole chunks.
+// Piece j >= 1 of the sequence at row s is item s / seg + j: cuts of one sequence are seg rows apart and
+// those of the next one begin seg rows after its start, so no two share an item, and row item * seg lies in
+// the item's sequence.  Batch rows all have the same number of pieces, numbered without gaps, so that a
+// launch has no idle blocks.  seg == 0: whole sequences.
+__device__ __forceinline__ int64_t piece_count(int64_t s, int64_t e, int64_t seg) { return (e - s + seg - 1) / seg; }
+__device__ __forceinline__ int64_t piece_item(const Seqs& q, int64_t seq, int64_t s, int64_t seg, int64_t n_slots, int64_t j) {
+  if (j == 0) return n_slots + seq;
+  return q.cu ? s / seg + j : seq * (piece_count(0, q.seqlen, seg) - 1) + j - 1;
+}
+__device__ __forceinline__ Piece find_piece(const Seqs& q, int64_t it, int64_t seg, int64_t n_slots) {
+  if (seg == 0) return find_part(q, it, 0, 0);
+  Piece p;
+  p.ok = false;
+  p.s = p.e = p.r0 = p.r1 = 0;
+  int64_t j = 0;
+  if (it >= n_slots) {
+    p.seq = it - n_slots;
+  } else if (q.cu) {
+    p.seq = seq_of_row(q, it * seg);
+    if (p.seq < 0 || p.seq >= q.nseq) return p;
+  } else {
+    const int64_t more = piece_count(0, q.seqlen, seg) - 1;
+    p.seq = it / more;
+    j = it % more + 1;
+  }
+  seq_bounds(q, p.seq, p.s, p.e);
+  if (it < n_slots && q.cu) j = it - p.s / seg;
+  p.r0 = j == 0 ? p.s : (p.s + j * seg) / kChunk * kChunk;
+  const int64_t cut = (p.s + (j + 1) * seg) / kChunk * kChunk;
+  p.r1 = p.s + (j + 1) * seg < p.e ? cut : p.e;
+  p.ok = p.s + j * seg < p.e && (j > 0 || it >= n_slots);
   return p;
 }
 
@@ -180,11 +222,13 @@ __device__ __forceinline__ int64_t chunk_end(int64_t r, int64_t r1) {
 // and the transposing reads of 4 rows by 16 columns a quarter wave, then fall on different banks (64
 // of 4 bytes), and every address is one lane's base plus a constant.  (A permutation of each row's pieces
 // has no such constants: its addresses took over a hundred registers.)
-template <int W>
-constexpr int kLd = W + 8;
-template <int W>
+// PAD: 8 elements suit reads of a 16-byte or two 8-byte pieces of 16 rows, 16 the transposing reads (two
+// quarter waves at a time: 8 rows of 32 bytes).
+template <int W, int PAD = 8>
+constexpr int kLd = W + PAD;
+template <int W, int PAD = 8>
 __device__ __forceinline__ int at(int row, int col) {
-  return row * kLd<W> + col;
+  return row * kLd<W, PAD> + col;
 }
 
 // Blocks of the scan's kernels have 8 waves.
@@ -212,14 +256,14 @@ struct Rows {
 };
 constexpr uint32_t kOutside = 0xffffff00u;  // an offset past every buffer's end
 
-// Columns [0, ncols) of a chunk's rows into registers, kThreads threads, zeros outside.  VEC: ncols is a
-// multiple of 8.
+// Columns [0, ncols) of a chunk's rows, from column `col0` of the buffer on, into registers, kThreads
+// threads, zeros outside.  VEC: ncols is a multiple of 8.
 template <int W, bool VEC>
-__device__ __forceinline__ void load_tile(TileRegs<W>& t, const Rows& rows, uint32_t ld, int ncols) {
+__device__ __forceinline__ void load_tile(TileRegs<W>& t, const Rows& rows, uint32_t ld, int ncols, uint32_t col0 = 0) {
 #pragma unroll
   for (int k = 0; k < W / 64; ++k) {
     const int q = threadIdx.x + kThreads * k, row = q / (W / 8), c = (q % (W / 8)) * 8;
-    const uint32_t off = (row * ld + c) * 2;
+    const uint32_t off = (row * ld + c) * 2 + col0 * 2;
     if constexpr (VEC) {
       t.v[k] = __builtin_amdgcn_raw_buffer_load_b128(rows.r, (int)(c < ncols ? off : kOutside), 0, 0);
     } else {
@@ -248,40 +292,46 @@ __device__ __forceinline__ void store4(const Rows& rows, uint32_t ld, int row, i
   }
 }
 
-template <int W>
+template <int W, int PAD = 8>
 __device__ __forceinline__ void store_tile(uint16_t* lds, const TileRegs<W>& t) {
 #pragma unroll
   for (int k = 0; k < W / 64; ++k) {
     const int q = threadIdx.x + kThreads * k;
-    *reinterpret_cast<u32x4*>(lds + at<W>(q / (W / 8), q % (W / 8) * 8)) = t.v[k];
+    *reinterpret_cast<u32x4*>(lds + at<W, PAD>(q / (W / 8), q % (W / 8) * 8)) = t.v[k];
   }
 }
 
-// What a block of the scan or of the state walk works on: two units (64 columns of one head each) of one
-// group, which share the group's B and C rows; a group with an odd number of units ends with a single one.
-// Workgroups are dealt to the 8 XCDs in turn, each with its own L2: the pairs of one piece and group stay
-// on one XCD, and pieces and groups go to the XCDs in turn, so that long and absent pieces spread over them.
+// What a block of the scan or of the state walk works on: U units (64 columns of one head each) of one
+// group, which share the group's B and C rows; a group's last block may have fewer.  Workgroups are dealt to
+// the 8 XCDs in turn, each with its own L2: the blocks of one piece and group stay on one XCD, and pieces and
+// groups go to the XCDs in turn, so that long and absent pieces spread over them.
+template <int U>
 struct Units {
   int64_t item;
   int group, first, count;  // units first .. first + count - 1 of the group
   bool ok;
   __device__ __forceinline__ Units(const ScanArgs& a, uint32_t block) {
-    const uint32_t units = a.H / a.G * a.ptiles, pairs = (units + 1) / 2;
-    const uint32_t set = block / 8 / pairs * 8 + block % 8;  // (piece, group)
+    const uint32_t units = a.H / a.G * a.ptiles, sets = (units + U - 1) / U;
+    const uint32_t set = block / 8 / sets * 8 + block % 8;  // (piece, group)
     item = set / (uint32_t)a.G;
     group = set % (uint32_t)a.G;
-    first = block / 8 % pairs * 2;
-    count = (int)units - first < 2 ? 1 : 2;
+    first = block / 8 % sets * U;
+    count = (int)units - first < U ? (int)units - first : U;
     ok = item < a.n_slots + a.q.nseq;
   }
 };
 struct Unit {
-  int tile, h, p_first, pn;  // head_tile over all heads, head, first column, columns
-  __device__ __forceinline__ Unit(const ScanArgs& a, const Units& u, int k) {
-    tile = u.group * (a.H / a.G) * a.ptiles + u.first + k;
+  int tile, h, p_first, pn;  // head_tile over all heads, head, first column of the head, columns
+  uint32_t col;              // first column of a row of x
+  // unit k of the block; past the block's last one it has no columns
+  template <int U>
+  __device__ __forceinline__ Unit(const ScanArgs& a, const Units<U>& u, int k) {
+    const bool in = k < u.count;
+    tile = u.group * (a.H / a.G) * a.ptiles + u.first + (in ? k : 0);
     h = tile / a.ptiles;
     p_first = tile % a.ptiles * kPTile;
-    pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
+    pn = !in ? 0 : (a.P - p_first < kPTile ? a.P - p_first : kPTile);
+    col = (uint32_t)h * a.P + p_first;
   }
 };
 
@@ -306,27 +356,27 @@ __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 // index = rows of the tile, contracted = columns k0 .. k0 + 31, straight
-template <int W>
+template <int W, int PAD = 8>
 __device__ __forceinline__ bf16x8 op_straight(const uint16_t* lds, int row0, int k0) {
   const int l = threadIdx.x & 63;
-  return *reinterpret_cast<const bf16x8*>(lds + at<W>(row0 + (l & 15), k0 + (l >> 4) * 8));
+  return *reinterpret_cast<const bf16x8*>(lds + at<W, PAD>(row0 + (l & 15), k0 + (l >> 4) * 8));
 }
 // the same, split
-template <int W>
+template <int W, int PAD = 8>
 __device__ __forceinline__ bf16x8 op_split(const uint16_t* lds, int row0, int k0) {
   const int l = threadIdx.x & 63, row = row0 + (l & 15), c = k0 + (l >> 4) * 4;
-  const u32x2 a = *reinterpret_cast<const u32x2*>(lds + at<W>(row, c));
-  const u32x2 b = *reinterpret_cast<const u32x2*>(lds + at<W>(row, c + 16));
+  const u32x2 a = *reinterpret_cast<const u32x2*>(lds + at<W, PAD>(row, c));
+  const u32x2 b = *reinterpret_cast<const u32x2*>(lds + at<W, PAD>(row, c + 16));
   const u32x4 v = {a.x, a.y, b.x, b.y};
   return __builtin_bit_cast(bf16x8, v);
 }
 // index = columns c0 .. c0 + 15, contracted = rows k0 .. k0 + 31, split (the transposing read gives
 // lane i of 16 column i of the 4 rows x 16 columns that the 16 lanes address)
-template <int W>
+template <int W, int PAD = 8>
 __device__ __forceinline__ bf16x8 op_cols(const uint16_t* lds, int k0, int c0) {
   const int l = threadIdx.x & 63, row = k0 + (l >> 4) * 4 + ((l & 15) >> 2), c = c0 + (l & 3) * 4;
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at<W>(row, c)));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at<W>(row + 16, c)));
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at<W, PAD>(row, c)));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at<W, PAD>(row + 16, c)));
   const u32x2 ua = __builtin_bit_cast(u32x2, a), ub = __builtin_bit_cast(u32x2, b);
   const u32x4 v = {ua.x, ua.y, ub.x, ub.y};
   return __builtin_bit_cast(bf16x8, v);

@@ -21,8 +21,8 @@ struct Seqs {
 };
 
 // What the scan's kernels share.  Chunks begin at sequence starts and at multiples of kChunk rows of
-// the packed array; pieces (the unit of one block's sequential walk) begin at sequence starts and at
-// multiples of seg rows, so both are found from a row number alone.  seg == 0: a piece is a sequence.
+// the packed array, so a chunk is found from a row number alone; pieces (the unit of one block's sequential
+// walk) are whole chunks.  seg == 0: a piece is a sequence.
 struct ScanArgs {
   const uint16_t* x;   // [rows, H, P]
   const uint16_t* B;   // [rows, G, N]
@@ -35,7 +35,8 @@ struct ScanArgs {
   int dt_f32, softplus;
   int H, P, G, N, ptiles;
   Seqs q;
-  int64_t seg, n_slots;  // n_slots = ceil(rows / seg), 0 when seg == 0
+  int units;             // units a block of the scan or of the state walk takes: 2 or 4
+  int64_t seg, n_slots;  // pieces other than a sequence's first: with offsets, at most one every seg rows
   // states [slot, H, P, N] of FP32; slot = ci ? ci[seq] : seq
   const float* init;     // nullptr: zeros
   float* fin;            // nullptr: not wanted
@@ -110,12 +111,11 @@ hipError_t launch_gated_bwd(const NormArgs& a, hipStream_t s);
 hipError_t launch_residual_fwd(const NormArgs& a, hipStream_t s);
 hipError_t launch_residual_bwd(const NormArgs& a, hipStream_t s);
 
-// blocks of the scan and of the state walk: pairs of 64-column units for every piece and group, these in
-// sets of 8 (one an XCD)
-inline int64_t pair_blocks(int64_t items, int64_t H, int64_t G, int64_t ptiles) {
-  return (items * G + 7) / 8 * 8 * ((H / G * ptiles + 1) / 2);
+// blocks of the scan and of the state walk: U 64-column units for every piece and group, these in sets of 8
+// (one an XCD)
+inline int64_t unit_blocks(int64_t items, int64_t H, int64_t G, int64_t ptiles, int U) {
+  return (items * G + 7) / 8 * 8 * ((H / G * ptiles + U - 1) / U);
 }
-
 inline int state_tile(int64_t N) { return N <= 64 ? 64 : (N <= 128 ? 128 : 256); }
 
 // threads that share one (row, group) of a norm

@@ -1,97 +1,106 @@
 // ssm_scan.hip -- forward selective state space scan over packed rows.
 //
-// A block walks one piece of one sequence for two units (64 columns of a head) of one group, a chunk of
+// A block walks one piece of one sequence for U units (64 columns of a head) of one group, a chunk of
 // 64 rows at a time, with the FP32 states in registers from chunk to chunk (no state travels through memory):
 //   Y = e^{L} (C S) + (M * dt * (C B^T)) X + D X,    S' = e^{L_Q} S + X^T (e^{L_Q - L} dt B)
 // The units share the chunk's B and C rows and its 64 x 64 scores C B^T, whose ten 16 x 16 blocks up to the
-// diagonal go to the eight waves; each wave decays its blocks for both units.  Then a wave owns 16 columns p of
-// its unit's Y and state, which it holds transposed ([n, p]: registers n), as the operand that C S needs.
+// diagonal go to the eight waves; each wave decays its blocks for every unit.  Then a wave owns 16 * PB columns
+// p of its unit's Y and state, which it holds transposed ([n, p]: registers n), as the operand that C S needs.
+// Shared memory feeds the matrix instructions and is what bounds the chunk: with four units a wave uses every
+// B, C and score operand twice (125 KB a unit and chunk against 226 KB with two).
 #include "ssm_state.h"
 
 namespace cssm {
 
-template <int NT, bool VEC>
+template <int NT, int U, bool VEC>
 __global__ __launch_bounds__(kThreads, 2) void ssm_scan_fwd_kernel(ScanArgs a) {
-  constexpr int NB = NT / 16;
-  __shared__ __align__(16) uint16_t sx_[2][64 * kLd<64>];
-  __shared__ __align__(16) uint16_t sB[64 * kLd<NT>];
+  constexpr int NB = NT / 16, WU = 8 / U, PB = 4 / WU;
+  __shared__ __align__(16) uint16_t sx_[U][64 * kLd<64, 16>];
+  __shared__ __align__(16) uint16_t sB[64 * kLd<NT, 16>];
   __shared__ __align__(16) uint16_t sC[64 * kLd<NT>];
-  __shared__ __align__(16) uint16_t sP_[2][64 * kLd<64>];
-  __shared__ __align__(16) float sdecay[2][2][4][64];  // this chunk's and the next one's, by unit
+  __shared__ __align__(16) uint16_t sP_[U][64 * kLd<64>];
+  __shared__ __align__(16) float sdecay[2][U][4][64];  // this chunk's and the next one's, by unit
   const int hp = a.H * a.ptiles;
-  const Units us(a, blockIdx.x);
+  const Units<U> us(a, blockIdx.x);
   if (!us.ok) return;
-  const int wave = wave_id(), un = wave >> 2, w = wave & 3;
-  const bool mine = un < us.count;
-  const Unit me(a, us, mine ? un : 0), u0(a, us, 0), u1(a, us, us.count - 1);
-  const int pn = mine ? me.pn : 0;
+  const int wave = wave_id(), un = wave / WU, w = wave % WU;
+  const Unit me(a, us, un);
+  const int pn = me.pn;
   const Piece pc = find_piece(a.q, us.item, a.seg, a.n_slots);
   const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
-  const int p_in = 16 * w + i;         // this lane's state column
-  const int p_out = 16 * w + 4 * g;    // this lane's first of four output columns
+  const int p_in = 16 * PB * w + i;       // this lane's first state column
+  const int p_out = 16 * PB * w + 4 * g;  // this lane's first of four output columns
   const int64_t state_at = ((int64_t)me.h * a.P + me.p_first) * a.N;
   int64_t slot = 0;
   if (!pc.ok) {
     // an empty sequence: a separate final state array still gets the start state
     if (us.item >= a.n_slots && a.fin && a.fin != a.init && state_slot(a, pc.seq, slot)) {
       const bool from = starts_from_state(a, pc.seq);
-      for (int e = threadIdx.x & 255; e < pn * a.N; e += 256)
+      for (int e = threadIdx.x % (64 * WU); e < pn * a.N; e += 64 * WU)
         a.fin[slot * a.s_slot + state_at + e] = from ? a.init[slot * a.s_slot + state_at + e] : 0.f;
     }
     return;
   }
   uint16_t* yb = a.y + (int64_t)me.h * a.P + me.p_first;
   if (!state_slot(a, pc.seq, slot)) {  // no slot: zero rows, no state access
-    for (int64_t r = pc.r0 + w; r < pc.r1; r += 4)
+    for (int64_t r = pc.r0 + w; r < pc.r1; r += WU)
       if (lane < pn) yb[r * a.y_ld + lane] = 0;
     return;
   }
 
-  f32x4 S[NB];
+  f32x4 S[PB][NB];
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) S[nb] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (a.seg > 0) {
+  for (int pb = 0; pb < PB; ++pb)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) S[pb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (a.seg > 0 && pc.e - pc.s > a.seg) {
     const float* src = a.piece + (us.item * hp + me.tile) * (64 * NT) + p_in * NT + 4 * g;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) S[nb] = *reinterpret_cast<const f32x4*>(src + 16 * nb);
-  } else if (starts_from_state(a, pc.seq) && p_in < pn) {
-    const float* src = a.init + slot * a.s_slot + state_at + (int64_t)p_in * a.N + 4 * g;
+    for (int pb = 0; pb < PB; ++pb)
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      if (16 * nb + 4 * g + 3 < a.N) {
-        S[nb] = *reinterpret_cast<const f32x4_a4*>(src + 16 * nb);
-      } else {
+      for (int nb = 0; nb < NB; ++nb) S[pb][nb] = *reinterpret_cast<const f32x4*>(src + pb * 16 * NT + 16 * nb);
+  } else if (starts_from_state(a, pc.seq)) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (16 * nb + 4 * g + r < a.N) S[nb][r] = src[16 * nb + r];
+    for (int pb = 0; pb < PB; ++pb) {
+      if (p_in + 16 * pb >= pn) continue;
+      const float* src = a.init + slot * a.s_slot + state_at + (int64_t)(p_in + 16 * pb) * a.N + 4 * g;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        if (16 * nb + 4 * g + 3 < a.N) {
+          S[pb][nb] = *reinterpret_cast<const f32x4_a4*>(src + 16 * nb);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (16 * nb + 4 * g + r < a.N) S[pb][nb][r] = src[16 * nb + r];
+        }
       }
     }
   }
 
   const Rate rate(a, me.h);
   const float Dh = a.D ? uniform(a.D[me.h]) : 0.f;
-  const uint16_t* xb0 = a.x + (int64_t)u0.h * a.P + u0.p_first;
-  const uint16_t* xb1 = a.x + (int64_t)u1.h * a.P + u1.p_first;
-  const int pn1 = us.count > 1 ? u1.pn : 0;
   const int64_t gn = (int64_t)us.group * a.N;
   const uint16_t *Bb = a.B + gn, *Cb = a.C + gn;
-  TileRegs<64> tx0, tx1;
+  TileRegs<64> tx[U];
   TileRegs<NT> tB, tC;
   auto load = [&](const Chunks<false>& c, int rows) {
-    load_tile<64, VEC>(tx0, Rows(xb0 + c.c0 * a.x_ld, a.x_ld, rows, u0.pn, 2), (uint32_t)a.x_ld, u0.pn);
-    load_tile<64, VEC>(tx1, Rows(xb1 + c.c0 * a.x_ld, a.x_ld, rows, pn1, 2), (uint32_t)a.x_ld, pn1);
+    const Rows xr(a.x + c.c0 * a.x_ld, a.x_ld, rows, a.H * a.P, 2);
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const Unit o(a, us, q);
+      load_tile<64, VEC>(tx[q], xr, (uint32_t)a.x_ld, o.pn, o.col);
+    }
     load_tile<NT, VEC>(tB, Rows(Bb + c.c0 * a.B_ld, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
     load_tile<NT, VEC>(tC, Rows(Cb + c.c0 * a.C_ld, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
   };
-  // a chunk's decays into buffer `at`: a unit's wave 2 the prefix sums, steps and their powers, its wave 3,
-  // whose lanes count from the chunk's end, the weights of the state update (waves 0 and 1 of the block have
-  // two score blocks, these one)
+  // a chunk's decays into buffer `at`: a unit's last wave but one the prefix sums, steps and their powers, its
+  // last, whose lanes count from the chunk's end, the weights of the state update
   RawStep raw{};
-  const int my = w == 2 ? lane : 63 - lane;
+  const int my = w == WU - 2 ? lane : 63 - lane;
   auto decays = [&](int rows, int at) {
     const float d = rate.step(raw, my < rows);
     const float L = wave_prefix(d * rate.A2);
-    if (w == 2) {
+    if (w == WU - 2) {
       sdecay[at][un][0][lane] = L;
       sdecay[at][un][1][lane] = d;
       sdecay[at][un][2][lane] = ex2(L);
@@ -103,24 +112,24 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_fwd_kernel(ScanArgs a) {
   int rows = c.rows();
   load(c, rows);
   raw = raw_step(a, c.c0, rows, my, me.h);
-  if (w >= 2) decays(rows, 0);
+  if (w >= WU - 2) decays(rows, 0);
   Chunks<false> after = c;
   int after_rows = rows;  // the chunk whose raw steps come next
   after = step_chunk(after, after_rows);
   raw = raw_step(a, after.c0, after_rows, my, me.h);
   // products over 32 columns read two blocks past the diagonal, which no wave writes
-  for (int e = threadIdx.x; e < 2 * 64 * kLd<64> / 2; e += kThreads) reinterpret_cast<uint32_t*>(sP_)[e] = 0u;
+  for (int e = threadIdx.x; e < U * 64 * kLd<64> / 2; e += kThreads) reinterpret_cast<uint32_t*>(sP_)[e] = 0u;
   const uint16_t *sx = sx_[un], *sP = sP_[un];
   for (int buf = 0;; buf ^= 1) {
-    store_tile<64>(sx_[0], tx0);
-    store_tile<64>(sx_[1], tx1);
-    store_tile<NT>(sB, tB);
+#pragma unroll
+    for (int q = 0; q < U; ++q) store_tile<64, 16>(sx_[q], tx[q]);
+    store_tile<NT, 16>(sB, tB);
     store_tile<NT>(sC, tC);
     __syncthreads();
     const Rows out(yb + c.c0 * a.y_ld, a.y_ld, rows, pn, 2);
     c = step_chunk(c, rows);  // rows == 0: that was the last one
     load(c, rows);
-    if (w >= 2) decays(rows, buf ^ 1);
+    if (w >= WU - 2) decays(rows, buf ^ 1);
     after = step_chunk(after, after_rows);
     raw = raw_step(a, after.c0, after_rows, my, me.h);
     // score block (ib, jb): rows i in the lanes, columns j in the registers, decayed, times dt_j
@@ -128,9 +137,9 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_fwd_kernel(ScanArgs a) {
       f32x4 t = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < NT / 32; ++ks)
-        t = mma(op_straight<NT>(sB, 16 * jb, 32 * ks), op_straight<NT>(sC, 16 * ib, 32 * ks), t);
+        t = mma(op_straight<NT, 16>(sB, 16 * jb, 32 * ks), op_straight<NT>(sC, 16 * ib, 32 * ks), t);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < U; ++q) {
         const float(*s)[64] = sdecay[buf][q];
         const float Li = s[0][16 * ib + i];
         const f32x4 Lj = *reinterpret_cast<const f32x4*>(s[0] + 16 * jb + 4 * g);
@@ -151,71 +160,102 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_fwd_kernel(ScanArgs a) {
     if (wave < 2) scores(1 - wave, 1 - wave);
     phase();
     // Y^T (registers p, lanes i) from the state before the chunk
-    f32x4 y[4];
+    f32x4 y[PB][4];
 #pragma unroll
-    for (int ib = 0; ib < 4; ++ib) y[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int pb = 0; pb < PB; ++pb)
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) y[pb][ib] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < NT / 32; ++ks) {
-      const bf16x8 s = op_result(S[2 * ks], S[2 * ks + 1]);
+      bf16x8 s[PB];
 #pragma unroll
-      for (int ib = 0; ib < 4; ++ib) y[ib] = mma(s, op_split<NT>(sC, 16 * ib, 32 * ks), y[ib]);
+      for (int pb = 0; pb < PB; ++pb) s[pb] = op_result(S[pb][2 * ks], S[pb][2 * ks + 1]);
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) {
+        const bf16x8 cv = op_split<NT>(sC, 16 * ib, 32 * ks);
+#pragma unroll
+        for (int pb = 0; pb < PB; ++pb) y[pb][ib] = mma(s[pb], cv, y[pb][ib]);
+      }
     }
     const float *se = sdecay[buf][un][2], *sw = sdecay[buf][un][3];
 #pragma unroll
-    for (int ib = 0; ib < 4; ++ib) y[ib] *= se[16 * ib + i];
+    for (int ib = 0; ib < 4; ++ib)
+#pragma unroll
+      for (int pb = 0; pb < PB; ++pb) y[pb][ib] *= se[16 * ib + i];
     phase();
     __syncthreads();
     const float et = se[63];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) S[nb] *= et;
+    for (int pb = 0; pb < PB; ++pb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) S[pb][nb] *= et;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      const bf16x8 x = op_cols<64>(sx, 32 * ks, 16 * w);
+      bf16x8 hi[PB], lo[PB];
+      {
+        bf16x8 x[PB];
 #pragma unroll
-      for (int ib = 2 * ks; ib < 4; ++ib) y[ib] = mma(x, op_split<64>(sP, 16 * ib, 32 * ks), y[ib]);
-      const f32x4 wa = *reinterpret_cast<const f32x4*>(sw + 32 * ks + 4 * g);
-      const f32x4 wb = *reinterpret_cast<const f32x4*>(sw + 32 * ks + 16 + 4 * g);
-      bf16x8 hi, lo;
-      split_scaled(x, wa, wb, hi, lo);
+        for (int pb = 0; pb < PB; ++pb) x[pb] = op_cols<64, 16>(sx, 32 * ks, 16 * (PB * w + pb));
+#pragma unroll
+        for (int ib = 2 * ks; ib < 4; ++ib) {
+          const bf16x8 pv = op_split<64>(sP, 16 * ib, 32 * ks);
+#pragma unroll
+          for (int pb = 0; pb < PB; ++pb) y[pb][ib] = mma(x[pb], pv, y[pb][ib]);
+        }
+        const f32x4 wa = *reinterpret_cast<const f32x4*>(sw + 32 * ks + 4 * g);
+        const f32x4 wb = *reinterpret_cast<const f32x4*>(sw + 32 * ks + 16 + 4 * g);
+#pragma unroll
+        for (int pb = 0; pb < PB; ++pb) split_scaled(x[pb], wa, wb, hi[pb], lo[pb]);
+      }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const bf16x8 b = op_cols<NT>(sB, 32 * ks, 16 * nb);
-        S[nb] = mma(b, hi, S[nb]);
-        S[nb] = mma(b, lo, S[nb]);
+        const bf16x8 b = op_cols<NT, 16>(sB, 32 * ks, 16 * nb);
+#pragma unroll
+        for (int pb = 0; pb < PB; ++pb) {
+          S[pb][nb] = mma(b, hi[pb], S[pb][nb]);
+          S[pb][nb] = mma(b, lo[pb], S[pb][nb]);
+        }
       }
       phase();
     }
 #pragma unroll
-    for (int ib = 0; ib < 4; ++ib) {
-      const int row = 16 * ib + i;
-      const u32x2 xv = *reinterpret_cast<const u32x2*>(sx + at<64>(row, p_out));
-      const u32x2 o = {pk_bf16(y[ib][0] + Dh * bf_lo(xv.x), y[ib][1] + Dh * bf_hi(xv.x)),
-                       pk_bf16(y[ib][2] + Dh * bf_lo(xv.y), y[ib][3] + Dh * bf_hi(xv.y))};
-      store4<VEC>(out, (uint32_t)a.y_ld, row, p_out, pn, o);
-    }
+    for (int ib = 0; ib < 4; ++ib)
+#pragma unroll
+      for (int pb = 0; pb < PB; ++pb) {
+        const int row = 16 * ib + i, p = p_out + 16 * pb;
+        const u32x2 xv = *reinterpret_cast<const u32x2*>(sx + at<64, 16>(row, p));
+        const f32x4 v = y[pb][ib];
+        const u32x2 o = {pk_bf16(v[0] + Dh * bf_lo(xv.x), v[1] + Dh * bf_hi(xv.x)),
+                         pk_bf16(v[2] + Dh * bf_lo(xv.y), v[3] + Dh * bf_hi(xv.y))};
+        store4<VEC>(out, (uint32_t)a.y_ld, row, p, pn, o);
+      }
     if (rows == 0) break;
     __syncthreads();
   }
 
-  if (a.fin && pc.r1 == pc.e && p_in < pn) {
-    float* dst = a.fin + slot * a.s_slot + state_at + (int64_t)p_in * a.N + 4 * g;
+  if (a.fin && pc.r1 == pc.e) {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      if (16 * nb + 4 * g + 3 < a.N) {
-        *reinterpret_cast<f32x4_a4*>(dst + 16 * nb) = S[nb];
-      } else {
+    for (int pb = 0; pb < PB; ++pb) {
+      if (p_in + 16 * pb >= pn) continue;
+      float* dst = a.fin + slot * a.s_slot + state_at + (int64_t)(p_in + 16 * pb) * a.N + 4 * g;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (16 * nb + 4 * g + r < a.N) dst[16 * nb + r] = S[nb][r];
+      for (int nb = 0; nb < NB; ++nb) {
+        if (16 * nb + 4 * g + 3 < a.N) {
+          *reinterpret_cast<f32x4_a4*>(dst + 16 * nb) = S[pb][nb];
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (16 * nb + 4 * g + r < a.N) dst[16 * nb + r] = S[pb][nb][r];
+        }
       }
     }
   }
 }
 
-template <int NT, bool VEC>
+template <int NT, int U, bool VEC>
 static hipError_t launch(const ScanArgs& a, hipStream_t s) {
   const int64_t items = a.n_slots + a.q.nseq, hp = (int64_t)a.H * a.ptiles;
-  const dim3 walk((uint32_t)(pair_blocks(items, a.H, a.G, a.ptiles)));
+  const dim3 walk((uint32_t)unit_blocks(items, a.H, a.G, a.ptiles, U));
   if (a.seg > 0) {
     StateArgs k{};
     k.s = a;
@@ -225,11 +265,18 @@ static hipError_t launch(const ScanArgs& a, hipStream_t s) {
     k.v_ld = a.B_ld;
     k.start = a.init;
     k.piece = a.piece;
-    ssm_state_local_kernel<NT, VEC><<<walk, kThreads, 0, s>>>(k);
+    ssm_state_local_kernel<NT, U, VEC><<<walk, kThreads, 0, s>>>(k);
     ssm_join_kernel<NT, false><<<dim3((uint32_t)(a.q.nseq * hp * (64 * NT / 1024))), 256, 0, s>>>(k);
   }
-  ssm_scan_fwd_kernel<NT, VEC><<<walk, kThreads, 0, s>>>(a);
+  ssm_scan_fwd_kernel<NT, U, VEC><<<walk, kThreads, 0, s>>>(a);
   return hipGetLastError();
+}
+template <int NT, bool VEC>
+static hipError_t launch(const ScanArgs& a, hipStream_t s) {
+  if constexpr (NT <= 128) {
+    if (a.units == 4) return launch<NT, 4, VEC>(a, s);
+  }
+  return launch<NT, 2, VEC>(a, s);
 }
 
 hipError_t launch_scan_fwd(const ScanArgs& a, bool vec, hipStream_t s) {

@@ -21,11 +21,11 @@
 
 namespace cssm {
 
-template <int NT, bool VEC, bool STORE>
-__global__ __launch_bounds__(kThreads, NT > 128 ? 2 : 4) void ssm_states_kernel(StateArgs f, StateArgs r) {
-  __shared__ StateShared<NT> sh;
-  if (blockIdx.y == 0) state_walk<NT, VEC, false, STORE>(f, sh);
-  else state_walk<NT, VEC, true, STORE>(r, sh);
+template <int NT, int U, bool VEC, bool STORE>
+__global__ __launch_bounds__(kThreads, 2) void ssm_states_kernel(StateArgs f, StateArgs r) {
+  __shared__ StateShared<NT, U> sh;
+  if (blockIdx.y == 0) state_walk<NT, U, VEC, false, STORE>(f, sh);
+  else state_walk<NT, U, VEC, true, STORE>(r, sh);
 }
 
 __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {  // two bf16 products in FP32
@@ -39,7 +39,7 @@ __device__ __forceinline__ float across16(float v) {  // sum over the four rows 
 // A block of 8 waves takes a chunk and walks the 64-column units of its heads.  A wave owns 16 * NBW columns n
 // of dB and dC (with NT = 64: two waves share 16, each with half of the rows) and two 16 x 16 blocks of dX.
 template <int NT, bool VEC>
-__global__ __launch_bounds__(kThreads, NT > 128 ? 2 : 4) void ssm_scan_bwd_kernel(ScanBwdArgs b) {
+__global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b) {
   constexpr int NBW = NT > 128 ? NT / 128 : 1;  // 16-column blocks n of a wave
   constexpr int KB = NT > 64 ? 4 : 2;           // 16-row blocks of a wave
   constexpr int R = (NT > 128 ? NT : 128) * kLd<64>;
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 2 : 4) void ssm_scan_bwd_kerne
   const int64_t id = blk / b.hsplit / a.G;
   const int hg = a.H / a.G, per = (hg + b.hsplit - 1) / b.hsplit;
   const int h_lo = grp * hg + part * per, h_hi = h_lo + per < (grp + 1) * hg ? h_lo + per : (grp + 1) * hg;
-  const Piece pc = find_piece(a.q, id, kChunk, b.n_chunk_slots);
+  const Piece pc = find_part(a.q, id, kChunk, b.n_chunk_slots);
   if (!pc.ok) {
     for (int e = threadIdx.x; e < (h_hi - h_lo) * 3; e += kThreads) b.head_part[(id * a.H + h_lo) * 3 + e] = 0.f;
     return;
@@ -441,7 +441,7 @@ __global__ __launch_bounds__(256) void ssm_head_reduce_kernel(ScanBwdArgs b, int
   }
 }
 
-template <int NT, bool VEC>
+template <int NT, int U, bool VEC>
 static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
   const ScanArgs& a = b.s;
   const int64_t hp = (int64_t)a.H * a.ptiles, items = a.n_slots + a.q.nseq, ids = b.n_chunk_slots + a.q.nseq;
@@ -456,14 +456,14 @@ static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
     ssm_head_reduce_kernel<<<dim3((uint32_t)a.H), 256, 0, s>>>(b, 0);
     return hipGetLastError();
   }
-  const dim3 walk((uint32_t)(pair_blocks(items, a.H, a.G, a.ptiles)), 2);
+  const dim3 walk((uint32_t)unit_blocks(items, a.H, a.G, a.ptiles, U), 2);
   if (a.seg > 0) {
     const dim3 join((uint32_t)(a.q.nseq * hp * (64 * NT / 1024)));
-    ssm_states_kernel<NT, VEC, false><<<walk, kThreads, 0, s>>>(f, r);
+    ssm_states_kernel<NT, U, VEC, false><<<walk, kThreads, 0, s>>>(f, r);
     ssm_join_kernel<NT, false><<<join, 256, 0, s>>>(f);
     ssm_join_kernel<NT, true><<<join, 256, 0, s>>>(r);
   }
-  ssm_states_kernel<NT, VEC, true><<<walk, kThreads, 0, s>>>(f, r);
+  ssm_states_kernel<NT, U, VEC, true><<<walk, kThreads, 0, s>>>(f, r);
   ssm_scan_bwd_kernel<NT, VEC><<<dim3((uint32_t)(ids * a.G * b.hsplit)), kThreads, 0, s>>>(b);
   if (b.hsplit > 1 && a.q.rows > 0) {
     const int64_t n = a.q.rows * a.G * a.N;
@@ -471,6 +471,14 @@ static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
   }
   ssm_head_reduce_kernel<<<dim3((uint32_t)a.H), 256, 0, s>>>(b, ids);
   return hipGetLastError();
+}
+
+template <int NT, bool VEC>
+static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
+  if constexpr (NT <= 128) {
+    if (b.s.units == 4) return launch<NT, 4, VEC>(b, s);
+  }
+  return launch<NT, 2, VEC>(b, s);
 }
 
 hipError_t launch_scan_bwd(const ScanBwdArgs& b, bool vec, hipStream_t s) {

@@ -100,27 +100,28 @@ __device__ __forceinline__ bool starts_from_state(const ScanArgs& a, int64_t seq
   return a.init && (!a.has_init || __builtin_amdgcn_readfirstlane(a.has_init[seq]));
 }
 
-// A block of 8 waves walks two units of a group (they share v): four waves a unit, each with 32 rows p and
-// NT / 2 columns n of the state.
+// A block of 8 waves walks U units of a group (they share v): 8 / U waves a unit, each with 16 * PB rows p of the
+// state and, with two units, half of them and half of the columns n.  A wave of four units reads a v operand
+// for two row blocks, which halves the shared memory traffic that bounds the walk.
 // LOCAL: from zeros, the end state goes to the piece's place (pieces whose end nobody needs do nothing).
 // STORE: from the piece's start state (or the sequence's), every chunk's start state goes to `store`.
-template <int NT>
+template <int NT, int U>
 struct StateShared {
-  __align__(16) uint16_t u[2][64 * kLd<64>];
-  __align__(16) uint16_t v[64 * kLd<NT>];
-  __align__(16) float w[2][2][64];  // weights of this chunk and the next one, by unit
-  float total[2][2];
+  __align__(16) uint16_t u[U][64 * kLd<64, 16>];
+  __align__(16) uint16_t v[64 * kLd<NT, 16>];
+  __align__(16) float w[2][U][64];  // weights of this chunk and the next one, by unit
+  float total[2][U];
 };
-template <int NT, bool VEC, bool REV, bool STORE>
-__device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& sh) {
-  constexpr int NB = NT / 32;  // 16-column blocks a wave holds
+template <int NT, int U, bool VEC, bool REV, bool STORE>
+__device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U>& sh) {
+  constexpr int WU = 8 / U;                   // waves a unit: two, or two by two
+  constexpr int NB = NT / 16 / (WU / 2);      // 16-column blocks a wave holds, with two 16-row blocks
   const ScanArgs& a = k.s;
   const int hp = a.H * a.ptiles;
-  const Units us(a, blockIdx.x);
+  const Units<U> us(a, blockIdx.x);
   if (!us.ok) return;
-  const int wave = wave_id(), un = wave >> 2, w = wave & 3;
-  const bool mine = un < us.count;
-  const Unit me(a, us, mine ? un : 0), u0(a, us, 0), u1(a, us, us.count - 1);
+  const int wave = wave_id(), un = wave / WU, w = wave % WU;
+  const Unit me(a, us, un);
   const Piece pc = find_piece(a.q, us.item, a.seg, a.n_slots);
   const bool first = pc.r0 == pc.s, last = pc.r1 == pc.e;
   const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
@@ -131,8 +132,9 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
   const uint16_t* sv = sh.v;
   if (!pc.ok) {
     // an empty sequence's adjoint passes through
-    if (REV && STORE && k.end && us.item >= a.n_slots && mine) {
-      for (int e = threadIdx.x & 255; e < me.pn * a.N; e += 256) k.end[state_at + e] = k.start ? k.start[state_at + e] : 0.f;
+    if (REV && STORE && k.end && us.item >= a.n_slots) {
+      for (int e = threadIdx.x % (64 * WU); e < me.pn * a.N; e += 64 * WU)
+        k.end[state_at + e] = k.start ? k.start[state_at + e] : 0.f;
     }
     return;
   }
@@ -144,7 +146,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) S[pb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
   if constexpr (STORE) {
-    if (a.seg > 0) {
+    if (a.seg > 0 && pc.e - pc.s > a.seg) {
 #pragma unroll
       for (int pb = 0; pb < 2; ++pb)
 #pragma unroll
@@ -166,17 +168,18 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
   }
 
   const Rate rate(a, me.h);
-  const uint16_t* ub0 = k.u + (int64_t)u0.h * a.P + u0.p_first;
-  const uint16_t* ub1 = k.u + (int64_t)u1.h * a.P + u1.p_first;
-  const int pn1 = us.count > 1 ? u1.pn : 0;
   const uint16_t* vb = k.v + (int64_t)us.group * a.N;
   float log_total = 0.f;
   RawStep raw{};
-  TileRegs<64> t0, t1;
+  TileRegs<64> tu[U];
   TileRegs<NT> tv;
   auto load = [&](const Chunks<REV>& c, int rows) {
-    load_tile<64, VEC>(t0, Rows(ub0 + c.c0 * k.u_ld, k.u_ld, rows, u0.pn, 2), (uint32_t)k.u_ld, u0.pn);
-    load_tile<64, VEC>(t1, Rows(ub1 + c.c0 * k.u_ld, k.u_ld, rows, pn1, 2), (uint32_t)k.u_ld, pn1);
+    const Rows ur(k.u + c.c0 * k.u_ld, k.u_ld, rows, a.H * a.P, 2);
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const Unit o(a, us, q);
+      load_tile<64, VEC>(tu[q], ur, (uint32_t)k.u_ld, o.pn, o.col);
+    }
     load_tile<NT, VEC>(tv, Rows(vb + c.c0 * k.v_ld, k.v_ld, rows, a.N, 2), (uint32_t)k.v_ld, a.N);
   };
   // a chunk's weights into buffer `at` by a unit's first wave; forward, a lane's row counts from the end
@@ -198,9 +201,9 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
   after = step_chunk(after, after_rows);
   raw = raw_step(a, after.c0, after_rows, my, me.h);
   for (int buf = 0;; buf ^= 1) {
-    store_tile<64>(sh.u[0], t0);
-    store_tile<64>(sh.u[1], t1);
-    store_tile<NT>(sh.v, tv);
+#pragma unroll
+    for (int q = 0; q < U; ++q) store_tile<64, 16>(sh.u[q], tu[q]);
+    store_tile<NT, 16>(sh.v, tv);
     __syncthreads();
     const int64_t here = c.c0;
     const float* sw = sh.w[buf][un];
@@ -211,7 +214,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
     raw = raw_step(a, after.c0, after_rows, my, me.h);
     if constexpr (STORE) {  // operand order: [n block of 16][p step of 32][lane] 16 bytes, high plane then low
       const int64_t id = here == pc.s ? k.n_chunk_slots + pc.seq : here / kChunk;
-      const Rows dst(k.store + (id * hp + me.tile) * (2 * 64 * NT), 2 * 64 * NT, 1, mine ? 2 * 64 * NT : 0, 2);
+      const Rows dst(k.store + (id * hp + me.tile) * (2 * 64 * NT), 2 * 64 * NT, 1, me.pn ? 2 * 64 * NT : 0, 2);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         u32x4 hi, lo;
@@ -239,10 +242,10 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
       const f32x4 wb = *reinterpret_cast<const f32x4*>(sw + 32 * ks + 16 + 4 * g);
       bf16x8 hi[2], lo[2];
 #pragma unroll
-      for (int pb = 0; pb < 2; ++pb) split_scaled(op_cols<64>(su, 32 * ks, p0 + 16 * pb), wa, wb, hi[pb], lo[pb]);
+      for (int pb = 0; pb < 2; ++pb) split_scaled(op_cols<64, 16>(su, 32 * ks, p0 + 16 * pb), wa, wb, hi[pb], lo[pb]);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const bf16x8 b = op_cols<NT>(sv, 32 * ks, n0 + 16 * nb);
+        const bf16x8 b = op_cols<NT, 16>(sv, 32 * ks, n0 + 16 * nb);
 #pragma unroll
         for (int pb = 0; pb < 2; ++pb) {
           S[pb][nb] = mma(hi[pb], b, S[pb][nb]);
@@ -254,7 +257,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
     __syncthreads();
   }
 
-  if (!mine) return;
+  if (me.pn == 0) return;
   if constexpr (!STORE) {
 #pragma unroll
     for (int pb = 0; pb < 2; ++pb)
@@ -277,10 +280,10 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT>& 
   }
 }
 
-template <int NT, bool VEC>
-__global__ __launch_bounds__(kThreads, NT > 128 ? 2 : 4) void ssm_state_local_kernel(StateArgs k) {
-  __shared__ StateShared<NT> sh;
-  state_walk<NT, VEC, false, false>(k, sh);
+template <int NT, int U, bool VEC>
+__global__ __launch_bounds__(kThreads, 2) void ssm_state_local_kernel(StateArgs k) {
+  __shared__ StateShared<NT, U> sh;
+  state_walk<NT, U, VEC, false, false>(k, sh);
 }
 
 // Local end states of a sequence's pieces -> start states, in place, in the order of the walk:
@@ -307,10 +310,10 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(StateArgs k) {
     for (int r = 0; r < 4; ++r)
       if (n + r < a.N) S[r] = src[n + r];
   }
-  const int64_t slot0 = s / a.seg + 1, pieces = (e - 1) / a.seg - s / a.seg + 1;
+  const int64_t pieces = piece_count(s, e, a.seg);
+  if (pieces == 1) return;  // starts from the sequence's own state
   for (int64_t m = 0; m < pieces; ++m) {
-    const int64_t j = REV ? pieces - 1 - m : m;
-    const int64_t item = j == 0 ? a.n_slots + seq : slot0 + j - 1;
+    const int64_t item = piece_item(a.q, seq, s, a.seg, a.n_slots, REV ? pieces - 1 - m : m);
     f32x4* place = reinterpret_cast<f32x4*>(k.piece + (item * hp + head_tile) * (64 * NT) + at);
     if (m + 1 == pieces) {
       *place = S;
