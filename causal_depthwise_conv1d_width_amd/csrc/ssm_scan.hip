@@ -266,7 +266,7 @@ static hipError_t launch(const ScanArgs& a, hipStream_t s) {
     k.start = a.init;
     k.piece = a.piece;
     ssm_state_local_kernel<NT, U, VEC><<<walk, kThreads, 0, s>>>(k);
-    ssm_join_kernel<NT, false><<<dim3((uint32_t)(a.q.nseq * hp * (64 * NT / 1024))), 256, 0, s>>>(k);
+    ssm_join_kernel<NT, false><<<dim3((uint32_t)(a.q.nseq * hp * (64 * NT / 4096))), 1024, 0, s>>>(k);
   }
   ssm_scan_fwd_kernel<NT, U, VEC><<<walk, kThreads, 0, s>>>(a);
   return hipGetLastError();

@@ -31,9 +31,14 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_states_kernel(StateArgs f, St
 __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {  // two bf16 products in FP32
   return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
 }
-__device__ __forceinline__ float across16(float v) {  // sum over the four rows of 16 lanes
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+// sum over the four rows of 16 lanes, in every lane: swapping the odd rows of a copy with the even rows of
+// another puts the rows' neighbours side by side, and the same for halves
+__device__ __forceinline__ float across16(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t x = __float_as_uint(__uint_as_float(p[0]) + __uint_as_float(p[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
 // A block of 8 waves takes a chunk and walks the 64-column units of its heads.  A wave owns 16 * NBW columns n
@@ -48,11 +53,12 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
   __shared__ __align__(16) uint16_t sB[64 * kLd<NT>];
   __shared__ __align__(16) uint16_t sC[64 * kLd<NT>];
   __shared__ __align__(16) uint16_t sR[R];  // T^T [n][p], then Z and G M [i][j]
-  // this head's and the next one's (differences of FP32 prefix sums would lose a fast decay's weights)
+  // three heads': the last one's gradients are put together while the next one's decays are made
+  // (differences of FP32 prefix sums would lose a fast decay's weights)
   __shared__ __align__(16) double sdecay[2][64];
-  __shared__ __align__(16) float ssteps[2][3][64];
-  __shared__ __align__(16) float s_col[4][64];
-  __shared__ float s_row[4][64], s_diag[64], s_rint[8][64], s_u[8][64], s_dot[8], s_trace[4];
+  __shared__ __align__(16) float ssteps[3][3][64];
+  __shared__ __align__(16) float s_col[2][4][64];
+  __shared__ float s_row[2][4][64], s_diag[2][64], s_trace[2][4], s_rint[8][64], s_u[8][64], s_dot[8];
   uint16_t *sZ = sR, *sG = sR + 64 * kLd<64>;
   const ScanArgs& a = b.s;
   const int lane = threadIdx.x & 63, w = wave_id(), g = lane >> 4, i = lane & 15;
@@ -102,29 +108,28 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
     const double L = wave_prefix((double)(d * rate.A2));
     if (w == 6) {
       sdecay[t & 1][lane] = L;
-      ssteps[t & 1][0][lane] = d;
-      ssteps[t & 1][1][lane] = ex2((float)L);
+      ssteps[t % 3][0][lane] = d;
+      ssteps[t % 3][1][lane] = ex2((float)L);
     } else {
-      ssteps[t & 1][2][my] = ex2((float)dpp0<0x138, 0xf>(L));
+      ssteps[t % 3][2][my] = ex2((float)dpp0<0x138, 0xf>(L));
     }
   };
-  auto load_states = [&](int t) {
-    const int64_t o = (id * hp + h_lo * a.ptiles + t) * (2 * 64 * NT);
+  // one of the chunk's states of head t: high and low parts
+  auto load_states = [&](int t, const uint16_t* from, u32x4(&hi)[NBW][2], u32x4(&lo)[NBW][2]) {
     const int n = t < tiles ? 2 * 64 * NT : 0;
-    const Rows cs(b.cs + o, n, 1, n, 2), ct(b.ct + o, n, 1, n, 2);
+    const Rows r(from + (id * hp + h_lo * a.ptiles + t) * (2 * 64 * NT), n, 1, n, 2);
 #pragma unroll
     for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const int at = (((nw / 16 + nb) * 2 + ks) * 64 + lane) * 16;
-        Th[nb][ks] = __builtin_amdgcn_raw_buffer_load_b128(ct.r, at, 0, 0);
-        Sh[nb][ks] = __builtin_amdgcn_raw_buffer_load_b128(cs.r, at, 0, 0);
-        Sl[nb][ks] = __builtin_amdgcn_raw_buffer_load_b128(cs.r, at + 64 * NT * 2, 0, 0);
-        Tl[nb][ks] = __builtin_amdgcn_raw_buffer_load_b128(ct.r, at + 64 * NT * 2, 0, 0);
+        hi[nb][ks] = __builtin_amdgcn_raw_buffer_load_b128(r.r, at, 0, 0);
+        lo[nb][ks] = __builtin_amdgcn_raw_buffer_load_b128(r.r, at + 64 * NT * 2, 0, 0);
       }
   };
   load_rows(0);
-  load_states(0);
+  load_states(0, b.ct, Th, Tl);
+  load_states(0, b.cs, Sh, Sl);
   load_raw(0);
   if (w >= 6) decays(0);
   load_raw(1);
@@ -146,12 +151,57 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
     if (w < 2) G1 = mma(op_straight<NT>(sB, 16 * (1 - w), 32 * ks), op_straight<NT>(sC, 16 * (1 - w), 32 * ks), G1);
   }
 
-  float dl_sum = 0.f, q_sum = 0.f, trace_sum = 0.f;  // wave 0: over a head's column tiles
+  float dl_sum = 0.f, q_sum = 0.f, trace_sum = 0.f;  // wave 5: over a head's column tiles
+  // lane = row: the gradients of head t's decays and steps, by wave 5
+  auto finish = [&](const int t) {
+    const int h = h_lo + t / a.ptiles, ptile = t % a.ptiles;
+    const float *sd = ssteps[t % 3][0], *se = ssteps[t % 3][1];
+    const float d = sd[lane];
+    float rint = 0.f, u = 0.f, row = 0.f, col = 0.f, dots = 0.f, trace = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dots += s_dot[k];
+#pragma unroll
+    for (int k = 0; k < (NT > 64 ? 8 : 4); ++k) {
+      const int from = NT > 64 ? k : k + 4 * (lane >> 5);
+      rint += s_rint[from][lane];
+      u += s_u[from][lane];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // blocks up to the diagonal
+      const float r = s_row[t & 1][k][lane], c = s_col[t & 1][k][lane];
+      row += k <= (lane >> 4) ? r : 0.f;
+      col += k >= (lane >> 4) ? c : 0.f;
+      trace += s_trace[t & 1][k];
+    }
+    const float from_later = rint + (row - d * col);
+    const float suffix = __shfl(wave_prefix(__shfl(from_later, 63 - lane)), 63 - lane);  // rows >= this one
+    const float before = dpp0<0x138, 0xf>(wave_prefix(d * u));                            // rows < this one
+    dl_sum += se[63] * dots + suffix + before;
+    q_sum += col + s_diag[t & 1][lane] + u;
+    trace_sum += trace;
+    if (ptile + 1 == a.ptiles) {
+      const float step = a.A[h] * dl_sum + q_sum;
+      const float grad = a.softplus ? step * -expm1f(-d) : step;  // softplus' = 1 - e^{-softplus}
+      const int size = a.dt_f32 ? 4 : 2;
+      const Rows to(static_cast<char*>(b.ddt) + (pc.r0 * b.ddt_ld + h) * size, b.ddt_ld, rows, 1, size);
+      const int off = (int)((uint32_t)lane * (uint32_t)b.ddt_ld * size);
+      if (a.dt_f32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(grad), to.r, off, 0, 0);
+      else __builtin_amdgcn_raw_buffer_store_b16(to_bf16(grad), to.r, off, 0, 0);
+      const float sum_A = wave_sum(lane < rows ? d * dl_sum : 0.f), sum_b = wave_sum(lane < rows ? grad : 0.f);
+      if (lane == 0) {
+        float* dst = b.head_part + (id * a.H + h) * 3;
+        dst[0] = sum_A;
+        dst[1] = sum_b;
+        dst[2] = trace_sum;
+      }
+      dl_sum = q_sum = trace_sum = 0.f;
+    }
+  };
   for (int t = 0; t < tiles; ++t) {
     const int h = h_lo + t / a.ptiles, ptile = t % a.ptiles, p_first = ptile * kPTile;
     const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
     const double* sL = sdecay[t & 1];
-    const float *sd = ssteps[t & 1][0], *se = ssteps[t & 1][1], *sr = ssteps[t & 1][2];
+    const float *sd = ssteps[t % 3][0], *se = ssteps[t % 3][1], *sr = ssteps[t % 3][2];
     store_tile<64>(sx, tx);
     store_tile<64>(sy, ty);
     if (owner) {
@@ -204,16 +254,16 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
         K = here ? 0.f : K;
         row = __builtin_fmaf(dj[r], K, row);
         const float c = row16_sum(K);
-        if (i == 15) s_col[ib][16 * jb + 4 * g + r] = c;
+        if (i == 15) s_col[t & 1][ib][16 * jb + 4 * g + r] = c;
       }
       *reinterpret_cast<u32x2*>(sZ + at<64>(16 * ib + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(z[0], z[1]), pk_bf16(z[2], z[3])};
       *reinterpret_cast<u32x2*>(sG + at<64>(16 * ib + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(gm[0], gm[1]), pk_bf16(gm[2], gm[3])};
       row = across16(row);
-      if (g == 0) s_row[jb][16 * ib + i] = row;
+      if (g == 0) s_row[t & 1][jb][16 * ib + i] = row;
       if (ib == jb) {
-        if ((i >> 2) == g) s_diag[16 * ib + i] = on_diagonal;
+        if ((i >> 2) == g) s_diag[t & 1][16 * ib + i] = on_diagonal;
         trace = wave_sum(trace);
-        if (lane == 0) s_trace[ib] = trace;
+        if (lane == 0) s_trace[t & 1][ib] = trace;
       }
       phase();
     };
@@ -225,10 +275,26 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
       *reinterpret_cast<u32x2*>(sG + at<64>(16 * z + i, 16 * z + 16 + 4 * g)) = u32x2{0u, 0u};
     }
     if (w >= 6 && t + 1 < tiles) decays(t + 1);
+    if (w == 5 && t > 0) finish(t - 1);
     load_raw(t + 2);
     phase();
     __syncthreads();
 
+    float dot = 0.f;
+#pragma unroll
+    for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          dot = dot2(Sh[nb][ks][e], Th[nb][ks][e], dot);
+          dot = dot2(Sh[nb][ks][e], Tl[nb][ks][e], dot);
+          dot = dot2(Sl[nb][ks][e], Th[nb][ks][e], dot);
+          dot = dot2(Sl[nb][ks][e], Tl[nb][ks][e], dot);
+        }
+    dot = wave_sum(dot);
+    if (lane == 0) s_dot[w] = owner ? dot : 0.f;
+    phase();
     // dC and the rows' sums with S
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
@@ -254,8 +320,10 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
       }
       rint = across16(rint);
       if (g == 0) s_rint[w][16 * ib + i] = rint;
-      phase();
     }
+    phase();
+    load_states(t + 1, b.cs, Sh, Sl);
+    phase();
     // dB and the rows' sums with T
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
@@ -281,24 +349,8 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
       }
       u = across16(u);
       if (g == 0) s_u[w][16 * jb + i] = u;
-      phase();
     }
-    float dot = 0.f;
-#pragma unroll
-    for (int nb = 0; nb < NBW; ++nb)
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          dot = dot2(Sh[nb][ks][e], Th[nb][ks][e], dot);
-          dot = dot2(Sh[nb][ks][e], Tl[nb][ks][e], dot);
-          dot = dot2(Sl[nb][ks][e], Th[nb][ks][e], dot);
-          dot = dot2(Sl[nb][ks][e], Tl[nb][ks][e], dot);
-        }
-    dot = wave_sum(dot);
-    if (lane == 0) s_dot[w] = owner ? dot : 0.f;
-    phase();
-    load_states(t + 1);
+    load_states(t + 1, b.ct, Th, Tl);
     phase();
 
 #pragma unroll
@@ -323,49 +375,9 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
     phase();
     __syncthreads();
 
-    if (w == 0) {  // lane = row: the gradients of the decays and steps
-      const float d = sd[lane];
-      float rint = 0.f, u = 0.f, row = 0.f, col = 0.f, dots = 0.f, trace = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) dots += s_dot[k];
-#pragma unroll
-      for (int k = 0; k < (NT > 64 ? 8 : 4); ++k) {
-        const int from = NT > 64 ? k : k + 4 * (lane >> 5);
-        rint += s_rint[from][lane];
-        u += s_u[from][lane];
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {  // blocks up to the diagonal
-        const float r = s_row[k][lane], c = s_col[k][lane];
-        row += k <= (lane >> 4) ? r : 0.f;
-        col += k >= (lane >> 4) ? c : 0.f;
-        trace += s_trace[k];
-      }
-      const float from_later = rint + (row - d * col);
-      const float suffix = __shfl(wave_prefix(__shfl(from_later, 63 - lane)), 63 - lane);  // rows >= this one
-      const float before = dpp0<0x138, 0xf>(wave_prefix(d * u));                            // rows < this one
-      dl_sum += se[63] * dots + suffix + before;
-      q_sum += col + s_diag[lane] + u;
-      trace_sum += trace;
-      if (ptile + 1 == a.ptiles) {
-        const float step = a.A[h] * dl_sum + q_sum;
-        const float grad = a.softplus ? step * -expm1f(-d) : step;  // softplus' = 1 - e^{-softplus}
-        const int size = a.dt_f32 ? 4 : 2;
-        const Rows to(static_cast<char*>(b.ddt) + (pc.r0 * b.ddt_ld + h) * size, b.ddt_ld, rows, 1, size);
-        const int off = (int)((uint32_t)lane * (uint32_t)b.ddt_ld * size);
-        if (a.dt_f32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(grad), to.r, off, 0, 0);
-        else __builtin_amdgcn_raw_buffer_store_b16(to_bf16(grad), to.r, off, 0, 0);
-        const float sum_A = wave_sum(lane < rows ? d * dl_sum : 0.f), sum_b = wave_sum(lane < rows ? grad : 0.f);
-        if (lane == 0) {
-          float* dst = b.head_part + (id * a.H + h) * 3;
-          dst[0] = sum_A;
-          dst[1] = sum_b;
-          dst[2] = trace_sum;
-        }
-        dl_sum = q_sum = trace_sum = 0.f;
-      }
-    }
   }
+  __syncthreads();
+  if (w == 5) finish(tiles - 1);
 
 #pragma unroll
   for (int nb = 0; nb < NBW; ++nb)
@@ -458,10 +470,10 @@ static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
   }
   const dim3 walk((uint32_t)unit_blocks(items, a.H, a.G, a.ptiles, U), 2);
   if (a.seg > 0) {
-    const dim3 join((uint32_t)(a.q.nseq * hp * (64 * NT / 1024)));
+    const dim3 join((uint32_t)(a.q.nseq * hp * (64 * NT / 4096)));
     ssm_states_kernel<NT, U, VEC, false><<<walk, kThreads, 0, s>>>(f, r);
-    ssm_join_kernel<NT, false><<<join, 256, 0, s>>>(f);
-    ssm_join_kernel<NT, true><<<join, 256, 0, s>>>(r);
+    ssm_join_kernel<NT, false><<<join, 1024, 0, s>>>(f);
+    ssm_join_kernel<NT, true><<<join, 1024, 0, s>>>(r);
   }
   ssm_states_kernel<NT, U, VEC, true><<<walk, kThreads, 0, s>>>(f, r);
   ssm_scan_bwd_kernel<NT, VEC><<<dim3((uint32_t)(ids * a.G * b.hsplit)), kThreads, 0, s>>>(b);

@@ -289,13 +289,13 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_state_local_kernel(StateArgs 
 // Local end states of a sequence's pieces -> start states, in place, in the order of the walk:
 // start[m + 1] = decay[m] start[m] + local[m].  One thread per four columns of a state.
 template <int NT, bool REV>
-__global__ __launch_bounds__(256) void ssm_join_kernel(StateArgs k) {
+__global__ __launch_bounds__(1024) void ssm_join_kernel(StateArgs k) {
   const ScanArgs& a = k.s;
-  constexpr int kPer = 64 * NT / 4 / 256;  // blocks a tile
+  constexpr int kPer = 64 * NT / 4 / 1024;  // blocks a tile
   const int hp = a.H * a.ptiles;
   const int64_t seq = blockIdx.x / ((int64_t)hp * kPer);
   const int rest = blockIdx.x % (hp * kPer), head_tile = rest / kPer, h = head_tile / a.ptiles;
-  const int at = (rest % kPer * 256 + threadIdx.x) * 4, p = at / NT, n = at % NT;
+  const int at = (rest % kPer * 1024 + threadIdx.x) * 4, p = at / NT, n = at % NT;
   const int p_abs = head_tile % a.ptiles * kPTile + p;
   int64_t s, e;
   seq_bounds(a.q, seq, s, e);
