@@ -7,15 +7,15 @@
 //   du = (d - n mean(d n)) / rms(u),   dw = sum over rows of (gradient of w n) n.
 //
 // These are streams: one pass over the rows, each value read and written once, all arithmetic FP32.
-// T threads share a row's group (64: one wave, up to 2048 channels; 256 or 1024 threads: a block)
-// and keep it in registers, four pieces of 8 channels a thread.  A thread keeps its channels' weights
-// (and, backward, its dw sums) in registers over all the rows it visits; the sums go to one partial row
-// per row split, and a second kernel adds those in ascending order (no atomics: the same bits every run).
+// T threads share a row's group and keep it in registers, V pieces of 8 channels a thread (one wave up to
+// 2048 channels, then 256 or 1024 threads), the bf16 inputs packed as they are in memory: with FP32 copies of x, z and dy
+// the gated backward had 262 registers and 2 waves a SIMD, too few to cover its loads (302 us at
+// 16384 x 4096 in groups of 1024, against 128 us).  A thread keeps its channels' weights (and, backward, its dw sums) in
+// registers over all the rows it visits; the sums go to one partial row per row split, and a second kernel adds
+// those in ascending order (no atomics: the same bits every run).
 #include "ssm_device.h"
 
 namespace cssm {
-
-constexpr int kVec = 4;  // pieces of 8 channels a thread holds
 
 struct F8 {
   float f[8];
@@ -35,6 +35,48 @@ __device__ __forceinline__ F8 unpack8(u32x4 u) {
   }
   return v;
 }
+// 8 values as they are in memory
+struct Raw16 {
+  u32x4 v;
+  // forget what was computed from v: a second pass unpacks again instead of keeping the first one's FP32
+  // values (twice the registers, and the gates beside them)
+  __device__ __forceinline__ void again() { asm("" : "+v"(v)); }
+  __device__ __forceinline__ F8 get() const { return unpack8(v); }
+};
+struct Raw32 {
+  f32x4 a, b;
+  __device__ __forceinline__ void again() {}
+  __device__ __forceinline__ F8 get() const { return F8{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}}; }
+};
+__device__ __forceinline__ Raw16 raw8(const uint16_t* p, int64_t n) {
+  Raw16 r;
+  if (n >= 8) {
+    r.v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
+    return r;
+  }
+  r.v = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (e < n) r.v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+  return r;
+}
+__device__ __forceinline__ Raw32 raw8(const float* p, int64_t n) {
+  Raw32 r;
+  if (n >= 8) {
+    r.a = __builtin_nontemporal_load(reinterpret_cast<const f32x4_a4*>(p));
+    r.b = __builtin_nontemporal_load(reinterpret_cast<const f32x4_a4*>(p + 4));
+    return r;
+  }
+  r.a = r.b = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (e < n) (e < 4 ? r.a : r.b)[e & 3] = p[e];
+  return r;
+}
+__device__ __forceinline__ Raw16 zero_raw(const uint16_t*) { return Raw16{u32x4{0u, 0u, 0u, 0u}}; }
+__device__ __forceinline__ Raw32 zero_raw(const float*) { return Raw32{f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}}; }
+template <typename R>
+using RawOf = decltype(raw8((const R*)nullptr, 0));
 __device__ __forceinline__ F8 load8(const uint16_t* p, int64_t n) {  // the first n (>= 8: all) of 8 values
   if (n >= 8) return unpack8(__builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p)));
   F8 v = zero8();
@@ -117,84 +159,93 @@ struct Place {
   }
 };
 
-template <int T, bool NORM_FIRST>
+// Weights of a thread's channels: kept in registers, or, where 1024 threads leave too few, read for each row.
+template <int T, int V>
+struct Weights {
+  static constexpr bool kKept = T < 1024;
+  F8 w[kKept ? V : 1];
+  __device__ __forceinline__ Weights(const NormArgs& a, int64_t col0, int t) {
+    if constexpr (kKept) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) w[v] = load_w(a, col0 + (v * T + t) * 8, a.group - (v * T + t) * 8);
+    }
+  }
+  __device__ __forceinline__ F8 get(const NormArgs& a, int64_t col0, int t, int v) const {
+    if constexpr (kKept) return w[v];
+    else return load_w(a, col0 + (v * T + t) * 8, a.group - (v * T + t) * 8);
+  }
+};
+
+template <int T, int V, bool NORM_FIRST>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void gated_norm_fwd_kernel(NormArgs a) {
   __shared__ float lds[16];
   const Place<T> u(a);
   if (!u.ok) return;  // whole waves (T == 64); never with T > 64
-  F8 w[kVec];
-#pragma unroll
-  for (int v = 0; v < kVec; ++v) {
-    const int64_t c = (v * T + u.t) * 8;
-    w[v] = load_w(a, u.col0 + c, a.group - c);
-  }
+  const Weights<T, V> ww(a, u.col0, u.t);
   for (int64_t row = u.split; row < a.rows; row += a.parts) {
-    F8 x[kVec], z[kVec];
+    Raw16 x[V], z[V];
     float s = 0.f;
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
+    for (int v = 0; v < V; ++v) {
       const int64_t c = (v * T + u.t) * 8;
-      if (v * T * 8 >= a.group) break;
-      x[v] = load8(a.x + row * a.x_ld + u.col0 + c, a.group - c);
-      z[v] = load8(a.z + row * a.z_ld + u.col0 + c, a.group - c);
+      x[v] = raw8(a.x + row * a.x_ld + u.col0 + c, a.group - c);
+      z[v] = raw8(a.z + row * a.z_ld + u.col0 + c, a.group - c);
     }
+    F8 f[V], gate[V];
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-      if (v * T * 8 >= a.group) break;
+    for (int v = 0; v < V; ++v) {
+      f[v] = x[v].get();
+      gate[v] = z[v].get();
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        z[v].f[e] *= sigmoid(z[v].f[e]);
-        if (!NORM_FIRST) x[v].f[e] *= z[v].f[e];
-        s = __builtin_fmaf(x[v].f[e], x[v].f[e], s);
+        gate[v].f[e] *= sigmoid(gate[v].f[e]);
+        if (!NORM_FIRST) f[v].f[e] *= gate[v].f[e];
+        s = __builtin_fmaf(f[v].f[e], f[v].f[e], s);
       }
     }
     const float inv = rsqrtf(unit_sum<T>(s, lds) / (float)a.group + a.eps);
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
+    for (int v = 0; v < V; ++v) {
       const int64_t c = (v * T + u.t) * 8;
-      if (v * T * 8 >= a.group) break;
+      const F8 w = ww.get(a, u.col0, u.t, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[v].f[e] *= inv * w[v].f[e];
-        if (NORM_FIRST) x[v].f[e] *= z[v].f[e];
+        f[v].f[e] *= inv * w.f[e];
+        if (NORM_FIRST) f[v].f[e] *= gate[v].f[e];
       }
-      store8(a.y + row * a.y_ld + u.col0 + c, x[v], a.group - c);
+      store8(a.y + row * a.y_ld + u.col0 + c, f[v], a.group - c);
     }
   }
 }
 
-template <int T, bool NORM_FIRST>
+template <int T, int V, bool NORM_FIRST>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void gated_norm_bwd_kernel(NormArgs a) {
   __shared__ float lds[16];
   const Place<T> u(a);
   if (!u.ok) return;
-  F8 w[kVec], dw[kVec];
+  const Weights<T, V> ww(a, u.col0, u.t);
+  F8 dw[V];
 #pragma unroll
-  for (int v = 0; v < kVec; ++v) {
-    const int64_t c = (v * T + u.t) * 8;
-    w[v] = load_w(a, u.col0 + c, a.group - c);
-    dw[v] = zero8();
-  }
+  for (int v = 0; v < V; ++v) dw[v] = zero8();
   for (int64_t row = u.split; row < a.rows; row += a.parts) {
-    F8 x[kVec], z[kVec], d[kVec];
+    Raw16 x[V], z[V], d[V];
     float s = 0.f, sd = 0.f;
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
+    for (int v = 0; v < V; ++v) {
       const int64_t c = (v * T + u.t) * 8;
-      if (v * T * 8 >= a.group) break;
-      x[v] = load8(a.x + row * a.x_ld + u.col0 + c, a.group - c);
-      z[v] = load8(a.z + row * a.z_ld + u.col0 + c, a.group - c);
-      d[v] = load8(a.dy + row * a.dy_ld + u.col0 + c, a.group - c);
+      x[v] = raw8(a.x + row * a.x_ld + u.col0 + c, a.group - c);
+      z[v] = raw8(a.z + row * a.z_ld + u.col0 + c, a.group - c);
+      d[v] = raw8(a.dy + row * a.dy_ld + u.col0 + c, a.group - c);
     }
     // s = sum u^2, sd = sum u d w (both before the division by the rms)
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-      if (v * T * 8 >= a.group) break;
+    for (int v = 0; v < V; ++v) {
+      const F8 fx = x[v].get(), fz = z[v].get(), fd = d[v].get(), w = ww.get(a, u.col0, u.t, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float gate = z[v].f[e] * sigmoid(z[v].f[e]);
-        const float uu = NORM_FIRST ? x[v].f[e] : x[v].f[e] * gate;
-        const float dn = (NORM_FIRST ? d[v].f[e] * gate : d[v].f[e]) * w[v].f[e];
+        const float gate = fz.f[e] * sigmoid(fz.f[e]);
+        const float uu = NORM_FIRST ? fx.f[e] : fx.f[e] * gate;
+        const float dn = (NORM_FIRST ? fd.f[e] * gate : fd.f[e]) * w.f[e];
         s = __builtin_fmaf(uu, uu, s);
         sd = __builtin_fmaf(uu, dn, sd);
       }
@@ -203,63 +254,61 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void gated_norm_bwd_kernel(NormA
     const float inv = rsqrtf(unit_sum<T>(s, lds) / n + a.eps);
     const float m = unit_sum<T>(sd, lds) * inv / n;  // mean of d n
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
+    for (int v = 0; v < V; ++v) {
       const int64_t c = (v * T + u.t) * 8;
-      if (v * T * 8 >= a.group) break;
-      F8 dz;
+      x[v].again(), z[v].again(), d[v].again();
+      const F8 fx = x[v].get(), fz = z[v].get(), fd = d[v].get(), w = ww.get(a, u.col0, u.t, v);
+      F8 dx, dz;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float zz = z[v].f[e], sg = sigmoid(zz), gate = zz * sg;
+        const float zz = fz.f[e], sg = sigmoid(zz), gate = zz * sg;
         const float slope = sg * (1.f + zz * (1.f - sg));
-        const float uu = NORM_FIRST ? x[v].f[e] : x[v].f[e] * gate;
-        const float nn = uu * inv, dy = d[v].f[e];
+        const float uu = NORM_FIRST ? fx.f[e] : fx.f[e] * gate;
+        const float nn = uu * inv, dy = fd.f[e];
         const float dn = NORM_FIRST ? dy * gate : dy;
         dw[v].f[e] = __builtin_fmaf(dn, nn, dw[v].f[e]);
-        const float du = inv * (dn * w[v].f[e] - nn * m);
-        dz.f[e] = (NORM_FIRST ? dy * nn * w[v].f[e] : du * x[v].f[e]) * slope;
-        x[v].f[e] = NORM_FIRST ? du : du * gate;
+        const float du = inv * (dn * w.f[e] - nn * m);
+        dz.f[e] = (NORM_FIRST ? dy * nn * w.f[e] : du * fx.f[e]) * slope;
+        dx.f[e] = NORM_FIRST ? du : du * gate;
       }
-      store8(a.dx + row * a.dx_ld + u.col0 + c, x[v], a.group - c);
+      store8(a.dx + row * a.dx_ld + u.col0 + c, dx, a.group - c);
       store8(a.dz + row * a.dz_ld + u.col0 + c, dz, a.group - c);
     }
   }
   float* part = a.part + u.split * a.groups * a.group + u.col0;
 #pragma unroll
-  for (int v = 0; v < kVec; ++v) {
+  for (int v = 0; v < V; ++v) {
     const int64_t c = (v * T + u.t) * 8;
     if (c < a.group) store8(part + c, dw[v], a.group - c);
   }
 }
 
-template <int T, typename R>
+template <int T, int V, typename R>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void residual_norm_fwd_kernel(NormArgs a) {
   __shared__ float lds[16];
   const Place<T> u(a);
   if (!u.ok) return;
-  F8 w[kVec];
-#pragma unroll
-  for (int v = 0; v < kVec; ++v) {
-    const int64_t c = (v * T + u.t) * 8;
-    w[v] = load_w(a, c, a.group - c);
-  }
+  const Weights<T, V> ww(a, 0, u.t);
   const R* r_in = static_cast<const R*>(a.r);
   R* r_out = static_cast<R*>(a.r_out);
   for (int64_t row = u.split; row < a.rows; row += a.parts) {
-    F8 h[kVec];
+    Raw16 x[V];
+    RawOf<R> r[V];
+    F8 h[V];
     float s = 0.f;
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
+    for (int v = 0; v < V; ++v) {
       const int64_t c = (v * T + u.t) * 8;
-      if (v * T * 8 >= a.group) break;
-      const F8 x = load8(a.x + row * a.x_ld + c, a.group - c);
-      h[v] = load8(r_in + row * a.r_ld + c, a.group - c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[v].f[e] = __builtin_fmaf(a.scale, x.f[e], h[v].f[e]);
+      x[v] = raw8(a.x + row * a.x_ld + c, a.group - c);
+      r[v] = raw8(r_in + row * a.r_ld + c, a.group - c);
     }
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
+    for (int v = 0; v < V; ++v) {
       const int64_t c = (v * T + u.t) * 8;
-      if (v * T * 8 >= a.group) break;
+      const F8 fx = x[v].get();
+      h[v] = r[v].get();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[v].f[e] = __builtin_fmaf(a.scale, fx.f[e], h[v].f[e]);
       store8(r_out + row * a.ro_ld + c, h[v], a.group - c);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -269,72 +318,71 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void residual_norm_fwd_kernel(No
     }
     const float inv = rsqrtf(unit_sum<T>(s, lds) / (float)a.group + a.eps);
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
+    for (int v = 0; v < V; ++v) {
       const int64_t c = (v * T + u.t) * 8;
-      if (v * T * 8 >= a.group) break;
+      const F8 w = ww.get(a, 0, u.t, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[v].f[e] *= inv * w[v].f[e];
+      for (int e = 0; e < 8; ++e) h[v].f[e] *= inv * w.f[e];
       store8(a.y + row * a.y_ld + c, h[v], a.group - c);
     }
   }
 }
 
-template <int T, typename R>
+template <int T, int V, typename R>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void residual_norm_bwd_kernel(NormArgs a) {
   __shared__ float lds[16];
   const Place<T> u(a);
   if (!u.ok) return;
-  F8 w[kVec], dw[kVec];
+  const Weights<T, V> ww(a, 0, u.t);
+  F8 dw[V];
 #pragma unroll
-  for (int v = 0; v < kVec; ++v) {
-    const int64_t c = (v * T + u.t) * 8;
-    w[v] = load_w(a, c, a.group - c);
-    dw[v] = zero8();
-  }
+  for (int v = 0; v < V; ++v) dw[v] = zero8();
   const R* r = static_cast<const R*>(a.r);
   const R* dri = static_cast<const R*>(a.dr_in);
   R* dro = static_cast<R*>(a.r_out);
   for (int64_t row = u.split; row < a.rows; row += a.parts) {
-    F8 h[kVec], d[kVec], o[kVec];
+    RawOf<R> h[V], o[V];
+    Raw16 d[V];
     float s = 0.f, sd = 0.f;
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
+    for (int v = 0; v < V; ++v) {
       const int64_t c = (v * T + u.t) * 8;
-      if (v * T * 8 >= a.group) break;
-      h[v] = load8(r + row * a.r_ld + c, a.group - c);
-      d[v] = load8(a.dy + row * a.dy_ld + c, a.group - c);
-      o[v] = dri ? load8(dri + row * a.dri_ld + c, a.group - c) : zero8();
+      h[v] = raw8(r + row * a.r_ld + c, a.group - c);
+      d[v] = raw8(a.dy + row * a.dy_ld + c, a.group - c);
+      o[v] = dri ? raw8(dri + row * a.dri_ld + c, a.group - c) : zero_raw(dri);
     }
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-      if (v * T * 8 >= a.group) break;
+    for (int v = 0; v < V; ++v) {
+      const F8 fh = h[v].get(), fd = d[v].get(), w = ww.get(a, 0, u.t, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        s = __builtin_fmaf(h[v].f[e], h[v].f[e], s);
-        sd = __builtin_fmaf(h[v].f[e], d[v].f[e] * w[v].f[e], sd);
+        s = __builtin_fmaf(fh.f[e], fh.f[e], s);
+        sd = __builtin_fmaf(fh.f[e], fd.f[e] * w.f[e], sd);
       }
     }
     const float n = (float)a.group;
     const float inv = rsqrtf(unit_sum<T>(s, lds) / n + a.eps);
     const float m = unit_sum<T>(sd, lds) * inv / n;
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
+    for (int v = 0; v < V; ++v) {
       const int64_t c = (v * T + u.t) * 8;
-      if (v * T * 8 >= a.group) break;
+      h[v].again(), d[v].again();
+      const F8 fh = h[v].get(), fd = d[v].get(), w = ww.get(a, 0, u.t, v);
+      F8 g = o[v].get(), dx;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float nn = h[v].f[e] * inv;
-        dw[v].f[e] = __builtin_fmaf(d[v].f[e], nn, dw[v].f[e]);
-        o[v].f[e] += inv * (d[v].f[e] * w[v].f[e] - nn * m);
-        h[v].f[e] = a.scale * o[v].f[e];
+        const float nn = fh.f[e] * inv;
+        dw[v].f[e] = __builtin_fmaf(fd.f[e], nn, dw[v].f[e]);
+        g.f[e] += inv * (fd.f[e] * w.f[e] - nn * m);
+        dx.f[e] = a.scale * g.f[e];
       }
-      store8(dro + row * a.ro_ld + c, o[v], a.group - c);
-      store8(a.dx + row * a.dx_ld + c, h[v], a.group - c);
+      store8(dro + row * a.ro_ld + c, g, a.group - c);
+      store8(a.dx + row * a.dx_ld + c, dx, a.group - c);
     }
   }
   float* part = a.part + u.split * a.group;
 #pragma unroll
-  for (int v = 0; v < kVec; ++v) {
+  for (int v = 0; v < V; ++v) {
     const int64_t c = (v * T + u.t) * 8;
     if (c < a.group) store8(part + c, dw[v], a.group - c);
   }
@@ -371,50 +419,58 @@ static hipError_t reduce_dw(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int T>
+template <int T, int V>
 static void gated(const NormArgs& a, bool bwd, hipStream_t s) {
   const dim3 grid(blocks(a, T)), block(T == 64 ? 256 : T);
   if (bwd) {
-    if (a.norm_first) gated_norm_bwd_kernel<T, true><<<grid, block, 0, s>>>(a);
-    else gated_norm_bwd_kernel<T, false><<<grid, block, 0, s>>>(a);
+    if (a.norm_first) gated_norm_bwd_kernel<T, V, true><<<grid, block, 0, s>>>(a);
+    else gated_norm_bwd_kernel<T, V, false><<<grid, block, 0, s>>>(a);
   } else {
-    if (a.norm_first) gated_norm_fwd_kernel<T, true><<<grid, block, 0, s>>>(a);
-    else gated_norm_fwd_kernel<T, false><<<grid, block, 0, s>>>(a);
+    if (a.norm_first) gated_norm_fwd_kernel<T, V, true><<<grid, block, 0, s>>>(a);
+    else gated_norm_fwd_kernel<T, V, false><<<grid, block, 0, s>>>(a);
   }
 }
-template <int T>
+template <int T, int V>
 static void residual(const NormArgs& a, bool bwd, hipStream_t s) {
   const dim3 grid(blocks(a, T)), block(T == 64 ? 256 : T);
   if (bwd) {
-    if (a.r_f32) residual_norm_bwd_kernel<T, float><<<grid, block, 0, s>>>(a);
-    else residual_norm_bwd_kernel<T, uint16_t><<<grid, block, 0, s>>>(a);
+    if (a.r_f32) residual_norm_bwd_kernel<T, V, float><<<grid, block, 0, s>>>(a);
+    else residual_norm_bwd_kernel<T, V, uint16_t><<<grid, block, 0, s>>>(a);
   } else {
-    if (a.r_f32) residual_norm_fwd_kernel<T, float><<<grid, block, 0, s>>>(a);
-    else residual_norm_fwd_kernel<T, uint16_t><<<grid, block, 0, s>>>(a);
+    if (a.r_f32) residual_norm_fwd_kernel<T, V, float><<<grid, block, 0, s>>>(a);
+    else residual_norm_fwd_kernel<T, V, uint16_t><<<grid, block, 0, s>>>(a);
   }
 }
 
-#define CSSM_BY_THREADS(fn, bwd)                          \
-  switch (norm_threads(a.group)) {                        \
-    case 64: fn<64>(a, bwd, s); break;                    \
-    case 256: fn<256>(a, bwd, s); break;                  \
-    default: fn<1024>(a, bwd, s); break;                  \
-  }
+// threads and pieces a thread by the group's channels (norm_threads gives the same threads)
+#define CSSM_BY_GROUP(fn, bwd)                              \
+  do {                                                      \
+    switch (norm_threads(a.group)) {                        \
+      case 64: fn<64, 1>(a, bwd, s); break;                 \
+      case 128: fn<128, 1>(a, bwd, s); break;               \
+      case 256: fn<256, 1>(a, bwd, s); break;               \
+      case 512: fn<512, 1>(a, bwd, s); break;               \
+      default:                                              \
+        if (a.group <= 8192) fn<1024, 1>(a, bwd, s);        \
+        else if (a.group <= 16384) fn<1024, 2>(a, bwd, s);  \
+        else fn<1024, 4>(a, bwd, s);                        \
+    }                                                       \
+  } while (0)
 
 hipError_t launch_gated_fwd(const NormArgs& a, hipStream_t s) {
-  CSSM_BY_THREADS(gated, false)
+  CSSM_BY_GROUP(gated, false);
   return hipGetLastError();
 }
 hipError_t launch_gated_bwd(const NormArgs& a, hipStream_t s) {
-  if (a.rows > 0) CSSM_BY_THREADS(gated, true)
+  if (a.rows > 0) CSSM_BY_GROUP(gated, true);
   return reduce_dw(a, s);
 }
 hipError_t launch_residual_fwd(const NormArgs& a, hipStream_t s) {
-  CSSM_BY_THREADS(residual, false)
+  CSSM_BY_GROUP(residual, false);
   return hipGetLastError();
 }
 hipError_t launch_residual_bwd(const NormArgs& a, hipStream_t s) {
-  if (a.rows > 0) CSSM_BY_THREADS(residual, true)
+  if (a.rows > 0) CSSM_BY_GROUP(residual, true);
   return reduce_dw(a, s);
 }
 

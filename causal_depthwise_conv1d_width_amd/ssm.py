@@ -11,30 +11,40 @@ from . import _lib
 SsmGrads = collections.namedtuple("SsmGrads", "dx ddt dA dB dC dD ddt_bias dinitial_state")
 
 
-def _on(dev, **tensors):
-    if dev.type != "cuda":
-        raise ValueError(f"x: must be a GPU tensor (got device {dev})")
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: must be on {dev}, the device of x (got {t.device})")
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(x, *tensors):
+    """Every (tensor, name) must live on x's GPU.  Returns its index."""
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError(f"x: must be a GPU tensor (got device {x.device})")
+    for t, name in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: must be on {x.device}, the device of x (got {t.device})")
+    return dev
 
 
 def _stream(stream, dev):
-    return ctypes.c_void_p((torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
-def _rows(t, name, shape, dtype=torch.bfloat16):
+def _rows(t, name, shape, dtype=_BF16):
     """(pointer, row stride) of [rows, ...] whose trailing dimensions are contiguous."""
-    if t is None or tuple(t.shape) != tuple(shape):
+    if t is None or t.shape != shape:
         raise ValueError(f"{name}: need a tensor of shape {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: need dtype {dtype} (got {t.dtype})")
-    width = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size > 1 and stride != width and t.shape[0] > 0:
-            raise ValueError(f"{name}: a row's elements must be contiguous")
-        width *= size
-    ld = t.stride(0) if t.shape[0] > 1 else width
+    width = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    st = t.stride()
+    if t.shape[0] > 0 and (st[-1] != 1 and shape[-1] > 1 or len(shape) == 3 and shape[1] > 1 and st[1] != shape[2]):
+        raise ValueError(f"{name}: a row's elements must be contiguous")
+    ld = st[0] if t.shape[0] > 1 else width
     if ld < width:
         raise ValueError(f"{name}: rows overlap")
     return t.data_ptr(), ld
@@ -45,7 +55,7 @@ def _vec(t, name, n, optional=True):
         if optional:
             return None
         raise ValueError(f"{name}: required")
-    if tuple(t.shape) != (n,) or t.dtype != torch.float32 or not t.is_contiguous():
+    if t.shape != (n,) or t.dtype is not _F32 or not t.is_contiguous():
         raise ValueError(f"{name}: need a contiguous float32 tensor of shape {(n,)}")
     return t.data_ptr()
 
@@ -53,7 +63,7 @@ def _vec(t, name, n, optional=True):
 def _ints(t, name, n):
     if t is None:
         return None
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
+    if t.dtype is not _I32 or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{name}: need a contiguous int32 tensor of at least {n} entries")
     return t.data_ptr()
 
@@ -83,29 +93,29 @@ def _seq(rows, cu_seqlens, seqlen):
 def _shape(x, dt, B, dt_softplus):
     if x.dim() != 3 or B.dim() != 3:
         raise ValueError("x, B: need [rows, heads, head_dim] and [rows, groups, state] tensors")
-    if dt.dtype not in (torch.float32, torch.bfloat16):
+    if dt.dtype is not _F32 and dt.dtype is not _BF16:
         raise ValueError("dt: dtype must be float32 or bfloat16")
     _, H, P = x.shape
     G, N = B.shape[1:]
     if min(H, P, G, N) < 1 or H % G or N > 256:
         raise ValueError("x, B: need heads divisible by groups and 1 <= state <= 256")
-    return _lib.SsmShape(H, P, G, N, _lib.F32 if dt.dtype == torch.float32 else _lib.BF16, int(bool(dt_softplus)))
+    return _lib.SsmShape(H, P, G, N, _lib.F32 if dt.dtype is _F32 else _lib.BF16, 1 if dt_softplus else 0)
 
 
 def _state_array(t, name, H, P, N, least):
     """(pointer, slots, slot stride) of FP32 [slots, H, P, N] with contiguous slots."""
-    if t.dim() != 4 or tuple(t.shape[1:]) != (H, P, N) or t.dtype != torch.float32:
+    if t.dim() != 4 or t.shape[1:] != (H, P, N) or t.dtype is not _F32:
         raise ValueError(f"{name}: need a float32 tensor [slots, {H}, {P}, {N}]")
     if t.shape[0] < least:
         raise ValueError(f"{name}: needs at least {least} states, has {t.shape[0]}")
-    if t.numel() and not t[0].is_contiguous():
+    if not t.is_contiguous() and t.numel() and not t[0].is_contiguous():
         raise ValueError(f"{name}: a state must be contiguous")
     return t.data_ptr(), t.shape[0], (t.stride(0) if t.shape[0] > 1 else H * P * N)
 
 
-def _work(lib, need, workspace, dev):
+def _work(x, need, workspace):
     if workspace is None and need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = x.new_empty((need,), dtype=torch.uint8)
     if workspace is None:
         return None, None, 0
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -154,7 +164,7 @@ def ssm_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, *, cu_seqlens=None, seqle
         st.has_initial_state = _flags(has_initial_state, "has_initial_state", nseq)
         st.initial = st.final
         if has_initial_state is None:  # all false: in place, so the pool is only written
-            has_initial_state = torch.zeros((max(nseq, 1),), dtype=torch.uint8, device=x.device)
+            has_initial_state = x.new_zeros((max(nseq, 1),), dtype=torch.uint8)
             st.has_initial_state = has_initial_state.data_ptr()
     else:
         if cache_indices is not None or has_initial_state is not None:
@@ -166,16 +176,16 @@ def ssm_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, *, cu_seqlens=None, seqle
                     raise ValueError(f"{name}: need a contiguous tensor of {nseq} states")
                 st.slots, st.s_slot = max(n, 1), H * P * N
                 setattr(st, "initial" if name == "initial_state" else "final", p if n else None)
-    _on(x.device, dt=dt, A=A, B=B, C=C, D=D, dt_bias=dt_bias, cu_seqlens=cu_seqlens, state_pool=state_pool,
-        cache_indices=cache_indices, has_initial_state=has_initial_state, initial_state=initial_state,
-        final_state=final_state, out=out, workspace=workspace)
+    dev = _on(x, (dt, "dt"), (A, "A"), (B, "B"), (C, "C"), (D, "D"), (dt_bias, "dt_bias"), (cu_seqlens, "cu_seqlens"),
+              (state_pool, "state_pool"), (cache_indices, "cache_indices"), (has_initial_state, "has_initial_state"),
+              (initial_state, "initial_state"), (final_state, "final_state"), (out, "out"), (workspace, "workspace"))
     if out is None:
-        out = torch.empty((rows, H, P), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((rows, H, P))
     yp, yl = _rows(out, "out", (rows, H, P))
     need = lib.ssm_scan_fwd_workspace_bytes(ctypes.byref(sh), rows, nseq)
-    workspace, wp, wb = _work(lib, need, workspace, x.device)
+    workspace, wp, wb = _work(x, need, workspace)
     code = lib.ssm_scan_fwd(ctypes.byref(sh), rows, xp, xl, dp, dl, Ap, Bp, Bl, Cp, Cl, Dp, bp, ctypes.byref(seq),
-                            ctypes.byref(st), yp, yl, wp, wb, _stream(stream, x.device))
+                            ctypes.byref(st), yp, yl, wp, wb, _stream(stream, dev))
     _lib.check(lib, code, "ssm_scan_fwd")
     return out
 
@@ -190,7 +200,6 @@ def ssm_scan_bwd(dy, x, dt, A, B, C, D=None, dt_bias=None, *, cu_seqlens=None, s
     sh = _shape(x, dt, B, dt_softplus)
     rows, H, P = x.shape
     G, N = B.shape[1:]
-    dev = x.device
     seq, nseq = _seq(rows, cu_seqlens, seqlen)
     gp, gl = _rows(dy, "dy", (rows, H, P))
     xp, xl = _rows(x, "x", (rows, H, P))
@@ -198,11 +207,12 @@ def ssm_scan_bwd(dy, x, dt, A, B, C, D=None, dt_bias=None, *, cu_seqlens=None, s
     Bp, Bl = _rows(B, "B", (rows, G, N))
     Cp, Cl = _rows(C, "C", (rows, G, N))
     Ap, Dp, bp = _vec(A, "A", H, False), _vec(D, "D", H), _vec(dt_bias, "dt_bias", H)
-    _on(dev, dy=dy, dt=dt, A=A, B=B, C=C, D=D, dt_bias=dt_bias, cu_seqlens=cu_seqlens, initial_state=initial_state,
-        dfinal_state=dfinal_state, dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC, dD=dD, ddt_bias=ddt_bias,
-        dinitial_state=dinitial_state, workspace=workspace)
+    dev = _on(x, (dy, "dy"), (dt, "dt"), (A, "A"), (B, "B"), (C, "C"), (D, "D"), (dt_bias, "dt_bias"),
+              (cu_seqlens, "cu_seqlens"), (initial_state, "initial_state"), (dfinal_state, "dfinal_state"), (dx, "dx"),
+              (ddt, "ddt"), (dA, "dA"), (dB, "dB"), (dC, "dC"), (dD, "dD"), (ddt_bias, "ddt_bias"),
+              (dinitial_state, "dinitial_state"), (workspace, "workspace"))
     if dinitial_state is None and initial_state is not None:
-        dinitial_state = torch.empty((nseq, H, P, N), dtype=torch.float32, device=dev)
+        dinitial_state = x.new_empty((nseq, H, P, N), dtype=_F32)
     ptrs = []
     for t, name in ((initial_state, "initial_state"), (dfinal_state, "dfinal_state"), (dinitial_state, "dinitial_state")):
         if t is not None and (tuple(t.shape) != (nseq, H, P, N) or t.dtype != torch.float32 or not t.is_contiguous()):
@@ -210,7 +220,7 @@ def ssm_scan_bwd(dy, x, dt, A, B, C, D=None, dt_bias=None, *, cu_seqlens=None, s
         ptrs.append(t.data_ptr() if t is not None and nseq else None)
 
     def new(t, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=dev) if t is None else t
+        return x.new_empty(shape, dtype=dtype) if t is None else t
 
     dx, ddt = new(dx, (rows, H, P), torch.bfloat16), new(ddt, (rows, H), dt.dtype)
     dB, dC = new(dB, (rows, G, N), torch.bfloat16), new(dC, (rows, G, N), torch.bfloat16)
@@ -220,7 +230,7 @@ def ssm_scan_bwd(dy, x, dt, A, B, C, D=None, dt_bias=None, *, cu_seqlens=None, s
     if dt_bias is not None:
         ddt_bias = new(ddt_bias, (H,), torch.float32)
     need = lib.ssm_scan_bwd_workspace_bytes(ctypes.byref(sh), rows, nseq)
-    workspace, wp, wb = _work(lib, need, workspace, dev)
+    workspace, wp, wb = _work(x, need, workspace)
     code = lib.ssm_scan_bwd(ctypes.byref(sh), rows, gp, gl, xp, xl, dp, dl, Ap, Bp, Bl, Cp, Cl, Dp, bp, ctypes.byref(seq),
                             ptrs[0], ptrs[1], *_rows(dx, "dx", (rows, H, P)), *_rows(ddt, "ddt", (rows, H), dt.dtype),
                             _vec(dA, "dA", H), *_rows(dB, "dB", (rows, G, N)), *_rows(dC, "dC", (rows, G, N)),
@@ -247,21 +257,22 @@ def ssm_state_update(x, dt, A, B, C, D=None, dt_bias=None, *, state_pool, cache_
     st.final, st.slots, st.s_slot = _state_array(state_pool, "state_pool", H, P, N, 1)
     st.initial = st.final
     st.cache_indices = _ints(cache_indices, "cache_indices", n)
-    _on(x.device, dt=dt, A=A, B=B, C=C, D=D, dt_bias=dt_bias, state_pool=state_pool, cache_indices=cache_indices, out=out)
+    dev = _on(x, (dt, "dt"), (A, "A"), (B, "B"), (C, "C"), (D, "D"), (dt_bias, "dt_bias"), (state_pool, "state_pool"),
+              (cache_indices, "cache_indices"), (out, "out"))
     if out is None:
-        out = torch.empty((n, H, P), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((n, H, P))
     yp, yl = _rows(out, "out", (n, H, P))
     code = lib.ssm_state_update(ctypes.byref(sh), n, xp, xl, dp, dl, Ap, Bp, Bl, Cp, Cl, Dp, bp, ctypes.byref(st), yp, yl,
-                                _stream(stream, x.device))
+                                _stream(stream, dev))
     _lib.check(lib, code, "ssm_state_update")
     return out
 
 
 # ------------------------------------------------------------------ norms
 def _weight(w, d):
-    if w is None or tuple(w.shape) != (d,) or not w.is_contiguous() or w.dtype not in (torch.float32, torch.bfloat16):
+    if w is None or w.shape != (d,) or not w.is_contiguous() or (w.dtype is not _F32 and w.dtype is not _BF16):
         raise ValueError(f"weight: need a contiguous float32 or bfloat16 tensor of shape {(d,)}")
-    return w.data_ptr(), _lib.F32 if w.dtype == torch.float32 else _lib.BF16
+    return w.data_ptr(), _lib.F32 if w.dtype is _F32 else _lib.BF16
 
 
 def _group(d, group_size):
@@ -274,7 +285,7 @@ def _group(d, group_size):
 def _matrix(x, name):
     if x.dim() != 2:
         raise ValueError(f"{name}: need a 2-D tensor [rows, channels]")
-    return x.shape
+    return x.shape[0], x.shape[1]
 
 
 def gated_norm_fwd(x, gate, weight, *, group_size=None, norm_before_gate=False, eps=1e-5, out=None, stream=None):
@@ -284,11 +295,11 @@ def gated_norm_fwd(x, gate, weight, *, group_size=None, norm_before_gate=False, 
     rows, d = _matrix(x, "x")
     g = _group(d, group_size)
     xr, zr, (wp, wd) = _rows(x, "x", (rows, d)), _rows(gate, "gate", (rows, d)), _weight(weight, d)
-    _on(x.device, gate=gate, weight=weight, out=out)
+    dev = _on(x, (gate, "gate"), (weight, "weight"), (out, "out"))
     if out is None:
-        out = torch.empty((rows, d), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((rows, d))
     code = lib.gated_norm_fwd(rows, d, g, *xr, *zr, wp, wd, int(bool(norm_before_gate)), eps, *_rows(out, "out", (rows, d)),
-                              _stream(stream, x.device))
+                              _stream(stream, dev))
     _lib.check(lib, code, "gated_norm_fwd")
     return out
 
@@ -301,12 +312,12 @@ def gated_norm_bwd(dy, x, gate, weight, *, group_size=None, norm_before_gate=Fal
     g = _group(d, group_size)
     dyr, xr, zr = _rows(dy, "dy", (rows, d)), _rows(x, "x", (rows, d)), _rows(gate, "gate", (rows, d))
     wp, wd = _weight(weight, d)
-    dev = x.device
-    _on(dev, dy=dy, gate=gate, weight=weight, dx=dx, dgate=dgate, dweight=dweight, workspace=workspace)
-    dx = torch.empty((rows, d), dtype=torch.bfloat16, device=dev) if dx is None else dx
-    dgate = torch.empty((rows, d), dtype=torch.bfloat16, device=dev) if dgate is None else dgate
-    dweight = torch.empty((d,), dtype=torch.float32, device=dev) if dweight is None else dweight
-    workspace, sp, sb = _work(lib, lib.norm_bwd_workspace_bytes(rows, d, g), workspace, dev)
+    dev = _on(x, (dy, "dy"), (gate, "gate"), (weight, "weight"), (dx, "dx"), (dgate, "dgate"), (dweight, "dweight"),
+              (workspace, "workspace"))
+    dx = x.new_empty((rows, d)) if dx is None else dx
+    dgate = x.new_empty((rows, d)) if dgate is None else dgate
+    dweight = x.new_empty((d,), dtype=_F32) if dweight is None else dweight
+    workspace, sp, sb = _work(x, lib.norm_bwd_workspace_bytes(rows, d, g), workspace)
     code = lib.gated_norm_bwd(rows, d, g, *dyr, *xr, *zr, wp, wd, int(bool(norm_before_gate)), eps,
                               *_rows(dx, "dx", (rows, d)), *_rows(dgate, "dgate", (rows, d)), _vec(dweight, "dweight", d),
                               sp, sb, _stream(stream, dev))
@@ -315,9 +326,9 @@ def gated_norm_bwd(dy, x, gate, weight, *, group_size=None, norm_before_gate=Fal
 
 
 def _res_dtype(t, name):
-    if t.dtype not in (torch.float32, torch.bfloat16):
+    if t.dtype is not _F32 and t.dtype is not _BF16:
         raise ValueError(f"{name}: dtype must be float32 or bfloat16")
-    return _lib.F32 if t.dtype == torch.float32 else _lib.BF16
+    return _lib.F32 if t.dtype is _F32 else _lib.BF16
 
 
 def residual_norm_fwd(x, residual, weight, *, scale=1.0, eps=1e-5, out=None, residual_out=None, stream=None):
@@ -328,13 +339,13 @@ def residual_norm_fwd(x, residual, weight, *, scale=1.0, eps=1e-5, out=None, res
     _group(d, None)
     xr, rt = _rows(x, "x", (rows, d)), _res_dtype(residual, "residual")
     rr, (wp, wd) = _rows(residual, "residual", (rows, d), residual.dtype), _weight(weight, d)
-    _on(x.device, residual=residual, weight=weight, out=out, residual_out=residual_out)
+    dev = _on(x, (residual, "residual"), (weight, "weight"), (out, "out"), (residual_out, "residual_out"))
     if out is None:
-        out = torch.empty((rows, d), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((rows, d))
     if residual_out is None:
-        residual_out = torch.empty((rows, d), dtype=residual.dtype, device=x.device)
+        residual_out = residual.new_empty((rows, d))
     code = lib.residual_norm_fwd(rows, d, *xr, *rr, rt, scale, wp, wd, eps, *_rows(out, "out", (rows, d)),
-                                 *_rows(residual_out, "residual_out", (rows, d), residual.dtype), _stream(stream, x.device))
+                                 *_rows(residual_out, "residual_out", (rows, d), residual.dtype), _stream(stream, dev))
     _lib.check(lib, code, "residual_norm_fwd")
     return out, residual_out
 
@@ -346,17 +357,17 @@ def residual_norm_bwd(dy, dresidual_out, residual_out, weight, *, scale=1.0, eps
     lib = _lib.load_ssm()
     rows, d = _matrix(residual_out, "residual_out")
     _group(d, None)
-    dev, rdt = residual_out.device, residual_out.dtype
+    rdt = residual_out.dtype
     rt = _res_dtype(residual_out, "residual_out")
     dyr, ror = _rows(dy, "dy", (rows, d)), _rows(residual_out, "residual_out", (rows, d), rdt)
     drr = _rows(dresidual_out, "dresidual_out", (rows, d), rdt) if dresidual_out is not None else (None, 0)
     wp, wd = _weight(weight, d)
-    _on(dev, dy=dy, dresidual_out=dresidual_out, weight=weight, dx=dx, dresidual=dresidual, dweight=dweight,
-        workspace=workspace)
-    dx = torch.empty((rows, d), dtype=torch.bfloat16, device=dev) if dx is None else dx
-    dresidual = torch.empty((rows, d), dtype=rdt, device=dev) if dresidual is None else dresidual
-    dweight = torch.empty((d,), dtype=torch.float32, device=dev) if dweight is None else dweight
-    workspace, sp, sb = _work(lib, lib.norm_bwd_workspace_bytes(rows, d, d), workspace, dev)
+    dev = _on(residual_out, (dy, "dy"), (dresidual_out, "dresidual_out"), (weight, "weight"), (dx, "dx"),
+              (dresidual, "dresidual"), (dweight, "dweight"), (workspace, "workspace"))
+    dx = dy.new_empty((rows, d)) if dx is None else dx
+    dresidual = residual_out.new_empty((rows, d)) if dresidual is None else dresidual
+    dweight = dy.new_empty((d,), dtype=_F32) if dweight is None else dweight
+    workspace, sp, sb = _work(dy, lib.norm_bwd_workspace_bytes(rows, d, d), workspace)
     code = lib.residual_norm_bwd(rows, d, *dyr, *drr, *ror, rt, scale, wp, wd, eps, *_rows(dx, "dx", (rows, d)),
                                  *_rows(dresidual, "dresidual", (rows, d), rdt), _vec(dweight, "dweight", d), sp, sb,
                                  _stream(stream, dev))
