@@ -59,40 +59,28 @@ bool clash(const Span (&outs)[NO], const Span (&ins)[NI]) {
   return false;
 }
 
-// How the scan's walks are cut.  A block walks a piece chunk by chunk for 4 units (2 where the state tile is 256
-// columns, or where 4 would leave most of the chip idle).  Sequences are cut into pieces where whole ones
-// give too few blocks, or, with offsets (the host does not know the lengths), where one could be long against
-// the rest; the cost is a first walk for the pieces' states and a join.
+// Rows a piece has at most, 0 for whole sequences.  A block walks a piece chunk by chunk for kUnits units.
+// Sequences are cut into pieces where whole ones give too few blocks, or, with offsets (the host does not
+// know the lengths), where one could be long against the rest; the cost is a first walk for the pieces' states
+// and a join.
 constexpr int64_t kWantBlocks = 256, kMinSeg = 256;
-struct Cut {
-  int units;
-  int64_t seg;  // rows a piece has at most, 0 for whole sequences
-};
-Cut cut_rows(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows) {
-  const int64_t per_group = s->H / s->G * ceil_div(s->P, kPTile);
-  Cut c{2, 0};
-  if (nseq <= 0) return c;
-  if (state_tile(s->N) <= 128 && ceil_div(rows, kMinSeg) * s->G * ceil_div(per_group, 4) >= kWantBlocks / 2) c.units = 4;
-  const int64_t sets = s->G * ceil_div(per_group, c.units);
+int64_t piece_rows(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows) {
+  const int64_t sets = s->G * ceil_div(s->H / s->G * ceil_div(s->P, kPTile), kUnits);
   const bool enough = nseq * sets >= kWantBlocks;
-  if (batch_rows && enough) return c;
+  if (nseq <= 0 || (batch_rows && enough)) return 0;
   int64_t seg = ceil_div(ceil_div(rows * sets, kWantBlocks * (enough ? 2 : 1)), kChunk) * kChunk;
   if (seg < kMinSeg) seg = kMinSeg;
-  if (seg < (batch_rows ? rows / nseq : rows - nseq + 1)) c.seg = seg;
-  return c;
+  return seg < (batch_rows ? rows / nseq : rows - nseq + 1) ? seg : 0;
 }
 
 int64_t align_up(int64_t v) { return (v + 255) / 256 * 256; }
 
 struct FwdPlan {
-  int units;
   int64_t seg, n_slots, piece, decay, bytes;  // byte offsets into the workspace
 };
 FwdPlan plan_fwd(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows) {
   FwdPlan p{};
-  const Cut cut = cut_rows(s, rows, nseq, batch_rows);
-  p.units = cut.units;
-  p.seg = cut.seg;
+  p.seg = piece_rows(s, rows, nseq, batch_rows);
   if (!p.seg) return p;
   p.n_slots = batch_rows ? nseq * (ceil_div(rows / nseq, p.seg) - 1) : ceil_div(rows, p.seg);
   const int64_t items = p.n_slots + nseq, hp = s->H * ceil_div(s->P, kPTile);
@@ -200,7 +188,6 @@ void fill(ScanArgs* a, const ssm_shape* s, int64_t rows, const void* x, int64_t 
   a->H = (int)s->H, a->P = (int)s->P, a->G = (int)s->G, a->N = (int)s->N;
   a->ptiles = (int)ceil_div(s->P, kPTile);
   a->q = Seqs{seq->cu_seqlens, nseq, seq->cu_seqlens ? 1 : seq->seqlen, rows};
-  a->units = p.units;
   a->seg = p.seg;
   a->n_slots = p.n_slots;
   if (p.seg) {

@@ -231,14 +231,13 @@ __device__ __forceinline__ int at(int row, int col) {
   return row * kLd<W, PAD> + col;
 }
 
-// Blocks of the scan's kernels have 8 waves.
-constexpr int kThreads = 512;
 // this thread's wave, as a scalar (the compiler takes threadIdx.x / 64 for a value of each lane)
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-template <int W>
+// a tile in the registers of T threads
+template <int W, int T>
 struct TileRegs {
-  u32x4 v[W / 64];
+  u32x4 v[W * 8 / T];
 };
 
 // The rows of one chunk of a global array, as a buffer: offsets past its end read zeros and write nothing.
@@ -256,13 +255,13 @@ struct Rows {
 };
 constexpr uint32_t kOutside = 0xffffff00u;  // an offset past every buffer's end
 
-// Columns [0, ncols) of a chunk's rows, from column `col0` of the buffer on, into registers, kThreads
+// Columns [0, ncols) of a chunk's rows, from column `col0` of the buffer on, into registers of T
 // threads, zeros outside.  VEC: ncols is a multiple of 8.
-template <int W, bool VEC>
-__device__ __forceinline__ void load_tile(TileRegs<W>& t, const Rows& rows, uint32_t ld, int ncols, uint32_t col0 = 0) {
+template <bool VEC, int W, int T>
+__device__ __forceinline__ void load_tile(TileRegs<W, T>& t, const Rows& rows, uint32_t ld, int ncols, uint32_t col0 = 0) {
 #pragma unroll
-  for (int k = 0; k < W / 64; ++k) {
-    const int q = threadIdx.x + kThreads * k, row = q / (W / 8), c = (q % (W / 8)) * 8;
+  for (int k = 0; k < W * 8 / T; ++k) {
+    const int q = threadIdx.x + T * k, row = q / (W / 8), c = (q % (W / 8)) * 8;
     const uint32_t off = (row * ld + c) * 2 + col0 * 2;
     if constexpr (VEC) {
       t.v[k] = __builtin_amdgcn_raw_buffer_load_b128(rows.r, (int)(c < ncols ? off : kOutside), 0, 0);
@@ -292,11 +291,11 @@ __device__ __forceinline__ void store4(const Rows& rows, uint32_t ld, int row, i
   }
 }
 
-template <int W, int PAD = 8>
-__device__ __forceinline__ void store_tile(uint16_t* lds, const TileRegs<W>& t) {
+template <int PAD = 8, int W, int T>
+__device__ __forceinline__ void store_tile(uint16_t* lds, const TileRegs<W, T>& t) {
 #pragma unroll
-  for (int k = 0; k < W / 64; ++k) {
-    const int q = threadIdx.x + kThreads * k;
+  for (int k = 0; k < W * 8 / T; ++k) {
+    const int q = threadIdx.x + T * k;
     *reinterpret_cast<u32x4*>(lds + at<W, PAD>(q / (W / 8), q % (W / 8) * 8)) = t.v[k];
   }
 }
@@ -339,11 +338,10 @@ struct Unit {
 // kernels need more registers than 16 waves a CU leave them.
 __device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
 
-// The ten 16 x 16 blocks (ib, jb) of a 64 x 64 tile up to the diagonal, over 8 waves: (3, 0..3), (2, 0..2),
-// (1, 0) one a wave, then (1, 1) and (0, 0) for waves 0 and 1.
-__device__ __forceinline__ void first_block(int wave, int& ib, int& jb) {
-  ib = wave < 4 ? 3 : (wave < 7 ? 2 : 1);
-  jb = wave < 4 ? wave : (wave < 7 ? wave - 4 : 0);
+// The ten 16 x 16 blocks (ib, jb) of a 64 x 64 tile up to the diagonal: (3, 0..3), (2, 0..2), (1, 0), (1, 1), (0, 0)
+__device__ __forceinline__ void lower_block(int k, int& ib, int& jb) {
+  ib = k < 4 ? 3 : (k < 7 ? 2 : (k < 9 ? 1 : 0));
+  jb = k < 4 ? k : (k < 7 ? k - 4 : (k < 9 ? k - 7 : 0));
 }
 
 // ------------------------------------------------------------------ matrix operands

@@ -35,7 +35,6 @@ struct ScanArgs {
   int dt_f32, softplus;
   int H, P, G, N, ptiles;
   Seqs q;
-  int units;             // units a block of the scan or of the state walk takes: 2 or 4
   int64_t seg, n_slots;  // pieces other than a sequence's first: with offsets, at most one every seg rows
   // states [slot, H, P, N] of FP32; slot = ci ? ci[seq] : seq
   const float* init;     // nullptr: zeros
@@ -111,6 +110,8 @@ hipError_t launch_gated_bwd(const NormArgs& a, hipStream_t s);
 hipError_t launch_residual_fwd(const NormArgs& a, hipStream_t s);
 hipError_t launch_residual_bwd(const NormArgs& a, hipStream_t s);
 
+// units a block of the scan or of the state walk takes
+constexpr int kUnits = 4;
 // blocks of the scan and of the state walk: U 64-column units for every piece and group, these in sets of 8
 // (one an XCD)
 inline int64_t unit_blocks(int64_t items, int64_t H, int64_t G, int64_t ptiles, int U) {

@@ -4,17 +4,17 @@
 // 64 rows at a time, with the FP32 states in registers from chunk to chunk (no state travels through memory):
 //   Y = e^{L} (C S) + (M * dt * (C B^T)) X + D X,    S' = e^{L_Q} S + X^T (e^{L_Q - L} dt B)
 // The units share the chunk's B and C rows and its 64 x 64 scores C B^T, whose ten 16 x 16 blocks up to the
-// diagonal go to the eight waves; each wave decays its blocks for every unit.  Then a wave owns 16 * PB columns
-// p of its unit's Y and state, which it holds transposed ([n, p]: registers n), as the operand that C S needs.
-// Shared memory feeds the matrix instructions and is what bounds the chunk: with four units a wave uses every
-// B, C and score operand twice (125 KB a unit and chunk against 226 KB with two).
+// diagonal go to the waves; each wave decays its blocks for every unit.  Then a wave owns 16 * PB columns p of Y
+// and of its unit's state, which it holds transposed ([n, p]: registers n), as the operand that C S needs.
+// Shared memory feeds the matrix instructions: with four units and PB = 2 a wave uses every B, C and score operand
+// twice.  The 256-column state tile leaves no registers for that: two units, PB = 1.
 #include "ssm_state.h"
 
 namespace cssm {
 
-template <int NT, int U, bool VEC>
-__global__ __launch_bounds__(kThreads, 2) void ssm_scan_fwd_kernel(ScanArgs a) {
-  constexpr int NB = NT / 16, WU = 8 / U, PB = 4 / WU;
+template <int NT, int U, int PB, bool VEC>
+__global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs a) {
+  constexpr int T = 256 / PB * U, NB = NT / 16, WU = 4 / PB;  // threads, state blocks, waves a unit
   __shared__ __align__(16) uint16_t sx_[U][64 * kLd<64, 16>];
   __shared__ __align__(16) uint16_t sB[64 * kLd<NT, 16>];
   __shared__ __align__(16) uint16_t sC[64 * kLd<NT>];
@@ -81,26 +81,26 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_fwd_kernel(ScanArgs a) {
   const float Dh = a.D ? uniform(a.D[me.h]) : 0.f;
   const int64_t gn = (int64_t)us.group * a.N;
   const uint16_t *Bb = a.B + gn, *Cb = a.C + gn;
-  TileRegs<64> tx[U];
-  TileRegs<NT> tB, tC;
+  TileRegs<64, T> tx[U];
+  TileRegs<NT, T> tB, tC;
   auto load = [&](const Chunks<false>& c, int rows) {
     const Rows xr(a.x + c.c0 * a.x_ld, a.x_ld, rows, a.H * a.P, 2);
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       const Unit o(a, us, q);
-      load_tile<64, VEC>(tx[q], xr, (uint32_t)a.x_ld, o.pn, o.col);
+      load_tile<VEC>(tx[q], xr, (uint32_t)a.x_ld, o.pn, o.col);
     }
-    load_tile<NT, VEC>(tB, Rows(Bb + c.c0 * a.B_ld, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
-    load_tile<NT, VEC>(tC, Rows(Cb + c.c0 * a.C_ld, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
+    load_tile<VEC>(tB, Rows(Bb + c.c0 * a.B_ld, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
+    load_tile<VEC>(tC, Rows(Cb + c.c0 * a.C_ld, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
   };
-  // a chunk's decays into buffer `at`: a unit's last wave but one the prefix sums, steps and their powers, its
-  // last, whose lanes count from the chunk's end, the weights of the state update
+  // a chunk's decays into buffer `at`: a unit's first wave the prefix sums, steps and their powers, its
+  // second, whose lanes count from the chunk's end, the weights of the state update
   RawStep raw{};
-  const int my = w == WU - 2 ? lane : 63 - lane;
+  const int my = w == 0 ? lane : 63 - lane;
   auto decays = [&](int rows, int at) {
     const float d = rate.step(raw, my < rows);
     const float L = wave_prefix(d * rate.A2);
-    if (w == WU - 2) {
+    if (w == 0) {
       sdecay[at][un][0][lane] = L;
       sdecay[at][un][1][lane] = d;
       sdecay[at][un][2][lane] = ex2(L);
@@ -112,24 +112,24 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_fwd_kernel(ScanArgs a) {
   int rows = c.rows();
   load(c, rows);
   raw = raw_step(a, c.c0, rows, my, me.h);
-  if (w >= WU - 2) decays(rows, 0);
+  if (w < 2) decays(rows, 0);
   Chunks<false> after = c;
   int after_rows = rows;  // the chunk whose raw steps come next
   after = step_chunk(after, after_rows);
   raw = raw_step(a, after.c0, after_rows, my, me.h);
   // products over 32 columns read two blocks past the diagonal, which no wave writes
-  for (int e = threadIdx.x; e < U * 64 * kLd<64> / 2; e += kThreads) reinterpret_cast<uint32_t*>(sP_)[e] = 0u;
+  for (int e = threadIdx.x; e < U * 64 * kLd<64> / 2; e += T) reinterpret_cast<uint32_t*>(sP_)[e] = 0u;
   const uint16_t *sx = sx_[un], *sP = sP_[un];
   for (int buf = 0;; buf ^= 1) {
 #pragma unroll
-    for (int q = 0; q < U; ++q) store_tile<64, 16>(sx_[q], tx[q]);
-    store_tile<NT, 16>(sB, tB);
-    store_tile<NT>(sC, tC);
+    for (int q = 0; q < U; ++q) store_tile<16>(sx_[q], tx[q]);
+    store_tile<16>(sB, tB);
+    store_tile(sC, tC);
     __syncthreads();
     const Rows out(yb + c.c0 * a.y_ld, a.y_ld, rows, pn, 2);
     c = step_chunk(c, rows);  // rows == 0: that was the last one
     load(c, rows);
-    if (w >= WU - 2) decays(rows, buf ^ 1);
+    if (w < 2) decays(rows, buf ^ 1);
     after = step_chunk(after, after_rows);
     raw = raw_step(a, after.c0, after_rows, my, me.h);
     // score block (ib, jb): rows i in the lanes, columns j in the registers, decayed, times dt_j
@@ -154,10 +154,12 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_fwd_kernel(ScanArgs a) {
             u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
       }
     };
-    int ib0, jb0;
-    first_block(wave, ib0, jb0);
-    scores(ib0, jb0);
-    if (wave < 2) scores(1 - wave, 1 - wave);
+#pragma unroll
+    for (int k = 0; k < 10; k += T / 64) {
+      int ib, jb;
+      lower_block(wave + k, ib, jb);
+      if (wave + k < 10) scores(ib, jb);
+    }
     phase();
     // Y^T (registers p, lanes i) from the state before the chunk
     f32x4 y[PB][4];
@@ -252,10 +254,9 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_fwd_kernel(ScanArgs a) {
   }
 }
 
-template <int NT, int U, bool VEC>
+template <int NT, bool VEC>
 static hipError_t launch(const ScanArgs& a, hipStream_t s) {
   const int64_t items = a.n_slots + a.q.nseq, hp = (int64_t)a.H * a.ptiles;
-  const dim3 walk((uint32_t)unit_blocks(items, a.H, a.G, a.ptiles, U));
   if (a.seg > 0) {
     StateArgs k{};
     k.s = a;
@@ -265,18 +266,14 @@ static hipError_t launch(const ScanArgs& a, hipStream_t s) {
     k.v_ld = a.B_ld;
     k.start = a.init;
     k.piece = a.piece;
-    ssm_state_local_kernel<NT, U, VEC><<<walk, kThreads, 0, s>>>(k);
+    const dim3 walk((uint32_t)unit_blocks(items, a.H, a.G, a.ptiles, kUnits));
+    ssm_state_local_kernel<NT, kUnits, VEC><<<walk, 128 * kUnits, 0, s>>>(k);
     ssm_join_kernel<NT, false><<<dim3((uint32_t)(a.q.nseq * hp * (64 * NT / 4096))), 1024, 0, s>>>(k);
   }
-  ssm_scan_fwd_kernel<NT, U, VEC><<<walk, kThreads, 0, s>>>(a);
+  constexpr int U = NT > 128 ? 2 : kUnits, PB = NT > 128 ? 1 : 2;
+  ssm_scan_fwd_kernel<NT, U, PB, VEC>
+      <<<dim3((uint32_t)unit_blocks(items, a.H, a.G, a.ptiles, U)), 256 / PB * U, 0, s>>>(a);
   return hipGetLastError();
-}
-template <int NT, bool VEC>
-static hipError_t launch(const ScanArgs& a, hipStream_t s) {
-  if constexpr (NT <= 128) {
-    if (a.units == 4) return launch<NT, 4, VEC>(a, s);
-  }
-  return launch<NT, 2, VEC>(a, s);
 }
 
 hipError_t launch_scan_fwd(const ScanArgs& a, bool vec, hipStream_t s) {

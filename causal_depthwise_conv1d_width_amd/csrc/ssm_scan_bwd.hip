@@ -22,7 +22,7 @@
 namespace cssm {
 
 template <int NT, int U, bool VEC, bool STORE>
-__global__ __launch_bounds__(kThreads, 2) void ssm_states_kernel(StateArgs f, StateArgs r) {
+__global__ __launch_bounds__(128 * U, U > 2 || NT <= 128 ? 2 : 1) void ssm_states_kernel(StateArgs f, StateArgs r) {
   __shared__ StateShared<NT, U> sh;
   if (blockIdx.y == 0) state_walk<NT, U, VEC, false, STORE>(f, sh);
   else state_walk<NT, U, VEC, true, STORE>(r, sh);
@@ -40,6 +40,8 @@ __device__ __forceinline__ float across16(float v) {
   const auto q = __builtin_amdgcn_permlane32_swap(x, x, false, false);
   return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
+
+constexpr int kThreads = 512;
 
 // A block of 8 waves takes a chunk and walks the 64-column units of its heads.  A wave owns 16 * NBW columns n
 // of dB and dC (with NT = 64: two waves share 16, each with half of the rows) and two 16 x 16 blocks of dX.
@@ -87,15 +89,15 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
 #pragma unroll
     for (int k = 0; k < KB; ++k) dC[nb][k] = dB[nb][k] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  TileRegs<64> tx, ty;
+  TileRegs<64, kThreads> tx, ty;
   u32x4 Sh[NBW][2], Sl[NBW][2], Th[NBW][2], Tl[NBW][2];
   auto load_rows = [&](int t) {
     const int h = h_lo + t / a.ptiles, p_first = t % a.ptiles * kPTile;
     const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
     const int64_t o = (int64_t)h * a.P + p_first;
     const int n = t < tiles ? rows : 0;  // past the last one nothing is read
-    load_tile<64, VEC>(tx, Rows(a.x + pc.r0 * a.x_ld + o, a.x_ld, n, pn, 2), (uint32_t)a.x_ld, pn);
-    load_tile<64, VEC>(ty, Rows(b.dy + pc.r0 * b.dy_ld + o, b.dy_ld, n, pn, 2), (uint32_t)b.dy_ld, pn);
+    load_tile<VEC>(tx, Rows(a.x + pc.r0 * a.x_ld + o, a.x_ld, n, pn, 2), (uint32_t)a.x_ld, pn);
+    load_tile<VEC>(ty, Rows(b.dy + pc.r0 * b.dy_ld + o, b.dy_ld, n, pn, 2), (uint32_t)b.dy_ld, pn);
   };
   // a head's decays into its buffer: wave 6 the prefix sums, steps and powers, wave 7, whose lanes count
   // from the chunk's end, the decays to the end (waves 0 and 1 have two score blocks, these one)
@@ -134,16 +136,16 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
   if (w >= 6) decays(0);
   load_raw(1);
   {
-    TileRegs<NT> t;
-    load_tile<NT, VEC>(t, Rows(a.B + pc.r0 * a.B_ld + gn, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
-    store_tile<NT>(sB, t);
-    load_tile<NT, VEC>(t, Rows(a.C + pc.r0 * a.C_ld + gn, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
-    store_tile<NT>(sC, t);
+    TileRegs<NT, kThreads> t;
+    load_tile<VEC>(t, Rows(a.B + pc.r0 * a.B_ld + gn, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
+    store_tile(sB, t);
+    load_tile<VEC>(t, Rows(a.C + pc.r0 * a.C_ld + gn, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
+    store_tile(sC, t);
   }
   __syncthreads();
   // G^T blocks of this wave: rows i in the lanes, columns j in the registers
   int ib0, jb0;
-  first_block(w, ib0, jb0);
+  lower_block(w, ib0, jb0);
   f32x4 G0 = {0.f, 0.f, 0.f, 0.f}, G1 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int ks = 0; ks < NT / 32; ++ks) {
@@ -202,8 +204,8 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
     const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
     const double* sL = sdecay[t & 1];
     const float *sd = ssteps[t % 3][0], *se = ssteps[t % 3][1], *sr = ssteps[t % 3][2];
-    store_tile<64>(sx, tx);
-    store_tile<64>(sy, ty);
+    store_tile(sx, tx);
+    store_tile(sy, ty);
     if (owner) {
 #pragma unroll
       for (int nb = 0; nb < NBW; ++nb)
@@ -471,11 +473,11 @@ static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
   const dim3 walk((uint32_t)unit_blocks(items, a.H, a.G, a.ptiles, U), 2);
   if (a.seg > 0) {
     const dim3 join((uint32_t)(a.q.nseq * hp * (64 * NT / 4096)));
-    ssm_states_kernel<NT, U, VEC, false><<<walk, kThreads, 0, s>>>(f, r);
+    ssm_states_kernel<NT, U, VEC, false><<<walk, 128 * U, 0, s>>>(f, r);
     ssm_join_kernel<NT, false><<<join, 1024, 0, s>>>(f);
     ssm_join_kernel<NT, true><<<join, 1024, 0, s>>>(r);
   }
-  ssm_states_kernel<NT, U, VEC, true><<<walk, kThreads, 0, s>>>(f, r);
+  ssm_states_kernel<NT, U, VEC, true><<<walk, 128 * U, 0, s>>>(f, r);
   ssm_scan_bwd_kernel<NT, VEC><<<dim3((uint32_t)(ids * a.G * b.hsplit)), kThreads, 0, s>>>(b);
   if (b.hsplit > 1 && a.q.rows > 0) {
     const int64_t n = a.q.rows * a.G * a.N;
@@ -487,10 +489,7 @@ static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
 
 template <int NT, bool VEC>
 static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
-  if constexpr (NT <= 128) {
-    if (b.s.units == 4) return launch<NT, 4, VEC>(b, s);
-  }
-  return launch<NT, 2, VEC>(b, s);
+  return launch<NT, kUnits, VEC>(b, s);
 }
 
 hipError_t launch_scan_bwd(const ScanBwdArgs& b, bool vec, hipStream_t s) {

@@ -100,9 +100,8 @@ __device__ __forceinline__ bool starts_from_state(const ScanArgs& a, int64_t seq
   return a.init && (!a.has_init || __builtin_amdgcn_readfirstlane(a.has_init[seq]));
 }
 
-// A block of 8 waves walks U units of a group (they share v): 8 / U waves a unit, each with 16 * PB rows p of the
-// state and, with two units, half of them and half of the columns n.  A wave of four units reads a v operand
-// for two row blocks, which halves the shared memory traffic that bounds the walk.
+// A block walks U units of a group (they share v), two waves a unit, each with 32 rows p of the state: a wave reads
+// a v operand for two row blocks, which halves the shared memory traffic that bounds the walk.
 // LOCAL: from zeros, the end state goes to the piece's place (pieces whose end nobody needs do nothing).
 // STORE: from the piece's start state (or the sequence's), every chunk's start state goes to `store`.
 template <int NT, int U>
@@ -114,8 +113,8 @@ struct StateShared {
 };
 template <int NT, int U, bool VEC, bool REV, bool STORE>
 __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U>& sh) {
-  constexpr int WU = 8 / U;                   // waves a unit: two, or two by two
-  constexpr int NB = NT / 16 / (WU / 2);      // 16-column blocks a wave holds, with two 16-row blocks
+  constexpr int T = 128 * U, WU = 2;  // threads, and waves a unit
+  constexpr int NB = NT / 16;         // 16-column blocks of the state, with two 16-row blocks a wave
   const ScanArgs& a = k.s;
   const int hp = a.H * a.ptiles;
   const Units<U> us(a, blockIdx.x);
@@ -125,7 +124,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
   const Piece pc = find_piece(a.q, us.item, a.seg, a.n_slots);
   const bool first = pc.r0 == pc.s, last = pc.r1 == pc.e;
   const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
-  const int p0 = (w & 1) * 32, n0 = (w >> 1) * (NT / 2);
+  const int p0 = w * 32;
   const int64_t state_at = ((pc.seq * a.H + me.h) * a.P + me.p_first) * a.N;
   float* place = k.piece + (us.item * hp + me.tile) * (64 * NT);
   const uint16_t* su = sh.u[un];
@@ -152,7 +151,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[pb][nb][r] = place[(p0 + 16 * pb + 4 * g + r) * NT + n0 + 16 * nb + i];
+          for (int r = 0; r < 4; ++r) S[pb][nb][r] = place[(p0 + 16 * pb + 4 * g + r) * NT + 16 * nb + i];
     } else if (k.start) {
       const float* src = k.start + state_at;
 #pragma unroll
@@ -161,7 +160,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int p = p0 + 16 * pb + 4 * g + r, n = n0 + 16 * nb + i;
+            const int p = p0 + 16 * pb + 4 * g + r, n = 16 * nb + i;
             if (p < me.pn && n < a.N) S[pb][nb][r] = src[(int64_t)p * a.N + n];
           }
     }
@@ -171,16 +170,16 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
   const uint16_t* vb = k.v + (int64_t)us.group * a.N;
   float log_total = 0.f;
   RawStep raw{};
-  TileRegs<64> tu[U];
-  TileRegs<NT> tv;
+  TileRegs<64, T> tu[U];
+  TileRegs<NT, T> tv;
   auto load = [&](const Chunks<REV>& c, int rows) {
     const Rows ur(k.u + c.c0 * k.u_ld, k.u_ld, rows, a.H * a.P, 2);
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       const Unit o(a, us, q);
-      load_tile<64, VEC>(tu[q], ur, (uint32_t)k.u_ld, o.pn, o.col);
+      load_tile<VEC>(tu[q], ur, (uint32_t)k.u_ld, o.pn, o.col);
     }
-    load_tile<NT, VEC>(tv, Rows(vb + c.c0 * k.v_ld, k.v_ld, rows, a.N, 2), (uint32_t)k.v_ld, a.N);
+    load_tile<VEC>(tv, Rows(vb + c.c0 * k.v_ld, k.v_ld, rows, a.N, 2), (uint32_t)k.v_ld, a.N);
   };
   // a chunk's weights into buffer `at` by a unit's first wave; forward, a lane's row counts from the end
   const int my = REV ? lane : 63 - lane;
@@ -202,8 +201,8 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
   raw = raw_step(a, after.c0, after_rows, my, me.h);
   for (int buf = 0;; buf ^= 1) {
 #pragma unroll
-    for (int q = 0; q < U; ++q) store_tile<64, 16>(sh.u[q], tu[q]);
-    store_tile<NT, 16>(sh.v, tv);
+    for (int q = 0; q < U; ++q) store_tile<16>(sh.u[q], tu[q]);
+    store_tile<16>(sh.v, tv);
     __syncthreads();
     const int64_t here = c.c0;
     const float* sw = sh.w[buf][un];
@@ -224,7 +223,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
           hi[e] = pk_bf16(x, y);
           lo[e] = pk_bf16(x - bf_lo(hi[e]), y - bf_hi(hi[e]));
         }
-        const int o = ((((n0 >> 4) + nb) * 2 + (w & 1)) * 64 + lane) * 16;
+        const int o = ((nb * 2 + w) * 64 + lane) * 16;
         __builtin_amdgcn_raw_buffer_store_b128(hi, dst.r, o, 0, 0);
         __builtin_amdgcn_raw_buffer_store_b128(lo, dst.r, o + 64 * NT * 2, 0, 0);
       }
@@ -245,7 +244,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
       for (int pb = 0; pb < 2; ++pb) split_scaled(op_cols<64, 16>(su, 32 * ks, p0 + 16 * pb), wa, wb, hi[pb], lo[pb]);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const bf16x8 b = op_cols<NT, 16>(sv, 32 * ks, n0 + 16 * nb);
+        const bf16x8 b = op_cols<NT, 16>(sv, 32 * ks, 16 * nb);
 #pragma unroll
         for (int pb = 0; pb < 2; ++pb) {
           S[pb][nb] = mma(hi[pb], b, S[pb][nb]);
@@ -264,7 +263,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) place[(p0 + 16 * pb + 4 * g + r) * NT + n0 + 16 * nb + i] = S[pb][nb][r];
+        for (int r = 0; r < 4; ++r) place[(p0 + 16 * pb + 4 * g + r) * NT + 16 * nb + i] = S[pb][nb][r];
     if (w == 0 && lane == 0 && me.p_first == 0) a.piece_decay[us.item * a.H + me.h] = log_total;
   } else if (REV && first && k.end) {
     float* dst = k.end + state_at;
@@ -274,14 +273,14 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int p = p0 + 16 * pb + 4 * g + r, n = n0 + 16 * nb + i;
+          const int p = p0 + 16 * pb + 4 * g + r, n = 16 * nb + i;
           if (p < me.pn && n < a.N) dst[(int64_t)p * a.N + n] = S[pb][nb][r];
         }
   }
 }
 
 template <int NT, int U, bool VEC>
-__global__ __launch_bounds__(kThreads, 2) void ssm_state_local_kernel(StateArgs k) {
+__global__ __launch_bounds__(128 * U, U > 2 || NT <= 128 ? 2 : 1) void ssm_state_local_kernel(StateArgs k) {
   __shared__ StateShared<NT, U> sh;
   state_walk<NT, U, VEC, false, false>(k, sh);
 }
