@@ -59,30 +59,32 @@ bool clash(const Span (&outs)[NO], const Span (&ins)[NI]) {
   return false;
 }
 
-// Rows a piece has at most, 0 for whole sequences.  A block walks a piece chunk by chunk for kUnits units.
+// log2 of a piece's rows, 0 for whole sequences.  A block walks a piece chunk by chunk for kUnits units.
 // Sequences are cut into pieces where whole ones give too few blocks, or, with offsets (the host does not
 // know the lengths), where one could be long against the rest; the cost is a first walk for the pieces' states
 // and a join.
-constexpr int64_t kWantBlocks = 256, kMinSeg = 256;
-int64_t piece_rows(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows) {
+constexpr int64_t kWantBlocks = 256;
+constexpr int kMinSeg = 7;
+int piece_log2(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows) {
   const int64_t sets = s->G * ceil_div(s->H / s->G * ceil_div(s->P, kPTile), kUnits);
   const bool enough = nseq * sets >= kWantBlocks;
   if (nseq <= 0 || (batch_rows && enough)) return 0;
-  int64_t seg = ceil_div(ceil_div(rows * sets, kWantBlocks * (enough ? 2 : 1)), kChunk) * kChunk;
-  if (seg < kMinSeg) seg = kMinSeg;
-  return seg < (batch_rows ? rows / nseq : rows - nseq + 1) ? seg : 0;
+  int seg = kMinSeg;
+  while (((int64_t)1 << seg) * kWantBlocks * (enough ? 2 : 1) < rows * sets) ++seg;
+  return ((int64_t)1 << seg) < (batch_rows ? rows / nseq : rows - nseq + 1) ? seg : 0;
 }
 
 int64_t align_up(int64_t v) { return (v + 255) / 256 * 256; }
 
 struct FwdPlan {
-  int64_t seg, n_slots, piece, decay, bytes;  // byte offsets into the workspace
+  int seg;
+  int64_t n_slots, piece, decay, bytes;  // byte offsets into the workspace
 };
 FwdPlan plan_fwd(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows) {
   FwdPlan p{};
-  p.seg = piece_rows(s, rows, nseq, batch_rows);
+  p.seg = piece_log2(s, rows, nseq, batch_rows);
   if (!p.seg) return p;
-  p.n_slots = batch_rows ? nseq * (ceil_div(rows / nseq, p.seg) - 1) : ceil_div(rows, p.seg);
+  p.n_slots = batch_rows ? nseq * (ceil_div(rows / nseq, (int64_t)1 << p.seg) - 1) : ceil_div(rows, (int64_t)1 << p.seg);
   const int64_t items = p.n_slots + nseq, hp = s->H * ceil_div(s->P, kPTile);
   p.decay = align_up(items * hp * 64 * state_tile(s->N) * 4);
   p.bytes = p.decay + align_up(items * s->H * 4);

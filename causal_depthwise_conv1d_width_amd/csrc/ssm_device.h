@@ -151,44 +151,40 @@ __device__ __forceinline__ int64_t seq_of_row(const Seqs& q, int64_t row) {
   return lo + __popcll(__ballot(le)) - 1;
 }
 
-// The cut of the packed rows at sequence starts and at multiples of `step` rows: items below n_slots are the
-// parts that begin at row it * step inside a sequence, item n_slots + i is sequence i's first.
-__device__ __forceinline__ Piece find_part(const Seqs& q, int64_t it, int64_t step, int64_t n_slots) {
+// Chunk `id` of the packed rows: ids below n_slots are the chunks that begin at row id * kChunk inside a
+// sequence, id n_slots + i is sequence i's first.
+__device__ __forceinline__ Piece find_chunk(const Seqs& q, int64_t id, int64_t n_slots) {
   Piece p;
   p.ok = false;
-  if (it >= n_slots) {
-    p.seq = it - n_slots;
+  p.s = p.e = p.r1 = 0;
+  if (id >= n_slots) {
+    p.seq = id - n_slots;
     seq_bounds(q, p.seq, p.s, p.e);
     p.r0 = p.s;
     p.ok = p.e > p.s;
   } else {
-    p.r0 = it * step;
+    p.r0 = id * kChunk;
     p.seq = seq_of_row(q, p.r0);
-    p.s = p.e = p.r1 = 0;
     if (p.seq < 0 || p.seq >= q.nseq) return p;
     seq_bounds(q, p.seq, p.s, p.e);
     p.ok = p.r0 > p.s && p.r0 < p.e;
   }
-  p.r1 = p.e;
-  if (step > 0) {
-    const int64_t cut = (p.r0 / step + 1) * step;
-    if (cut < p.r1) p.r1 = cut;
-  }
+  const int64_t cut = (p.r0 & ~(int64_t)(kChunk - 1)) + kChunk;
+  p.r1 = cut < p.e ? cut : p.e;
   return p;
 }
 
-// The pieces of the scan: a sequence is cut every seg rows from its start, rounded down to whole chunks.
-// Piece j >= 1 of the sequence at row s is item s / seg + j: cuts of one sequence are seg rows apart and
-// those of the next one begin seg rows after its start, so no two share an item, and row item * seg lies in
+// The pieces of the scan: a sequence is cut every 2^seg rows from its start, rounded down to whole chunks.
+// Piece j >= 1 of the sequence at row s is item (s >> seg) + j: cuts of one sequence are 2^seg rows apart and
+// those of the next one begin 2^seg rows after its start, so no two share an item, and row item << seg lies in
 // the item's sequence.  Batch rows all have the same number of pieces, numbered without gaps, so that a
 // launch has no idle blocks.  seg == 0: whole sequences.
-__device__ __forceinline__ int64_t piece_count(int64_t s, int64_t e, int64_t seg) { return (e - s + seg - 1) / seg; }
-__device__ __forceinline__ int64_t piece_item(const Seqs& q, int64_t seq, int64_t s, int64_t seg, int64_t n_slots, int64_t j) {
+__device__ __forceinline__ int64_t piece_count(int64_t rows, int seg) { return (rows + ((int64_t)1 << seg) - 1) >> seg; }
+__device__ __forceinline__ int64_t piece_item(const Seqs& q, int64_t seq, int64_t s, int seg, int64_t n_slots, int64_t j) {
   if (j == 0) return n_slots + seq;
-  return q.cu ? s / seg + j : seq * (piece_count(0, q.seqlen, seg) - 1) + j - 1;
+  return q.cu ? (s >> seg) + j : seq * (piece_count(q.seqlen, seg) - 1) + j - 1;
 }
-__device__ __forceinline__ Piece find_piece(const Seqs& q, int64_t it, int64_t seg, int64_t n_slots) {
-  if (seg == 0) return find_part(q, it, 0, 0);
+__device__ __forceinline__ Piece find_piece(const Seqs& q, int64_t it, int seg, int64_t n_slots) {
   Piece p;
   p.ok = false;
   p.s = p.e = p.r0 = p.r1 = 0;
@@ -196,24 +192,30 @@ __device__ __forceinline__ Piece find_piece(const Seqs& q, int64_t it, int64_t s
   if (it >= n_slots) {
     p.seq = it - n_slots;
   } else if (q.cu) {
-    p.seq = seq_of_row(q, it * seg);
+    p.seq = seq_of_row(q, it << seg);
     if (p.seq < 0 || p.seq >= q.nseq) return p;
-  } else {
-    const int64_t more = piece_count(0, q.seqlen, seg) - 1;
-    p.seq = it / more;
-    j = it % more + 1;
+  } else {  // n_slots and so `it` is below 2^31
+    const uint32_t more = (uint32_t)(piece_count(q.seqlen, seg) - 1);
+    p.seq = (uint32_t)it / more;
+    j = (uint32_t)it % more + 1;
   }
   seq_bounds(q, p.seq, p.s, p.e);
-  if (it < n_slots && q.cu) j = it - p.s / seg;
-  p.r0 = j == 0 ? p.s : (p.s + j * seg) / kChunk * kChunk;
-  const int64_t cut = (p.s + (j + 1) * seg) / kChunk * kChunk;
-  p.r1 = p.s + (j + 1) * seg < p.e ? cut : p.e;
-  p.ok = p.s + j * seg < p.e && (j > 0 || it >= n_slots);
+  if (seg == 0) {
+    p.r0 = p.s;
+    p.r1 = p.e;
+    p.ok = p.e > p.s;
+    return p;
+  }
+  if (it < n_slots && q.cu) j = it - (p.s >> seg);
+  const int64_t from = p.s + (j << seg), to = p.s + ((j + 1) << seg);
+  p.r0 = j == 0 ? p.s : from & ~(int64_t)(kChunk - 1);
+  p.r1 = to < p.e ? to & ~(int64_t)(kChunk - 1) : p.e;
+  p.ok = from < p.e && (j > 0 || it >= n_slots);
   return p;
 }
 
 __device__ __forceinline__ int64_t chunk_end(int64_t r, int64_t r1) {
-  const int64_t c = (r / kChunk + 1) * kChunk;
+  const int64_t c = (r & ~(int64_t)(kChunk - 1)) + kChunk;
   return c < r1 ? c : r1;
 }
 
@@ -307,15 +309,17 @@ __device__ __forceinline__ void store_tile(uint16_t* lds, const TileRegs<W, T>& 
 template <int U>
 struct Units {
   int64_t item;
-  int group, first, count;  // units first .. first + count - 1 of the group
+  int group, units, first, count;  // units first .. first + count - 1 of the group's
   bool ok;
   __device__ __forceinline__ Units(const ScanArgs& a, uint32_t block) {
-    const uint32_t units = a.H / a.G * a.ptiles, sets = (units + U - 1) / U;
-    const uint32_t set = block / 8 / sets * 8 + block % 8;  // (piece, group)
-    item = set / (uint32_t)a.G;
-    group = set % (uint32_t)a.G;
-    first = block / 8 % sets * U;
-    count = (int)units - first < U ? (int)units - first : U;
+    units = (uint32_t)a.H / (uint32_t)a.G * a.ptiles;
+    const uint32_t sets = (units + U - 1) / U, eighth = block / 8, k = eighth / sets;
+    const uint32_t set = k * 8 + block % 8;  // (piece, group)
+    const uint32_t it = set / (uint32_t)a.G;
+    item = it;
+    group = set - it * a.G;
+    first = (eighth - k * sets) * U;
+    count = units - first < U ? units - first : U;
     ok = item < a.n_slots + a.q.nseq;
   }
 };
@@ -326,9 +330,9 @@ struct Unit {
   template <int U>
   __device__ __forceinline__ Unit(const ScanArgs& a, const Units<U>& u, int k) {
     const bool in = k < u.count;
-    tile = u.group * (a.H / a.G) * a.ptiles + u.first + (in ? k : 0);
-    h = tile / a.ptiles;
-    p_first = tile % a.ptiles * kPTile;
+    tile = u.group * u.units + u.first + (in ? k : 0);
+    h = a.ptiles == 1 ? tile : (uint32_t)tile / (uint32_t)a.ptiles;
+    p_first = (tile - h * a.ptiles) * kPTile;
     pn = !in ? 0 : (a.P - p_first < kPTile ? a.P - p_first : kPTile);
     col = (uint32_t)h * a.P + p_first;
   }

@@ -22,7 +22,7 @@ struct Seqs {
 
 // What the scan's kernels share.  Chunks begin at sequence starts and at multiples of kChunk rows of
 // the packed array, so a chunk is found from a row number alone; pieces (the unit of one block's sequential
-// walk) are whole chunks.  seg == 0: a piece is a sequence.
+// walk) are whole chunks.
 struct ScanArgs {
   const uint16_t* x;   // [rows, H, P]
   const uint16_t* B;   // [rows, G, N]
@@ -35,7 +35,8 @@ struct ScanArgs {
   int dt_f32, softplus;
   int H, P, G, N, ptiles;
   Seqs q;
-  int64_t seg, n_slots;  // pieces other than a sequence's first: with offsets, at most one every seg rows
+  int seg;               // log2 of a piece's rows, 0: a piece is a sequence
+  int64_t n_slots;       // pieces other than a sequence's first: with offsets, at most one every 2^seg rows
   // states [slot, H, P, N] of FP32; slot = ci ? ci[seq] : seq
   const float* init;     // nullptr: zeros
   float* fin;            // nullptr: not wanted

@@ -53,7 +53,7 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
   for (int pb = 0; pb < PB; ++pb)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) S[pb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (a.seg > 0 && pc.e - pc.s > a.seg) {
+  if (a.seg > 0 && piece_count(pc.e - pc.s, a.seg) > 1) {
     const float* src = a.piece + (us.item * hp + me.tile) * (64 * NT) + p_in * NT + 4 * g;
 #pragma unroll
     for (int pb = 0; pb < PB; ++pb)
@@ -256,7 +256,7 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
 
 template <int NT, bool VEC>
 static hipError_t launch(const ScanArgs& a, hipStream_t s) {
-  const int64_t items = a.n_slots + a.q.nseq, hp = (int64_t)a.H * a.ptiles;
+  const int64_t items = a.n_slots + a.q.nseq;
   if (a.seg > 0) {
     StateArgs k{};
     k.s = a;
@@ -268,7 +268,7 @@ static hipError_t launch(const ScanArgs& a, hipStream_t s) {
     k.piece = a.piece;
     const dim3 walk((uint32_t)unit_blocks(items, a.H, a.G, a.ptiles, kUnits));
     ssm_state_local_kernel<NT, kUnits, VEC><<<walk, 128 * kUnits, 0, s>>>(k);
-    ssm_join_kernel<NT, false><<<dim3((uint32_t)(a.q.nseq * hp * (64 * NT / 4096))), 1024, 0, s>>>(k);
+    ssm_join_kernel<NT, false><<<join_grid(a, NT), 1024, 0, s>>>(k);
   }
   constexpr int U = NT > 128 ? 2 : kUnits, PB = NT > 128 ? 1 : 2;
   ssm_scan_fwd_kernel<NT, U, PB, VEC>

@@ -69,7 +69,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
   const int64_t id = blk / b.hsplit / a.G;
   const int hg = a.H / a.G, per = (hg + b.hsplit - 1) / b.hsplit;
   const int h_lo = grp * hg + part * per, h_hi = h_lo + per < (grp + 1) * hg ? h_lo + per : (grp + 1) * hg;
-  const Piece pc = find_part(a.q, id, kChunk, b.n_chunk_slots);
+  const Piece pc = find_chunk(a.q, id, b.n_chunk_slots);
   if (!pc.ok) {
     for (int e = threadIdx.x; e < (h_hi - h_lo) * 3; e += kThreads) b.head_part[(id * a.H + h_lo) * 3 + e] = 0.f;
     return;
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
     load_tile<VEC>(ty, Rows(b.dy + pc.r0 * b.dy_ld + o, b.dy_ld, n, pn, 2), (uint32_t)b.dy_ld, pn);
   };
   // a head's decays into its buffer: wave 6 the prefix sums, steps and powers, wave 7, whose lanes count
-  // from the chunk's end, the decays to the end (waves 0 and 1 have two score blocks, these one)
+  // from the chunk's end, the decays to the end (these two and wave 5 have no score blocks)
   RawStep raw{};
   const int my = w == 6 ? lane : 63 - lane;
   auto load_raw = [&](int t) { raw = raw_step(a, pc.r0, t < tiles ? rows : 0, my, h_lo + t / a.ptiles); };
@@ -143,14 +143,17 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
     store_tile(sC, t);
   }
   __syncthreads();
-  // G^T blocks of this wave: rows i in the lanes, columns j in the registers
-  int ib0, jb0;
-  lower_block(w, ib0, jb0);
+  // G^T blocks of waves 0 .. 4, two each: rows i in the lanes, columns j in the registers
+  int ib0, jb0, ib1, jb1;
+  lower_block(w < 5 ? w : 0, ib0, jb0);
+  lower_block(w < 5 ? w + 5 : 5, ib1, jb1);
   f32x4 G0 = {0.f, 0.f, 0.f, 0.f}, G1 = {0.f, 0.f, 0.f, 0.f};
+  if (w < 5) {
 #pragma unroll
-  for (int ks = 0; ks < NT / 32; ++ks) {
-    G0 = mma(op_straight<NT>(sB, 16 * jb0, 32 * ks), op_straight<NT>(sC, 16 * ib0, 32 * ks), G0);
-    if (w < 2) G1 = mma(op_straight<NT>(sB, 16 * (1 - w), 32 * ks), op_straight<NT>(sC, 16 * (1 - w), 32 * ks), G1);
+    for (int ks = 0; ks < NT / 32; ++ks) {
+      G0 = mma(op_straight<NT>(sB, 16 * jb0, 32 * ks), op_straight<NT>(sC, 16 * ib0, 32 * ks), G0);
+      G1 = mma(op_straight<NT>(sB, 16 * jb1, 32 * ks), op_straight<NT>(sC, 16 * ib1, 32 * ks), G1);
+    }
   }
 
   float dl_sum = 0.f, q_sum = 0.f, trace_sum = 0.f;  // wave 5: over a head's column tiles
@@ -267,17 +270,19 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
         trace = wave_sum(trace);
         if (lane == 0) s_trace[t & 1][ib] = trace;
       }
-      phase();
     };
-    scores(ib0, jb0, G0);
-    if (w < 2) scores(1 - w, 1 - w, G1);
-    if (w == 4 || w == 5) {  // blocks (0, 1), (2, 3): products over 32 columns read them
-      const int z = 2 * (w - 4);
+    if (w < 5) {
+      scores(ib0, jb0, G0);
+      scores(ib1, jb1, G1);
+    } else if (w == 5) {
+      if (t > 0) finish(t - 1);
+    } else {
+      // blocks (0, 1), (2, 3): products over 32 columns read them
+      const int z = 2 * (w - 6);
       *reinterpret_cast<u32x2*>(sZ + at<64>(16 * z + i, 16 * z + 16 + 4 * g)) = u32x2{0u, 0u};
       *reinterpret_cast<u32x2*>(sG + at<64>(16 * z + i, 16 * z + 16 + 4 * g)) = u32x2{0u, 0u};
+      if (t + 1 < tiles) decays(t + 1);
     }
-    if (w >= 6 && t + 1 < tiles) decays(t + 1);
-    if (w == 5 && t > 0) finish(t - 1);
     load_raw(t + 2);
     phase();
     __syncthreads();
@@ -458,7 +463,7 @@ __global__ __launch_bounds__(256) void ssm_head_reduce_kernel(ScanBwdArgs b, int
 template <int NT, int U, bool VEC>
 static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
   const ScanArgs& a = b.s;
-  const int64_t hp = (int64_t)a.H * a.ptiles, items = a.n_slots + a.q.nseq, ids = b.n_chunk_slots + a.q.nseq;
+  const int64_t items = a.n_slots + a.q.nseq, ids = b.n_chunk_slots + a.q.nseq;
   StateArgs f{}, r{};
   f.s = r.s = a;
   f.u = a.x, f.u_ld = a.x_ld, f.v = a.B, f.v_ld = a.B_ld;
@@ -472,7 +477,7 @@ static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
   }
   const dim3 walk((uint32_t)unit_blocks(items, a.H, a.G, a.ptiles, U), 2);
   if (a.seg > 0) {
-    const dim3 join((uint32_t)(a.q.nseq * hp * (64 * NT / 4096)));
+    const dim3 join = join_grid(a, NT);
     ssm_states_kernel<NT, U, VEC, false><<<walk, 128 * U, 0, s>>>(f, r);
     ssm_join_kernel<NT, false><<<join, 1024, 0, s>>>(f);
     ssm_join_kernel<NT, true><<<join, 1024, 0, s>>>(r);

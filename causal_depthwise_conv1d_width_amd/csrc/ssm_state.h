@@ -58,7 +58,7 @@ struct Chunks {
   int64_t r0, r1, c0, c1;
   __device__ __forceinline__ Chunks(int64_t r0_, int64_t r1_) : r0(r0_), r1(r1_) {
     if (REV) {
-      c0 = (r1 - 1) / kChunk * kChunk;
+      c0 = (r1 - 1) & ~(int64_t)(kChunk - 1);
       if (c0 < r0) c0 = r0;
       c1 = r1;
     } else {
@@ -71,7 +71,7 @@ struct Chunks {
     Chunks n = *this;
     if (REV) {
       n.c1 = c0;
-      n.c0 = (c0 - 1) / kChunk * kChunk;
+      n.c0 = (c0 - 1) & ~(int64_t)(kChunk - 1);
       if (n.c0 < r0) n.c0 = r0;
     } else {
       n.c0 = c1;
@@ -145,7 +145,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) S[pb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
   if constexpr (STORE) {
-    if (a.seg > 0 && pc.e - pc.s > a.seg) {
+    if (a.seg > 0 && piece_count(pc.e - pc.s, a.seg) > 1) {
 #pragma unroll
       for (int pb = 0; pb < 2; ++pb)
 #pragma unroll
@@ -212,7 +212,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
     after = step_chunk(after, after_rows);
     raw = raw_step(a, after.c0, after_rows, my, me.h);
     if constexpr (STORE) {  // operand order: [n block of 16][p step of 32][lane] 16 bytes, high plane then low
-      const int64_t id = here == pc.s ? k.n_chunk_slots + pc.seq : here / kChunk;
+      const int64_t id = here == pc.s ? k.n_chunk_slots + pc.seq : here >> 6;
       const Rows dst(k.store + (id * hp + me.tile) * (2 * 64 * NT), 2 * 64 * NT, 1, me.pn ? 2 * 64 * NT : 0, 2);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -286,42 +286,45 @@ __global__ __launch_bounds__(128 * U, U > 2 || NT <= 128 ? 2 : 1) void ssm_state
 }
 
 // Local end states of a sequence's pieces -> start states, in place, in the order of the walk:
-// start[m + 1] = decay[m] start[m] + local[m].  One thread per four columns of a state.
+// start[m + 1] = decay[m] start[m] + local[m].  Sequences of one piece start from their own state.  A thread
+// takes four columns of a state; gridDim.y blocks share a sequence (few, where there are many sequences: blocks
+// with nothing to do cost more than the copies themselves).
 template <int NT, bool REV>
 __global__ __launch_bounds__(1024) void ssm_join_kernel(StateArgs k) {
   const ScanArgs& a = k.s;
-  constexpr int kPer = 64 * NT / 4 / 1024;  // blocks a tile
+  constexpr int kPer = 64 * NT / 4;  // threads' worth of a state tile
   const int hp = a.H * a.ptiles;
-  const int64_t seq = blockIdx.x / ((int64_t)hp * kPer);
-  const int rest = blockIdx.x % (hp * kPer), head_tile = rest / kPer, h = head_tile / a.ptiles;
-  const int at = (rest % kPer * 1024 + threadIdx.x) * 4, p = at / NT, n = at % NT;
-  const int p_abs = head_tile % a.ptiles * kPTile + p;
+  const int64_t seq = blockIdx.x;
   int64_t s, e;
   seq_bounds(a.q, seq, s, e);
-  if (e <= s) return;
+  const int64_t pieces = e > s ? piece_count(e - s, a.seg) : 0;
+  if (pieces <= 1) return;
   int64_t slot = seq;
   const bool live = state_slot(a, seq, slot);
   const bool from = REV ? k.start != nullptr : live && starts_from_state(a, seq);
-  f32x4 S = {0.f, 0.f, 0.f, 0.f};
-  if (from && p_abs < a.P) {
-    const float* src = k.start + (REV ? seq * (int64_t)a.H * a.P * a.N : slot * a.s_slot) + ((int64_t)h * a.P + p_abs) * a.N;
+  for (int w = blockIdx.y * 1024 + threadIdx.x; w < hp * kPer; w += gridDim.y * 1024) {
+    const int tile = w / kPer, at = w % kPer * 4, h = tile / a.ptiles, p = tile % a.ptiles * kPTile + at / NT, n = at % NT;
+    f32x4 S = {0.f, 0.f, 0.f, 0.f};
+    if (from && p < a.P) {
+      const float* src = k.start + (REV ? seq * (int64_t)a.H * a.P * a.N : slot * a.s_slot) + ((int64_t)h * a.P + p) * a.N;
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (n + r < a.N) S[r] = src[n + r];
-  }
-  const int64_t pieces = piece_count(s, e, a.seg);
-  if (pieces == 1) return;  // starts from the sequence's own state
-  for (int64_t m = 0; m < pieces; ++m) {
-    const int64_t item = piece_item(a.q, seq, s, a.seg, a.n_slots, REV ? pieces - 1 - m : m);
-    f32x4* place = reinterpret_cast<f32x4*>(k.piece + (item * hp + head_tile) * (64 * NT) + at);
-    if (m + 1 == pieces) {
+      for (int r = 0; r < 4; ++r)
+        if (n + r < a.N) S[r] = src[n + r];
+    }
+    for (int64_t m = 0; m < pieces; ++m) {
+      const int64_t item = piece_item(a.q, seq, s, a.seg, a.n_slots, REV ? pieces - 1 - m : m);
+      f32x4* place = reinterpret_cast<f32x4*>(k.piece + (item * hp + tile) * (64 * NT) + at);
+      const f32x4 local = m + 1 < pieces ? *place : S;
       *place = S;
-    } else {
-      const f32x4 local = *place;
-      *place = S;
-      S = S * ex2(a.piece_decay[item * a.H + h]) + local;
+      if (m + 1 < pieces) S = S * ex2(a.piece_decay[item * a.H + h]) + local;
     }
   }
+}
+inline dim3 join_grid(const ScanArgs& a, int NT) {
+  const int64_t all = ((int64_t)a.H * a.ptiles * 64 * NT / 4 + 1023) / 1024;
+  int64_t y = 2048 / a.q.nseq;
+  y = y < 4 ? 4 : y;
+  return dim3((uint32_t)a.q.nseq, (uint32_t)(y < all ? y : all));
 }
 
 }  // namespace cssm
