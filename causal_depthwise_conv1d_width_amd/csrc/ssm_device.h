@@ -349,6 +349,13 @@ __device__ __forceinline__ void lower_block(int k, int& ib, int& jb) {
 }
 
 // ------------------------------------------------------------------ matrix operands
+// A lane number the compiler cannot follow out of a loop: addresses computed from it are made again in every
+// pass (a few instructions) instead of all being kept, or spilled, over the whole loop.
+__device__ __forceinline__ int fresh(int lane) {
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 // 16x16x32 bf16: lane l holds index l % 16 of its operand and 8 of the 32 contracted positions; the
 // result has the first operand's index in the registers (4 * (l / 16) + r) and the second's in the
 // lanes.  The contracted positions may be taken in any order that both operands share.  Two orders
@@ -359,14 +366,13 @@ __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
 }
 // index = rows of the tile, contracted = columns k0 .. k0 + 31, straight
 template <int W, int PAD = 8>
-__device__ __forceinline__ bf16x8 op_straight(const uint16_t* lds, int row0, int k0) {
-  const int l = threadIdx.x & 63;
+__device__ __forceinline__ bf16x8 op_straight(const uint16_t* lds, int row0, int k0, int l) {
   return *reinterpret_cast<const bf16x8*>(lds + at<W, PAD>(row0 + (l & 15), k0 + (l >> 4) * 8));
 }
 // the same, split
 template <int W, int PAD = 8>
-__device__ __forceinline__ bf16x8 op_split(const uint16_t* lds, int row0, int k0) {
-  const int l = threadIdx.x & 63, row = row0 + (l & 15), c = k0 + (l >> 4) * 4;
+__device__ __forceinline__ bf16x8 op_split(const uint16_t* lds, int row0, int k0, int l) {
+  const int row = row0 + (l & 15), c = k0 + (l >> 4) * 4;
   const u32x2 a = *reinterpret_cast<const u32x2*>(lds + at<W, PAD>(row, c));
   const u32x2 b = *reinterpret_cast<const u32x2*>(lds + at<W, PAD>(row, c + 16));
   const u32x4 v = {a.x, a.y, b.x, b.y};
@@ -375,8 +381,8 @@ __device__ __forceinline__ bf16x8 op_split(const uint16_t* lds, int row0, int k0
 // index = columns c0 .. c0 + 15, contracted = rows k0 .. k0 + 31, split (the transposing read gives
 // lane i of 16 column i of the 4 rows x 16 columns that the 16 lanes address)
 template <int W, int PAD = 8>
-__device__ __forceinline__ bf16x8 op_cols(const uint16_t* lds, int k0, int c0) {
-  const int l = threadIdx.x & 63, row = k0 + (l >> 4) * 4 + ((l & 15) >> 2), c = c0 + (l & 3) * 4;
+__device__ __forceinline__ bf16x8 op_cols(const uint16_t* lds, int k0, int c0, int l) {
+  const int row = k0 + (l >> 4) * 4 + ((l & 15) >> 2), c = c0 + (l & 3) * 4;
   const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at<W, PAD>(row, c)));
   const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at<W, PAD>(row + 16, c)));
   const u32x2 ua = __builtin_bit_cast(u32x2, a), ub = __builtin_bit_cast(u32x2, b);

@@ -27,9 +27,8 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
   const Unit me(a, us, un);
   const int pn = me.pn;
   const Piece pc = find_piece(a.q, us.item, a.seg, a.n_slots);
-  const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+  int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
   const int p_in = 16 * PB * w + i;       // this lane's first state column
-  const int p_out = 16 * PB * w + 4 * g;  // this lane's first of four output columns
   const int64_t state_at = ((int64_t)me.h * a.P + me.p_first) * a.N;
   int64_t slot = 0;
   if (!pc.ok) {
@@ -96,7 +95,7 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
   // a chunk's decays into buffer `at`: a unit's first wave the prefix sums, steps and their powers, its
   // second, whose lanes count from the chunk's end, the weights of the state update
   RawStep raw{};
-  const int my = w == 0 ? lane : 63 - lane;
+  const int my = w == 0 ? (int)(threadIdx.x & 63) : 63 - (int)(threadIdx.x & 63);
   auto decays = [&](int rows, int at) {
     const float d = rate.step(raw, my < rows);
     const float L = wave_prefix(d * rate.A2);
@@ -121,6 +120,9 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
   for (int e = threadIdx.x; e < U * 64 * kLd<64> / 2; e += T) reinterpret_cast<uint32_t*>(sP_)[e] = 0u;
   const uint16_t *sx = sx_[un], *sP = sP_[un];
   for (int buf = 0;; buf ^= 1) {
+    lane = fresh(lane);
+    g = lane >> 4, i = lane & 15;
+    const int p_out = 16 * PB * w + 4 * g;  // this lane's first of four output columns
 #pragma unroll
     for (int q = 0; q < U; ++q) store_tile<16>(sx_[q], tx[q]);
     store_tile<16>(sB, tB);
@@ -137,7 +139,7 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
       f32x4 t = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < NT / 32; ++ks)
-        t = mma(op_straight<NT, 16>(sB, 16 * jb, 32 * ks), op_straight<NT>(sC, 16 * ib, 32 * ks), t);
+        t = mma(op_straight<NT, 16>(sB, 16 * jb, 32 * ks, lane), op_straight<NT>(sC, 16 * ib, 32 * ks, lane), t);
 #pragma unroll
       for (int q = 0; q < U; ++q) {
         const float(*s)[64] = sdecay[buf][q];
@@ -174,7 +176,7 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
       for (int pb = 0; pb < PB; ++pb) s[pb] = op_result(S[pb][2 * ks], S[pb][2 * ks + 1]);
 #pragma unroll
       for (int ib = 0; ib < 4; ++ib) {
-        const bf16x8 cv = op_split<NT>(sC, 16 * ib, 32 * ks);
+        const bf16x8 cv = op_split<NT>(sC, 16 * ib, 32 * ks, lane);
 #pragma unroll
         for (int pb = 0; pb < PB; ++pb) y[pb][ib] = mma(s[pb], cv, y[pb][ib]);
       }
@@ -197,10 +199,10 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
       {
         bf16x8 x[PB];
 #pragma unroll
-        for (int pb = 0; pb < PB; ++pb) x[pb] = op_cols<64, 16>(sx, 32 * ks, 16 * (PB * w + pb));
+        for (int pb = 0; pb < PB; ++pb) x[pb] = op_cols<64, 16>(sx, 32 * ks, 16 * (PB * w + pb), lane);
 #pragma unroll
         for (int ib = 2 * ks; ib < 4; ++ib) {
-          const bf16x8 pv = op_split<64>(sP, 16 * ib, 32 * ks);
+          const bf16x8 pv = op_split<64>(sP, 16 * ib, 32 * ks, lane);
 #pragma unroll
           for (int pb = 0; pb < PB; ++pb) y[pb][ib] = mma(x[pb], pv, y[pb][ib]);
         }
@@ -211,7 +213,7 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const bf16x8 b = op_cols<NT, 16>(sB, 32 * ks, 16 * nb);
+        const bf16x8 b = op_cols<NT, 16>(sB, 32 * ks, 16 * nb, lane);
 #pragma unroll
         for (int pb = 0; pb < PB; ++pb) {
           S[pb][nb] = mma(b, hi[pb], S[pb][nb]);

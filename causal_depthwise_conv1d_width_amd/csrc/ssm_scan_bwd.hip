@@ -41,14 +41,16 @@ __device__ __forceinline__ float across16(float v) {
   return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 
-// A block of 8 waves takes a chunk and walks the 64-column units of its heads.  A wave owns 16 * NBW columns n
-// of dB and dC (with NT = 64: two waves share 16, each with half of the rows) and two 16 x 16 blocks of dX.
+// A block of 4 waves takes a chunk and walks the 64-column units of its heads.  A wave owns a quarter of the
+// columns n of dB and dC, and 16 columns of dX.  Two blocks share a CU (with the 256-column state tile, one), so that
+// one's loads from shared memory run beside the other's products: 8 waves in one block go through the phases
+// together, and took 600 us where two blocks take @@ us (16384 rows, 64 heads of 64 columns, N = 128).
 template <int NT, bool VEC>
-__global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b) {
-  constexpr int NBW = NT > 128 ? NT / 128 : 1;  // 16-column blocks n of a wave
-  constexpr int KB = NT > 64 ? 4 : 2;           // 16-row blocks of a wave
+__global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(ScanBwdArgs b) {
+  constexpr int NBW = NT / 64;  // 16-column blocks n of a wave
+  constexpr int KB = 4;         // 16-row blocks
   constexpr int R = (NT > 128 ? NT : 128) * kLd<64>;
   __shared__ __align__(16) uint16_t sx[64 * kLd<64>];
   __shared__ __align__(16) uint16_t sy[64 * kLd<64>];
@@ -60,10 +62,11 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
   __shared__ __align__(16) double sdecay[2][64];
   __shared__ __align__(16) float ssteps[3][3][64];
   __shared__ __align__(16) float s_col[2][4][64];
-  __shared__ float s_row[2][4][64], s_diag[2][64], s_trace[2][4], s_rint[8][64], s_u[8][64], s_dot[8];
+  __shared__ float s_row[2][4][64], s_diag[2][64], s_trace[2][4], s_rint[4][64], s_u[4][64], s_dot[4];
   uint16_t *sZ = sR, *sG = sR + 64 * kLd<64>;
   const ScanArgs& a = b.s;
-  const int lane = threadIdx.x & 63, w = wave_id(), g = lane >> 4, i = lane & 15;
+  int lane = threadIdx.x & 63;
+  const int w = wave_id();
   const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
   const int part = blk % b.hsplit, grp = blk / b.hsplit % a.G;
   const int64_t id = blk / b.hsplit / a.G;
@@ -78,10 +81,8 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
   const int hp = a.H * a.ptiles;
   const int tiles = (h_hi - h_lo) * a.ptiles;
   const int64_t gn = (int64_t)grp * a.N;
-  const int nw = NT > 64 ? 16 * NBW * w : 16 * (w & 3);  // this wave's first column n
-  const int kb0 = NT > 64 ? 0 : 2 * (w >> 2);            // and its first block of rows
-  const bool owner = NT > 64 || w < 4;                   // of the columns, where two waves share them
-  const int pw = 16 * (w & 3), jw = 2 * (w >> 2);        // its blocks of dX: columns pw, rows 16 jw, 16 jw + 16
+  const int nw = 16 * NBW * w;  // this wave's first column n
+  const int pw = 16 * w;        // and of dX
 
   f32x4 dC[NBW][KB], dB[NBW][KB];
 #pragma unroll
@@ -99,22 +100,19 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
     load_tile<VEC>(tx, Rows(a.x + pc.r0 * a.x_ld + o, a.x_ld, n, pn, 2), (uint32_t)a.x_ld, pn);
     load_tile<VEC>(ty, Rows(b.dy + pc.r0 * b.dy_ld + o, b.dy_ld, n, pn, 2), (uint32_t)b.dy_ld, pn);
   };
-  // a head's decays into its buffer: wave 6 the prefix sums, steps and powers, wave 7, whose lanes count
-  // from the chunk's end, the decays to the end (these two and wave 5 have no score blocks)
+  // a head's decays into its buffer, by wave 3 (waves 0 and 1 have three score blocks, these two): prefix sums,
+  // steps and powers, and the decays to the chunk's end, summed from there
   RawStep raw{};
-  const int my = w == 6 ? lane : 63 - lane;
-  auto load_raw = [&](int t) { raw = raw_step(a, pc.r0, t < tiles ? rows : 0, my, h_lo + t / a.ptiles); };
+  auto load_raw = [&](int t) { raw = raw_step(a, pc.r0, t < tiles ? rows : 0, lane, h_lo + (uint32_t)t / (uint32_t)a.ptiles); };
   auto decays = [&](int t) {
-    const Rate rate(a, h_lo + t / a.ptiles);
-    const float d = rate.step(raw, my < rows);
-    const double L = wave_prefix((double)(d * rate.A2));
-    if (w == 6) {
-      sdecay[t & 1][lane] = L;
-      ssteps[t % 3][0][lane] = d;
-      ssteps[t % 3][1][lane] = ex2((float)L);
-    } else {
-      ssteps[t % 3][2][my] = ex2((float)dpp0<0x138, 0xf>(L));
-    }
+    const Rate rate(a, h_lo + (uint32_t)t / (uint32_t)a.ptiles);
+    const float d = rate.step(raw, lane < rows), l = d * rate.A2;
+    const double L = wave_prefix((double)l);
+    const double back = wave_prefix((double)__shfl(l, 63 - lane));
+    sdecay[t & 1][lane] = L;
+    ssteps[t % 3][0][lane] = d;
+    ssteps[t % 3][1][lane] = ex2((float)L);
+    ssteps[t % 3][2][63 - lane] = ex2((float)dpp0<0x138, 0xf>(back));  // the rows after this one
   };
   // one of the chunk's states of head t: high and low parts
   auto load_states = [&](int t, const uint16_t* from, u32x4(&hi)[NBW][2], u32x4(&lo)[NBW][2]) {
@@ -133,7 +131,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
   load_states(0, b.ct, Th, Tl);
   load_states(0, b.cs, Sh, Sl);
   load_raw(0);
-  if (w >= 6) decays(0);
+  if (w == 3) decays(0);
   load_raw(1);
   {
     TileRegs<NT, kThreads> t;
@@ -143,33 +141,32 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
     store_tile(sC, t);
   }
   __syncthreads();
-  // G^T blocks of waves 0 .. 4, two each: rows i in the lanes, columns j in the registers
-  int ib0, jb0, ib1, jb1;
-  lower_block(w < 5 ? w : 0, ib0, jb0);
-  lower_block(w < 5 ? w + 5 : 5, ib1, jb1);
-  f32x4 G0 = {0.f, 0.f, 0.f, 0.f}, G1 = {0.f, 0.f, 0.f, 0.f};
-  if (w < 5) {
+  // G^T blocks of this wave: rows i in the lanes, columns j in the registers
+  f32x4 G[3];
 #pragma unroll
-    for (int ks = 0; ks < NT / 32; ++ks) {
-      G0 = mma(op_straight<NT>(sB, 16 * jb0, 32 * ks), op_straight<NT>(sC, 16 * ib0, 32 * ks), G0);
-      G1 = mma(op_straight<NT>(sB, 16 * jb1, 32 * ks), op_straight<NT>(sC, 16 * ib1, 32 * ks), G1);
+  for (int k = 0; k < 3; ++k) {
+    G[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int ib, jb;
+    lower_block(w + 4 * k, ib, jb);
+    if (w + 4 * k < 10) {
+#pragma unroll
+      for (int ks = 0; ks < NT / 32; ++ks)
+        G[k] = mma(op_straight<NT>(sB, 16 * jb, 32 * ks, lane), op_straight<NT>(sC, 16 * ib, 32 * ks, lane), G[k]);
     }
   }
 
-  float dl_sum = 0.f, q_sum = 0.f, trace_sum = 0.f;  // wave 5: over a head's column tiles
-  // lane = row: the gradients of head t's decays and steps, by wave 5
+  float dl_sum = 0.f, q_sum = 0.f, trace_sum = 0.f;  // wave 2: over a head's column tiles
+  // lane = row: the gradients of head t's decays and steps, by wave 2
   auto finish = [&](const int t) {
     const int h = h_lo + t / a.ptiles, ptile = t % a.ptiles;
     const float *sd = ssteps[t % 3][0], *se = ssteps[t % 3][1];
     const float d = sd[lane];
     float rint = 0.f, u = 0.f, row = 0.f, col = 0.f, dots = 0.f, trace = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dots += s_dot[k];
-#pragma unroll
-    for (int k = 0; k < (NT > 64 ? 8 : 4); ++k) {
-      const int from = NT > 64 ? k : k + 4 * (lane >> 5);
-      rint += s_rint[from][lane];
-      u += s_u[from][lane];
+    for (int k = 0; k < 4; ++k) {
+      dots += s_dot[k];
+      rint += s_rint[k][lane];
+      u += s_u[k][lane];
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {  // blocks up to the diagonal
@@ -203,37 +200,38 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
     }
   };
   for (int t = 0; t < tiles; ++t) {
+    lane = fresh(lane);
+    const int g = lane >> 4, i = lane & 15;
     const int h = h_lo + t / a.ptiles, ptile = t % a.ptiles, p_first = ptile * kPTile;
     const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
     const double* sL = sdecay[t & 1];
     const float *sd = ssteps[t % 3][0], *se = ssteps[t % 3][1], *sr = ssteps[t % 3][2];
     store_tile(sx, tx);
     store_tile(sy, ty);
-    if (owner) {
 #pragma unroll
-      for (int nb = 0; nb < NBW; ++nb)
+    for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const int n = nw + 16 * nb + i;
-          *reinterpret_cast<u32x2*>(sR + at<64>(n, 32 * ks + 4 * g)) = u32x2{Th[nb][ks].x, Th[nb][ks].y};
-          *reinterpret_cast<u32x2*>(sR + at<64>(n, 32 * ks + 16 + 4 * g)) = u32x2{Th[nb][ks].z, Th[nb][ks].w};
-        }
-    }
+      for (int ks = 0; ks < 2; ++ks) {
+        const int n = nw + 16 * nb + i;
+        *reinterpret_cast<u32x2*>(sR + at<64>(n, 32 * ks + 4 * g)) = u32x2{Th[nb][ks].x, Th[nb][ks].y};
+        *reinterpret_cast<u32x2*>(sR + at<64>(n, 32 * ks + 16 + 4 * g)) = u32x2{Th[nb][ks].z, Th[nb][ks].w};
+      }
     phase();
     __syncthreads();
     load_rows(t + 1);
     phase();
 
-    f32x4 dX[2];  // registers p = pw + 4 g + r, lanes j
-    dX[0] = dX[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 dX[4];  // registers p = pw + 4 g + r, lanes j
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dX[k] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < NT / 32; ++ks) {
-      const bf16x8 tt = op_cols<64>(sR, 32 * ks, pw);
+      const bf16x8 tt = op_cols<64>(sR, 32 * ks, pw, lane);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) dX[k] = mma(tt, op_split<NT>(sB, 16 * (jw + k), 32 * ks), dX[k]);
+      for (int k = 0; k < 4; ++k) dX[k] = mma(tt, op_split<NT>(sB, 16 * k, 32 * ks, lane), dX[k]);
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) dX[k] *= sr[16 * (jw + k) + i];
+    for (int k = 0; k < 4; ++k) dX[k] *= sr[16 * k + i];
     phase();
     __syncthreads();
 
@@ -242,7 +240,7 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
     auto scores = [&](const int ib, const int jb, const f32x4& G) {
       f32x4 W = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) W = mma(op_straight<64>(sx, 16 * jb, 32 * ks), op_straight<64>(sy, 16 * ib, 32 * ks), W);
+      for (int ks = 0; ks < 2; ++ks) W = mma(op_straight<64>(sx, 16 * jb, 32 * ks, lane), op_straight<64>(sy, 16 * ib, 32 * ks, lane), W);
       const double Li = sL[16 * ib + i];
       const f32x4 dj = *reinterpret_cast<const f32x4*>(sd + 16 * jb + 4 * g);
       f32x4 z, gm;
@@ -270,18 +268,21 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
         trace = wave_sum(trace);
         if (lane == 0) s_trace[t & 1][ib] = trace;
       }
+      phase();
     };
-    if (w < 5) {
-      scores(ib0, jb0, G0);
-      scores(ib1, jb1, G1);
-    } else if (w == 5) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      int ib, jb;
+      lower_block(w + 4 * k, ib, jb);
+      if (w + 4 * k < 10) scores(ib, jb, G[k]);
+    }
+    if (w < 2) {  // blocks (0, 1), (2, 3): products over 32 columns read them
+      *reinterpret_cast<u32x2*>(sZ + at<64>(32 * w + i, 32 * w + 16 + 4 * g)) = u32x2{0u, 0u};
+      *reinterpret_cast<u32x2*>(sG + at<64>(32 * w + i, 32 * w + 16 + 4 * g)) = u32x2{0u, 0u};
+    } else if (w == 2) {
       if (t > 0) finish(t - 1);
-    } else {
-      // blocks (0, 1), (2, 3): products over 32 columns read them
-      const int z = 2 * (w - 6);
-      *reinterpret_cast<u32x2*>(sZ + at<64>(16 * z + i, 16 * z + 16 + 4 * g)) = u32x2{0u, 0u};
-      *reinterpret_cast<u32x2*>(sG + at<64>(16 * z + i, 16 * z + 16 + 4 * g)) = u32x2{0u, 0u};
-      if (t + 1 < tiles) decays(t + 1);
+    } else if (t + 1 < tiles) {
+      decays(t + 1);
     }
     load_raw(t + 2);
     phase();
@@ -300,19 +301,19 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
           dot = dot2(Sl[nb][ks][e], Tl[nb][ks][e], dot);
         }
     dot = wave_sum(dot);
-    if (lane == 0) s_dot[w] = owner ? dot : 0.f;
+    if (lane == 0) s_dot[w] = dot;
     phase();
     // dC and the rows' sums with S
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
-      const int ib = kb0 + k;
+      const int ib = k;
       float rint = 0.f;
 #pragma unroll
       for (int nb = 0; nb < NBW; ++nb) {
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          const bf16x8 y = op_split<64>(sy, 16 * ib, 32 * ks);
+          const bf16x8 y = op_split<64>(sy, 16 * ib, 32 * ks, lane);
           v = mma(__builtin_bit_cast(bf16x8, Sh[nb][ks]), y, v);
           v = mma(__builtin_bit_cast(bf16x8, Sl[nb][ks]), y, v);
         }
@@ -322,11 +323,12 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
         f32x4 acc = dC[nb][k] + v;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
-          if (ks <= ib / 2) acc = mma(op_cols<NT>(sB, 32 * ks, nw + 16 * nb), op_split<64>(sZ, 16 * ib, 32 * ks), acc);
+          if (ks <= ib / 2) acc = mma(op_cols<NT>(sB, 32 * ks, nw + 16 * nb, lane), op_split<64>(sZ, 16 * ib, 32 * ks, lane), acc);
         dC[nb][k] = acc;
       }
       rint = across16(rint);
       if (g == 0) s_rint[w][16 * ib + i] = rint;
+      phase();
     }
     phase();
     load_states(t + 1, b.cs, Sh, Sl);
@@ -334,14 +336,14 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
     // dB and the rows' sums with T
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
-      const int jb = kb0 + k;
+      const int jb = k;
       float u = 0.f;
 #pragma unroll
       for (int nb = 0; nb < NBW; ++nb) {
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          const bf16x8 x = op_split<64>(sx, 16 * jb, 32 * ks);
+          const bf16x8 x = op_split<64>(sx, 16 * jb, 32 * ks, lane);
           v = mma(__builtin_bit_cast(bf16x8, Th[nb][ks]), x, v);
           v = mma(__builtin_bit_cast(bf16x8, Tl[nb][ks]), x, v);
         }
@@ -351,28 +353,28 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
         f32x4 acc = dB[nb][k] + v * sd[16 * jb + i];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
-          if (ks >= jb / 2) acc = mma(op_cols<NT>(sC, 32 * ks, nw + 16 * nb), op_cols<64>(sZ, 32 * ks, 16 * jb), acc);
+          if (ks >= jb / 2) acc = mma(op_cols<NT>(sC, 32 * ks, nw + 16 * nb, lane), op_cols<64>(sZ, 32 * ks, 16 * jb, lane), acc);
         dB[nb][k] = acc;
       }
       u = across16(u);
       if (g == 0) s_u[w][16 * jb + i] = u;
+      phase();
     }
     load_states(t + 1, b.ct, Th, Tl);
     phase();
 
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      if (ks < jw / 2) continue;
-      const bf16x8 y = op_cols<64>(sy, 32 * ks, pw);
+      const bf16x8 y = op_cols<64>(sy, 32 * ks, pw, lane);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) dX[k] = mma(y, op_cols<64>(sG, 32 * ks, 16 * (jw + k)), dX[k]);
+      for (int k = 0; k < 2 * ks + 2; ++k) dX[k] = mma(y, op_cols<64>(sG, 32 * ks, 16 * k, lane), dX[k]);
     }
     const int p_out = pw + 4 * g;
     const Rows out(b.dx + pc.r0 * b.dx_ld + (int64_t)h * a.P + p_first, b.dx_ld, rows, pn, 2);
     const float Dh = a.D ? uniform(a.D[h]) : 0.f;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int row = 16 * (jw + k) + i;
+    for (int k = 0; k < 4; ++k) {
+      const int row = 16 * k + i;
       const float d = sd[row];
       const u32x2 yv = *reinterpret_cast<const u32x2*>(sy + at<64>(row, p_out));
       const u32x2 o = {pk_bf16(d * dX[k][0] + Dh * bf_lo(yv.x), d * dX[k][1] + Dh * bf_hi(yv.x)),
@@ -384,13 +386,13 @@ __global__ __launch_bounds__(kThreads, 2) void ssm_scan_bwd_kernel(ScanBwdArgs b
 
   }
   __syncthreads();
-  if (w == 5) finish(tiles - 1);
+  if (w == 2) finish(tiles - 1);
 
 #pragma unroll
   for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
-      const int row = 16 * (kb0 + k) + i, n = nw + 16 * nb + 4 * g;
+      const int row = 16 * k + (lane & 15), n = nw + 16 * nb + 4 * (lane >> 4);
       if (row >= rows || n >= a.N) continue;
       const int64_t r = pc.r0 + row;
       if (b.hsplit > 1) {

@@ -241,10 +241,10 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
       const f32x4 wb = *reinterpret_cast<const f32x4*>(sw + 32 * ks + 16 + 4 * g);
       bf16x8 hi[2], lo[2];
 #pragma unroll
-      for (int pb = 0; pb < 2; ++pb) split_scaled(op_cols<64, 16>(su, 32 * ks, p0 + 16 * pb), wa, wb, hi[pb], lo[pb]);
+      for (int pb = 0; pb < 2; ++pb) split_scaled(op_cols<64, 16>(su, 32 * ks, p0 + 16 * pb, lane), wa, wb, hi[pb], lo[pb]);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const bf16x8 b = op_cols<NT, 16>(sv, 32 * ks, 16 * nb);
+        const bf16x8 b = op_cols<NT, 16>(sv, 32 * ks, 16 * nb, lane);
 #pragma unroll
         for (int pb = 0; pb < 2; ++pb) {
           S[pb][nb] = mma(hi[pb], b, S[pb][nb]);
