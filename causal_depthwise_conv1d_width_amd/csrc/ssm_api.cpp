@@ -315,8 +315,8 @@ int ssm_scan_bwd(const ssm_shape* shape, int64_t rows, const void* dy, int64_t d
     b.dB = static_cast<uint16_t*>(dB), b.dB_ld = dB_ld;
     b.dC = static_cast<uint16_t*>(dC), b.dC_ld = dC_ld;
     b.piece_t = reinterpret_cast<float*>(w + p.piece_t);
-    b.cs = reinterpret_cast<uint16_t*>(w + p.cs);
-    b.ct = reinterpret_cast<uint16_t*>(w + p.ct);
+    b.cs = reinterpret_cast<float*>(w + p.cs);
+    b.ct = reinterpret_cast<float*>(w + p.ct);
     b.n_chunk_slots = p.n_chunk_slots;
     b.head_part = reinterpret_cast<float*>(w + p.head);
     b.bc_part = reinterpret_cast<float*>(w + p.bc);

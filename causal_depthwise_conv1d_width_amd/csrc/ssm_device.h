@@ -394,19 +394,36 @@ __device__ __forceinline__ bf16x8 op_result(f32x4 a, f32x4 b) {
   const u32x4 v = {pk_bf16(a[0], a[1]), pk_bf16(a[2], a[3]), pk_bf16(b[0], b[1]), pk_bf16(b[2], b[3])};
   return __builtin_bit_cast(bf16x8, v);
 }
-// w[e] * v[e] in FP32 as the sum of two bf16 operands: the remainder is at most 2^-16 of the product
-__device__ __forceinline__ void split_scaled(bf16x8 v, f32x4 wa, f32x4 wb, bf16x8& hi, bf16x8& lo) {
-  const u32x4 u = __builtin_bit_cast(u32x4, v);
-  u32x4 h, l;
+// An FP32 operand as the sum of three bf16 ones: 8 bits each, so that its products keep FP32's 24 (with
+// the first two, 16)
+struct Parts {
+  bf16x8 p[3];
+};
+__device__ __forceinline__ Parts split(f32x4 a, f32x4 b) {
+  u32x4 q[3];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float a = bf_lo(u[e]) * (e < 2 ? wa[2 * e] : wb[2 * e - 4]);
-    const float b = bf_hi(u[e]) * (e < 2 ? wa[2 * e + 1] : wb[2 * e - 3]);
-    h[e] = pk_bf16(a, b);
-    l[e] = pk_bf16(a - bf_lo(h[e]), b - bf_hi(h[e]));
+    float x = e < 2 ? a[2 * e] : b[2 * e - 4], y = e < 2 ? a[2 * e + 1] : b[2 * e - 3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      q[k][e] = pk_bf16(x, y);
+      x -= bf_lo(q[k][e]);
+      y -= bf_hi(q[k][e]);
+    }
   }
-  hi = __builtin_bit_cast(bf16x8, h);
-  lo = __builtin_bit_cast(bf16x8, l);
+  return Parts{{__builtin_bit_cast(bf16x8, q[0]), __builtin_bit_cast(bf16x8, q[1]), __builtin_bit_cast(bf16x8, q[2])}};
+}
+// w[e] * v[e] in FP32, in three parts
+__device__ __forceinline__ Parts split_scaled(bf16x8 v, f32x4 wa, f32x4 wb) {
+  const u32x4 u = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    wa[2 * e] *= bf_lo(u[e]);
+    wa[2 * e + 1] *= bf_hi(u[e]);
+    wb[2 * e] *= bf_lo(u[e + 2]);
+    wb[2 * e + 1] *= bf_hi(u[e + 2]);
+  }
+  return split(wa, wb);
 }
 
 // ------------------------------------------------------------------ XCD-aware block order

@@ -63,9 +63,9 @@ struct ScanBwdArgs {
   int64_t dx_ld, ddt_ld, dB_ld, dC_ld;
   float *dA, *dD, *dbias;   // [H]; dD, dbias may be nullptr
   float* piece_t;           // pieces' adjoints, as s.piece
-  // chunk states before (S) and adjoints after (T) every chunk: two bf16 planes (high and low parts)
-  // in matrix-operand order; chunk id = row / kChunk, or n_chunk_slots + seq for a sequence's first
-  uint16_t *cs, *ct;
+  // FP32 states before (S) and adjoints after (T) every chunk, in matrix-operand order; chunk id =
+  // row / kChunk, or n_chunk_slots + seq for a sequence's first
+  float *cs, *ct;
   int64_t n_chunk_slots;
   float* head_part;         // [chunk id, H, 3]: sums for dA, d(dt_bias), dD
   float* bc_part;           // [2, hsplit, rows, G, N] when hsplit > 1

@@ -11,10 +11,12 @@
 //   d(dt_t) = A dl_t + e^{L_Q - L_t} x_t . T B_t + sum_i K_it
 // The first kernel walks the states forward and the adjoints in reverse and stores both at every chunk;
 // then every chunk is independent: a block takes one chunk and the heads of one group (or a part of
-// them), keeps dB and dC in registers over its heads, and sums nothing through memory.  S and T are
-// stored as a high and a low bf16 part, already in matrix-operand order: with both parts the row
-// sums that feed d(dt) and dA keep FP32's weight (dC and dB share those products); dx, rounded to
-// bf16 in the end, takes the high part of T.  Z and G M are rounded to bf16 once, as operands.
+// them), keeps dB and dC in registers over its heads, and sums nothing through memory.  S and T are stored as
+// FP32, already in matrix-operand order, and enter their products as three bf16 parts: the row sums that feed
+// d(dt) and dA share the products of dC and dB and keep FP32's precision (packed sequences: d(dt) 2.4e-7 off and
+// dA 3e-7; with two parts 1e-6 and 1.4e-6 in 2% less time; with states kept in 16 bits of two bf16 planes 1.4e-6 and
+// 3.4e-6 in 9% less).  dx, rounded to bf16 in the end, takes the first part of T alone; Z and G M are rounded
+// to bf16 once, as operands.
 #include <type_traits>
 
 #include "ssm_state.h"
@@ -24,13 +26,10 @@ namespace cssm {
 template <int NT, int U, bool VEC, bool STORE>
 __global__ __launch_bounds__(128 * U, U > 2 || NT <= 128 ? 2 : 1) void ssm_states_kernel(StateArgs f, StateArgs r) {
   __shared__ StateShared<NT, U> sh;
-  if (blockIdx.y == 0) state_walk<NT, U, VEC, false, STORE>(f, sh);
-  else state_walk<NT, U, VEC, true, STORE>(r, sh);
+  if (blockIdx.y == 0) state_walk<NT, U, 3, VEC, false, STORE>(f, sh);
+  else state_walk<NT, U, 3, VEC, true, STORE>(r, sh);
 }
 
-__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {  // two bf16 products in FP32
-  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
-}
 // sum over the four rows of 16 lanes, in every lane: swapping the odd rows of a copy with the even rows of
 // another puts the rows' neighbours side by side, and the same for halves
 __device__ __forceinline__ float across16(float v) {
@@ -46,7 +45,10 @@ constexpr int kThreads = 256;
 // A block of 4 waves takes a chunk and walks the 64-column units of its heads.  A wave owns a quarter of the
 // columns n of dB and dC, and 16 columns of dX.  Two blocks share a CU (with the 256-column state tile, one), so that
 // one's loads from shared memory run beside the other's products: 8 waves in one block go through the phases
-// together, and took 600 us where two blocks take @@ us (16384 rows, 64 heads of 64 columns, N = 128).
+// together, and took a tenth longer.  16384 rows, 64 heads of 64 columns, N = 128: 650 us, in which it reads 1.5 GB
+// (2.3 TB/s, the states two thirds of them) and 9 products a head are made; the states' walks take 250 us, a
+// store of 1.07 GB at 4.3 TB/s.  C B^T is made
+// anew for every head: kept, its 12 registers spill, and the kernel takes a fifth longer.
 template <int NT, bool VEC>
 __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(ScanBwdArgs b) {
   constexpr int NBW = NT / 64;  // 16-column blocks n of a wave
@@ -91,7 +93,7 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
     for (int k = 0; k < KB; ++k) dC[nb][k] = dB[nb][k] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   TileRegs<64, kThreads> tx, ty;
-  u32x4 Sh[NBW][2], Sl[NBW][2], Th[NBW][2], Tl[NBW][2];
+  f32x4 S[NBW][2][2], T[NBW][2][2];  // [n block][p step of 32][half of it]
   auto load_rows = [&](int t) {
     const int h = h_lo + t / a.ptiles, p_first = t % a.ptiles * kPTile;
     const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
@@ -114,22 +116,22 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
     ssteps[t % 3][1][lane] = ex2((float)L);
     ssteps[t % 3][2][63 - lane] = ex2((float)dpp0<0x138, 0xf>(back));  // the rows after this one
   };
-  // one of the chunk's states of head t: high and low parts
-  auto load_states = [&](int t, const uint16_t* from, u32x4(&hi)[NBW][2], u32x4(&lo)[NBW][2]) {
-    const int n = t < tiles ? 2 * 64 * NT : 0;
-    const Rows r(from + (id * hp + h_lo * a.ptiles + t) * (2 * 64 * NT), n, 1, n, 2);
+  // one of the chunk's states of head t
+  auto load_states = [&](int t, const float* from, f32x4(&v)[NBW][2][2]) {
+    const int n = t < tiles ? 64 * NT : 0;
+    const Rows r(from + (id * hp + h_lo * a.ptiles + t) * (64 * NT), n, 1, n, 4);
 #pragma unroll
     for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const int at = (((nw / 16 + nb) * 2 + ks) * 64 + lane) * 16;
-        hi[nb][ks] = __builtin_amdgcn_raw_buffer_load_b128(r.r, at, 0, 0);
-        lo[nb][ks] = __builtin_amdgcn_raw_buffer_load_b128(r.r, at + 64 * NT * 2, 0, 0);
-      }
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          v[nb][ks][q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+              r.r, ((q * (NT / 16) + nw / 16 + nb) * 2 + ks) * 1024 + lane * 16, 0, 0));
   };
   load_rows(0);
-  load_states(0, b.ct, Th, Tl);
-  load_states(0, b.cs, Sh, Sl);
+  load_states(0, b.ct, T);
+  load_states(0, b.cs, S);
   load_raw(0);
   if (w == 3) decays(0);
   load_raw(1);
@@ -141,20 +143,6 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
     store_tile(sC, t);
   }
   __syncthreads();
-  // G^T blocks of this wave: rows i in the lanes, columns j in the registers
-  f32x4 G[3];
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    G[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-    int ib, jb;
-    lower_block(w + 4 * k, ib, jb);
-    if (w + 4 * k < 10) {
-#pragma unroll
-      for (int ks = 0; ks < NT / 32; ++ks)
-        G[k] = mma(op_straight<NT>(sB, 16 * jb, 32 * ks, lane), op_straight<NT>(sC, 16 * ib, 32 * ks, lane), G[k]);
-    }
-  }
-
   float dl_sum = 0.f, q_sum = 0.f, trace_sum = 0.f;  // wave 2: over a head's column tiles
   // lane = row: the gradients of head t's decays and steps, by wave 2
   auto finish = [&](const int t) {
@@ -175,9 +163,10 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
       col += k >= (lane >> 4) ? c : 0.f;
       trace += s_trace[t & 1][k];
     }
-    const float from_later = rint + (row - d * col);
-    const float suffix = __shfl(wave_prefix(__shfl(from_later, 63 - lane)), 63 - lane);  // rows >= this one
-    const float before = dpp0<0x138, 0xf>(wave_prefix(d * u));                            // rows < this one
+    // the rows' and the columns' sums cancel: added in 64 bits (d(dt_bias) 1.0e-6 off instead of 1.4e-6, no time)
+    const double from_later = (double)rint + ((double)row - (double)d * col);
+    const float suffix = (float)__shfl(wave_prefix(__shfl(from_later, 63 - lane)), 63 - lane);  // rows >= this one
+    const float before = (float)dpp0<0x138, 0xf>(wave_prefix((double)d * u));                   // rows < this one
     dl_sum += se[63] * dots + suffix + before;
     q_sum += col + s_diag[t & 1][lane] + u;
     trace_sum += trace;
@@ -213,8 +202,11 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const int n = nw + 16 * nb + i;
-        *reinterpret_cast<u32x2*>(sR + at<64>(n, 32 * ks + 4 * g)) = u32x2{Th[nb][ks].x, Th[nb][ks].y};
-        *reinterpret_cast<u32x2*>(sR + at<64>(n, 32 * ks + 16 + 4 * g)) = u32x2{Th[nb][ks].z, Th[nb][ks].w};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const f32x4 v = T[nb][ks][q];
+          *reinterpret_cast<u32x2*>(sR + at<64>(n, 32 * ks + 16 * q + 4 * g)) = u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+        }
       }
     phase();
     __syncthreads();
@@ -237,7 +229,10 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
 
     // score block (ib, jb), G its C B^T; the diagonal's K is in its row's and its column's sum alike and is
     // kept out of both
-    auto scores = [&](const int ib, const int jb, const f32x4& G) {
+    auto scores = [&](const int ib, const int jb) {
+      f32x4 G = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ks = 0; ks < NT / 32; ++ks) G = mma(op_straight<NT>(sB, 16 * jb, 32 * ks, lane), op_straight<NT>(sC, 16 * ib, 32 * ks, lane), G);
       f32x4 W = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) W = mma(op_straight<64>(sx, 16 * jb, 32 * ks, lane), op_straight<64>(sy, 16 * ib, 32 * ks, lane), W);
@@ -274,7 +269,7 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
     for (int k = 0; k < 3; ++k) {
       int ib, jb;
       lower_block(w + 4 * k, ib, jb);
-      if (w + 4 * k < 10) scores(ib, jb, G[k]);
+      if (w + 4 * k < 10) scores(ib, jb);
     }
     if (w < 2) {  // blocks (0, 1), (2, 3): products over 32 columns read them
       *reinterpret_cast<u32x2*>(sZ + at<64>(32 * w + i, 32 * w + 16 + 4 * g)) = u32x2{0u, 0u};
@@ -294,73 +289,90 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          dot = dot2(Sh[nb][ks][e], Th[nb][ks][e], dot);
-          dot = dot2(Sh[nb][ks][e], Tl[nb][ks][e], dot);
-          dot = dot2(Sl[nb][ks][e], Th[nb][ks][e], dot);
-          dot = dot2(Sl[nb][ks][e], Tl[nb][ks][e], dot);
-        }
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(S[nb][ks][q][e], T[nb][ks][q][e], dot);
     dot = wave_sum(dot);
     if (lane == 0) s_dot[w] = dot;
     phase();
     // dC and the rows' sums with S
+    float rint[KB] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < KB; ++k) {
-      const int ib = k;
-      float rint = 0.f;
+    for (int nb = 0; nb < NBW; ++nb) {
+      f32x4 p[KB];
 #pragma unroll
-      for (int nb = 0; nb < NBW; ++nb) {
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      for (int ib = 0; ib < KB; ++ib) p[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
+      for (int ks = 0; ks < 2; ++ks) {
+        const Parts sp = split(S[nb][ks][0], S[nb][ks][1]);
+#pragma unroll
+        for (int ib = 0; ib < KB; ++ib) {
           const bf16x8 y = op_split<64>(sy, 16 * ib, 32 * ks, lane);
-          v = mma(__builtin_bit_cast(bf16x8, Sh[nb][ks]), y, v);
-          v = mma(__builtin_bit_cast(bf16x8, Sl[nb][ks]), y, v);
+#pragma unroll
+          for (int q = 0; q < 3; ++q) p[ib] = mma(sp.p[q], y, p[ib]);
         }
+        phase();
+      }
+#pragma unroll
+      for (int ib = 0; ib < KB; ++ib) {
+        f32x4 v = p[ib];
         v *= se[16 * ib + i];
         const u32x2 c = *reinterpret_cast<const u32x2*>(sC + at<NT>(16 * ib + i, nw + 16 * nb + 4 * g));
-        rint += v[0] * bf_lo(c.x) + v[1] * bf_hi(c.x) + v[2] * bf_lo(c.y) + v[3] * bf_hi(c.y);
-        f32x4 acc = dC[nb][k] + v;
+        rint[ib] += v[0] * bf_lo(c.x) + v[1] * bf_hi(c.x) + v[2] * bf_lo(c.y) + v[3] * bf_hi(c.y);
+        f32x4 acc = dC[nb][ib] + v;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
           if (ks <= ib / 2) acc = mma(op_cols<NT>(sB, 32 * ks, nw + 16 * nb, lane), op_split<64>(sZ, 16 * ib, 32 * ks, lane), acc);
-        dC[nb][k] = acc;
+        dC[nb][ib] = acc;
+        phase();
       }
-      rint = across16(rint);
-      if (g == 0) s_rint[w][16 * ib + i] = rint;
-      phase();
+    }
+#pragma unroll
+    for (int ib = 0; ib < KB; ++ib) {
+      const float v = across16(rint[ib]);
+      if (g == 0) s_rint[w][16 * ib + i] = v;
     }
     phase();
-    load_states(t + 1, b.cs, Sh, Sl);
+    load_states(t + 1, b.cs, S);
     phase();
     // dB and the rows' sums with T
+    float u[KB] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < KB; ++k) {
-      const int jb = k;
-      float u = 0.f;
+    for (int nb = 0; nb < NBW; ++nb) {
+      f32x4 p[KB];
 #pragma unroll
-      for (int nb = 0; nb < NBW; ++nb) {
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      for (int jb = 0; jb < KB; ++jb) p[jb] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
+      for (int ks = 0; ks < 2; ++ks) {
+        const Parts tp = split(T[nb][ks][0], T[nb][ks][1]);
+#pragma unroll
+        for (int jb = 0; jb < KB; ++jb) {
           const bf16x8 x = op_split<64>(sx, 16 * jb, 32 * ks, lane);
-          v = mma(__builtin_bit_cast(bf16x8, Th[nb][ks]), x, v);
-          v = mma(__builtin_bit_cast(bf16x8, Tl[nb][ks]), x, v);
+#pragma unroll
+          for (int q = 0; q < 3; ++q) p[jb] = mma(tp.p[q], x, p[jb]);
         }
+        phase();
+      }
+#pragma unroll
+      for (int jb = 0; jb < KB; ++jb) {
+        f32x4 v = p[jb];
         v *= sr[16 * jb + i];
         const u32x2 c = *reinterpret_cast<const u32x2*>(sB + at<NT>(16 * jb + i, nw + 16 * nb + 4 * g));
-        u += v[0] * bf_lo(c.x) + v[1] * bf_hi(c.x) + v[2] * bf_lo(c.y) + v[3] * bf_hi(c.y);
-        f32x4 acc = dB[nb][k] + v * sd[16 * jb + i];
+        u[jb] += v[0] * bf_lo(c.x) + v[1] * bf_hi(c.x) + v[2] * bf_lo(c.y) + v[3] * bf_hi(c.y);
+        f32x4 acc = dB[nb][jb] + v * sd[16 * jb + i];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
           if (ks >= jb / 2) acc = mma(op_cols<NT>(sC, 32 * ks, nw + 16 * nb, lane), op_cols<64>(sZ, 32 * ks, 16 * jb, lane), acc);
-        dB[nb][k] = acc;
+        dB[nb][jb] = acc;
+        phase();
       }
-      u = across16(u);
-      if (g == 0) s_u[w][16 * jb + i] = u;
-      phase();
     }
-    load_states(t + 1, b.ct, Th, Tl);
+#pragma unroll
+    for (int jb = 0; jb < KB; ++jb) {
+      const float v = across16(u[jb]);
+      if (g == 0) s_u[w][16 * jb + i] = v;
+    }
+    load_states(t + 1, b.ct, T);
     phase();
 
 #pragma unroll

@@ -5,9 +5,10 @@
 //
 // with L the inclusive prefix sums of l_t = dt_t A over the chunk.  States are FP32 results held in
 // registers over the whole walk; the weights multiply u in FP32, and the product enters the matrix
-// instructions as a high and a low bf16 part, so a state is right to about 2^-16 of its terms (one bf16
-// part would leave 2^-8).  Decays to the chunk's end are summed from the end, so that the last tokens of
-// a fast-decaying chunk keep exact weights.
+// instructions as PARTS bf16 parts.  Backward, three: a state has FP32's precision (a gradient of initial states
+// was 2.5e-6 off with two, 1.4e-7 with three, for 1% of the time).  The forward scan's states take two, 2^-16 of a
+// term.  Decays to the chunk's end are summed from the end, so that the last tokens of a fast-decaying chunk
+// keep exact weights.
 #pragma once
 
 #include "ssm_device.h"
@@ -22,8 +23,8 @@ struct StateArgs {
   const float* start;      // state before the walk [slot or seq, H, P, N], nullptr: zeros
   float* end;              // reverse: state after the walk at the sequence's start, or nullptr
   float* piece;            // [item, H * ptiles, 64, NT]
-  uint16_t* store;         // chunk states (STORE), planes of `plane` elements
-  int64_t n_chunk_slots, plane;
+  float* store;            // chunk states (STORE)
+  int64_t n_chunk_slots;
 };
 
 // Decays and step sizes of one chunk, computed by one wave with a row a lane from the raw steps, which
@@ -111,7 +112,7 @@ struct StateShared {
   __align__(16) float w[2][U][64];  // weights of this chunk and the next one, by unit
   float total[2][U];
 };
-template <int NT, int U, bool VEC, bool REV, bool STORE>
+template <int NT, int U, int PARTS, bool VEC, bool REV, bool STORE>
 __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U>& sh) {
   constexpr int T = 128 * U, WU = 2;  // threads, and waves a unit
   constexpr int NB = NT / 16;         // 16-column blocks of the state, with two 16-row blocks a wave
@@ -211,22 +212,15 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
     if (w == 0) weights(rows, buf ^ 1);
     after = step_chunk(after, after_rows);
     raw = raw_step(a, after.c0, after_rows, my, me.h);
-    if constexpr (STORE) {  // operand order: [n block of 16][p step of 32][lane] 16 bytes, high plane then low
+    if constexpr (STORE) {  // operand order: [row half][n block of 16][p step of 32][lane] four FP32 values
       const int64_t id = here == pc.s ? k.n_chunk_slots + pc.seq : here >> 6;
-      const Rows dst(k.store + (id * hp + me.tile) * (2 * 64 * NT), 2 * 64 * NT, 1, me.pn ? 2 * 64 * NT : 0, 2);
+      const Rows dst(k.store + (id * hp + me.tile) * (64 * NT), 64 * NT, 1, me.pn ? 64 * NT : 0, 4);
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        u32x4 hi, lo;
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = S[e >> 1][nb][2 * (e & 1)], y = S[e >> 1][nb][2 * (e & 1) + 1];
-          hi[e] = pk_bf16(x, y);
-          lo[e] = pk_bf16(x - bf_lo(hi[e]), y - bf_hi(hi[e]));
-        }
-        const int o = ((nb * 2 + w) * 64 + lane) * 16;
-        __builtin_amdgcn_raw_buffer_store_b128(hi, dst.r, o, 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(lo, dst.r, o + 64 * NT * 2, 0, 0);
-      }
+        for (int pb = 0; pb < 2; ++pb)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[pb][nb]), dst.r,
+                                                 ((pb * (NT / 16) + nb) * 2 + w) * 1024 + lane * 16, 0, 0);
     }
     const float total = sh.total[buf][un];
     log_total += total;
@@ -239,17 +233,16 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
     for (int ks = 0; ks < 2; ++ks) {
       const f32x4 wa = *reinterpret_cast<const f32x4*>(sw + 32 * ks + 4 * g);
       const f32x4 wb = *reinterpret_cast<const f32x4*>(sw + 32 * ks + 16 + 4 * g);
-      bf16x8 hi[2], lo[2];
+      Parts x[2];
 #pragma unroll
-      for (int pb = 0; pb < 2; ++pb) split_scaled(op_cols<64, 16>(su, 32 * ks, p0 + 16 * pb, lane), wa, wb, hi[pb], lo[pb]);
+      for (int pb = 0; pb < 2; ++pb) x[pb] = split_scaled(op_cols<64, 16>(su, 32 * ks, p0 + 16 * pb, lane), wa, wb);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const bf16x8 b = op_cols<NT, 16>(sv, 32 * ks, 16 * nb, lane);
 #pragma unroll
-        for (int pb = 0; pb < 2; ++pb) {
-          S[pb][nb] = mma(hi[pb], b, S[pb][nb]);
-          S[pb][nb] = mma(lo[pb], b, S[pb][nb]);
-        }
+        for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+          for (int pb = 0; pb < 2; ++pb) S[pb][nb] = mma(x[pb].p[q], b, S[pb][nb]);
       }
     }
     if (rows == 0) break;
@@ -282,7 +275,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
 template <int NT, int U, bool VEC>
 __global__ __launch_bounds__(128 * U, U > 2 || NT <= 128 ? 2 : 1) void ssm_state_local_kernel(StateArgs k) {
   __shared__ StateShared<NT, U> sh;
-  state_walk<NT, U, VEC, false, false>(k, sh);
+  state_walk<NT, U, 2, VEC, false, false>(k, sh);
 }
 
 // Local end states of a sequence's pieces -> start states, in place, in the order of the walk:
