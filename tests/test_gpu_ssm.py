@@ -3,7 +3,7 @@
 Tolerances count roundings.  bf16 rounds by at most 2^-8 of a value.  y: the result, and the terms'
 operands (the state for C S, the decayed scores) once each: 2^-8 |y| + 2^-8 (1 + 2^-6) times the sum of
 the terms' magnitudes.  dx and dB, dC the same with their operands.  States, ddt, dA, d(dt_bias) and
-d(initial state) only see products whose operands are two bf16 parts (2^-16 of a term), FP32 sums and
+d(initial state) only see products whose operands are two or three bf16 parts (2^-16 of a term or less), FP32 sums and
 decays whose exponents are FP32 sums: 2^-14 of the sum of magnitudes (two such factors and the
 exponents); dD sums exact products in FP32: 2^-18 over these lengths.
 """
