@@ -63,14 +63,27 @@ bool clash(const Span (&outs)[NO], const Span (&ins)[NI]) {
 // Sequences are cut into pieces where whole ones give too few blocks, or, with offsets (the host does not
 // know the lengths), where one could be long against the rest; the cost is a first walk for the pieces' states
 // and a join.
-constexpr int64_t kWantBlocks = 256;
-constexpr int kMinSeg = 7;
-int piece_log2(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows) {
+//
+// Forward (64 heads of 64 columns, N = 128), `want` blocks: 4 sequences of 4096 rows 191 us with 256, 312 with
+// 128, 230 with 512, 411 whole; 2048 rows of one sequence 60 us with 256, 69 with 128, 206 whole; 64 mixed
+// prompts 437 us with pieces for 512 blocks, 467 for 256, 423 whole (but only because none is long).
+//
+// Backward: the walk is bound by its stores, both directions are one launch, and few blocks reach that bound.
+// 4 sequences of 4096 rows (64 walks a direction) 908 us whole, 967 for 128, 985 for 256; 2 sequences of 8192 1129
+// whole, 967 for 128; one of 16384 1516 whole, 1145 for 64, 975 for 128, 998 for 256.  Nine mixed sequences in 2777 rows
+// (24 heads, 54 walks) 124 us whole, 129 with pieces of 1024 rows, 161 with 512; one sequence of 2048 rows 248 us
+// whole, 260 with 1024 rows, 212 with 512.
+struct Cut {
+  int64_t whole, want;  // blocks that make equal sequences stay whole; blocks wanted of pieces
+  int least, least_few; // log2 of the fewest rows of a piece; where whole sequences make fewer than 32 blocks
+};
+constexpr Cut kCutFwd{256, 256, 7, 7}, kCutBwd{64, 128, 10, 9};
+int piece_log2(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows, const Cut& cut) {
   const int64_t sets = s->G * ceil_div(s->H / s->G * ceil_div(s->P, kPTile), kUnits);
-  const bool enough = nseq * sets >= kWantBlocks;
-  if (nseq <= 0 || (batch_rows && enough)) return 0;
-  int seg = kMinSeg;
-  while (((int64_t)1 << seg) * kWantBlocks * (enough ? 2 : 1) < rows * sets) ++seg;
+  if (nseq <= 0 || (batch_rows && nseq * sets >= cut.whole)) return 0;
+  const int64_t want = nseq * sets >= cut.want ? 2 * cut.want : cut.want;
+  int seg = nseq * sets < 32 ? cut.least_few : cut.least;
+  while (((int64_t)1 << seg) * want < rows * sets) ++seg;
   return ((int64_t)1 << seg) < (batch_rows ? rows / nseq : rows - nseq + 1) ? seg : 0;
 }
 
@@ -80,9 +93,9 @@ struct FwdPlan {
   int seg;
   int64_t n_slots, piece, decay, bytes;  // byte offsets into the workspace
 };
-FwdPlan plan_fwd(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows) {
+FwdPlan plan_fwd(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows, const Cut& cut = kCutFwd) {
   FwdPlan p{};
-  p.seg = piece_log2(s, rows, nseq, batch_rows);
+  p.seg = piece_log2(s, rows, nseq, batch_rows, cut);
   if (!p.seg) return p;
   p.n_slots = batch_rows ? nseq * (ceil_div(rows / nseq, (int64_t)1 << p.seg) - 1) : ceil_div(rows, (int64_t)1 << p.seg);
   const int64_t items = p.n_slots + nseq, hp = s->H * ceil_div(s->P, kPTile);
@@ -97,11 +110,12 @@ struct BwdPlan {
   int hsplit;
 };
 // Blocks of the chunk kernel: one a chunk and group; heads of a group go to several blocks (FP32
-// parts of dB and dC, added by another kernel) only where that many blocks would leave CUs idle.
+// parts of dB and dC, added by another kernel) only where that many blocks would leave CUs idle
+// (2777 rows, 24 heads in 2 groups: 150 us with 256, 152 with 512, 168 with 1024).
 constexpr int64_t kWantChunkBlocks = 512;
 BwdPlan plan_bwd(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows) {
   BwdPlan p{};
-  p.f = plan_fwd(s, rows, nseq, batch_rows);
+  p.f = plan_fwd(s, rows, nseq, batch_rows, kCutBwd);
   p.n_chunk_slots = ceil_div(rows, kChunk);
   p.ids = p.n_chunk_slots + nseq;
   const int64_t hp = s->H * ceil_div(s->P, kPTile), tile = 64 * state_tile(s->N), chunks = ceil_div(rows, kChunk);
