@@ -139,6 +139,14 @@ def test_long_sequences_in_pieces(lens):
     check_bwd(p, p.S0, p.dS)
 
 
+@pytest.mark.parametrize("N", [40, 200])
+def test_batch_rows_in_pieces(N):
+    print(f"[gpu] scan batch rows in pieces N={N}", flush=True)
+    p = Problem([1100, 1100], 2, 40, 1, N, seed=6, step=-3.0)
+    check_fwd(p, seqlen=1100)
+    check_bwd(p, None, None, seqlen=1100)
+
+
 @pytest.mark.parametrize("decay,step", [(60.0, 2.0), (0.001, -6.0), (4.0, 25.0)])
 def test_fast_and_slow_decay(decay, step):
     """Decays that leave nothing of a chunk's start, that keep everything, and softplus past its bend."""
