@@ -149,24 +149,35 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
     const int h = h_lo + t / a.ptiles, ptile = t % a.ptiles;
     const float *sd = ssteps[t % 3][0], *se = ssteps[t % 3][1];
     const float d = sd[lane];
-    float rint = 0.f, u = 0.f, row = 0.f, col = 0.f, dots = 0.f, trace = 0.f;
+    float rint = 0.f, u = 0.f, col = 0.f, dots = 0.f, trace = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       dots += s_dot[k];
       rint += s_rint[k][lane];
       u += s_u[k][lane];
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {  // blocks up to the diagonal
-      const float r = s_row[t & 1][k][lane], c = s_col[t & 1][k][lane];
-      row += k <= (lane >> 4) ? r : 0.f;
-      col += k >= (lane >> 4) ? c : 0.f;
       trace += s_trace[t & 1][k];
     }
-    // the rows' and the columns' sums cancel: added in 64 bits (d(dt_bias) 1.0e-6 off instead of 1.4e-6, no time)
-    const double from_later = (double)rint + ((double)row - (double)d * col);
-    const float suffix = (float)__shfl(wave_prefix(__shfl(from_later, 63 - lane)), 63 - lane);  // rows >= this one
-    const float before = (float)dpp0<0x138, 0xf>(wave_prefix((double)d * u));                   // rows < this one
+    // dl of row r takes K_ij d_j of all i >= r > j.  Differences of the 64 rows' and columns' sums would lose it in
+    // what cancels; by blocks of 16, with r in block m: rows i >= r of the blocks left of the diagonal's, columns j < r
+    // of those below it, all of the blocks below and left of it, and only in the diagonal's a difference
+    const int m = lane >> 4;
+    float left = 0.f, below = 0.f, on = 0.f, corner[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float r = s_row[t & 1][k][lane], c = s_col[t & 1][k][lane];
+      left += k < m ? r : 0.f;
+      below += k > m ? d * c : 0.f;
+      on += k == m ? r - d * c : 0.f;
+      col += k >= m ? c : 0.f;
+      if (k == 0) corner[0] = m >= 2 ? r : 0.f;
+      if (k <= 1) corner[1] += m == 3 ? r : 0.f;
+    }
+    const float corner1 = wave_sum(corner[0]), corner2 = wave_sum(corner[1]);
+    const float rows_on = dpp0<0x140, 0xf>(row16_sum(dpp0<0x140, 0xf>(left + on)));  // mirrored: rows >= this one
+    const float columns = dpp0<0x111, 0xf>(row16_sum(below));
+    const float inside = rows_on + columns + (m == 1 ? corner1 : m == 2 ? corner2 : 0.f);
+    const float suffix = __shfl(wave_prefix(__shfl(rint, 63 - lane)), 63 - lane) + inside;  // rows >= this one
+    const float before = dpp0<0x138, 0xf>(wave_prefix(d * u));                              // rows < this one
     dl_sum += se[63] * dots + suffix + before;
     q_sum += col + s_diag[t & 1][lane] + u;
     trace_sum += trace;
