@@ -7,8 +7,8 @@
 //   du = (d - n mean(d n)) / rms(u),   dw = sum over rows of (gradient of w n) n.
 //
 // These are streams: one pass over the rows, each value read and written once, all arithmetic FP32.
-// T threads share a row's group and keep it in registers, V pieces of 8 channels a thread (one wave up to
-// 2048 channels, then 256 or 1024 threads), the bf16 inputs packed as they are in memory: with FP32 copies of x, z and dy
+// T threads share a row's group and keep it in registers, V pieces of 8 channels a thread (64 up to
+// 512 channels, 1024 from 8192), the bf16 inputs packed as they are in memory: with FP32 copies of x, z and dy
 // the gated backward had 262 registers and 2 waves a SIMD, too few to cover its loads (302 us at
 // 16384 x 4096 in groups of 1024, against 128 us).  A thread keeps its channels' weights (and, backward, its dw sums) in
 // registers over all the rows it visits; the sums go to one partial row per row split, and a second kernel adds

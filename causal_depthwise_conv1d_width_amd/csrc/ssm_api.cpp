@@ -386,7 +386,7 @@ int gated_norm_fwd(int64_t rows, int64_t d, int64_t group, const void* x, int64_
   a.x_ld = x_ld, a.z_ld = z_ld, a.y_ld = y_ld;
   a.w = w, a.w_f32 = w_dtype == CONV1D_F32, a.norm_first = norm_before_gate != 0;
   a.rows = rows, a.groups = d / group, a.group = group, a.eps = eps;
-  a.parts = norm_fwd_parts(rows, a.groups, group);
+  a.parts = norm_fwd_parts(rows, a.groups, group, kGatedFwdWaves);
   return launch_gated_fwd(a, stream) == hipSuccess ? CONV1D_OK : CONV1D_EHIP;
 }
 
@@ -434,7 +434,7 @@ int residual_norm_fwd(int64_t rows, int64_t d, const void* x, int64_t x_ld, cons
   a.x_ld = x_ld, a.r_ld = residual_ld, a.y_ld = y_ld, a.ro_ld = residual_out_ld;
   a.w = w, a.w_f32 = w_dtype == CONV1D_F32, a.r_f32 = residual_dtype == CONV1D_F32;
   a.rows = rows, a.groups = 1, a.group = d, a.eps = eps, a.scale = scale;
-  a.parts = norm_fwd_parts(rows, 1, d);
+  a.parts = norm_fwd_parts(rows, 1, d, kResidualFwdWaves);
   return launch_residual_fwd(a, stream) == hipSuccess ? CONV1D_OK : CONV1D_EHIP;
 }
 

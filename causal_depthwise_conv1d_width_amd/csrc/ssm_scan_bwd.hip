@@ -496,10 +496,6 @@ static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
   f.start = a.init, f.piece = a.piece, f.store = b.cs;
   r.start = b.dfin, r.piece = b.piece_t, r.store = b.ct, r.end = b.dinit;
   f.n_chunk_slots = r.n_chunk_slots = b.n_chunk_slots;
-  if (a.q.nseq == 0) {  // no sequences: the parameters' gradients are zero
-    ssm_head_reduce_kernel<<<dim3((uint32_t)a.H), 256, 0, s>>>(b, 0);
-    return hipGetLastError();
-  }
   const dim3 walk((uint32_t)unit_blocks(items, a.H, a.G, a.ptiles, U), 2);
   if (a.seg > 0) {
     const dim3 join = join_grid(a, NT);
@@ -517,8 +513,18 @@ static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The walks take two units a block where four would leave half of the CUs without one (4 sequences of 4096 rows, 64
+// heads: 872 us against 910, 1024 rows of 2 sequences, 8 heads: 62 against 67); with more blocks four are faster, whose
+// rows of B and C serve more units (32 sequences, 16384 rows: 1074 us against 1106).
 template <int NT, bool VEC>
 static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
+  const ScanArgs& a = b.s;
+  if (a.q.nseq == 0) {  // no sequences: the parameters' gradients are zero
+    ssm_head_reduce_kernel<<<dim3((uint32_t)a.H), 256, 0, s>>>(b, 0);
+    return hipGetLastError();
+  }
+  if constexpr (NT <= 128)
+    if (2 * unit_blocks(a.n_slots + a.q.nseq, a.H, a.G, a.ptiles, kUnits) <= 128) return launch<NT, 2, VEC>(b, s);
   return launch<NT, kUnits, VEC>(b, s);
 }
 

@@ -2,13 +2,15 @@
 //
 //   S = e^{dt A} S + dt x B^T,   y = S C + D x
 // A stream over the states (read and written once): 8 bytes for 5 operations, bound by memory.  A lane
-// holds four columns n of a row p; LN lanes (a power of two, up to 64) share a row, and a wave keeps 8
+// holds four columns n of a row p; LN lanes (a power of two, up to 64) share a row, and a wave keeps kStepRows
 // rows a lane in flight, so the whole of a small call is one memory round trip after the slot's.
 #include "ssm_device.h"
 
 namespace cssm {
 
-constexpr int kStepRows = 8;  // rows a lane holds
+// rows a lane holds: 64 sequences of 64 heads of 64 rows, N = 128, 50.3 us with 4 (5.4 TB/s), 52.3 with 8, 58 with 2,
+// 56 with 16
+constexpr int kStepRows = 4;
 
 template <int LN, bool VEC>
 __global__ __launch_bounds__(256) void ssm_step_kernel(StepArgs a) {
