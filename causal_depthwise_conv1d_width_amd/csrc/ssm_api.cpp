@@ -70,19 +70,19 @@ bool clash(const Span (&outs)[NO], const Span (&ins)[NI]) {
 //
 // Backward: the walk is bound by its stores, both directions are one launch, and few blocks reach that bound.
 // 4 sequences of 4096 rows (64 walks a direction) 908 us whole, 967 for 128, 985 for 256; 2 sequences of 8192 1129
-// whole, 967 for 128; one of 16384 1516 whole, 1145 for 64, 975 for 128, 998 for 256.  Nine mixed sequences in 2777 rows
-// (24 heads, 54 walks) 124 us whole, 129 with pieces of 1024 rows, 161 with 512; one sequence of 2048 rows 248 us
-// whole, 260 with 1024 rows, 212 with 512.
+// whole, 967 for 128; one of 16384 1516 whole, 1145 for 64, 975 for 128, 998 for 256.  Mixed sequences, means over
+// six draws: nine in 2777 rows (24 heads) 142 us with pieces of at least 256 rows, 155 with 512, 162 with 1024 (128 to
+// 189, by the longest); six in 8192 rows 323, 322 and 352 us.
 struct Cut {
   int64_t whole, want;  // blocks that make equal sequences stay whole; blocks wanted of pieces
-  int least, least_few; // log2 of the fewest rows of a piece; where whole sequences make fewer than 32 blocks
+  int least;            // log2 of the fewest rows of a piece
 };
-constexpr Cut kCutFwd{256, 256, 7, 7}, kCutBwd{64, 128, 10, 9};
+constexpr Cut kCutFwd{256, 256, 7}, kCutBwd{64, 128, 8};
 int piece_log2(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows, const Cut& cut) {
   const int64_t sets = s->G * ceil_div(s->H / s->G * ceil_div(s->P, kPTile), kUnits);
   if (nseq <= 0 || (batch_rows && nseq * sets >= cut.whole)) return 0;
   const int64_t want = nseq * sets >= cut.want ? 2 * cut.want : cut.want;
-  int seg = nseq * sets < 32 ? cut.least_few : cut.least;
+  int seg = cut.least;
   while (((int64_t)1 << seg) * want < rows * sets) ++seg;
   return ((int64_t)1 << seg) < (batch_rows ? rows / nseq : rows - nseq + 1) ? seg : 0;
 }

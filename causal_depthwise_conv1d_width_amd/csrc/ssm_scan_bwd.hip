@@ -513,9 +513,10 @@ static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The walks take two units a block where four would leave half of the CUs without one (4 sequences of 4096 rows, 64
-// heads: 872 us against 910, 1024 rows of 2 sequences, 8 heads: 62 against 67); with more blocks four are faster, whose
-// rows of B and C serve more units (32 sequences, 16384 rows: 1074 us against 1106).
+// The walks take two units a block where four would leave many CUs without one (4 sequences of 4096 rows, 64
+// heads: 872 us against 910; nine mixed sequences in 2777 rows, 24 heads: 153 against 158; 1024 rows of 2
+// sequences, 8 heads: 62 against 67); with more blocks four are faster, whose rows of B and C serve more units (32
+// sequences, 16384 rows: 1074 us against 1106).
 template <int NT, bool VEC>
 static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
   const ScanArgs& a = b.s;
@@ -524,7 +525,7 @@ static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
     return hipGetLastError();
   }
   if constexpr (NT <= 128)
-    if (2 * unit_blocks(a.n_slots + a.q.nseq, a.H, a.G, a.ptiles, kUnits) <= 128) return launch<NT, 2, VEC>(b, s);
+    if (2 * unit_blocks(a.n_slots + a.q.nseq, a.H, a.G, a.ptiles, kUnits) <= 192) return launch<NT, 2, VEC>(b, s);
   return launch<NT, kUnits, VEC>(b, s);
 }
 
