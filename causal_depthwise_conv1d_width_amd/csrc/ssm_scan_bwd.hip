@@ -45,10 +45,10 @@ constexpr int kThreads = 256;
 // A block of 4 waves takes a chunk and walks the 64-column units of its heads.  A wave owns a quarter of the
 // columns n of dB and dC, and 16 columns of dX.  Two blocks share a CU (with the 256-column state tile, one), so that
 // one's loads from shared memory run beside the other's products: 8 waves in one block go through the phases
-// together, and took a tenth longer.  16384 rows, 64 heads of 64 columns, N = 128: 650 us, in which it reads 1.5 GB
-// (2.3 TB/s, the states two thirds of them) and 9 products a head are made; the states' walks take 250 us, a
-// store of 1.07 GB at 4.3 TB/s.  C B^T is made
-// anew for every head: kept, its 12 registers spill, and the kernel takes a fifth longer.
+// together, and took a tenth longer.  16384 rows, 64 heads of 64 columns, N = 128: 590 us, in which it reads 1.5 GB
+// (2.5 TB/s, the states two thirds of them) and 9 products a head are made; the states' walks take 290 us, a
+// store of 1.07 GB at 3.7 TB/s.  C B^T is made anew for every head: kept, its 12 registers spill, and the kernel
+// takes a fifth longer.
 template <int NT, bool VEC>
 __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kernel(ScanBwdArgs b) {
   constexpr int NBW = NT / 64;  // 16-column blocks n of a wave
