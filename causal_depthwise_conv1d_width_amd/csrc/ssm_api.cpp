@@ -106,7 +106,7 @@ FwdPlan plan_fwd(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows
 
 struct BwdPlan {
   FwdPlan f;
-  int64_t ids, n_chunk_slots, piece_t, cs, ct, head, bc, bytes;
+  int64_t ids, n_chunk_slots, piece_t, piece_t_decay, cs, ct, head, bc, bytes;
   int hsplit;
 };
 // Blocks of the chunk kernel: one a chunk and group; heads of a group go to several blocks (FP32
@@ -127,6 +127,8 @@ BwdPlan plan_bwd(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows
   int64_t at = align_up(p.f.bytes);
   p.piece_t = at;
   if (p.f.seg) at += align_up((p.f.n_slots + nseq) * hp * tile * 4);
+  p.piece_t_decay = at;
+  if (p.f.seg) at += align_up((p.f.n_slots + nseq) * s->H * 4);
   p.cs = at;
   at += align_up(p.ids * hp * tile * 4);
   p.ct = at;
@@ -329,6 +331,7 @@ int ssm_scan_bwd(const ssm_shape* shape, int64_t rows, const void* dy, int64_t d
     b.dB = static_cast<uint16_t*>(dB), b.dB_ld = dB_ld;
     b.dC = static_cast<uint16_t*>(dC), b.dC_ld = dC_ld;
     b.piece_t = reinterpret_cast<float*>(w + p.piece_t);
+    b.piece_t_decay = reinterpret_cast<float*>(w + p.piece_t_decay);
     b.cs = reinterpret_cast<float*>(w + p.cs);
     b.ct = reinterpret_cast<float*>(w + p.ct);
     b.n_chunk_slots = p.n_chunk_slots;

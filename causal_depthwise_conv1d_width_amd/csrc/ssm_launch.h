@@ -62,7 +62,9 @@ struct ScanBwdArgs {
   uint16_t *dB, *dC;
   int64_t dx_ld, ddt_ld, dB_ld, dC_ld;
   float *dA, *dD, *dbias;   // [H]; dD, dbias may be nullptr
-  float* piece_t;           // pieces' adjoints, as s.piece
+  // pieces' adjoints and log2 decays, as s.piece and s.piece_decay: both walks run in one launch and sum a
+  // piece's decays in their own order, so each has its own
+  float *piece_t, *piece_t_decay;
   // FP32 states before (S) and adjoints after (T) every chunk, in matrix-operand order; chunk id =
   // row / kChunk, or n_chunk_slots + seq for a sequence's first
   float *cs, *ct;

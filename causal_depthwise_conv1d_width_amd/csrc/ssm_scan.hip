@@ -273,6 +273,7 @@ static hipError_t launch(const ScanArgs& a, hipStream_t s) {
     k.v_ld = a.B_ld;
     k.start = a.init;
     k.piece = a.piece;
+    k.decay = a.piece_decay;
     const dim3 walk((uint32_t)unit_blocks(items, a.H, a.G, a.ptiles, kUnits));
     ssm_state_local_kernel<NT, kUnits, VEC><<<walk, 128 * kUnits, 0, s>>>(k);
     ssm_join_kernel<NT, false><<<join_grid(a, NT), 1024, 0, s>>>(k);

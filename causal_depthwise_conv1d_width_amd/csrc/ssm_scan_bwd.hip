@@ -495,6 +495,7 @@ static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
   r.u = b.dy, r.u_ld = b.dy_ld, r.v = a.C, r.v_ld = a.C_ld;
   f.start = a.init, f.piece = a.piece, f.store = b.cs;
   r.start = b.dfin, r.piece = b.piece_t, r.store = b.ct, r.end = b.dinit;
+  f.decay = a.piece_decay, r.decay = b.piece_t_decay;
   f.n_chunk_slots = r.n_chunk_slots = b.n_chunk_slots;
   const dim3 walk((uint32_t)unit_blocks(items, a.H, a.G, a.ptiles, U), 2);
   if (a.seg > 0) {

@@ -23,6 +23,7 @@ struct StateArgs {
   const float* start;      // state before the walk [slot or seq, H, P, N], nullptr: zeros
   float* end;              // reverse: state after the walk at the sequence's start, or nullptr
   float* piece;            // [item, H * ptiles, 64, NT]
+  float* decay;            // [item, H]: log2 decays of pieces, this walk's own
   float* store;            // chunk states (STORE)
   int64_t n_chunk_slots;
 };
@@ -257,7 +258,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int r = 0; r < 4; ++r) place[(p0 + 16 * pb + 4 * g + r) * NT + 16 * nb + i] = S[pb][nb][r];
-    if (w == 0 && lane == 0 && me.p_first == 0) a.piece_decay[us.item * a.H + me.h] = log_total;
+    if (w == 0 && lane == 0 && me.p_first == 0) k.decay[us.item * a.H + me.h] = log_total;
   } else if (REV && first && k.end) {
     float* dst = k.end + state_at;
 #pragma unroll
@@ -309,7 +310,7 @@ __global__ __launch_bounds__(1024) void ssm_join_kernel(StateArgs k) {
       f32x4* place = reinterpret_cast<f32x4*>(k.piece + (item * hp + tile) * (64 * NT) + at);
       const f32x4 local = m + 1 < pieces ? *place : S;
       *place = S;
-      if (m + 1 < pieces) S = S * ex2(a.piece_decay[item * a.H + h]) + local;
+      if (m + 1 < pieces) S = S * ex2(k.decay[item * a.H + h]) + local;
     }
   }
 }
