@@ -98,8 +98,9 @@ __device__ __forceinline__ bool state_slot(const ScanArgs& a, int64_t seq, int64
   if (!a.ci) return true;
   return slot >= 0 && slot < a.slots;
 }
+// no flags: all false for slots of a pool, all true for arrays of one state a sequence
 __device__ __forceinline__ bool starts_from_state(const ScanArgs& a, int64_t seq) {
-  return a.init && (!a.has_init || __builtin_amdgcn_readfirstlane(a.has_init[seq]));
+  return a.init && (a.has_init ? __builtin_amdgcn_readfirstlane(a.has_init[seq]) != 0 : a.ci == nullptr);
 }
 
 // A block walks U units of a group (they share v), two waves a unit, each with 32 rows p of the state: a wave reads

@@ -141,8 +141,8 @@ def ssm_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, *, cu_seqlens=None, seqle
     """y [rows, H, P] of the scan of x [rows, H, P], dt [rows, H], B, C [rows, G, N] (A, D, dt_bias: [H]).
 
     Sequences: cu_seqlens, or batch rows of seqlen rows (default: one sequence).  States: either a
-    state_pool [slots, H, P, N] fp32 with cache_indices, read where has_initial_state is true and updated
-    in place (as the convolution's conv_state), or initial_state / final_state [nseq, H, P, N]."""
+    state_pool [slots, H, P, N] fp32 with cache_indices, read where has_initial_state is true (None:
+    nowhere) and updated in place (as the convolution's conv_state), or initial_state / final_state [nseq, H, P, N]."""
     lib = _lib.load_ssm()
     sh = _shape(x, dt, B, dt_softplus)
     rows, H, P = x.shape
@@ -163,9 +163,6 @@ def ssm_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, *, cu_seqlens=None, seqle
         st.cache_indices = _ints(cache_indices, "cache_indices", nseq)
         st.has_initial_state = _flags(has_initial_state, "has_initial_state", nseq)
         st.initial = st.final
-        if has_initial_state is None:  # all false: in place, so the pool is only written
-            has_initial_state = x.new_zeros((max(nseq, 1),), dtype=torch.uint8)
-            st.has_initial_state = has_initial_state.data_ptr()
     else:
         if cache_indices is not None or has_initial_state is not None:
             raise ValueError("cache_indices, has_initial_state: need a state_pool")

@@ -46,9 +46,10 @@ typedef struct {
 /* FP32 states [slots, H, P, N], [H, P, N] contiguous, slots s_slot elements apart (s_slot >= H*P*N).
    Sequence i uses slot cache_indices[i] (int32, -1: +0 output rows and no state access), or slot i
    when cache_indices is NULL (then slots >= nseq).  initial: read where has_initial_state (uint8
-   [nseq], NULL = everywhere) is true, zeros elsewhere; NULL = zeros everywhere.  final: written with
-   the state after the sequence's last row; NULL = not wanted.  initial == final updates a pool in
-   place: slots of empty sequences then stay as they are; a separate final array gets their start. */
+   [nseq]) is true, zeros elsewhere; NULL = zeros everywhere.  has_initial_state NULL: all false with
+   cache_indices, as in conv1d_pool, and all true without.  final: written with the state after the
+   sequence's last row; NULL = not wanted.  initial == final updates a pool in place: slots of empty
+   sequences then stay as they are; a separate final array gets their start. */
 typedef struct {
   const float* initial;
   float* final;

@@ -1,4 +1,4 @@
-"""GPU: the scan where it went wrong once: bits of calls in many pieces.
+"""GPU: the scan where it went wrong once: bits of calls in many pieces, calls on a stream of their own.
 
 Tolerances are those of test_gpu_ssm.py, whose problems and checks are used."""
 import pytest
@@ -25,3 +25,28 @@ def test_backward_in_many_pieces_has_the_same_bits(lens):
         got = cc.ssm_scan_bwd(p.dy, *p.args(), cu_seqlens=p.cu, initial_state=p.S0, dfinal_state=p.dS, workspace=ws)
         for name, a, b in zip(want._fields, got, want):
             assert torch.equal(a, b), (k, name)
+
+
+def busy():
+    """Work ahead of everything that the current stream gets from here on."""
+    torch.cuda._sleep(200_000_000)
+
+
+def test_pool_without_flags_on_another_stream():
+    """The prompts start from zeros although the current stream is busy and the slots hold values."""
+    p = base.Problem([200, 70], 4, 64, 2, 64, seed=21)
+    before = torch.randn(4, 4, 64, 64, device="cuda")
+    ci = torch.tensor([3, 1], dtype=torch.int32, device="cuda")
+    pools = [before.clone() for _ in range(2)]
+    # memory that a small array on the current stream would get: bytes that are not zero
+    stale = [torch.full((2,), 1, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    out, side = torch.empty_like(p.x, memory_format=torch.contiguous_format), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    del stale
+    busy()
+    cc.ssm_scan_fwd(*p.args(), cu_seqlens=p.cu, state_pool=pools[0], cache_indices=ci, out=out, stream=side)
+    torch.cuda.synchronize()
+    want = cc.ssm_scan_fwd(*p.args(), cu_seqlens=p.cu, state_pool=pools[1], cache_indices=ci,
+                           has_initial_state=torch.zeros(2, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(out, want) and torch.equal(pools[0], pools[1])
+    assert torch.equal(pools[0][[0, 2]], before[[0, 2]]) and not torch.equal(pools[0][1], before[1])
