@@ -1,6 +1,9 @@
 """Torch binding of include/ssm.h: the selective state space scan, its step and backward, and the
 norms around a mixer block.  As in the package's other entry points, every function only checks tensor
-metadata, marshals pointers, sizes and the current stream, and calls the library."""
+metadata, marshals pointers, sizes and the current stream, and calls the library.
+
+`stream`: the stream the kernels run on (None: the current one).  The caller orders it with the streams that the
+arguments come from and go to; results and workspaces that a call makes itself are allocated on it."""
 import collections
 import ctypes
 
@@ -30,6 +33,23 @@ def _stream(stream, dev):
     if stream is not None:
         return stream.cuda_stream
     return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _empty(like, shape, dtype, stream):
+    """A new array for the kernels of `stream`.  Allocated there: memory of the current stream may still be
+    used, now or after this call, by work that is not ordered with the kernels."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _result(like, shape, dtype, stream):
+    """A new array for the caller, who may drop it while the current stream still uses it."""
+    t = _empty(like, shape, dtype, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
 
 
 def _rows(t, name, shape, dtype=_BF16):
@@ -113,9 +133,9 @@ def _state_array(t, name, H, P, N, least):
     return t.data_ptr(), t.shape[0], (t.stride(0) if t.shape[0] > 1 else H * P * N)
 
 
-def _work(x, need, workspace):
+def _work(x, need, workspace, stream):
     if workspace is None and need:
-        workspace = x.new_empty((need,), dtype=torch.uint8)
+        workspace = _empty(x, (need,), torch.uint8, stream)
     if workspace is None:
         return None, None, 0
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -177,10 +197,10 @@ def ssm_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, *, cu_seqlens=None, seqle
               (state_pool, "state_pool"), (cache_indices, "cache_indices"), (has_initial_state, "has_initial_state"),
               (initial_state, "initial_state"), (final_state, "final_state"), (out, "out"), (workspace, "workspace"))
     if out is None:
-        out = x.new_empty((rows, H, P))
+        out = _result(x, (rows, H, P), _BF16, stream)
     yp, yl = _rows(out, "out", (rows, H, P))
     need = lib.ssm_scan_fwd_workspace_bytes(ctypes.byref(sh), rows, nseq)
-    workspace, wp, wb = _work(x, need, workspace)
+    workspace, wp, wb = _work(x, need, workspace, stream)
     code = lib.ssm_scan_fwd(ctypes.byref(sh), rows, xp, xl, dp, dl, Ap, Bp, Bl, Cp, Cl, Dp, bp, ctypes.byref(seq),
                             ctypes.byref(st), yp, yl, wp, wb, _stream(stream, dev))
     _lib.check(lib, code, "ssm_scan_fwd")
@@ -209,7 +229,7 @@ def ssm_scan_bwd(dy, x, dt, A, B, C, D=None, dt_bias=None, *, cu_seqlens=None, s
               (ddt, "ddt"), (dA, "dA"), (dB, "dB"), (dC, "dC"), (dD, "dD"), (ddt_bias, "ddt_bias"),
               (dinitial_state, "dinitial_state"), (workspace, "workspace"))
     if dinitial_state is None and initial_state is not None:
-        dinitial_state = x.new_empty((nseq, H, P, N), dtype=_F32)
+        dinitial_state = _result(x, (nseq, H, P, N), _F32, stream)
     ptrs = []
     for t, name in ((initial_state, "initial_state"), (dfinal_state, "dfinal_state"), (dinitial_state, "dinitial_state")):
         if t is not None and (tuple(t.shape) != (nseq, H, P, N) or t.dtype != torch.float32 or not t.is_contiguous()):
@@ -217,7 +237,7 @@ def ssm_scan_bwd(dy, x, dt, A, B, C, D=None, dt_bias=None, *, cu_seqlens=None, s
         ptrs.append(t.data_ptr() if t is not None and nseq else None)
 
     def new(t, shape, dtype):
-        return x.new_empty(shape, dtype=dtype) if t is None else t
+        return _result(x, shape, dtype, stream) if t is None else t
 
     dx, ddt = new(dx, (rows, H, P), torch.bfloat16), new(ddt, (rows, H), dt.dtype)
     dB, dC = new(dB, (rows, G, N), torch.bfloat16), new(dC, (rows, G, N), torch.bfloat16)
@@ -227,7 +247,7 @@ def ssm_scan_bwd(dy, x, dt, A, B, C, D=None, dt_bias=None, *, cu_seqlens=None, s
     if dt_bias is not None:
         ddt_bias = new(ddt_bias, (H,), torch.float32)
     need = lib.ssm_scan_bwd_workspace_bytes(ctypes.byref(sh), rows, nseq)
-    workspace, wp, wb = _work(x, need, workspace)
+    workspace, wp, wb = _work(x, need, workspace, stream)
     code = lib.ssm_scan_bwd(ctypes.byref(sh), rows, gp, gl, xp, xl, dp, dl, Ap, Bp, Bl, Cp, Cl, Dp, bp, ctypes.byref(seq),
                             ptrs[0], ptrs[1], *_rows(dx, "dx", (rows, H, P)), *_rows(ddt, "ddt", (rows, H), dt.dtype),
                             _vec(dA, "dA", H), *_rows(dB, "dB", (rows, G, N)), *_rows(dC, "dC", (rows, G, N)),
@@ -257,7 +277,7 @@ def ssm_state_update(x, dt, A, B, C, D=None, dt_bias=None, *, state_pool, cache_
     dev = _on(x, (dt, "dt"), (A, "A"), (B, "B"), (C, "C"), (D, "D"), (dt_bias, "dt_bias"), (state_pool, "state_pool"),
               (cache_indices, "cache_indices"), (out, "out"))
     if out is None:
-        out = x.new_empty((n, H, P))
+        out = _result(x, (n, H, P), _BF16, stream)
     yp, yl = _rows(out, "out", (n, H, P))
     code = lib.ssm_state_update(ctypes.byref(sh), n, xp, xl, dp, dl, Ap, Bp, Bl, Cp, Cl, Dp, bp, ctypes.byref(st), yp, yl,
                                 _stream(stream, dev))
@@ -294,7 +314,7 @@ def gated_norm_fwd(x, gate, weight, *, group_size=None, norm_before_gate=False, 
     xr, zr, (wp, wd) = _rows(x, "x", (rows, d)), _rows(gate, "gate", (rows, d)), _weight(weight, d)
     dev = _on(x, (gate, "gate"), (weight, "weight"), (out, "out"))
     if out is None:
-        out = x.new_empty((rows, d))
+        out = _result(x, (rows, d), _BF16, stream)
     code = lib.gated_norm_fwd(rows, d, g, *xr, *zr, wp, wd, int(bool(norm_before_gate)), eps, *_rows(out, "out", (rows, d)),
                               _stream(stream, dev))
     _lib.check(lib, code, "gated_norm_fwd")
@@ -311,10 +331,10 @@ def gated_norm_bwd(dy, x, gate, weight, *, group_size=None, norm_before_gate=Fal
     wp, wd = _weight(weight, d)
     dev = _on(x, (dy, "dy"), (gate, "gate"), (weight, "weight"), (dx, "dx"), (dgate, "dgate"), (dweight, "dweight"),
               (workspace, "workspace"))
-    dx = x.new_empty((rows, d)) if dx is None else dx
-    dgate = x.new_empty((rows, d)) if dgate is None else dgate
-    dweight = x.new_empty((d,), dtype=_F32) if dweight is None else dweight
-    workspace, sp, sb = _work(x, lib.norm_bwd_workspace_bytes(rows, d, g), workspace)
+    dx = _result(x, (rows, d), _BF16, stream) if dx is None else dx
+    dgate = _result(x, (rows, d), _BF16, stream) if dgate is None else dgate
+    dweight = _result(x, (d,), _F32, stream) if dweight is None else dweight
+    workspace, sp, sb = _work(x, lib.norm_bwd_workspace_bytes(rows, d, g), workspace, stream)
     code = lib.gated_norm_bwd(rows, d, g, *dyr, *xr, *zr, wp, wd, int(bool(norm_before_gate)), eps,
                               *_rows(dx, "dx", (rows, d)), *_rows(dgate, "dgate", (rows, d)), _vec(dweight, "dweight", d),
                               sp, sb, _stream(stream, dev))
@@ -338,9 +358,9 @@ def residual_norm_fwd(x, residual, weight, *, scale=1.0, eps=1e-5, out=None, res
     rr, (wp, wd) = _rows(residual, "residual", (rows, d), residual.dtype), _weight(weight, d)
     dev = _on(x, (residual, "residual"), (weight, "weight"), (out, "out"), (residual_out, "residual_out"))
     if out is None:
-        out = x.new_empty((rows, d))
+        out = _result(x, (rows, d), _BF16, stream)
     if residual_out is None:
-        residual_out = residual.new_empty((rows, d))
+        residual_out = _result(residual, (rows, d), residual.dtype, stream)
     code = lib.residual_norm_fwd(rows, d, *xr, *rr, rt, scale, wp, wd, eps, *_rows(out, "out", (rows, d)),
                                  *_rows(residual_out, "residual_out", (rows, d), residual.dtype), _stream(stream, dev))
     _lib.check(lib, code, "residual_norm_fwd")
@@ -361,10 +381,10 @@ def residual_norm_bwd(dy, dresidual_out, residual_out, weight, *, scale=1.0, eps
     wp, wd = _weight(weight, d)
     dev = _on(residual_out, (dy, "dy"), (dresidual_out, "dresidual_out"), (weight, "weight"), (dx, "dx"),
               (dresidual, "dresidual"), (dweight, "dweight"), (workspace, "workspace"))
-    dx = dy.new_empty((rows, d)) if dx is None else dx
-    dresidual = residual_out.new_empty((rows, d)) if dresidual is None else dresidual
-    dweight = dy.new_empty((d,), dtype=_F32) if dweight is None else dweight
-    workspace, sp, sb = _work(dy, lib.norm_bwd_workspace_bytes(rows, d, d), workspace)
+    dx = _result(dy, (rows, d), _BF16, stream) if dx is None else dx
+    dresidual = _result(residual_out, (rows, d), rdt, stream) if dresidual is None else dresidual
+    dweight = _result(dy, (d,), _F32, stream) if dweight is None else dweight
+    workspace, sp, sb = _work(dy, lib.norm_bwd_workspace_bytes(rows, d, d), workspace, stream)
     code = lib.residual_norm_bwd(rows, d, *dyr, *drr, *ror, rt, scale, wp, wd, eps, *_rows(dx, "dx", (rows, d)),
                                  *_rows(dresidual, "dresidual", (rows, d), rdt), _vec(dweight, "dweight", d), sp, sb,
                                  _stream(stream, dev))

@@ -50,3 +50,30 @@ def test_pool_without_flags_on_another_stream():
                            has_initial_state=torch.zeros(2, dtype=torch.uint8, device="cuda"))
     assert torch.equal(out, want) and torch.equal(pools[0], pools[1])
     assert torch.equal(pools[0][[0, 2]], before[[0, 2]]) and not torch.equal(pools[0][1], before[1])
+
+
+def test_work_arrays_of_another_stream():
+    """Calls on a side stream while the current stream still writes memory that it has given back."""
+    p = base.Problem([1300, 40], 4, 64, 2, 64, seed=22, step=-3.0)
+    m = torch.randn(300, 256, device="cuda").bfloat16()
+    w, side = torch.rand(256, device="cuda"), torch.cuda.Stream()
+
+    def work(**k):
+        fin = torch.empty_like(p.S0) if not k else keep
+        y = cc.ssm_scan_fwd(*p.args(), cu_seqlens=p.cu, initial_state=p.S0, final_state=fin, **k)
+        g = cc.ssm_scan_bwd(p.dy, *p.args(), cu_seqlens=p.cu, initial_state=p.S0, dfinal_state=p.dS, **k)
+        return [y, fin, *g, *cc.gated_norm_bwd(m, m, m, w, **k), *cc.residual_norm_bwd(m, m, m, w, **k)]
+
+    want = work()
+    need = cc.ssm_scan_bwd_workspace_bytes(p.x, p.dt, p.B, 2)
+    keep = torch.empty_like(p.S0)
+    torch.cuda.synchronize()
+    busy()
+    for size in (need, 1 << 20, 1 << 16, 1 << 10):
+        for _ in range(6):
+            torch.empty((size,), dtype=torch.uint8, device="cuda").fill_(255)  # NaN, written when the sleep ends
+    got = work(stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

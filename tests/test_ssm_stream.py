@@ -83,3 +83,38 @@ def test_missing_flags_stay_missing(lib):
     calls()["scan_fwd_pool"]()
     assert lib.states.has_initial_state is None and lib.states.cache_indices
     assert lib.states.initial == lib.states.final
+
+
+@pytest.mark.parametrize("name", list(calls()))
+def test_new_arrays_belong_to_the_stream(lib, name, monkeypatch):
+    """Results and workspaces are allocated on the stream argument, and the current stream's use of the results is
+    made known to the allocator."""
+    call, side, inside, kept = calls()[name], object(), [], []
+
+    class On:
+        def __init__(self, s):
+            assert s is side
+
+        def __enter__(self):
+            inside.append(True)
+
+        def __exit__(self, *args):
+            inside.pop()
+
+    where = []
+
+    class Allocations(Ops):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            out = super().__torch_dispatch__(func, types, args, kwargs)
+            if "empty" in self.names[-1]:
+                where.append((bool(inside), out.data_ptr()))
+            return out
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: "current")
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: kept.append((t.data_ptr(), s)), raising=False)
+    with Allocations():
+        got = call(stream=side)
+    got = [got] if isinstance(got, torch.Tensor) else [t for t in got if t is not None]
+    assert where and all(on for on, _ in where)
+    assert sorted(kept) == sorted((t.data_ptr(), "current") for t in got)
