@@ -450,9 +450,10 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
 // dB, dC from the head parts, in ascending order of the parts
 __global__ __launch_bounds__(256) void ssm_bc_reduce_kernel(ScanBwdArgs b) {
   const int64_t width = (int64_t)b.s.G * b.s.N, rows = b.s.q.rows;
-  const int64_t end = b.s.q.cu ? cu_at(b.s.q, b.s.q.nseq) : rows;
+  // the rows of sequences: the chunks wrote no parts of others
+  const int64_t begin = b.s.q.cu ? cu_at(b.s.q, 0) : 0, end = b.s.q.cu ? cu_at(b.s.q, b.s.q.nseq) : rows;
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (e >= end * width) return;
+  if (e < begin * width || e >= end * width) return;
   const float* src = b.bc_part + (blockIdx.y ? (int64_t)b.hsplit * rows * width : 0) + e;
   float s = src[0];
   for (int k = 1; k < b.hsplit; ++k) s += src[(int64_t)k * rows * width];

@@ -1,4 +1,5 @@
-"""GPU: the scan where it went wrong once: bits of calls in many pieces, calls on a stream of their own.
+"""GPU: the scan where it went wrong once: bits of calls in many pieces, calls on a stream of their own,
+rows outside every sequence.
 
 Tolerances are those of test_gpu_ssm.py, whose problems and checks are used."""
 import pytest
@@ -77,3 +78,25 @@ def test_work_arrays_of_another_stream():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_rows_before_the_first_sequence():
+    """Offsets that begin past row 0: the rows before them belong to no sequence, like those after the last."""
+    H, P, G, N = 4, 64, 1, 64
+    p = base.Problem([9, 100, 30], H, P, G, N, seed=23, pad=4)
+    cu, S0, dS = p.cu[1:].contiguous(), p.S0[1:].contiguous(), p.dS[1:].contiguous()
+    bounds, (s, e) = p.bounds[1:], (9, 139)
+    (y, _, g), (ym, _, gm) = [base.ref.scan(*p.host(), bounds, S0.cpu(), dy=p.dy.cpu(), dS=dS.cpu(), magnitudes=m)
+                              for m in (False, True)]
+    new = {k: torch.full_like(t, 7.0, memory_format=torch.contiguous_format)
+           for k, t in dict(dx=p.x, ddt=p.dt, dB=p.B, dC=p.C).items()}
+    ws = torch.full((cc.ssm_scan_bwd_workspace_bytes(p.x, p.dt, p.B, 2),), 255, dtype=torch.uint8, device="cuda")
+    out = torch.full((p.R, H, P), 7.0, dtype=torch.bfloat16, device="cuda")
+    cc.ssm_scan_fwd(*p.args(), cu_seqlens=cu, initial_state=S0, out=out)
+    got = cc.ssm_scan_bwd(p.dy, *p.args(), cu_seqlens=cu, initial_state=S0, dfinal_state=dS, workspace=ws, **new)
+    base.close(out[s:e], y[s:e], ym[s:e], base.HALF, base.HALF, "y")
+    for k, own, terms in (("dx", base.HALF, base.HALF), ("dB", base.HALF, base.HALF), ("dC", base.HALF, base.HALF),
+                          ("ddt", 0.0, base.FINE)):
+        base.close(getattr(got, k)[s:e], g[k][s:e], gm[k][s:e], own, terms, k)
+    for k, t in dict(new, y=out).items():
+        assert (t[:s] == 7).all() and (t[e:] == 7).all(), k
