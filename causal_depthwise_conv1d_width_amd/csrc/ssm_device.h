@@ -39,7 +39,8 @@ __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x)
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + ex2(-kLog2e * z)); }
 
 // The step size: v, or log(1 + e^v) = max(v, 0) + log1p(e^-|v|).  The exponent's argument keeps its low
-// part, and log1p(u) = log(w) u / (w - 1) with w = 1 + u rounded: right to a few ulp at every v.
+// part, and log1p(u) = log(w) u / (w - 1) with w = 1 + u rounded: right to a few ulp at every v.  Both
+// comparisons of the result are false for a NaN, which is kept.
 __device__ __forceinline__ float step_size(float v, int softplus) {
   if (!softplus) return v;
   const float a = __builtin_fabsf(v), t = a * kLog2e;
@@ -47,7 +48,7 @@ __device__ __forceinline__ float step_size(float v, int softplus) {
   const float u = ex2(-t) * __builtin_fmaf(rest, -0.693147181f, 1.f);
   const float w = 1.f + u, m = w - 1.f;
   const float l = m > 0.f ? __builtin_amdgcn_logf(w) * 0.693147181f * u * __builtin_amdgcn_rcpf(m) : u;
-  return (v > 0.f ? v : 0.f) + (a < 126.f ? l : 0.f);
+  return (v <= 0.f ? 0.f : v) + (a >= 126.f ? 0.f : l);
 }
 
 __device__ __forceinline__ float load_num(const void* p, int64_t i, int f32) {

@@ -1,5 +1,5 @@
 """GPU: the scan where it went wrong once: bits of calls in many pieces, calls on a stream of their own,
-rows outside every sequence.
+rows outside every sequence, NaN steps.
 
 Tolerances are those of test_gpu_ssm.py, whose problems and checks are used."""
 import pytest
@@ -100,3 +100,59 @@ def test_rows_before_the_first_sequence():
         base.close(getattr(got, k)[s:e], g[k][s:e], gm[k][s:e], own, terms, k)
     for k, t in dict(new, y=out).items():
         assert (t[:s] == 7).all() and (t[e:] == 7).all(), k
+
+
+def same_but(got, want, at, what):
+    """got has want's bits outside `at`."""
+    a, b = got.clone(), want.clone()
+    a[at] = b[at] = 0
+    assert torch.equal(a, b), what
+
+
+@pytest.mark.parametrize("dt32", [True, False])
+def test_nan_step_is_seen(dt32):
+    """A NaN step makes its head NaN from its row on, and nothing else; -inf is a step of zero."""
+    H, P, G, N, h, t = 4, 64, 2, 64, 2, 90
+    p = base.Problem([50, 70, 30], H, P, G, N, seed=24, dt32=dt32)
+    rows = slice(t, 120)  # the second sequence's from row t on
+
+    def run():
+        fin = torch.empty_like(p.S0)
+        y = cc.ssm_scan_fwd(*p.args(), cu_seqlens=p.cu, initial_state=p.S0, final_state=fin)
+        return y, fin, cc.ssm_scan_bwd(p.dy, *p.args(), cu_seqlens=p.cu, initial_state=p.S0, dfinal_state=p.dS)
+
+    y, fin, g = run()
+    keep = p.dt[t, h].clone()
+    p.dt[t, h] = float("nan")
+    ny, nfin, ng = run()
+    assert ny[rows, h].isnan().all() and nfin[1, h].isnan().all()
+    same_but(ny, y, (rows, h), "y")
+    same_but(nfin, fin, (1, h), "final state")
+    assert ng.ddt[t, h].isnan() and ng.dA[h].isnan() and ng.ddt_bias[h].isnan()
+    same_but(ng.dx, g.dx, (slice(50, 120), h), "dx")
+    same_but(ng.ddt, g.ddt, (slice(50, 120), h), "ddt")
+    same_but(ng.dA, g.dA, h, "dA")
+    p.dt[t, h] = float("-inf")
+    iy, ifin, ig = run()
+    p.dt[t, h] = -1e4
+    for a, b in zip((iy, ifin, *ig), (lambda r: (r[0], r[1], *r[2]))(run())):
+        assert torch.equal(a, b)
+    p.dt[t, h] = keep
+    p.bias[1] = float("nan")
+    ny, nfin, _ = run()
+    assert ny[:, 1].isnan().all() and nfin[:, 1].isnan().all()
+    same_but(ny, y, (slice(None), 1), "y")
+
+
+def test_nan_step_is_seen_by_one_token():
+    H, P, G, N = 4, 64, 2, 64
+    p = base.Problem([1] * 5, H, P, G, N, seed=25)
+    start = torch.randn(5, H, P, N, device="cuda")
+    ci = torch.arange(5, dtype=torch.int32, device="cuda")
+    pool, bad = start.clone(), start.clone()
+    y = cc.ssm_state_update(*p.args(), state_pool=pool, cache_indices=ci)
+    p.dt[3, 1] = float("nan")
+    ny = cc.ssm_state_update(*p.args(), state_pool=bad, cache_indices=ci)
+    assert ny[3, 1].isnan().all() and bad[3, 1].isnan().all()
+    same_but(ny, y, (3, 1), "y")
+    same_but(bad, pool, (3, 1), "pool")
