@@ -25,7 +25,9 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
   __shared__ __align__(16) uint16_t sB[64 * kLd<NT, 16>];
   __shared__ __align__(16) uint16_t sC[64 * kLd<NT>];
   __shared__ __align__(16) uint16_t sP_[U][64 * kLd<64>];
-  __shared__ __align__(16) float sdecay[2][U][4][64];  // this chunk's and the next one's, by unit
+  // this chunk's and the next one's, by unit: prefix sums L; steps, 2^L, weights of the state update
+  __shared__ __align__(16) double ssum[2][U][64];
+  __shared__ __align__(16) float sdecay[2][U][3][64];
   const int hp = a.H * a.ptiles;
   const Units<U> us(a, blockIdx.x);
   if (!us.ok) return;
@@ -104,13 +106,13 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
   const int my = w == 0 ? (int)(threadIdx.x & 63) : 63 - (int)(threadIdx.x & 63);
   auto decays = [&](int rows, int at) {
     const float d = rate.step(raw, my < rows);
-    const float L = wave_prefix(d * rate.A2);
     if (w == 0) {
-      sdecay[at][un][0][lane] = L;
-      sdecay[at][un][1][lane] = d;
-      sdecay[at][un][2][lane] = ex2(L);
+      const double L = wave_prefix(rate.exponent(d));
+      ssum[at][un][lane] = L;
+      sdecay[at][un][0][lane] = d;
+      sdecay[at][un][1][lane] = ex2((float)L);
     } else {
-      sdecay[at][un][3][my] = ex2(dpp0<0x138, 0xf>(L)) * d;
+      sdecay[at][un][2][my] = ex2(dpp0<0x138, 0xf>(wave_prefix(d * rate.A2))) * d;
     }
   };
   Chunks<false> c(pc.r0, pc.r1);
@@ -148,14 +150,12 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
         t = mma(op_straight<NT, 16>(sB, 16 * jb, 32 * ks, lane), op_straight<NT>(sC, 16 * ib, 32 * ks, lane), t);
 #pragma unroll
       for (int q = 0; q < U; ++q) {
-        const float(*s)[64] = sdecay[buf][q];
-        const float Li = s[0][16 * ib + i];
-        const f32x4 Lj = *reinterpret_cast<const f32x4*>(s[0] + 16 * jb + 4 * g);
-        const f32x4 dj = *reinterpret_cast<const f32x4*>(s[1] + 16 * jb + 4 * g);
+        const double *sL = ssum[buf][q], Li = sL[16 * ib + i];
+        const f32x4 dj = *reinterpret_cast<const f32x4*>(sdecay[buf][q][0] + 16 * jb + 4 * g);
         f32x4 v;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          v[r] = t[r] * (ex2(Li - Lj[r]) * dj[r]);
+          v[r] = t[r] * (ex2((float)(Li - sL[16 * jb + 4 * g + r])) * dj[r]);
           v[r] = 16 * jb + 4 * g + r <= 16 * ib + i ? v[r] : 0.f;
         }
         *reinterpret_cast<u32x2*>(sP_[q] + at<64>(16 * ib + i, 16 * jb + 4 * g)) =
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
         for (int pb = 0; pb < PB; ++pb) y[pb][ib] = mma(s[pb], cv, y[pb][ib]);
       }
     }
-    const float *se = sdecay[buf][un][2], *sw = sdecay[buf][un][3];
+    const float *se = sdecay[buf][un][1], *sw = sdecay[buf][un][2];
 #pragma unroll
     for (int ib = 0; ib < 4; ++ib)
 #pragma unroll

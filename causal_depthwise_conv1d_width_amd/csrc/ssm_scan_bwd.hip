@@ -60,7 +60,6 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
   __shared__ __align__(16) uint16_t sC[64 * kLd<NT>];
   __shared__ __align__(16) uint16_t sR[R];  // T^T [n][p], then Z and G M [i][j]
   // three heads': the last one's gradients are put together while the next one's decays are made
-  // (differences of FP32 prefix sums would lose a fast decay's weights)
   __shared__ __align__(16) double sdecay[2][64];
   __shared__ __align__(16) float ssteps[3][3][64];
   __shared__ __align__(16) float s_col[2][4][64];
@@ -108,9 +107,9 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
   auto load_raw = [&](int t) { raw = raw_step(a, pc.r0, t < tiles ? rows : 0, lane, h_lo + (uint32_t)t / (uint32_t)a.ptiles); };
   auto decays = [&](int t) {
     const Rate rate(a, h_lo + (uint32_t)t / (uint32_t)a.ptiles);
-    const float d = rate.step(raw, lane < rows), l = d * rate.A2;
-    const double L = wave_prefix((double)l);
-    const double back = wave_prefix((double)__shfl(l, 63 - lane));
+    const float d = rate.step(raw, lane < rows);
+    const double l = rate.exponent(d), L = wave_prefix(l);
+    const double back = wave_prefix(__shfl(l, 63 - lane));
     sdecay[t & 1][lane] = L;
     ssteps[t % 3][0][lane] = d;
     ssteps[t % 3][1][lane] = ex2((float)L);

@@ -52,6 +52,13 @@ struct Rate {
     const float v = __uint_as_float(((uint32_t)raw.hi << 16) | (f32 ? raw.lo : 0u));
     return in ? step_size(v + bias, softplus) : 0.f;
   }
+  // A term of the 64-bit prefix sums whose differences are the exponents of M_ij.  FP32 sums would lose the slow
+  // decays that follow a sudden one; a decay below 2^-(2^20) counts as that, still a zero, so that 64 of them leave
+  // 27 bits behind the binary point and no infinities to subtract.  A NaN stays one.
+  __device__ __forceinline__ double exponent(float d) const {
+    const float l = d * A2;
+    return (double)(l < -1048576.f ? -1048576.f : l);
+  }
 };
 
 // The chunks of rows [r0, r1) in the order of the walk.

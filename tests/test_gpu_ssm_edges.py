@@ -1,5 +1,6 @@
 """GPU: the scan where it went wrong once: bits of calls in many pieces, calls on a stream of their own,
-rows outside every sequence, NaN steps.
+rows outside every sequence, NaN steps,
+slow decays after sudden ones.
 
 Tolerances are those of test_gpu_ssm.py, whose problems and checks are used."""
 import pytest
@@ -156,3 +157,23 @@ def test_nan_step_is_seen_by_one_token():
     assert ny[3, 1].isnan().all() and bad[3, 1].isnan().all()
     same_but(ny, y, (3, 1), "y")
     same_but(bad, pool, (3, 1), "pool")
+
+
+@pytest.mark.parametrize("drop", [100.0, 1e5, 1e7, 1e30])
+@pytest.mark.parametrize("N", [64, 200])
+def test_slow_decay_after_a_sudden_one(drop, N):
+    """Tokens that drop the state (x = 0 and B = 0 there, a step of `drop`), with slow decays between them in the
+    same chunk.  A decay's exponent is a sum of the steps between two rows, whatever came before them."""
+    p = base.Problem([150, 64], 4, 64, 2, N, seed=26, decay=1.0)
+    p.dt = p.dt.abs() * 0.1
+    p.bias = torch.zeros_like(p.bias)
+    for t in (10, 33, 34, 80, 150, 163):
+        p.dt[t], p.x[t], p.B[t] = drop, 0, 0
+    (y, fin, g), (ym, fm, gm) = p.reference(p.S0, sp=False, dy=p.dy.cpu(), dS=p.dS.cpu())
+    got_fin = torch.empty_like(p.S0)
+    got = cc.ssm_scan_fwd(*p.args(), cu_seqlens=p.cu, dt_softplus=False, initial_state=p.S0, final_state=got_fin)
+    base.close(got, y, ym, base.HALF, base.HALF, "y")
+    base.close(got_fin, fin, fm, 0.0, base.FINE, "final state")
+    b = cc.ssm_scan_bwd(p.dy, *p.args(), cu_seqlens=p.cu, dt_softplus=False, initial_state=p.S0, dfinal_state=p.dS)
+    for k in ("dx", "dB", "dC"):
+        base.close(getattr(b, k), g[k], gm[k], base.HALF, base.HALF, k)
