@@ -18,6 +18,44 @@
 
 namespace cssm {
 
+// Non-finite x.  The decayed scores hold zeros past the diagonal, and zero times a non-finite x of a later row is a
+// NaN.  A product of x with zeros finds them: any in a wave's columns of the chunk makes it NaN.  64 mixed prompts (head of
+// the file) 456 us, 445 without; a look per 32 rows at their use 461, at the bits on their way to shared memory 469.
+template <int PB>
+__device__ __forceinline__ bool any_non_finite(const bf16x8 (&x)[2][PB]) {
+  f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+    for (int pb = 0; pb < PB; ++pb) t = mma(x[ks][pb], bf16x8{}, t);
+  const float v = (t[0] + t[1]) + (t[2] + t[3]);
+  return __ballot(v != v) != 0;
+}
+// Makes Y NaN in the column of a non-finite x from its row on (the rows i with a one at j <= i in the product of the
+// places of such x with the lower triangle), and that x zero in the operand.  ks: the operand's half of the chunk.
+__device__ __forceinline__ void contain_non_finite(bf16x8& x, f32x4 (&y)[4], int ks, int g, int i) {
+  u32x4 u = __builtin_bit_cast(u32x4, x), at;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const bool lo = (u[e] & 0x7f80u) == 0x7f80u, hi = (u[e] & 0x7f800000u) == 0x7f800000u;
+    at[e] = (lo ? 0x3f80u : 0u) | (hi ? 0x3f800000u : 0u);
+    u[e] &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
+  }
+  x = __builtin_bit_cast(bf16x8, u);
+#pragma unroll
+  for (int ib = 0; ib < 4; ++ib) {
+    u32x4 lower;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {  // positions 2 e, 2 e + 1 of the split order
+      const int j = 32 * ks + 16 * (e >> 1) + 4 * g + 2 * (e & 1), row = 16 * ib + i;
+      lower[e] = (j <= row ? 0x3f80u : 0u) | (j < row ? 0x3f800000u : 0u);
+    }
+    const f32x4 n = mma(__builtin_bit_cast(bf16x8, at), __builtin_bit_cast(bf16x8, lower), f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+    for (int r = 0; r < 4; ++r) y[ib][r] = n[r] > 0.f ? __builtin_nanf("") : y[ib][r];
+  }
+}
+
 template <int NT, int U, int PB, bool VEC>
 __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs a) {
   constexpr int T = 256 / PB * U, NB = NT / 16, WU = 4 / PB;  // threads, state blocks, waves a unit
@@ -193,6 +231,18 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
 #pragma unroll
       for (int pb = 0; pb < PB; ++pb) y[pb][ib] *= se[16 * ib + i];
     phase();
+    bf16x8 x[2][PB];  // x as an operand: columns p, contracted rows
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int pb = 0; pb < PB; ++pb) x[ks][pb] = op_cols<64, 16>(sx, 32 * ks, 16 * (PB * w + pb), lane);
+    const bool bad = any_non_finite(x);
+    if (__builtin_expect(bad, 0)) {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int pb = 0; pb < PB; ++pb) contain_non_finite(x[ks][pb], y[pb], ks, g, i);
+    }
     __syncthreads();
     const float et = se[63];
 #pragma unroll
@@ -203,19 +253,20 @@ __global__ __launch_bounds__(256 / PB * U, 2) void ssm_scan_fwd_kernel(ScanArgs 
     for (int ks = 0; ks < 2; ++ks) {
       Parts xw[PB];
       {
-        bf16x8 x[PB];
-#pragma unroll
-        for (int pb = 0; pb < PB; ++pb) x[pb] = op_cols<64, 16>(sx, 32 * ks, 16 * (PB * w + pb), lane);
 #pragma unroll
         for (int ib = 2 * ks; ib < 4; ++ib) {
           const bf16x8 pv = op_split<64>(sP, 16 * ib, 32 * ks, lane);
 #pragma unroll
-          for (int pb = 0; pb < PB; ++pb) y[pb][ib] = mma(x[pb], pv, y[pb][ib]);
+          for (int pb = 0; pb < PB; ++pb) y[pb][ib] = mma(x[ks][pb], pv, y[pb][ib]);
+        }
+        if (__builtin_expect(bad, 0)) {  // the state takes them as they are
+#pragma unroll
+          for (int pb = 0; pb < PB; ++pb) x[ks][pb] = op_cols<64, 16>(sx, 32 * ks, 16 * (PB * w + pb), lane);
         }
         const f32x4 wa = *reinterpret_cast<const f32x4*>(sw + 32 * ks + 4 * g);
         const f32x4 wb = *reinterpret_cast<const f32x4*>(sw + 32 * ks + 16 + 4 * g);
 #pragma unroll
-        for (int pb = 0; pb < PB; ++pb) xw[pb] = split_scaled(x[pb], wa, wb);
+        for (int pb = 0; pb < PB; ++pb) xw[pb] = split_scaled(x[ks][pb], wa, wb);
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {

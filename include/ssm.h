@@ -59,7 +59,9 @@ typedef struct {
 } ssm_states;
 
 /* Forward.  states: NULL for zero start and no final states.  D, dt_bias: FP32 [H] or NULL.  y must
-   not overlap any input; rows outside every sequence are not written.  ws: at least
+   not overlap any input; rows outside every sequence are not written.  An infinity or NaN makes
+   not finite what the recurrence takes it to and changes nothing else: of x, its column from its row on; of dt
+   and B, their head and group from the row on; of C, its group in the row.  ws: at least
    ssm_scan_fwd_workspace_bytes(...) bytes, 16-byte aligned (NULL when that is 0). */
 int ssm_scan_fwd(const ssm_shape* shape, int64_t rows, const void* x, int64_t x_ld, const void* dt, int64_t dt_ld,
                  const float* A, const void* B, int64_t B_ld, const void* C, int64_t C_ld, const float* D,
@@ -72,8 +74,9 @@ size_t ssm_scan_fwd_workspace_bytes(const ssm_shape* shape, int64_t rows, int64_
    (gradient of the raw dt, dt's type), dB, dC (summed over the group's heads in FP32, rounded once),
    dA [H], and, unless NULL, dD [H], ddt_bias [H], dinitial_state [nseq, H, P, N] (an empty sequence's
    is its dfinal_state).  Outputs must not overlap inputs or one another.  Rows outside every sequence
-   are not written.  It recomputes everything from the inputs; ws: at least
-   ssm_scan_bwd_workspace_bytes(...) bytes, 16-byte aligned. */
+   are not written.  An infinity or NaN stays in its sequence and its head (that of B and C, and all in dB
+   and dC, in the group); there it may reach rows on either side.  It recomputes everything from the
+   inputs; ws: at least ssm_scan_bwd_workspace_bytes(...) bytes, 16-byte aligned. */
 int ssm_scan_bwd(const ssm_shape* shape, int64_t rows, const void* dy, int64_t dy_ld, const void* x, int64_t x_ld,
                  const void* dt, int64_t dt_ld, const float* A, const void* B, int64_t B_ld, const void* C,
                  int64_t C_ld, const float* D, const float* dt_bias, const conv1d_seq* seq,

@@ -1,6 +1,6 @@
 """GPU: the scan where it went wrong once: bits of calls in many pieces, calls on a stream of their own,
 rows outside every sequence, NaN steps,
-slow decays after sudden ones.
+slow decays after sudden ones, values that are not finite.
 
 Tolerances are those of test_gpu_ssm.py, whose problems and checks are used."""
 import pytest
@@ -177,3 +177,41 @@ def test_slow_decay_after_a_sudden_one(drop, N):
     b = cc.ssm_scan_bwd(p.dy, *p.args(), cu_seqlens=p.cu, dt_softplus=False, initial_state=p.S0, dfinal_state=p.dS)
     for k in ("dx", "dB", "dC"):
         base.close(getattr(b, k), g[k], gm[k], base.HALF, base.HALF, k)
+
+
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("lens,H,P,G,N", [([150, 40], 4, 64, 2, 128), ([130, 60], 6, 40, 2, 60), ([120, 70], 4, 72, 2, 200),
+                                          ([1300, 90], 2, 64, 1, 64)])
+def test_non_finite_x_reaches_no_earlier_row(value, lens, H, P, G, N):
+    """A non-finite x makes its column of y and its row of the state non-finite from there on, and changes no other bit."""
+    p = base.Problem(lens, H, P, G, N, seed=27, wide=3)
+    h, c, end = 1, 37, lens[0]
+
+    def run():
+        fin = torch.empty_like(p.S0)
+        return cc.ssm_scan_fwd(*p.args(), cu_seqlens=p.cu, initial_state=p.S0, final_state=fin), fin
+
+    y, fin = run()
+    for t in (0, 5, 15, 16, 31, 37, 63, 64, 100, end - 1):
+        keep = p.x[t, h, c].clone()
+        p.x[t, h, c] = float(value)
+        ny, nfin = run()
+        p.x[t, h, c] = keep
+        assert not ny[t:end, h, c].isfinite().any(), t
+        assert not nfin[0, h, c].isfinite().any(), t
+        same_but(ny, y, (slice(t, end), h, c), f"y, row {t}")
+        same_but(nfin, fin, (0, h, c), f"final state, row {t}")
+
+
+def test_non_finite_rows_of_B_and_C():
+    """Of B: its group's heads from there on.  Of C: its group's heads in that row."""
+    p = base.Problem([150, 40], 4, 64, 2, 128, seed=28)
+    y = cc.ssm_scan_fwd(*p.args(), cu_seqlens=p.cu)
+    for t in (3, 20, 50, 77, 149):
+        for which, rows in ((p.B, slice(t, 150)), (p.C, slice(t, t + 1))):
+            keep = which[t, 1, 9].clone()
+            which[t, 1, 9] = float("nan")
+            ny = cc.ssm_scan_fwd(*p.args(), cu_seqlens=p.cu)
+            which[t, 1, 9] = keep
+            assert ny[rows, 2:].isnan().all()
+            same_but(ny, y, (rows, slice(2, 4)), t)
