@@ -21,8 +21,14 @@
  *     A, D, dt_bias, states and all parameter gradients: FP32.
  *   - 1 <= N <= SSM_MAX_STATE, G divides H, any P >= 1.
  *   - seq: the cu_seqlens or the batch-row form of conv1d_seq (seq_idx must be NULL).
- *   - State sums, decays and every reduction are FP32 or better; results do not depend on the
- *     workspace's contents or address, and there are no atomics: equal calls give equal bits.
+ *   - States, their sums over rows, decays, norms and every reduction are FP32 or better.  Matrix
+ *     instructions take bf16 operands: x, B, C and dy as they are; what is FP32 is rounded or cut into
+ *     parts.  Scan: the decayed scores and the state in S_t C_t are rounded to bf16, 2^-8 of a term of y at
+ *     most each; a state's new terms enter as two parts, 2^-16 of a term.  Its backward: the decayed scores in
+ *     dx, dB and dC and the state's adjoint in dx are rounded to bf16; all else (states and adjoints, ddt, dA,
+ *     dinitial_state) enters as three parts, FP32's 24 bits.  The step and the norms are FP32 throughout.
+ *   - Results do not depend on the workspace's contents or address, and there are no atomics: equal calls
+ *     give equal bits.
  */
 #ifndef SSM_H
 #define SSM_H
