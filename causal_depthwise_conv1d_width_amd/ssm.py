@@ -138,6 +138,8 @@ def _work(x, need, workspace, stream):
         workspace = _empty(x, (need,), torch.uint8, stream)
     if workspace is None:
         return None, None, 0
+    if not workspace.is_contiguous():  # its bytes would not be its own
+        raise ValueError("workspace: must be contiguous")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

@@ -118,3 +118,13 @@ def test_new_arrays_belong_to_the_stream(lib, name, monkeypatch):
     got = [got] if isinstance(got, torch.Tensor) else [t for t in got if t is not None]
     assert where and all(on for on, _ in where)
     assert sorted(kept) == sorted((t.data_ptr(), "current") for t in got)
+
+
+@pytest.mark.parametrize("name", ["scan_fwd", "scan_bwd", "gated_bwd", "residual_bwd"])
+def test_a_workspace_that_repeats_its_bytes_is_refused(lib, name):
+    """An expanded tensor counts more bytes than it has, and kernels would write past them."""
+    byte = torch.zeros(1, dtype=torch.uint8)
+    calls()[name](workspace=byte.repeat(64))
+    for ws in (byte.expand(64), torch.zeros(128, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            calls()[name](workspace=ws)
