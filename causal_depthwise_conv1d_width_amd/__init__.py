@@ -30,18 +30,29 @@ What follows the convolution in a mixer block (C ABI in include/ssm.h, binding i
 import ctypes
 
 from . import _lib
-from .ssm import (SsmGrads, gated_norm_bwd, gated_norm_fwd, norm_bwd_workspace_bytes, residual_norm_bwd,
-                  residual_norm_fwd, ssm_scan_bwd, ssm_scan_bwd_workspace_bytes, ssm_scan_fwd,
-                  ssm_scan_fwd_workspace_bytes, ssm_state_update)
 
+_SSM = ["ssm_scan_fwd", "ssm_scan_bwd", "SsmGrads", "ssm_state_update", "ssm_scan_fwd_workspace_bytes",
+        "ssm_scan_bwd_workspace_bytes", "gated_norm_fwd", "gated_norm_bwd", "residual_norm_fwd", "residual_norm_bwd",
+        "norm_bwd_workspace_bytes"]
 __all__ = ["conv1d_fwd", "conv1d_state_update", "conv1d_state_update_spec", "conv1d_bwd", "conv1d_bwd_combine",
            "conv1d_bwd_noalloc", "conv1d_fwd_cf",
            "conv1d_bwd_cf", "conv1d_bwd_cf_workspace_bytes", "conv1d_fwd_workspace_bytes",
-           "conv1d_bwd_workspace_bytes", "library_path", "ssm_scan_fwd", "ssm_scan_bwd", "SsmGrads",
-           "ssm_state_update", "ssm_scan_fwd_workspace_bytes", "ssm_scan_bwd_workspace_bytes", "gated_norm_fwd",
-           "gated_norm_bwd", "residual_norm_fwd", "residual_norm_bwd", "norm_bwd_workspace_bytes"]
+           "conv1d_bwd_workspace_bytes", "library_path"] + _SSM
 
 library_path = _lib.LIB_PATH
+
+
+def __getattr__(name):
+    """The functions of ssm.py at their first use: that module needs torch, this package's import does not."""
+    if name not in _SSM:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import ssm
+    globals().update((n, getattr(ssm, n)) for n in _SSM)
+    return globals()[name]
+
+
+def __dir__():
+    return sorted(set(globals()) | set(__all__))
 
 
 def _torch():
