@@ -64,15 +64,15 @@ bool clash(const Span (&outs)[NO], const Span (&ins)[NI]) {
 // know the lengths), where one could be long against the rest; the cost is a first walk for the pieces' states
 // and a join.
 //
-// Forward (64 heads of 64 columns, N = 128), `want` blocks: 4 sequences of 4096 rows 191 us with 256, 312 with
-// 128, 230 with 512, 411 whole; 2048 rows of one sequence 60 us with 256, 69 with 128, 206 whole; 64 mixed
-// prompts 437 us with pieces for 512 blocks, 467 for 256, 423 whole (but only because none is long).
+// Forward (64 heads of 64 columns, N = 128), `want` blocks: 4 sequences of 4096 rows 194 us with 256, 324 with
+// 128, 212 with 512, 437 whole; 2048 rows of one sequence 60 us with 256, 69 with 128, 60 with 512, 218 whole; 64 mixed
+// prompts 458 us with pieces for 512 blocks, 493 for 256, 451 whole (but only because none is long).
 //
 // Backward: the walk is bound by its stores, both directions are one launch, and few blocks reach that bound.
-// 4 sequences of 4096 rows (64 walks a direction) 908 us whole, 967 for 128, 985 for 256; 2 sequences of 8192 1129
-// whole, 967 for 128; one of 16384 1516 whole, 1145 for 64, 975 for 128, 998 for 256.  Mixed sequences, means over
-// six draws: nine in 2777 rows (24 heads) 142 us with pieces of at least 256 rows, 155 with 512, 162 with 1024 (128 to
-// 189, by the longest); six in 8192 rows 323, 322 and 352 us.
+// 4 sequences of 4096 rows (64 walks a direction) 870 us whole, 967 for 128, 981 for 256; 2 sequences of 8192 1088
+// whole, 971 for 128; one of 16384 1500 whole, 1056 for 64, 978 for 128, 995 for 256.  Mixed sequences, means over
+// six draws: nine in 2777 rows (24 heads) 140 us with pieces of at least 256 rows, 154 with 512, 160 with 1024; six in
+// 8192 rows 292, 292 and 324 us.
 struct Cut {
   int64_t whole, want;  // blocks that make equal sequences stay whole; blocks wanted of pieces
   int least;            // log2 of the fewest rows of a piece

@@ -514,10 +514,10 @@ static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The walks take two units a block where four would leave many CUs without one (4 sequences of 4096 rows, 64
-// heads: 872 us against 910; nine mixed sequences in 2777 rows, 24 heads: 153 against 158; 1024 rows of 2
-// sequences, 8 heads: 62 against 67); with more blocks four are faster, whose rows of B and C serve more units (32
-// sequences, 16384 rows: 1074 us against 1106).
+// The walks take two units a block where four would leave many CUs without one (4 sequences of 4096 rows, 64 heads,
+// 128 blocks of four: 870 us against 912; 1024 rows of 2 sequences, 8 heads: 73 against 80); with more blocks four are
+// faster, whose rows of B and C serve more units (nine mixed sequences in 2777 rows, 24 heads, 240 blocks: 140 us
+// against 142; 32 sequences in 16384 rows, 64 heads: 829 against 840).
 template <int NT, bool VEC>
 static hipError_t launch(const ScanBwdArgs& b, hipStream_t s) {
   const ScanArgs& a = b.s;
