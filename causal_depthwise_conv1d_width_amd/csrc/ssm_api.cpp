@@ -110,9 +110,10 @@ struct BwdPlan {
   int hsplit;
 };
 // Blocks of the chunk kernel: one a chunk and group; heads of a group go to several blocks (FP32
-// parts of dB and dC, added by another kernel) only where that many blocks would leave CUs idle
-// (2777 rows, 24 heads in 2 groups: 150 us with 256, 152 with 512, 168 with 1024).
-constexpr int64_t kWantChunkBlocks = 512;
+// parts of dB and dC, added by another kernel) only where that many blocks would leave CUs idle: up to one a CU, as more
+// parts cost more than they hide.  The backward with 256, 512 and 1024 blocks: 2777 rows, 24 heads in 2 groups, 133, 140
+// and 151 us; 1024 rows, 64 heads in 4 groups, 124, 133 and 149; 4096 rows, 64 heads in one group, 343, 339 and 333.
+constexpr int64_t kWantChunkBlocks = 256;
 BwdPlan plan_bwd(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows) {
   BwdPlan p{};
   p.f = plan_fwd(s, rows, nseq, batch_rows, kCutBwd);
