@@ -8,12 +8,13 @@
 // and of its unit's state, which it holds transposed ([n, p]: registers n), as the operand that C S needs.
 // Shared memory feeds the matrix instructions: with four units and PB = 2 a wave uses every B, C and score operand
 // twice.  The 256-column state tile leaves no registers for that: two units, PB = 1.
-// The decayed scores and the state's operand in C S are rounded to bf16 once each: y is bf16.  The new state's
+// Exponents of decays between two rows are differences of 64-bit sums (Rate::exponent).  The decayed scores and the
+// state's operand in C S are rounded to bf16 once each: y is bf16.  The new state's
 // terms enter as two bf16 parts, 2^-16 of a term: a pool came out 0.6e-7 to 3.5e-7 off; a third part costs 6%.
 // Bound by what two waves a SIMD leave of the waves' own latency, shared memory reads first.  64 heads of 64
 // columns, N = 128:
-// 16384 rows of 4 sequences 134 us (290 TFLOP/s of the formula's products) and 64 us for the walk before
-// and the join; 32512 rows of 64 prompts 376 us.
+// 16384 rows of 4 sequences 140 us (280 TFLOP/s of the formula's products) and 64 us for the walk before
+// and the join; 32512 rows of 64 prompts 385 us.
 #include "ssm_state.h"
 
 namespace cssm {

@@ -46,9 +46,10 @@ def _empty(like, shape, dtype, stream):
 
 def _result(like, shape, dtype, stream):
     """A new array for the caller, who may drop it while the current stream still uses it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
     t = _empty(like, shape, dtype, stream)
-    if stream is not None:
-        t.record_stream(torch.cuda.current_stream(t.device))
+    t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
 
