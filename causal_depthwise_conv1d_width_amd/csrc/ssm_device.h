@@ -97,6 +97,14 @@ __device__ __forceinline__ float row16_sum(float v) {
   v += dpp0<0x118, 0xf>(v);
   return v;
 }
+// sums over the lanes from this one to the end of its row; the row's sum in lane 0 of the row
+__device__ __forceinline__ float row16_suffix(float v) {
+  v += dpp0<0x101, 0xf>(v);
+  v += dpp0<0x102, 0xf>(v);
+  v += dpp0<0x104, 0xf>(v);
+  v += dpp0<0x108, 0xf>(v);
+  return v;
+}
 __device__ __forceinline__ float wave_sum(float v) { return lane_value(wave_prefix(v), 63); }
 
 // ------------------------------------------------------------------ sequences, pieces, chunks

@@ -160,9 +160,9 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
       u += s_u[k][lane];
       trace += s_trace[t & 1][k];
     }
-    // dl of row r takes K_ij d_j of all i >= r > j.  Differences of the 64 rows' and columns' sums would lose it in
+    // dl of row r takes K_ij d_j of all i >= r > j.  Differences of rows' and columns' sums would lose it in
     // what cancels; by blocks of 16, with r in block m: rows i >= r of the blocks left of the diagonal's, columns j < r
-    // of those below it, all of the blocks below and left of it, and only in the diagonal's a difference
+    // of those below it, all of the blocks below and left of it, and the diagonal's own sum as the scores left it
     const int m = lane >> 4;
     float left = 0.f, below = 0.f, on = 0.f, corner[2] = {0.f, 0.f};
 #pragma unroll
@@ -170,15 +170,15 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
       const float r = s_row[t & 1][k][lane], c = s_col[t & 1][k][lane];
       left += k < m ? r : 0.f;
       below += k > m ? d * c : 0.f;
-      on += k == m ? r - d * c : 0.f;
+      on += k == m ? r : 0.f;
       col += k >= m ? c : 0.f;
       if (k == 0) corner[0] = m >= 2 ? r : 0.f;
       if (k <= 1) corner[1] += m == 3 ? r : 0.f;
     }
     const float corner1 = wave_sum(corner[0]), corner2 = wave_sum(corner[1]);
-    const float rows_on = dpp0<0x140, 0xf>(row16_sum(dpp0<0x140, 0xf>(left + on)));  // mirrored: rows >= this one
+    const float rows_on = row16_suffix(left);  // rows >= this one
     const float columns = dpp0<0x111, 0xf>(row16_sum(below));
-    const float inside = rows_on + columns + (m == 1 ? corner1 : m == 2 ? corner2 : 0.f);
+    const float inside = rows_on + on + columns + (m == 1 ? corner1 : m == 2 ? corner2 : 0.f);
     const float suffix = __shfl(wave_prefix(__shfl(rint, 63 - lane)), 63 - lane) + inside;  // rows >= this one
     const float before = dpp0<0x138, 0xf>(wave_prefix(d * u));                              // rows < this one
     dl_sum += se[63] * dots + suffix + before;
@@ -241,8 +241,8 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
     phase();
     __syncthreads();
 
-    // score block (ib, jb), G its C B^T; the diagonal's K is in its row's and its column's sum alike and is
-    // kept out of both
+    // score block (ib, jb), G its C B^T.  s_row: a row's sum of K_ij d_j, on the diagonal row r's of all i >= r > j of
+    // the block.  The diagonal's own K is kept out of both sums.
     auto scores = [&](const int ib, const int jb) {
       f32x4 G = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -264,9 +264,9 @@ __global__ __launch_bounds__(kThreads, NT > 128 ? 1 : 2) void ssm_scan_bwd_kerne
         on_diagonal = here ? K : on_diagonal;
         trace += here ? W[r] : 0.f;
         K = here ? 0.f : K;
-        row = __builtin_fmaf(dj[r], K, row);
-        const float c = row16_sum(K);
-        if (i == 15) s_col[t & 1][ib][16 * jb + 4 * g + r] = c;
+        const float from = row16_suffix(K);  // rows >= i of column j
+        if (i == 0) s_col[t & 1][ib][16 * jb + 4 * g + r] = from;
+        row = __builtin_fmaf(dj[r], ib != jb ? K : (4 * g + r < i ? from : 0.f), row);
       }
       *reinterpret_cast<u32x2*>(sZ + at<64>(16 * ib + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(z[0], z[1]), pk_bf16(z[2], z[3])};
       *reinterpret_cast<u32x2*>(sG + at<64>(16 * ib + i, 16 * jb + 4 * g)) = u32x2{pk_bf16(gm[0], gm[1]), pk_bf16(gm[2], gm[3])};

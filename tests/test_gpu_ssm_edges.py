@@ -215,3 +215,26 @@ def test_non_finite_rows_of_B_and_C():
             which[t, 1, 9] = keep
             assert ny[rows, 2:].isnan().all()
             same_but(ny, y, (rows, slice(2, 4)), t)
+
+
+@pytest.mark.parametrize("drop", [100.0, 1e5, 1e30])
+@pytest.mark.parametrize("N", [64, 200])
+def test_gradients_of_sudden_decays(drop, N):
+    """The gradient of a step that drops the state is not its neighbours' rounding errors, and so not that times the
+    step in dA."""
+    p = base.Problem([150, 64], 4, 64, 2, N, seed=29, decay=1.0)
+    p.dt = p.dt.abs() * 0.1
+    p.bias = torch.zeros_like(p.bias)
+    for t in (10, 33, 34, 80, 150, 163):
+        p.dt[t], p.x[t], p.B[t] = drop, 0, 0
+    (_, _, g), (_, _, gm) = p.reference(p.S0, sp=False, dy=p.dy.cpu(), dS=p.dS.cpu())
+    b = cc.ssm_scan_bwd(p.dy, *p.args(), cu_seqlens=p.cu, dt_softplus=False, initial_state=p.S0, dfinal_state=p.dS)
+    for k in ("ddt", "dA", "ddt_bias"):
+        base.close(getattr(b, k), g[k], gm[k], 0.0, base.FINE, k)
+    base.close(b.dinitial_state, g["dS0"], gm["dS0"], 0.0, base.FINE, "dinitial_state")
+
+
+def test_gradients_beside_much_larger_ones():
+    """Small products, fast decays: a row's ddt against its own terms."""
+    p = base.Problem([1100, 127, 200, 200], 4, 1, 2, 1, seed=936630773, dt32=True, decay=30.0, step=1.0)
+    base.check_bwd(p, p.S0, p.dS)
