@@ -223,6 +223,15 @@ __device__ __forceinline__ Piece find_piece(const Seqs& q, int64_t it, int seg, 
   return p;
 }
 
+// The rows of the piece that a chunk at `row` of the sequence [s, e) belongs to.
+__device__ __forceinline__ void piece_around(int64_t s, int64_t e, int64_t row, int seg, int64_t& r0, int64_t& r1) {
+  r0 = s, r1 = e;
+  if (seg == 0) return;
+  const int64_t last = (e - 1 - s) >> seg, at = (row + kChunk - 1 - s) >> seg, j = at < last ? at : last;
+  if (j > 0) r0 = (s + (j << seg)) & ~(int64_t)(kChunk - 1);
+  if (j < last) r1 = (s + ((j + 1) << seg)) & ~(int64_t)(kChunk - 1);
+}
+
 __device__ __forceinline__ int64_t chunk_end(int64_t r, int64_t r1) {
   const int64_t c = (r & ~(int64_t)(kChunk - 1)) + kChunk;
   return c < r1 ? c : r1;

@@ -110,6 +110,13 @@ __device__ __forceinline__ bool starts_from_state(const ScanArgs& a, int64_t seq
   return a.init && (a.has_init ? __builtin_amdgcn_readfirstlane(a.has_init[seq]) != 0 : a.ci == nullptr);
 }
 
+// The backward's walks (TURN) hold the state with a sign that turns from chunk to chunk of a piece, as does what they
+// store.  Accumulated by matrix instructions, it comes out a little low, whatever its sign (by 0.09 * 2^-24 of its rms
+// after 16 chunks).  With x, B and C that have a mean, such an offset of the adjoints adds up over all rows in dA,
+// whose own terms cancel with dy of both signs: 0.8e-6 to 1.9e-6 of dA over 16384 rows, 1e-7 to 3e-7 with the turns,
+// which cost nothing (the signs are those of the weights and of the decay).
+__device__ __forceinline__ float turn_of(int64_t chunks) { return chunks & 1 ? -1.f : 1.f; }
+
 // A block walks U units of a group (they share v), two waves a unit, each with 32 rows p of the state: a wave reads
 // a v operand for two row blocks, which halves the shared memory traffic that bounds the walk.
 // LOCAL: from zeros, the end state goes to the piece's place (pieces whose end nobody needs do nothing).
@@ -121,7 +128,7 @@ struct StateShared {
   __align__(16) float w[2][U][64];  // weights of this chunk and the next one, by unit
   float total[2][U];
 };
-template <int NT, int U, int PARTS, bool VEC, bool REV, bool STORE>
+template <int NT, int U, int PARTS, bool VEC, bool REV, bool STORE, bool TURN>
 __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U>& sh) {
   constexpr int T = 128 * U, WU = 2;  // threads, and waves a unit
   constexpr int NB = NT / 16;         // 16-column blocks of the state, with two 16-row blocks a wave
@@ -193,18 +200,20 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
   };
   // a chunk's weights into buffer `at` by a unit's first wave; forward, a lane's row counts from the end
   const int my = REV ? lane : 63 - lane;
-  auto weights = [&](int rows, int at) {
+  auto weights = [&](int rows, int at, float sign) {
     const float d = rate.step(raw, my < rows);
     const float L = wave_prefix(d * rate.A2);
     // the rows after this one: the previous lane's sum
-    sh.w[at][un][my] = REV ? ex2(L) : ex2(dpp0<0x138, 0xf>(L)) * d;
+    const float v = REV ? ex2(L) : ex2(dpp0<0x138, 0xf>(L)) * d;
+    sh.w[at][un][my] = TURN ? sign * v : v;
     if (lane == 63) sh.total[at][un] = L;
   };
   Chunks<REV> c(pc.r0, pc.r1);
   int rows = c.rows();
+  float turn = 1.f;  // the state's sign before the chunk
   load(c, rows);
   raw = raw_step(a, c.c0, rows, my, me.h);
-  if (w == 0) weights(rows, 0);
+  if (w == 0) weights(rows, 0, -turn);
   Chunks<REV> after = c;
   int after_rows = rows;  // the chunk whose raw steps come next
   after = step_chunk(after, after_rows);
@@ -218,7 +227,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
     const float* sw = sh.w[buf][un];
     c = step_chunk(c, rows);  // rows == 0: that was the last one
     load(c, rows);
-    if (w == 0) weights(rows, buf ^ 1);
+    if (w == 0) weights(rows, buf ^ 1, turn);  // the chunk after turns back
     after = step_chunk(after, after_rows);
     raw = raw_step(a, after.c0, after_rows, my, me.h);
     if constexpr (STORE) {  // operand order: [row half][n block of 16][p step of 32][lane] four FP32 values
@@ -233,7 +242,8 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
     }
     const float total = sh.total[buf][un];
     log_total += total;
-    const float et = ex2(total);
+    const float et = TURN ? -ex2(total) : ex2(total);
+    if (TURN) turn = -turn;
 #pragma unroll
     for (int pb = 0; pb < 2; ++pb)
 #pragma unroll
@@ -265,7 +275,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) place[(p0 + 16 * pb + 4 * g + r) * NT + 16 * nb + i] = S[pb][nb][r];
+        for (int r = 0; r < 4; ++r) place[(p0 + 16 * pb + 4 * g + r) * NT + 16 * nb + i] = turn * S[pb][nb][r];
     if (w == 0 && lane == 0 && me.p_first == 0) k.decay[us.item * a.H + me.h] = log_total;
   } else if (REV && first && k.end) {
     float* dst = k.end + state_at;
@@ -276,7 +286,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int p = p0 + 16 * pb + 4 * g + r, n = 16 * nb + i;
-          if (p < me.pn && n < a.N) dst[(int64_t)p * a.N + n] = S[pb][nb][r];
+          if (p < me.pn && n < a.N) dst[(int64_t)p * a.N + n] = turn * S[pb][nb][r];
         }
   }
 }
@@ -284,7 +294,7 @@ __device__ __forceinline__ void state_walk(const StateArgs& k, StateShared<NT, U
 template <int NT, int U, bool VEC>
 __global__ __launch_bounds__(128 * U, U > 2 || NT <= 128 ? 2 : 1) void ssm_state_local_kernel(StateArgs k) {
   __shared__ StateShared<NT, U> sh;
-  state_walk<NT, U, 2, VEC, false, false>(k, sh);
+  state_walk<NT, U, 2, VEC, false, false, false>(k, sh);
 }
 
 // Local end states of a sequence's pieces -> start states, in place, in the order of the walk:

@@ -238,3 +238,23 @@ def test_gradients_beside_much_larger_ones():
     """Small products, fast decays: a row's ddt against its own terms."""
     p = base.Problem([1100, 127, 200, 200], 4, 1, 2, 1, seed=936630773, dt32=True, decay=30.0, step=1.0)
     base.check_bwd(p, p.S0, p.dS)
+
+
+@pytest.mark.parametrize("rows,seqlen", [(4096, 4096), (4096, 1024)])
+def test_decay_rate_gradient_has_no_offset(rows, seqlen):
+    """dA is odd in dy.  Where x, B and C have a mean, an offset of the adjoints adds up in it over all rows while its
+    own terms cancel.  A term's four factors (step, decay, state, adjoint) are off by 2^-24 at most: 2^-22 a call if all
+    rows were off the same way, twice that for two calls."""
+    print(f"[gpu] offset of dA, {rows} rows of {seqlen}", flush=True)
+    H, P, N = 32, 64, 128
+    gen = torch.Generator().manual_seed(30)
+
+    def rnd(*shape):
+        return torch.nn.functional.silu(torch.randn(shape, generator=gen)).bfloat16().cuda()
+
+    x, B, C = rnd(rows, H, P), rnd(rows, 1, N), rnd(rows, 1, N)
+    dt = (0.02 * (1 + torch.rand(rows, H, generator=gen))).cuda()
+    A = -torch.linspace(0.2, 3, H).cuda()
+    dy = torch.randn(rows, H, P, generator=gen).bfloat16().cuda()
+    up, down = [cc.ssm_scan_bwd(s * dy, x, dt, A, B, C, seqlen=seqlen, dt_softplus=False).dA.double() for s in (1, -1)]
+    assert (up + down).norm() <= 2.0 ** -21 * up.norm(), float((up + down).norm() / up.norm())
