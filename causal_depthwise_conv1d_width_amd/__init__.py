@@ -26,6 +26,14 @@ What follows the convolution in a mixer block (C ABI in include/ssm.h, binding i
   ssm_state_update     one decode step per sequence against its state slot
   gated_norm_fwd / gated_norm_bwd        RMS norm with its gate, by groups of channels
   residual_norm_fwd / residual_norm_bwd  residual addition with a scale and the next RMS norm
+
+The gated delta rule instead of the scan, the layer norm instead of the RMS norm, and the pools' slots (C ABI in
+include/delta.h, binding in ``delta.py``):
+  delta_scan_fwd / delta_scan_bwd  gated delta rule over packed rows, chunked, with the scan's sequences and states,
+                       and its training backward
+  delta_state_update   one decode step per sequence against its state slot
+  layer_norm_fwd / layer_norm_bwd  layer norm, alone or of the residual's sum
+  state_copy           slots of any of the pools forked, swapped, moved or cleared in one call
 """
 import ctypes
 
@@ -34,20 +42,26 @@ from . import _lib
 _SSM = ["ssm_scan_fwd", "ssm_scan_bwd", "SsmGrads", "ssm_state_update", "ssm_scan_fwd_workspace_bytes",
         "ssm_scan_bwd_workspace_bytes", "gated_norm_fwd", "gated_norm_bwd", "residual_norm_fwd", "residual_norm_bwd",
         "norm_bwd_workspace_bytes"]
+_DELTA = ["delta_scan_fwd", "delta_scan_bwd", "DeltaGrads", "delta_state_update", "delta_scan_fwd_workspace_bytes",
+          "delta_scan_bwd_workspace_bytes", "layer_norm_fwd", "layer_norm_bwd", "LayerNormGrads",
+          "layer_norm_bwd_workspace_bytes", "state_copy"]
 __all__ = ["conv1d_fwd", "conv1d_state_update", "conv1d_state_update_spec", "conv1d_bwd", "conv1d_bwd_combine",
            "conv1d_bwd_noalloc", "conv1d_fwd_cf",
            "conv1d_bwd_cf", "conv1d_bwd_cf_workspace_bytes", "conv1d_fwd_workspace_bytes",
-           "conv1d_bwd_workspace_bytes", "library_path"] + _SSM
+           "conv1d_bwd_workspace_bytes", "library_path"] + _SSM + _DELTA
 
 library_path = _lib.LIB_PATH
 
 
 def __getattr__(name):
-    """The functions of ssm.py at their first use: that module needs torch, this package's import does not."""
-    if name not in _SSM:
+    """The functions of ssm.py and delta.py at their first use: these need torch, this package's import does not."""
+    if name in _SSM:
+        from . import ssm as module
+    elif name in _DELTA:
+        from . import delta as module
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import ssm
-    globals().update((n, getattr(ssm, n)) for n in _SSM)
+    globals().update((n, getattr(module, n)) for n in (_SSM if name in _SSM else _DELTA))
     return globals()[name]
 
 

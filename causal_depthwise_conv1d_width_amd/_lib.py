@@ -84,8 +84,37 @@ SSM_SIGNATURES = {
     "norm_bwd_workspace_bytes": (c_size, [c_i64, c_i64, c_i64]),
 }
 
+
+class DeltaShape(ctypes.Structure):
+    _fields_ = [("H", c_i64), ("P", c_i64), ("G", c_i64), ("N", c_i64), ("gate_dtype", c_int), ("dt_softplus", c_int),
+                ("qk_norm", c_int), ("scale", ctypes.c_float), ("beta_max", ctypes.c_float), ("norm_eps", ctypes.c_float)]
+
+
+class SlotPool(ctypes.Structure):
+    _fields_ = [("ptr", c_p), ("slots", c_i64), ("slot_bytes", c_i64), ("s_slot", c_i64)]
+
+
+_DELTA_SHAPE = ctypes.POINTER(DeltaShape)
+
+# name -> (restype, argtypes); must match include/delta.h
+DELTA_SIGNATURES = {
+    "delta_scan_fwd": (c_int, [_DELTA_SHAPE, c_i64, *_ROWS * 5, c_p, c_p, _SEQ, _STATES, *_ROWS, c_p, c_size, c_p]),
+    "delta_scan_fwd_workspace_bytes": (c_size, [_DELTA_SHAPE, c_i64, c_i64]),
+    "delta_scan_bwd": (c_int, [_DELTA_SHAPE, c_i64, *_ROWS * 6, c_p, c_p, _SEQ, c_p, c_p, *_ROWS * 5, c_p, c_p, c_p, c_p,
+                               c_size, c_p]),
+    "delta_scan_bwd_workspace_bytes": (c_size, [_DELTA_SHAPE, c_i64, c_i64]),
+    "delta_state_update": (c_int, [_DELTA_SHAPE, c_i64, *_ROWS * 5, c_p, c_p, _STATES, *_ROWS, c_p]),
+    "layer_norm_fwd": (c_int, [c_i64, c_i64, *_ROWS, *_ROWS, c_int, ctypes.c_float, c_p, c_p, c_int, ctypes.c_float, *_ROWS,
+                               *_ROWS, c_p]),
+    "layer_norm_bwd": (c_int, [c_i64, c_i64, *_ROWS, *_ROWS, *_ROWS, c_int, ctypes.c_float, c_p, c_int, ctypes.c_float,
+                               *_ROWS, *_ROWS, c_p, c_p, c_p, c_size, c_p]),
+    "layer_norm_bwd_workspace_bytes": (c_size, [c_i64, c_i64]),
+    "state_copy": (c_int, [ctypes.POINTER(SlotPool), c_int, c_i64, c_p, c_p, c_p]),
+}
+
 _LIB = None
 _SSM = None
+_DELTA = None
 
 
 def load(path=LIB_PATH):
@@ -108,17 +137,29 @@ def load(path=LIB_PATH):
     return lib
 
 
+def _with(signatures):
+    lib = load()
+    for name, (res, args) in signatures.items():
+        fn = getattr(lib, name)
+        fn.restype = res
+        fn.argtypes = args
+    return lib
+
+
 def load_ssm():
     """The same library with the entry points of include/ssm.h."""
     global _SSM
     if _SSM is None:
-        lib = load()
-        for name, (res, args) in SSM_SIGNATURES.items():
-            fn = getattr(lib, name)
-            fn.restype = res
-            fn.argtypes = args
-        _SSM = lib
+        _SSM = _with(SSM_SIGNATURES)
     return _SSM
+
+
+def load_delta():
+    """The same library with the entry points of include/delta.h."""
+    global _DELTA
+    if _DELTA is None:
+        _DELTA = _with(DELTA_SIGNATURES)
+    return _DELTA
 
 
 class Conv1dError(RuntimeError):

@@ -16,6 +16,8 @@ LIB = os.path.join(PKG, "libcausal_conv1d.so")
 SOURCES = ["conv1d_fwd.hip", "conv1d_bwd.hip", "conv1d_cf.hip", "conv1d_api.cpp"]
 # the scan, step and norm operators (include/ssm.h); the kernels tile through LDS, unlike SOURCES
 SSM_SOURCES = ["ssm_scan.hip", "ssm_scan_bwd.hip", "ssm_step.hip", "norm.hip", "ssm_api.cpp"]
+# the gated delta rule, the layer norm and slot copies (include/delta.h)
+DELTA_SOURCES = ["delta_chunk.hip", "delta_scan.hip", "delta_step.hip", "layer_norm.hip", "slots.hip", "delta_api.cpp"]
 ARCH = "gfx950"
 
 
@@ -42,7 +44,7 @@ def build(out=LIB, jobs=4, verbose=False, defines=()):
     objdir = os.path.join(PKG, "_build", os.path.basename(out))
     os.makedirs(objdir, exist_ok=True)
     objs, procs = [], []
-    for src in SOURCES + SSM_SOURCES:
+    for src in SOURCES + SSM_SOURCES + DELTA_SOURCES:
         obj = os.path.join(objdir, src + ".o")
         lang = ["-x", "hip"] if src.endswith(".hip") else []
         cmd = ["hipcc", *hipcc_flags(), *[f"-D{d}" for d in defines], *lang, "-c", os.path.join(CSRC, src), "-o", obj]

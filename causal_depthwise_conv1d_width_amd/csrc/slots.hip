@@ -1,0 +1,65 @@
+// slots.hip -- slots of the pools copied, swapped and cleared.
+//
+// Bytes read once and written once: bound by memory.  A source may be another pair's target, so every read of a byte range
+// has to come before its writes: a block takes one strip of 2^strip 16-byte pieces of all n pairs' slots, holds them in
+// registers (K pieces a thread), waits at one barrier and writes them.  Blocks share no bytes, so nothing else is ordered,
+// no copy in memory is needed, and all pools go in one launch.  A strip is the widest that the registers hold for n
+// pairs: 64 pairs, 256 bytes.
+#include "delta_launch.h"
+
+namespace cssm {
+
+typedef uint32_t piece __attribute__((ext_vector_type(4)));
+typedef uint32_t piece_a1 __attribute__((ext_vector_type(4), aligned(1)));
+
+template <int T, int K>
+__global__ __launch_bounds__(T) void slots_kernel(SlotArgs a) {
+  int p = 0;
+  while (p + 1 < a.pools && blockIdx.x >= a.first[p + 1]) ++p;
+  char* base = a.ptr[p];
+  const int64_t slots = a.slots[p], s_slot = a.s_slot[p], bytes = a.bytes[p];
+  const int64_t at0 = (int64_t)(blockIdx.x - a.first[p]) << (a.strip + 4);
+  const int all = a.n << a.strip;
+  piece v[K];
+  char* to[K];
+  int size[K];  // bytes of the piece, 0: nothing to write
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int e = threadIdx.x + T * k, pair = e >> a.strip;
+    const int64_t at = at0 + (int64_t)(e & ((1 << a.strip) - 1)) * 16;
+    size[k] = 0;
+    v[k] = piece{0u, 0u, 0u, 0u};
+    if (e >= all || at >= bytes) continue;
+    const int64_t s = a.source[pair], t = a.target[pair];
+    if (t < 0 || t >= slots || s >= slots || s == t) continue;
+    size[k] = bytes - at < 16 ? (int)(bytes - at) : 16;
+    to[k] = base + t * s_slot + at;
+    if (s < 0) continue;
+    const char* from = base + s * s_slot + at;
+    if (size[k] == 16) {
+      v[k] = *reinterpret_cast<const piece_a1*>(from);
+    } else {
+      for (int c = 0; c < 15; ++c)
+        if (c < size[k]) v[k][c >> 2] |= (uint32_t)(uint8_t)from[c] << (8 * (c & 3));
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's reads have their values before any wave writes
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (size[k] == 16) {
+      *reinterpret_cast<piece_a1*>(to[k]) = v[k];
+    } else if (size[k] > 0) {
+      for (int c = 0; c < 15; ++c)
+        if (c < size[k]) to[k][c] = (char)(v[k][c >> 2] >> (8 * (c & 3)));
+    }
+  }
+}
+
+hipError_t launch_slots(const SlotArgs& a, int threads, int pieces, uint32_t blocks, hipStream_t s) {
+  if (threads == 256 && pieces == 4) slots_kernel<256, 4><<<blocks, 256, 0, s>>>(a);
+  else slots_kernel<1024, 8><<<blocks, 1024, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace cssm

@@ -5,59 +5,11 @@
 
 #include <stdint.h>
 
-#include "ssm_launch.h"
+#include "api_checks.h"
 
 using namespace cssm;
 
 namespace {
-
-constexpr int64_t kMaxElems = (int64_t)1 << 48;  // no extent below overflows 64-bit bytes
-constexpr int64_t kMaxBlocks = 0x7fffffff;
-
-bool mul_ok(int64_t a, int64_t b) {
-  return a >= 0 && b >= 0 && a <= kMaxElems && b <= kMaxElems && (b == 0 || a <= kMaxElems / b);
-}
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-bool dtype_ok(int d) { return d == CONV1D_BF16 || d == CONV1D_F32; }
-int64_t dsize(int d) { return d == CONV1D_F32 ? 4 : 2; }
-
-// Byte range of a strided array: rows of `len` bytes, `ld` bytes apart.
-struct Span {
-  uintptr_t lo = 0, ld = 0, rows = 0, len = 0;
-  uintptr_t hi() const { return rows ? lo + (rows - 1) * ld + len : lo; }
-};
-Span span(const void* p, int64_t rows, int64_t len, int64_t ld, int64_t esz) {
-  Span s;
-  if (!p || rows <= 0 || len <= 0) return s;
-  s.lo = reinterpret_cast<uintptr_t>(p);
-  s.ld = (uintptr_t)(ld * esz);
-  s.rows = (uintptr_t)rows;
-  s.len = (uintptr_t)(len * esz);
-  return s;
-}
-Span span(const void* p, int64_t bytes) { return span(p, 1, bytes, bytes, 1); }
-// Whether two arrays share a byte.  Column ranges of the same wider rows (equal row strides) do not,
-// though their address ranges interleave.
-bool overlap(const Span& a, const Span& b) {
-  if (!a.rows || !b.rows || a.lo >= b.hi() || b.lo >= a.hi()) return false;
-  if (a.rows > 1 && b.rows > 1 && a.ld == b.ld) {
-    const uintptr_t ld = a.ld;
-    const uintptr_t off = a.lo >= b.lo ? (a.lo - b.lo) % ld : (ld - (b.lo - a.lo) % ld) % ld;  // a's start in b's rows
-    return !(off >= b.len && off + a.len <= ld);
-  }
-  return true;
-}
-template <int NO, int NI>
-bool clash(const Span (&outs)[NO], const Span (&ins)[NI]) {
-  for (int i = 0; i < NO; ++i) {
-    for (const Span& in : ins)
-      if (overlap(outs[i], in)) return true;
-    for (int j = i + 1; j < NO; ++j)
-      if (overlap(outs[i], outs[j])) return true;
-  }
-  return false;
-}
 
 // log2 of a piece's rows, 0 for whole sequences.  A block walks a piece chunk by chunk for kUnits units.
 // Sequences are cut into pieces where whole ones give too few blocks, or, with offsets (the host does not
@@ -86,8 +38,6 @@ int piece_log2(const ssm_shape* s, int64_t rows, int64_t nseq, bool batch_rows, 
   while (((int64_t)1 << seg) * want < rows * sets) ++seg;
   return ((int64_t)1 << seg) < (batch_rows ? rows / nseq : rows - nseq + 1) ? seg : 0;
 }
-
-int64_t align_up(int64_t v) { return (v + 255) / 256 * 256; }
 
 struct FwdPlan {
   int seg;
@@ -146,52 +96,6 @@ bool shape_ok(const ssm_shape* s) {
   return s && s->H >= 1 && s->P >= 1 && s->G >= 1 && s->N >= 1 && s->N <= kMaxState && s->H % s->G == 0 &&
          s->H <= (1 << 20) && s->P <= (1 << 20) && dtype_ok(s->dt_dtype) && (s->dt_softplus == 0 || s->dt_softplus == 1);
 }
-
-int check_seq(const conv1d_seq* q, int64_t rows, int64_t* nseq) {
-  if (!q || q->seq_idx) return CONV1D_EINVAL;
-  if (q->cu_seqlens) {
-    if (q->nseq < 0) return CONV1D_EINVAL;
-    *nseq = q->nseq;
-    return CONV1D_OK;
-  }
-  if (q->seqlen < 1 || rows % q->seqlen != 0) return CONV1D_EINVAL;
-  *nseq = rows / q->seqlen;
-  return CONV1D_OK;
-}
-
-// States argument against nseq; fills the kernel's fields and the byte ranges.
-int check_states(const ssm_shape* s, const ssm_states* st, int64_t nseq, ScanArgs* a, Span* init, Span* fin, Span* ci,
-                 Span* hi) {
-  if (!st || (!st->initial && !st->final)) {
-    if (st && st->cache_indices) return CONV1D_EINVAL;
-    return CONV1D_OK;
-  }
-  const int64_t hpn = s->H * s->P * s->N;
-  if (st->slots < 1 || st->s_slot < hpn || !mul_ok(st->slots, st->s_slot)) return CONV1D_EINVAL;
-  if (!st->cache_indices && st->slots < nseq) return CONV1D_EINVAL;
-  *init = span(st->initial, st->slots, hpn, st->s_slot, 4);
-  *fin = span(st->final, st->slots, hpn, st->s_slot, 4);
-  if (st->initial != st->final && overlap(*init, *fin)) return CONV1D_EINVAL;
-  *ci = span(st->cache_indices, nseq * 4);
-  *hi = span(st->has_initial_state, nseq);
-  a->init = st->initial;
-  a->fin = st->final;
-  a->slots = st->slots;
-  a->s_slot = st->s_slot;
-  a->ci = st->cache_indices;
-  a->has_init = st->has_initial_state;
-  return CONV1D_OK;
-}
-
-struct Operand {
-  const void* p;
-  int64_t ld, len;
-};
-bool operand_ok(const Operand& o, int64_t rows) {
-  return (rows == 0 || o.p) && o.ld >= o.len && mul_ok(rows, o.ld);
-}
-// The scan addresses the 64 rows of a chunk by 32-bit byte offsets from the first.
-bool scan_operand_ok(const Operand& o, int64_t rows) { return operand_ok(o, rows) && o.ld <= SSM_MAX_ROW_STRIDE; }
 
 void fill(ScanArgs* a, const ssm_shape* s, int64_t rows, const void* x, int64_t x_ld, const void* dt, int64_t dt_ld,
           const float* A, const void* B, int64_t B_ld, const void* C, int64_t C_ld, const float* D,
@@ -268,7 +172,7 @@ int ssm_scan_fwd(const ssm_shape* shape, int64_t rows, const void* x, int64_t x_
   if (!aligned(x, 2) || !aligned(B, 2) || !aligned(C, 2) || !aligned(y, 2) || !aligned(dt, dte)) return CONV1D_EINVAL;
   ScanArgs a{};
   Span si, sf, sci, shi;
-  if (check_states(shape, states, nseq, &a, &si, &sf, &sci, &shi) != CONV1D_OK) return CONV1D_EINVAL;
+  if (check_states(shape->H * shape->P * shape->N, states, nseq, &a, &si, &sf, &sci, &shi) != CONV1D_OK) return CONV1D_EINVAL;
   const FwdPlan p = plan_fwd(shape, rows, nseq, !seq->cu_seqlens);
   if ((size_t)p.bytes > ws_bytes || (p.bytes && !ws)) return CONV1D_EWORKSPACE;
   if (p.bytes && !aligned(ws, 16)) return CONV1D_EINVAL;
@@ -354,7 +258,7 @@ int ssm_state_update(const ssm_shape* shape, int64_t nseq, const void* x, int64_
     if (!operand_ok(o, nseq) || !aligned(o.p, o.p == dt ? dte : 2)) return CONV1D_EINVAL;
   ScanArgs s{};
   Span si, sf, sci, shi;
-  if (check_states(shape, pool, nseq, &s, &si, &sf, &sci, &shi) != CONV1D_OK) return CONV1D_EINVAL;
+  if (check_states(hp * shape->N, pool, nseq, &s, &si, &sf, &sci, &shi) != CONV1D_OK) return CONV1D_EINVAL;
   const Span reads[8] = {span(x, nseq, hp, x_ld, 2), span(dt, nseq, H, dt_ld, dte), span(B, nseq, gn, B_ld, 2),
                          span(C, nseq, gn, C_ld, 2), span(A, H * 4), span(D, H * 4), span(dt_bias, H * 4), sci};
   const Span outs[2] = {span(y, nseq, hp, y_ld, 2), sf};
