@@ -17,7 +17,7 @@ SOURCES = ["conv1d_fwd.hip", "conv1d_bwd.hip", "conv1d_cf.hip", "conv1d_api.cpp"
 # the scan, step and norm operators (include/ssm.h); the kernels tile through LDS, unlike SOURCES
 SSM_SOURCES = ["ssm_scan.hip", "ssm_scan_bwd.hip", "ssm_step.hip", "norm.hip", "ssm_api.cpp"]
 # the gated delta rule, the layer norm and slot copies (include/delta.h)
-DELTA_SOURCES = ["delta_chunk.hip", "delta_scan.hip", "delta_step.hip", "layer_norm.hip", "slots.hip", "delta_api.cpp"]
+DELTA_SOURCES = ["delta_chunk.hip", "delta_scan.hip", "delta_scan_bwd.hip", "delta_step.hip", "layer_norm.hip", "slots.hip", "delta_api.cpp"]
 ARCH = "gfx950"
 
 

@@ -55,6 +55,25 @@ int layer_check(int64_t rows, int64_t d, const void* w, const void* bias, int w_
   return aligned(w, dsize(w_dtype)) && aligned(bias, dsize(w_dtype)) ? CONV1D_OK : CONV1D_EINVAL;
 }
 
+// Byte offsets into the backward's workspace.
+struct BwdPlan {
+  int64_t rec_rev, cs, ct, u, f, head, bytes;
+};
+BwdPlan plan_bwd(const delta_shape* s, int64_t rows, int64_t nseq) {
+  BwdPlan p{};
+  const int64_t ids = chunk_ids(rows, nseq), tiles = ids * s->H * ceil_div(s->P, kPTile);
+  const int64_t state = align_up(tiles * 64 * state_tile(s->N) * 4), values = align_up(tiles * 64 * 64 * 4);
+  int64_t at = align_up(ids * s->H * kRecFwd);
+  p.rec_rev = at, at += align_up(ids * s->H * kRecRev);
+  p.cs = at, at += state;
+  p.ct = at, at += state;
+  p.u = at, at += values;
+  p.f = at, at += values;
+  p.head = at, at += align_up(ids * s->H * 2 * 4);
+  p.bytes = at;
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -94,6 +113,64 @@ int delta_scan_fwd(const delta_shape* shape, int64_t rows, const void* q, int64_
   d.s.y_ld = y_ld;
   d.rec = static_cast<char*>(ws);
   return launch_delta_fwd(d, vec_ok(shape), stream) == hipSuccess ? CONV1D_OK : CONV1D_EHIP;
+}
+
+size_t delta_scan_bwd_workspace_bytes(const delta_shape* shape, int64_t rows, int64_t nseq) {
+  if (!shape_ok(shape) || rows < 0 || nseq <= 0 || !sizes_ok(shape, rows, nseq)) return 0;
+  return (size_t)plan_bwd(shape, rows, nseq).bytes;
+}
+
+int delta_scan_bwd(const delta_shape* shape, int64_t rows, const void* dy, int64_t dy_ld, const void* q, int64_t q_ld,
+                   const void* k, int64_t k_ld, const void* v, int64_t v_ld, const void* dt, int64_t dt_ld,
+                   const void* b, int64_t b_ld, const float* A, const float* dt_bias, const conv1d_seq* seq,
+                   const float* initial_state, const float* dfinal_state, void* dq, int64_t dq_ld, void* dk,
+                   int64_t dk_ld, void* dv, int64_t dv_ld, void* ddt, int64_t ddt_ld, void* db, int64_t db_ld,
+                   float* dA, float* ddt_bias, float* dinitial_state, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!shape_ok(shape) || rows < 0 || !A || !dA) return CONV1D_EINVAL;
+  int64_t nseq = 0;
+  if (check_seq(seq, rows, &nseq) != CONV1D_OK || !sizes_ok(shape, rows, nseq)) return CONV1D_EINVAL;
+  const int64_t H = shape->H, hp = H * shape->P, gn = shape->G * shape->N, e = dsize(shape->gate_dtype);
+  if (!mul_ok(nseq, hp * shape->N)) return CONV1D_EINVAL;
+  const int64_t states = nseq * hp * shape->N * 4;
+  const Operand ops[11] = {{dy, dy_ld, hp}, {q, q_ld, gn}, {k, k_ld, gn}, {v, v_ld, hp}, {dq, dq_ld, gn}, {dk, dk_ld, gn},
+                           {dv, dv_ld, hp}, {dt, dt_ld, H}, {b, b_ld, H}, {ddt, ddt_ld, H}, {db, db_ld, H}};
+  for (int i = 0; i < 11; ++i)
+    if (!scan_operand_ok(ops[i], rows) || !aligned(ops[i].p, i < 7 ? 2 : e)) return CONV1D_EINVAL;
+  const size_t need = delta_scan_bwd_workspace_bytes(shape, rows, nseq);
+  if (need > ws_bytes || (need && !ws)) return CONV1D_EWORKSPACE;
+  if (need && !aligned(ws, 16)) return CONV1D_EINVAL;
+  const Span reads[11] = {span(dy, rows, hp, dy_ld, 2), span(q, rows, gn, q_ld, 2), span(k, rows, gn, k_ld, 2),
+                          span(v, rows, hp, v_ld, 2), span(dt, rows, H, dt_ld, e), span(b, rows, H, b_ld, e),
+                          span(A, H * 4), span(dt_bias, H * 4), span(initial_state, states), span(dfinal_state, states),
+                          span(seq->cu_seqlens, (nseq + 1) * 4)};
+  const Span outs[9] = {span(dq, rows, gn, dq_ld, 2), span(dk, rows, gn, dk_ld, 2), span(dv, rows, hp, dv_ld, 2),
+                        span(ddt, rows, H, ddt_ld, e), span(db, rows, H, db_ld, e), span(dA, H * 4), span(ddt_bias, H * 4),
+                        span(dinitial_state, states), span(ws, (int64_t)need)};
+  if (clash(outs, reads)) return CONV1D_EINVAL;
+  DeltaBwdArgs g{};
+  g.dA = dA, g.dbias = ddt_bias;
+  g.d.s.H = (int)H;
+  if (nseq > 0) {
+    if (!launches_ok(shape, rows, nseq)) return CONV1D_EINVAL;
+    const BwdPlan p = plan_bwd(shape, rows, nseq);
+    char* w = static_cast<char*>(ws);
+    fill(&g.d, shape, rows, q, q_ld, k, k_ld, v, v_ld, dt, dt_ld, b, b_ld, A, dt_bias, seq, nseq);
+    g.d.s.init = initial_state;
+    g.d.s.slots = nseq;
+    g.d.s.s_slot = hp * shape->N;
+    g.d.rec = w;
+    g.dy = static_cast<const uint16_t*>(dy), g.dy_ld = dy_ld;
+    g.dfin = dfinal_state, g.dinit = dinitial_state;
+    g.dq = static_cast<uint16_t*>(dq), g.dq_ld = dq_ld;
+    g.dk = static_cast<uint16_t*>(dk), g.dk_ld = dk_ld;
+    g.dv = static_cast<uint16_t*>(dv), g.dv_ld = dv_ld;
+    g.ddt = ddt, g.ddt_ld = ddt_ld, g.db = db, g.db_ld = db_ld;
+    g.rec_rev = w + p.rec_rev;
+    g.cs = reinterpret_cast<float*>(w + p.cs), g.ct = reinterpret_cast<float*>(w + p.ct);
+    g.u = reinterpret_cast<float*>(w + p.u), g.f = reinterpret_cast<float*>(w + p.f);
+    g.head_part = reinterpret_cast<float*>(w + p.head);
+  }
+  return launch_delta_bwd(g, vec_ok(shape), stream) == hipSuccess ? CONV1D_OK : CONV1D_EHIP;
 }
 
 int delta_state_update(const delta_shape* shape, int64_t nseq, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
@@ -242,5 +319,3 @@ int state_copy(const slot_pool* pools, int npools, int64_t n, const int32_t* sou
 }
 
 }  // extern "C"
-extern "C" size_t delta_scan_bwd_workspace_bytes(const delta_shape*, int64_t, int64_t) { return 0; }
-extern "C" int delta_scan_bwd(const delta_shape*, int64_t, const void*, int64_t, const void*, int64_t, const void*, int64_t, const void*, int64_t, const void*, int64_t, const void*, int64_t, const float*, const float*, const conv1d_seq*, const float*, const float*, void*, int64_t, void*, int64_t, void*, int64_t, void*, int64_t, void*, int64_t, float*, float*, float*, void*, size_t, hipStream_t) { return CONV1D_EUNSUPPORTED; }

@@ -106,7 +106,7 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs d, char* rec
       double l = rate.exponent(step);
       const bool fine = __builtin_isfinite((float)l) && __builtin_isfinite(r) && __builtin_isfinite(kn);
       const uint64_t not_fine = __ballot(!fine);
-      const int bad = not_fine ? __builtin_ctzll(not_fine) : 64;
+      const int bad = not_fine && !BWD ? __builtin_ctzll(not_fine) : 64;  // backward, they may reach every row
       if (lane >= bad) l = 0.0, r = kn = qn = 0.f;
       const double L = wave_prefix(l);
       const double end = __shfl(L, 63);
@@ -148,8 +148,9 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs d, char* rec
           p[r] = in && col + r <= row ? qk[t][r] * (m * qni) : 0.f;
         }
         *reinterpret_cast<f32x4*>(sX + row * LD + col) = x;
-        store_tri<1>(rec + kRecT, tri_block(ib, jb), p, lane);
-        if constexpr (BWD) {  // column 16 jb + i in the lanes, rows in the registers
+        if constexpr (!BWD) {
+          store_tri<1>(rec + kRecT, tri_block(ib, jb), p, lane);
+        } else {  // column 16 jb + i in the lanes, rows in the registers
           const int c = 16 * jb + i, r0 = 16 * ib + 4 * g;
           const float knc = s_kn[c];
           f32x4 pt;

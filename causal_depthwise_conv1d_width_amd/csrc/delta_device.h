@@ -79,6 +79,27 @@ __device__ __forceinline__ int64_t chunk_id(const Piece& pc, int64_t c0, int64_t
   return c0 == pc.s ? n_chunk_slots + pc.seq : c0 >> 6;
 }
 
+// A record that the four waves copy to shared memory, 16 bytes a thread and step
+template <int BYTES, int T>
+struct RecordRegs {
+  u32x4 v[(BYTES / 16 + T - 1) / T];
+};
+template <int BYTES, int T>
+__device__ __forceinline__ void load_record(RecordRegs<BYTES, T>& t, const char* rec, bool in) {
+  const Rows r(rec, BYTES, 1, in ? BYTES : 0, 1);
+#pragma unroll
+  for (int k = 0; k < (BYTES / 16 + T - 1) / T; ++k)
+    t.v[k] = __builtin_amdgcn_raw_buffer_load_b128(r.r, (int)((threadIdx.x + T * k) * 16), 0, 0);
+}
+template <int BYTES, int T>
+__device__ __forceinline__ void store_record(char* lds, const RecordRegs<BYTES, T>& t) {
+#pragma unroll
+  for (int k = 0; k < (BYTES / 16 + T - 1) / T; ++k) {
+    const int at = (threadIdx.x + T * k) * 16;
+    if (at < BYTES) *reinterpret_cast<u32x4*>(lds + at) = t.v[k];
+  }
+}
+
 // a state's column block: rows p of [P, N], this lane's row (nullptr: none), four columns n at 16 nb + 4 g
 template <int NB>
 __device__ __forceinline__ void load_state(f32x4 (&S)[NB], const float* row, int N, int g) {

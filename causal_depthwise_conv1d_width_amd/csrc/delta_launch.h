@@ -37,11 +37,11 @@ struct DeltaBwdArgs {
   int64_t dq_ld, dk_ld, dv_ld, ddt_ld, db_ld;
   float *dA, *dbias;         // [H]; dbias may be nullptr
   char* rec_rev;             // [chunk id, H] records of kRecRev bytes
-  float *cs, *ct;            // states before, adjoints after every chunk: [chunk id, H, ptiles, 64, NT]
-  float *u, *f;              // new values and their adjoints: [chunk id, H, ptiles, 64 rows, 64 columns]
-  float* head_part;          // [chunk id, H, 2]
-  float* qk_part;            // [2, hsplit, rows, G, N] when hsplit > 1
-  int hsplit;
+  // states before and adjoints after every chunk, [chunk id, H, ptiles, 4 blocks of 16 rows, NT / 16 blocks of 16 columns,
+  // 16 rows, 16 columns]
+  float *cs, *ct;
+  float *u, *f;              // new values and what reaches them: [chunk id, H, ptiles, 64 rows, 64 columns]
+  float* head_part;          // [chunk id, H, 2]: sums for dA, d(dt_bias)
 };
 
 struct DeltaStepArgs {

@@ -12,27 +12,6 @@
 
 namespace cssm {
 
-// A record that the four waves copy to shared memory, 16 bytes a thread and step
-template <int BYTES, int T>
-struct RecordRegs {
-  u32x4 v[(BYTES / 16 + T - 1) / T];
-};
-template <int BYTES, int T>
-__device__ __forceinline__ void load_record(RecordRegs<BYTES, T>& t, const char* rec, bool in) {
-  const Rows r(rec, BYTES, 1, in ? BYTES : 0, 1);
-#pragma unroll
-  for (int k = 0; k < (BYTES / 16 + T - 1) / T; ++k)
-    t.v[k] = __builtin_amdgcn_raw_buffer_load_b128(r.r, (int)((threadIdx.x + T * k) * 16), 0, 0);
-}
-template <int BYTES, int T>
-__device__ __forceinline__ void store_record(char* lds, const RecordRegs<BYTES, T>& t) {
-#pragma unroll
-  for (int k = 0; k < (BYTES / 16 + T - 1) / T; ++k) {
-    const int at = (threadIdx.x + T * k) * 16;
-    if (at < BYTES) *reinterpret_cast<u32x4*>(lds + at) = t.v[k];
-  }
-}
-
 template <int NT, bool VEC>
 __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_kernel(DeltaArgs d) {
   constexpr int T = 256, NB = NT / 16;

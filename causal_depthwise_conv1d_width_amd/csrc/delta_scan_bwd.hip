@@ -1,0 +1,654 @@
+// delta_scan_bwd.hip -- backward of the gated delta rule.
+//
+// For a chunk of 64 rows of one sequence and one head, with S the state before the chunk, D the adjoint of the state
+// after it, L, r, T = (I + X)^-1 and P as in delta_chunk.hip, k and q unit or as they are:
+//   U = T r (V - e^L K S^T)                                     forward walk
+//   F = T^T (P^T dY + e^{L_Q - L} K D^T)                        reverse walk: what reaches r (V - e^L K S^T)
+//   D' = e^{L_Q} D + dY^T (scale e^L Q) - F^T (r e^L K)
+// Neither walk needs the other's: both run in one launch and store S, U, D and F, FP32, at every chunk.  Then every chunk is
+// independent.  With W_ij = dY_i . U_j, Y_ij = F_i . U_j and m_ij = e^{L_i - L_j}:
+//   dv_i = r_i F_i
+//   dq_i = scale (e^{L_i} S^T dY_i + sum_{j <= i} m_ij W_ij k_j)                       summed over the key head's heads
+//   dk_i = e^{L_Q - L_i} D^T U_i - r_i e^{L_i} S^T F_i + sum_{j >= i} scale m_ji W_ji q_j
+//          - sum_{j < i} r_i m_ij Y_ij k_j - sum_{j > i} r_j m_ji Y_ji k_j
+//   db_i = F_i . U_i (1 - r_i / beta_max)
+//   dl_t = e^{L_Q} <D, S> + sum_{i >= t} (q_i . scale e^{L_i} S^T dY_i - k_i . r_i e^{L_i} S^T F_i)
+//          + sum_{j < t} k_j . e^{L_Q - L_j} D^T U_j + sum_{i >= t > j} (P_ij W_ij - X_ij Y_ij)
+//   d(dt_t) = A dl_t softplus',  and through the norms of q and k at the end.
+// All of dl's terms are sums of what decays over row t, by blocks of 16 rows: no differences of longer sums.
+// dl, db, dA and the initial states' gradient are FP32 results: S, D, U and F enter their products as three bf16 parts.
+// The decayed scores that go into dq and dk alone are rounded to bf16 once.
+#include "delta_device.h"
+
+namespace cssm {
+
+constexpr int kWalkThreads = 256;
+
+// a tile's element (at, where a place in the workspace has that name)
+template <int W, int PAD = 8>
+__device__ __forceinline__ int at_(int row, int col) {
+  return at<W, PAD>(row, col);
+}
+
+// 16 x 16 FP32 blocks of a state (registers n, lanes p) to its place
+template <int NB>
+__device__ __forceinline__ void store_blocks(float* to, const f32x4 (&S)[NB], int w, int lane, bool in) {
+  const Rows r(to + w * NB * 256, NB * 256, 1, in ? NB * 256 : 0, 4);
+  const int at = ((lane & 15) * 16 + (lane >> 4) * 4) * 4;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[nb]), r.r, nb * 1024 + at, 0, 0);
+}
+// 64 rows of 64 columns (registers rows, lanes columns), this wave's 16 columns
+__device__ __forceinline__ void store_rows(float* to, const f32x4 (&v)[4], int w, int lane, bool in) {
+  const Rows r(to, 4096, 1, in ? 4096 : 0, 4);
+#pragma unroll
+  for (int ib = 0; ib < 4; ++ib)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[ib][e]), r.r,
+                                            ((16 * ib + 4 * (lane >> 4) + e) * 64 + 16 * w + (lane & 15)) * 4, 0, 0);
+}
+
+template <int NT>
+struct WalkShared {
+  __align__(16) uint16_t k[64 * kLd<NT, 16>];
+  __align__(16) uint16_t q[64 * kLd<NT, 16>];
+  __align__(16) uint16_t v[64 * kLd<64, 16>];
+  __align__(16) char rec[kRecRev];
+};
+
+template <int NT, bool VEC, bool REV>
+__device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>& sh) {
+  constexpr int T = kWalkThreads, NB = NT / 16, kBytes = REV ? kRecRev : kRecFwd;
+  const DeltaArgs& d = b.d;
+  const ScanArgs& a = d.s;
+  const Units<1> us(a, blockIdx.x);
+  if (!us.ok) return;
+  const Unit me(a, us, 0);
+  const int w = wave_id(), pn = me.pn;
+  Piece pc;
+  pc.seq = us.item;
+  seq_bounds(a.q, pc.seq, pc.s, pc.e);
+  int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+  const int p_in = 16 * w + i;
+  const int64_t state_at = ((pc.seq * a.H + me.h) * a.P + me.p_first) * a.N;
+  const float* start = REV ? b.dfin : a.init;
+  if (pc.e <= pc.s) {  // an empty sequence's adjoint passes through
+    if (REV && b.dinit)
+      for (int e = threadIdx.x; e < pn * a.N; e += T) b.dinit[state_at + e] = start ? start[state_at + e] : 0.f;
+    return;
+  }
+  f32x4 S[NB];
+  load_state(S, start && p_in < pn ? start + state_at + (int64_t)p_in * a.N : nullptr, a.N, g);
+
+  const int64_t gn = (int64_t)us.group * a.N;
+  const uint16_t* vb = REV ? b.dy : a.x;
+  const int64_t v_ld = REV ? b.dy_ld : a.x_ld;
+  const char* recs = REV ? b.rec_rev : d.rec;
+  TileRegs<NT, T> tK, tQ;
+  TileRegs<64, T> tV;
+  RecordRegs<kBytes, T> tR;
+  auto load = [&](const Chunks<REV>& c, int rows) {
+    load_tile<VEC>(tK, Rows(a.B + c.c0 * a.B_ld + gn, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
+    if constexpr (REV) load_tile<VEC>(tQ, Rows(a.C + c.c0 * a.C_ld + gn, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
+    load_tile<VEC>(tV, Rows(vb + c.c0 * v_ld + me.col, v_ld, rows, pn, 2), (uint32_t)v_ld, pn);
+    load_record(tR, recs + (chunk_id(pc, c.c0, d.n_chunk_slots) * a.H + me.h) * kBytes, rows > 0);
+  };
+  Chunks<REV> c(pc.s, pc.e);
+  int rows = c.rows();
+  load(c, rows);
+  const char *sT = sh.rec, *sP = sh.rec + kRecT;
+  const Factors& fac = *reinterpret_cast<const Factors*>(sh.rec + kBytes - kRecVec);
+  for (;;) {
+    lane = fresh(lane);
+    g = lane >> 4, i = lane & 15;
+    store_tile<16>(sh.k, tK);
+    if constexpr (REV) store_tile<16>(sh.q, tQ);
+    store_tile<16>(sh.v, tV);
+    store_record(sh.rec, tR);
+    __syncthreads();
+    const int64_t at = (chunk_id(pc, c.c0, d.n_chunk_slots) * a.H + me.h) * a.ptiles + (me.p_first / kPTile);
+    c = step_chunk(c, rows);  // rows == 0: that was the last one
+    load(c, rows);
+    store_blocks((REV ? b.ct : b.cs) + at * (64 * NT), S, w, lane, true);
+    phase();
+    f32x4 r[4];  // K S: rows in the registers, columns p in the lanes
+#pragma unroll
+    for (int ib = 0; ib < 4; ++ib) r[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < NT / 32; ++ks) {
+      const Parts s = split(S[2 * ks], S[2 * ks + 1]);
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) r[ib] = mma3(op_split<NT, 16>(sh.k, 16 * ib, 32 * ks, lane), s, r[ib]);
+      phase();
+    }
+    const float decay = fac.decay;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) S[nb] *= decay;
+    f32x4 u[4];
+    if constexpr (!REV) {
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) {
+        const f32x4 f = *reinterpret_cast<const f32x4*>(fac.f[0] + 16 * ib + 4 * g);
+        const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4*)(sh.v + at_<64, 16>(16 * ib + 4 * g + (i >> 2), 16 * w + 4 * (i & 3))));
+        const u32x2 v = __builtin_bit_cast(u32x2, t);
+        r[ib] = f32x4{bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y)} - f * r[ib];
+      }
+      const Parts rp[2] = {split(r[0], r[1]), split(r[2], r[3])};
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) {
+        u[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks <= ib / 2; ++ks)
+          u[ib] = mma6(Parts{{tri_rows<3>(sT, ib, ks, 0, lane), tri_rows<3>(sT, ib, ks, 1, lane), tri_rows<3>(sT, ib, ks, 2, lane)}},
+                       rp[ks], u[ib]);
+        phase();
+      }
+      store_rows(b.u + at * 4096, u, w, lane, true);
+    } else {
+      bf16x8 y[2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) y[ks] = op_cols<64, 16>(sh.v, 32 * ks, 16 * w, lane);
+#pragma unroll
+      for (int jb = 0; jb < 4; ++jb) {
+        r[jb] *= *reinterpret_cast<const f32x4*>(fac.f[2] + 16 * jb + 4 * g);
+#pragma unroll
+        for (int ks = jb / 2; ks < 2; ++ks)
+          r[jb] = mma3(Parts{{tri_cols<3>(sP, jb, ks, 0, lane), tri_cols<3>(sP, jb, ks, 1, lane), tri_cols<3>(sP, jb, ks, 2, lane)}},
+                       y[ks], r[jb]);
+        phase();
+      }
+      const Parts rp[2] = {split(r[0], r[1]), split(r[2], r[3])};
+#pragma unroll
+      for (int jb = 0; jb < 4; ++jb) {
+        u[jb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = jb / 2; ks < 2; ++ks)
+          u[jb] = mma6(Parts{{tri_cols<3>(sT, jb, ks, 0, lane), tri_cols<3>(sT, jb, ks, 1, lane), tri_cols<3>(sT, jb, ks, 2, lane)}},
+                       rp[ks], u[jb]);
+        phase();
+      }
+      store_rows(b.f + at * 4096, u, w, lane, true);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const f32x4 wa = *reinterpret_cast<const f32x4*>(fac.f[1] + 32 * ks + 4 * g);
+        const f32x4 wb = *reinterpret_cast<const f32x4*>(fac.f[1] + 32 * ks + 16 + 4 * g);
+        const Parts yp = split_scaled(y[ks], wa, wb);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) S[nb] = mma3(op_cols<NT, 16>(sh.q, 32 * ks, 16 * nb, lane), yp, S[nb]);
+        phase();
+      }
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      f32x4 wt[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int row = 32 * ks + 16 * q + 4 * g;
+        if constexpr (REV)
+          wt[q] = -*reinterpret_cast<const f32x4*>(fac.f[0] + row) * *reinterpret_cast<const f32x4*>(fac.f[3] + row);
+        else wt[q] = *reinterpret_cast<const f32x4*>(fac.f[2] + row);
+      }
+      const Parts up = split(u[2 * ks] * wt[0], u[2 * ks + 1] * wt[1]);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) S[nb] = mma3(op_cols<NT, 16>(sh.k, 32 * ks, 16 * nb, lane), up, S[nb]);
+      phase();
+    }
+    if (rows == 0) break;
+    __syncthreads();
+  }
+  if (REV && b.dinit && p_in < pn) store_state(S, b.dinit + state_at + (int64_t)p_in * a.N, a.N, lane >> 4);
+}
+
+template <int NT, bool VEC>
+__global__ __launch_bounds__(kWalkThreads, NT <= 128 ? 2 : 1) void delta_walks_kernel(DeltaBwdArgs b) {
+  __shared__ WalkShared<NT> sh;
+  if (blockIdx.y == 0) delta_walk<NT, VEC, true>(b, sh);  // the longer one first
+  else delta_walk<NT, VEC, false>(b, sh);
+}
+
+// sum over the four rows of 16 lanes, in every lane
+__device__ __forceinline__ float across16(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t x = __float_as_uint(__uint_as_float(p[0]) + __uint_as_float(p[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+
+// 64 x 64 FP32 values as three bf16 tiles
+constexpr int kTile = 64 * kLd<64>;
+__device__ __forceinline__ Parts tile_parts(const uint16_t* tiles, int row0, int k0, int l) {
+  return Parts{{op_split<64>(tiles, row0, k0, l), op_split<64>(tiles + kTile, row0, k0, l),
+                op_split<64>(tiles + 2 * kTile, row0, k0, l)}};
+}
+
+// A block takes a chunk and a key head and walks the 64-column tiles of its value heads.  A wave owns 16 NBW columns n of
+// dq and dk and one or two of the ten score blocks.
+template <int NT, int WAVES, bool VEC>
+__global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(DeltaBwdArgs b) {
+  constexpr int T = 64 * WAVES, NBW = NT / 16 / WAVES, SB = (10 + WAVES - 1) / WAVES, PER = 64 * 64 / T;
+  __shared__ __align__(16) uint16_t sK[64 * kLd<NT, 16>];
+  __shared__ __align__(16) uint16_t sQ[64 * kLd<NT, 16>];
+  __shared__ __align__(16) uint16_t sY[kTile];
+  __shared__ __align__(16) uint16_t sUF[6 * kTile];  // U's and F's parts, then the four decayed scores
+  __shared__ __align__(16) double sL[64];
+  __shared__ __align__(16) float s_rate[64], s_kn[64], s_qn[64], s_step[64], s_grow[64], s_left[64];
+  __shared__ float s_row[4][64], s_col[4][64], s_diag[64], s_in[WAVES][64], s_out[WAVES][64], s_dot[WAVES];
+  uint16_t *sU = sUF, *sF = sUF + 3 * kTile;
+  uint16_t *sZk = sUF, *sZq = sUF + kTile, *sNj = sUF + 2 * kTile, *sNi = sUF + 3 * kTile;
+  const DeltaArgs& d = b.d;
+  const ScanArgs& a = d.s;
+  int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+  const int w = wave_id();
+  const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
+  const int grp = blk % (uint32_t)a.G;
+  const int64_t id = blk / (uint32_t)a.G;
+  const int hg = a.H / a.G;
+  const Piece pc = find_chunk(a.q, id, d.n_chunk_slots);
+  if (!pc.ok) {
+    for (int e = threadIdx.x; e < hg * 2; e += T) b.head_part[(id * a.H + grp * hg) * 2 + e] = 0.f;
+    return;
+  }
+  const int rows = (int)(pc.r1 - pc.r0);
+  const int64_t gn = (int64_t)grp * a.N;
+  {
+    TileRegs<NT, T> tk, tq;
+    load_tile<VEC>(tk, Rows(a.B + pc.r0 * a.B_ld + gn, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
+    load_tile<VEC>(tq, Rows(a.C + pc.r0 * a.C_ld + gn, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
+    store_tile<16>(sK, tk);
+    store_tile<16>(sQ, tq);
+    auto norms = [&](const TileRegs<NT, T>& t, float* to) {
+#pragma unroll
+      for (int k = 0; k < NT * 8 / T; ++k) {
+        const int row = (threadIdx.x + T * k) / (NT / 8);
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float lo = bf_lo(t.v[k][e]), hi = bf_hi(t.v[k][e]);
+          s = __builtin_fmaf(lo, lo, s);
+          s = __builtin_fmaf(hi, hi, s);
+        }
+#pragma unroll
+        for (int m = NT / 16; m > 0; m >>= 1) s += __shfl_xor(s, m);
+        if (threadIdx.x % (NT / 8) == 0) to[row] = row < rows ? (d.qk_norm ? rsqrtf(s + d.norm_eps) : 1.f) + (s - s) : 0.f;
+      }
+    };
+    norms(tk, s_kn);
+    norms(tq, s_qn);
+  }
+  __syncthreads();
+  f32x4 kk[SB], qk[SB];  // score blocks (ib, jb): columns j in the registers, rows i in the lanes
+#pragma unroll
+  for (int t = 0; t < SB; ++t) {
+    int ib, jb;
+    lower_block(w + WAVES * t, ib, jb);
+    kk[t] = qk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (w + WAVES * t < 10) {
+#pragma unroll
+      for (int ks = 0; ks < NT / 32; ++ks) {
+        const bf16x8 kj = op_straight<NT, 16>(sK, 16 * jb, 32 * ks, lane);
+        kk[t] = mma(kj, op_straight<NT, 16>(sK, 16 * ib, 32 * ks, lane), kk[t]);
+        qk[t] = mma(kj, op_straight<NT, 16>(sQ, 16 * ib, 32 * ks, lane), qk[t]);
+      }
+    }
+  }
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  f32x4 dQ[NBW][4], dK[NBW][4];  // registers n, lanes rows; summed over the heads
+#pragma unroll
+  for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+    for (int ib = 0; ib < 4; ++ib) dQ[nb][ib] = dK[nb][ib] = zero;
+
+  for (int hh = 0; hh < hg; ++hh) {
+    lane = fresh(lane);
+    g = lane >> 4, i = lane & 15;
+    const int h = grp * hg + hh;
+    float A_h = 0.f;
+    if (w == 0) {  // lane = row
+      const Rate rate(a, h);
+      const float step = rate.step(raw_step(a, pc.r0, rows, lane, h), lane < rows);
+      const float bv = lane < rows ? load_num(d.b, (pc.r0 + lane) * d.b_ld + h, a.dt_f32) : 0.f;
+      const double L = wave_prefix(rate.exponent(step));
+      const double end = __shfl(L, 63);
+      sL[lane] = L;
+      s_step[lane] = step;
+      s_rate[lane] = lane < rows ? d.beta_max / (1.f + ex2(-kLog2e * bv)) : 0.f;
+      s_grow[lane] = ex2((float)L);
+      s_left[lane] = ex2((float)(end - L));
+      A_h = a.A[h];
+    }
+    f32x4 aQ[NBW][4], aF[NBW][4], aU[NBW][4], W[SB], Y[SB];
+#pragma unroll
+    for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) aQ[nb][ib] = aF[nb][ib] = aU[nb][ib] = zero;
+#pragma unroll
+    for (int t = 0; t < SB; ++t) W[t] = Y[t] = zero;
+    float dot = 0.f;
+    for (int pt = 0; pt < a.ptiles; ++pt) {
+      const int p_first = pt * kPTile, pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
+      const int64_t col = (int64_t)h * a.P + p_first, at = (id * a.H + h) * a.ptiles + pt;
+      {
+        const int row = threadIdx.x / (64 / PER), c = threadIdx.x % (64 / PER) * PER;
+        f32x4 u[PER / 4], f[PER / 4];
+        const float *pu = b.u + at * 4096 + row * 64 + c, *pf = b.f + at * 4096 + row * 64 + c;
+#pragma unroll
+        for (int e = 0; e < PER / 4; ++e) {
+          u[e] = *reinterpret_cast<const f32x4*>(pu + 4 * e);
+          f[e] = *reinterpret_cast<const f32x4*>(pf + 4 * e);
+        }
+        TileRegs<64, T> ty;
+        load_tile<VEC>(ty, Rows(b.dy + pc.r0 * b.dy_ld + col, b.dy_ld, rows, pn, 2), (uint32_t)b.dy_ld, pn);
+        __syncthreads();  // the last tile's or head's reads are done; this head's factors are there
+        store_tile(sY, ty);
+        const Rows dv(b.dv + pc.r0 * b.dv_ld + col, b.dv_ld, rows, pn, 2);
+        const float rate = s_rate[row];
+#pragma unroll
+        for (int e = 0; e < PER / 4; ++e) {
+          const f32x4 o = f[e] * rate;
+          store4<VEC>(dv, (uint32_t)b.dv_ld, row, c + 4 * e, pn, u32x2{pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3])});
+#pragma unroll
+          for (int p = 0; p < 3; ++p) {
+            const u32x2 x = {pk_bf16(u[e][0], u[e][1]), pk_bf16(u[e][2], u[e][3])};
+            const u32x2 z = {pk_bf16(f[e][0], f[e][1]), pk_bf16(f[e][2], f[e][3])};
+            *reinterpret_cast<u32x2*>(sU + p * kTile + at_<64>(row, c + 4 * e)) = x;
+            *reinterpret_cast<u32x2*>(sF + p * kTile + at_<64>(row, c + 4 * e)) = z;
+            u[e] -= f32x4{bf_lo(x.x), bf_hi(x.x), bf_lo(x.y), bf_hi(x.y)};
+            f[e] -= f32x4{bf_lo(z.x), bf_hi(z.x), bf_lo(z.y), bf_hi(z.y)};
+          }
+        }
+      }
+      __syncthreads();
+      // the state and the adjoint as operands: this wave's columns n in the lanes, contracted rows p in the registers
+      const float *ps = b.cs + at * (64 * NT), *pd = b.ct + at * (64 * NT);
+#pragma unroll
+      for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          f32x4 s[2], t[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int64_t o = ((2 * ks + q) * (NT / 16) + w * NBW + nb) * 256 + 4 * g * 16 + i;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s[q][e] = ps[o + 16 * e];
+              t[q][e] = pd[o + 16 * e];
+              dot = __builtin_fmaf(s[q][e], t[q][e], dot);
+            }
+          }
+          const Parts sp = split(s[0], s[1]), tp = split(t[0], t[1]);
+#pragma unroll
+          for (int ib = 0; ib < 4; ++ib) {
+            aQ[nb][ib] = mma3(sp, op_split<64>(sY, 16 * ib, 32 * ks, lane), aQ[nb][ib]);
+            aF[nb][ib] = mma6(sp, tile_parts(sF, 16 * ib, 32 * ks, lane), aF[nb][ib]);
+            aU[nb][ib] = mma6(tp, tile_parts(sU, 16 * ib, 32 * ks, lane), aU[nb][ib]);
+            phase();
+          }
+        }
+#pragma unroll
+      for (int t = 0; t < SB; ++t) {
+        int ib, jb;
+        lower_block(w + WAVES * t, ib, jb);
+        if (w + WAVES * t < 10) {
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            const Parts u = tile_parts(sU, 16 * jb, 32 * ks, lane);
+            W[t] = mma3(u, op_split<64>(sY, 16 * ib, 32 * ks, lane), W[t]);
+            Y[t] = mma6(u, tile_parts(sF, 16 * ib, 32 * ks, lane), Y[t]);
+          }
+        }
+        phase();
+      }
+    }
+    dot = wave_sum(dot);
+    if (lane == 0) s_dot[w] = dot;
+    // the rows' sums with the state and the adjoint, and dQ's and dK's terms of them
+#pragma unroll
+    for (int ib = 0; ib < 4; ++ib) {
+      const int row = 16 * ib + i;
+      const float gq = d.scale * s_grow[row], gf = -s_rate[row] * s_grow[row], gu = s_left[row];
+      float in_q = 0.f, in_k = 0.f, out = 0.f;
+#pragma unroll
+      for (int nb = 0; nb < NBW; ++nb) {
+        const int n = 16 * (w * NBW + nb) + 4 * g;
+        const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + at_<NT, 16>(row, n));
+        const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + at_<NT, 16>(row, n));
+        const f32x4 q4 = {bf_lo(qv.x), bf_hi(qv.x), bf_lo(qv.y), bf_hi(qv.y)};
+        const f32x4 k4 = {bf_lo(kv.x), bf_hi(kv.x), bf_lo(kv.y), bf_hi(kv.y)};
+        const f32x4 vq = aQ[nb][ib] * gq, vf = aF[nb][ib] * gf, vu = aU[nb][ib] * gu;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          in_q = __builtin_fmaf(q4[e], vq[e], in_q);
+          in_k = __builtin_fmaf(k4[e], vf[e], in_k);
+          out = __builtin_fmaf(k4[e], vu[e], out);
+        }
+        dQ[nb][ib] += vq;
+        dK[nb][ib] += vf + vu;
+      }
+      const float in = across16(in_q * s_qn[row] + in_k * s_kn[row]), o = across16(out * s_kn[row]);
+      if (g == 0) {
+        s_in[w][row] = in;
+        s_out[w][row] = o;
+      }
+    }
+    __syncthreads();  // U's and F's parts are read
+#pragma unroll
+    for (int t = 0; t < SB; ++t) {
+      int ib, jb;
+      lower_block(w + WAVES * t, ib, jb);
+      if (w + WAVES * t < 10) {
+        const int row = 16 * ib + i, col = 16 * jb + 4 * g;
+        const double Li = sL[row];
+        const float ri = s_rate[row], kni = s_kn[row], qni = d.scale * s_qn[row];
+        const f32x4 knj = *reinterpret_cast<const f32x4*>(s_kn + col);
+        f32x4 zk, zq, nj, ni;
+        float sum = 0.f, diag = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool under = col + r < row, here = col + r == row;
+          const float m = under || here ? ex2((float)(Li - sL[col + r])) : 0.f;
+          const float z = m * W[t][r], n = under ? -(m * ri) * Y[t][r] : 0.f;
+          zk[r] = z * (d.scale * knj[r]);
+          zq[r] = z * qni;
+          nj[r] = n * knj[r];
+          ni[r] = n * kni;
+          // P W - X Y below the diagonal
+          const float x = under ? qk[t][r] * zq[r] * knj[r] + kk[t][r] * nj[r] * kni : 0.f;
+          diag = here ? Y[t][r] : diag;
+          const float from = row16_suffix(x);  // rows >= i of column j
+          if (i == 0) s_col[ib][col + r] = from;
+          sum += ib != jb ? x : (4 * g + r < i ? from : 0.f);
+        }
+        const int o = at_<64>(row, col);
+        *reinterpret_cast<u32x2*>(sZk + o) = u32x2{pk_bf16(zk[0], zk[1]), pk_bf16(zk[2], zk[3])};
+        *reinterpret_cast<u32x2*>(sZq + o) = u32x2{pk_bf16(zq[0], zq[1]), pk_bf16(zq[2], zq[3])};
+        *reinterpret_cast<u32x2*>(sNj + o) = u32x2{pk_bf16(nj[0], nj[1]), pk_bf16(nj[2], nj[3])};
+        *reinterpret_cast<u32x2*>(sNi + o) = u32x2{pk_bf16(ni[0], ni[1]), pk_bf16(ni[2], ni[3])};
+        sum = across16(sum);
+        if (g == 0) s_row[jb][row] = sum;
+        if (ib == jb && (i >> 2) == g) s_diag[row] = diag;
+      }
+    }
+    // blocks (0, 1), (2, 3): products over 32 rows or columns read them
+    if (w < 2) {
+      const int o = at_<64>(32 * w + i, 32 * w + 16 + 4 * g);
+      const u32x2 none = {0u, 0u};
+      *reinterpret_cast<u32x2*>(sZk + o) = none;
+      *reinterpret_cast<u32x2*>(sZq + o) = none;
+      *reinterpret_cast<u32x2*>(sNj + o) = none;
+      *reinterpret_cast<u32x2*>(sNi + o) = none;
+    }
+    __syncthreads();
+    if (w == 0) {  // lane = row
+      float in = 0.f, out = 0.f, dots = 0.f;
+#pragma unroll
+      for (int k = 0; k < WAVES; ++k) {
+        in += s_in[k][lane];
+        out += s_out[k][lane];
+        dots += s_dot[k];
+      }
+      const int m = lane >> 4;
+      float left = 0.f, below = 0.f, on = 0.f, corner[2] = {0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float r = k <= m ? s_row[k][lane] : 0.f, cl = k >= m ? s_col[k][lane] : 0.f;
+        left += k < m ? r : 0.f;
+        below += k > m ? cl : 0.f;
+        on += k == m ? r : 0.f;
+        if (k == 0) corner[0] = m >= 2 ? r : 0.f;
+        if (k <= 1) corner[1] += m == 3 ? r : 0.f;
+      }
+      const float corner1 = wave_sum(corner[0]), corner2 = wave_sum(corner[1]);
+      const float rows_on = row16_suffix(left);  // rows >= this one
+      const float columns = dpp0<0x111, 0xf>(row16_sum(below));
+      const float inside = rows_on + on + columns + (m == 1 ? corner1 : m == 2 ? corner2 : 0.f);
+      const float suffix = __shfl(wave_prefix(__shfl(in, 63 - lane)), 63 - lane);  // rows >= this one
+      const float before = dpp0<0x138, 0xf>(wave_prefix(out));                     // rows < this one
+      const float dl = s_grow[63] * dots + suffix + inside + before;
+      const float step = s_step[lane], rate = s_rate[lane];
+      const float dstep = A_h * dl, ddt = a.softplus ? dstep * -expm1f(-step) : dstep;
+      const float db = s_diag[lane] * (1.f - rate / d.beta_max);
+      const int size = a.dt_f32 ? 4 : 2;
+      const Rows to(static_cast<char*>(b.ddt) + (pc.r0 * b.ddt_ld + h) * size, b.ddt_ld, rows, 1, size);
+      const Rows tb(static_cast<char*>(b.db) + (pc.r0 * b.db_ld + h) * size, b.db_ld, rows, 1, size);
+      const int o = (int)((uint32_t)lane * (uint32_t)b.ddt_ld * size), ob = (int)((uint32_t)lane * (uint32_t)b.db_ld * size);
+      if (a.dt_f32) {
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(ddt), to.r, o, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(db), tb.r, ob, 0, 0);
+      } else {
+        __builtin_amdgcn_raw_buffer_store_b16(to_bf16(ddt), to.r, o, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b16(to_bf16(db), tb.r, ob, 0, 0);
+      }
+      const float sum_A = wave_sum(lane < rows ? step * dl : 0.f), sum_b = wave_sum(lane < rows ? ddt : 0.f);
+      if (lane == 0) {
+        b.head_part[(id * a.H + h) * 2] = sum_A;
+        b.head_part[(id * a.H + h) * 2 + 1] = sum_b;
+      }
+    }
+    phase();
+#pragma unroll
+    for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int n = 16 * (w * NBW + nb);
+        const bf16x8 k = op_cols<NT, 16>(sK, 32 * ks, n, lane), q = op_cols<NT, 16>(sQ, 32 * ks, n, lane);
+#pragma unroll
+        for (int ib = 0; ib < 4; ++ib) {
+          if (ks <= ib / 2) {  // contracted columns j of row block ib
+            dQ[nb][ib] = mma(k, op_split<64>(sZk, 16 * ib, 32 * ks, lane), dQ[nb][ib]);
+            dK[nb][ib] = mma(k, op_split<64>(sNj, 16 * ib, 32 * ks, lane), dK[nb][ib]);
+          }
+          if (ks >= ib / 2) {  // contracted rows i of column block ib
+            dK[nb][ib] = mma(q, op_cols<64>(sZq, 32 * ks, 16 * ib, lane), dK[nb][ib]);
+            dK[nb][ib] = mma(k, op_cols<64>(sNi, 32 * ks, 16 * ib, lane), dK[nb][ib]);
+          }
+        }
+        phase();
+      }
+  }
+  // through the norms: x = f y, f = (|y|^2 + eps)^(-1/2):  dy = f dx - f^3 y (y . dx)
+  __syncthreads();
+  if (d.qk_norm) {
+#pragma unroll
+    for (int ib = 0; ib < 4; ++ib) {
+      const int row = 16 * ib + i;
+      float dq = 0.f, dk = 0.f;
+#pragma unroll
+      for (int nb = 0; nb < NBW; ++nb) {
+        const int n = 16 * (w * NBW + nb) + 4 * g;
+        const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + at_<NT, 16>(row, n));
+        const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + at_<NT, 16>(row, n));
+        const f32x4 x = dQ[nb][ib], y = dK[nb][ib];
+        dq += x[0] * bf_lo(qv.x) + x[1] * bf_hi(qv.x) + x[2] * bf_lo(qv.y) + x[3] * bf_hi(qv.y);
+        dk += y[0] * bf_lo(kv.x) + y[1] * bf_hi(kv.x) + y[2] * bf_lo(kv.y) + y[3] * bf_hi(kv.y);
+      }
+      dq = across16(dq), dk = across16(dk);
+      if (g == 0) {
+        s_in[w][row] = dq;
+        s_out[w][row] = dk;
+      }
+    }
+  }
+  __syncthreads();
+  const Rows oq(b.dq + pc.r0 * b.dq_ld + gn, b.dq_ld, rows, a.N, 2), ok(b.dk + pc.r0 * b.dk_ld + gn, b.dk_ld, rows, a.N, 2);
+#pragma unroll
+  for (int ib = 0; ib < 4; ++ib) {
+    const int row = 16 * ib + i;
+    const float fq = s_qn[row], fk = s_kn[row];
+    float dq = 0.f, dk = 0.f;
+    if (d.qk_norm) {
+#pragma unroll
+      for (int k = 0; k < WAVES; ++k) {
+        dq += s_in[k][row];
+        dk += s_out[k][row];
+      }
+      dq *= fq * fq * fq;
+      dk *= fk * fk * fk;
+    }
+#pragma unroll
+    for (int nb = 0; nb < NBW; ++nb) {
+      const int n = 16 * (w * NBW + nb) + 4 * g;
+      const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + at_<NT, 16>(row, n));
+      const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + at_<NT, 16>(row, n));
+      const f32x4 x = dQ[nb][ib] * fq - f32x4{bf_lo(qv.x), bf_hi(qv.x), bf_lo(qv.y), bf_hi(qv.y)} * dq;
+      const f32x4 y = dK[nb][ib] * fk - f32x4{bf_lo(kv.x), bf_hi(kv.x), bf_lo(kv.y), bf_hi(kv.y)} * dk;
+      store4<VEC>(oq, (uint32_t)b.dq_ld, row, n, a.N, u32x2{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])});
+      store4<VEC>(ok, (uint32_t)b.dk_ld, row, n, a.N, u32x2{pk_bf16(y[0], y[1]), pk_bf16(y[2], y[3])});
+    }
+  }
+}
+
+// dA, d(dt_bias) of one head: the chunks' sums, 256 strided subsets and then a fixed tree
+__global__ __launch_bounds__(256) void delta_head_reduce_kernel(DeltaBwdArgs b, int64_t ids) {
+  __shared__ float lds[4][2];
+  const int h = blockIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  float s[2] = {0.f, 0.f};
+  for (int64_t id = threadIdx.x; id < ids; id += 256) {
+    const float* src = b.head_part + (id * b.d.s.H + h) * 2;
+    s[0] += src[0];
+    s[1] += src[1];
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float v = wave_sum(s[e]);
+    if (lane == 0) lds[w][e] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    const int e = threadIdx.x;
+    float* dst = e == 0 ? b.dA : b.dbias;
+    if (dst) dst[h] = lds[0][e] + lds[1][e] + lds[2][e] + lds[3][e];
+  }
+}
+
+template <int NT, int WAVES, bool VEC>
+static hipError_t launch(const DeltaBwdArgs& b, hipStream_t s) {
+  const ScanArgs& a = b.d.s;
+  const int64_t ids = b.d.n_chunk_slots + a.q.nseq;
+  delta_walks_kernel<NT, VEC><<<dim3((uint32_t)unit_blocks(a.q.nseq, a.H, a.G, a.ptiles, 1), 2), kWalkThreads, 0, s>>>(b);
+  if (a.q.rows > 0)
+    delta_scan_bwd_kernel<NT, WAVES, VEC><<<dim3((uint32_t)(ids * a.G)), 64 * WAVES, 0, s>>>(b);
+  delta_head_reduce_kernel<<<dim3((uint32_t)a.H), 256, 0, s>>>(b, a.q.rows > 0 ? ids : 0);
+  return hipGetLastError();
+}
+
+hipError_t launch_delta_bwd(const DeltaBwdArgs& b, bool vec, hipStream_t s) {
+  if (b.d.s.q.nseq == 0) {  // no sequences: the parameters' gradients are zero
+    delta_head_reduce_kernel<<<dim3((uint32_t)b.d.s.H), 256, 0, s>>>(b, 0);
+    return hipGetLastError();
+  }
+  if (b.d.s.q.rows > 0) {
+    const hipError_t e = launch_delta_chunks(b.d, b.rec_rev, vec, s);
+    if (e != hipSuccess) return e;
+  }
+  switch (state_tile(b.d.s.N)) {
+    case 64: return vec ? launch<64, 4, true>(b, s) : launch<64, 4, false>(b, s);
+    case 128: return vec ? launch<128, 8, true>(b, s) : launch<128, 8, false>(b, s);
+    default: return vec ? launch<256, 8, true>(b, s) : launch<256, 8, false>(b, s);
+  }
+}
+
+}  // namespace cssm
