@@ -7,7 +7,7 @@
 // beside the products, so nothing is rounded before T is complete.
 // T: the four 16 x 16 blocks on the diagonal by substitution, a column a lane; then pairs of them, then pairs of pairs,
 // [T1 0; -T2 X21 T1, T2], by FP32 matrix instructions.  The rates of the columns are taken into T, whose FP32 values are
-// stored as three bf16 parts, P's as one (forward).
+// stored as three bf16 parts, P's as two (forward).
 // A row of k, dt or b that is not finite makes the head's state and all later rows so; zeros times it would reach earlier
 // rows of the chunk.  Such rows are left out here, and the record names the first.
 #include "delta_device.h"
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs d, char* rec
         }
         *reinterpret_cast<f32x4*>(sX + row * LD + col) = x;
         if constexpr (!BWD) {
-          store_tri<1>(rec + kRecT, tri_block(ib, jb), p, lane);
+          store_tri<2>(rec + kRecT, tri_block(ib, jb), p, lane);
         } else {  // column 16 jb + i in the lanes, rows in the registers
           const int c = 16 * jb + i, r0 = 16 * ib + 4 * g;
           const float knc = s_kn[c];

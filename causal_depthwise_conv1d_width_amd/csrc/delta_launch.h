@@ -12,7 +12,7 @@ namespace cssm {
 constexpr int kTriBlocks = 10, kTriPart = 512;
 constexpr int kRecT = kTriBlocks * 3 * kTriPart;  // the triangular system's inverse, three parts
 constexpr int kRecVec = 4 * 64 * 4 + 64;          // four factors a row, then: decay of the chunk, first row not finite
-constexpr int kRecFwd = kRecT + kTriBlocks * kTriPart + kRecVec;  // the scores in one part
+constexpr int kRecFwd = kRecT + 2 * kTriBlocks * kTriPart + kRecVec;  // the scores in two parts
 constexpr int kRecRev = 2 * kRecT + kRecVec;                      // the reverse walk's, in three
 
 // s: x = v, B = k, C = q, init, fin and slots as in the scan; y

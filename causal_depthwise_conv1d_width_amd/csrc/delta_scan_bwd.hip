@@ -17,12 +17,20 @@
 //   d(dt_t) = A dl_t softplus',  and through the norms of q and k at the end.
 // All of dl's terms are sums of what decays over row t, by blocks of 16 rows: no differences of longer sums.
 // dl, db, dA and the initial states' gradient are FP32 results: S, D, U and F enter their products as three bf16 parts.
-// The decayed scores that go into dq and dk alone are rounded to bf16 once.
+// The decayed scores that go into dq and dk alone enter as two: with one these were up to 2.7e-3 off where terms cancel (their own
+// rounding: 1.66e-3).
 #include "delta_device.h"
 
 namespace cssm {
 
 constexpr int kWalkThreads = 256;
+
+// The walks hold their state, and with it U or F, with a sign that changes from chunk to chunk.  What matrix instructions add up
+// comes out a little low, whatever its sign; dl's terms are sums of both signs, and over all the rows of dA and d(dt_bias)
+// such offsets add up: 2.8e-6 of dA over 16384 rows, 8e-6 with rates up to two.  With the signs they cancel:
+// ERR.  The forward walk's change at every chunk, the reverse walk's at every second, so that their products'
+// change as well.
+__device__ __forceinline__ float sign_at(int64_t chunk, bool rev) { return (rev ? chunk >> 1 : chunk) & 1 ? -1.f : 1.f; }
 
 // a tile's element (at, where a place in the workspace has that name)
 template <int W, int PAD = 8>
@@ -98,6 +106,10 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
   Chunks<REV> c(pc.s, pc.e);
   int rows = c.rows();
   load(c, rows);
+  int64_t walked = pc.seq;  // sequences of few chunks do not all begin with the same signs
+  float turn = sign_at(walked, REV);  // the state's sign in the chunk
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) S[nb] *= turn;
   const char *sT = sh.rec, *sP = sh.rec + kRecT;
   const Factors& fac = *reinterpret_cast<const Factors*>(sh.rec + kBytes - kRecVec);
   for (;;) {
@@ -123,7 +135,8 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
       for (int ib = 0; ib < 4; ++ib) r[ib] = mma3(op_split<NT, 16>(sh.k, 16 * ib, 32 * ks, lane), s, r[ib]);
       phase();
     }
-    const float decay = fac.decay;
+    const float next = sign_at(++walked, REV), change = turn * next;
+    const float decay = change * fac.decay;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) S[nb] *= decay;
     f32x4 u[4];
@@ -134,7 +147,7 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
         const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (lds_s16x4*)(sh.v + at_<64, 16>(16 * ib + 4 * g + (i >> 2), 16 * w + 4 * (i & 3))));
         const u32x2 v = __builtin_bit_cast(u32x2, t);
-        r[ib] = f32x4{bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y)} - f * r[ib];
+        r[ib] = f32x4{bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y)} * turn - f * r[ib];
       }
       const Parts rp[2] = {split(r[0], r[1]), split(r[2], r[3])};
 #pragma unroll
@@ -150,7 +163,11 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
     } else {
       bf16x8 y[2];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) y[ks] = op_cols<64, 16>(sh.v, 32 * ks, 16 * w, lane);
+      for (int ks = 0; ks < 2; ++ks) {
+        u32x4 v = __builtin_bit_cast(u32x4, op_cols<64, 16>(sh.v, 32 * ks, 16 * w, lane));
+        v ^= turn < 0.f ? 0x80008000u : 0u;
+        y[ks] = __builtin_bit_cast(bf16x8, v);
+      }
 #pragma unroll
       for (int jb = 0; jb < 4; ++jb) {
         r[jb] *= *reinterpret_cast<const f32x4*>(fac.f[2] + 16 * jb + 4 * g);
@@ -175,7 +192,7 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
       for (int ks = 0; ks < 2; ++ks) {
         const f32x4 wa = *reinterpret_cast<const f32x4*>(fac.f[1] + 32 * ks + 4 * g);
         const f32x4 wb = *reinterpret_cast<const f32x4*>(fac.f[1] + 32 * ks + 16 + 4 * g);
-        const Parts yp = split_scaled(y[ks], wa, wb);
+        const Parts yp = split_scaled(y[ks], wa * change, wb * change);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) S[nb] = mma3(op_cols<NT, 16>(sh.q, 32 * ks, 16 * nb, lane), yp, S[nb]);
         phase();
@@ -188,17 +205,20 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
       for (int q = 0; q < 2; ++q) {
         const int row = 32 * ks + 16 * q + 4 * g;
         if constexpr (REV)
-          wt[q] = -*reinterpret_cast<const f32x4*>(fac.f[0] + row) * *reinterpret_cast<const f32x4*>(fac.f[3] + row);
-        else wt[q] = *reinterpret_cast<const f32x4*>(fac.f[2] + row);
+          wt[q] = *reinterpret_cast<const f32x4*>(fac.f[0] + row) * *reinterpret_cast<const f32x4*>(fac.f[3] + row) * -change;
+        else wt[q] = *reinterpret_cast<const f32x4*>(fac.f[2] + row) * change;
       }
       const Parts up = split(u[2 * ks] * wt[0], u[2 * ks + 1] * wt[1]);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) S[nb] = mma3(op_cols<NT, 16>(sh.k, 32 * ks, 16 * nb, lane), up, S[nb]);
       phase();
     }
+    turn = next;
     if (rows == 0) break;
     __syncthreads();
   }
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) S[nb] *= turn;
   if (REV && b.dinit && p_in < pn) store_state(S, b.dinit + state_at + (int64_t)p_in * a.N, a.N, lane >> 4);
 }
 
@@ -225,20 +245,29 @@ __device__ __forceinline__ Parts tile_parts(const uint16_t* tiles, int row0, int
                 op_split<64>(tiles + 2 * kTile, row0, k0, l)}};
 }
 
+// four values of a row as two parts
+__device__ __forceinline__ void store_parts(uint16_t* tiles, f32x4 v) {
+  const u32x2 u = {pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+  *reinterpret_cast<u32x2*>(tiles) = u;
+  v -= f32x4{bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y)};
+  *reinterpret_cast<u32x2*>(tiles + kTile) = u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+}
+
 // A block takes a chunk and a key head and walks the 64-column tiles of its value heads.  A wave owns 16 NBW columns n of
 // dq and dk and one or two of the ten score blocks.
 template <int NT, int WAVES, bool VEC>
 __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(DeltaBwdArgs b) {
   constexpr int T = 64 * WAVES, NBW = NT / 16 / WAVES, SB = (10 + WAVES - 1) / WAVES, PER = 64 * 64 / T;
-  __shared__ __align__(16) uint16_t sK[64 * kLd<NT, 16>];
-  __shared__ __align__(16) uint16_t sQ[64 * kLd<NT, 16>];
+  constexpr int PAD = NT > 128 ? 8 : 16;  // 256 columns leave no room for more
+  __shared__ __align__(16) uint16_t sK[64 * kLd<NT, PAD>];
+  __shared__ __align__(16) uint16_t sQ[64 * kLd<NT, PAD>];
   __shared__ __align__(16) uint16_t sY[kTile];
-  __shared__ __align__(16) uint16_t sUF[6 * kTile];  // U's and F's parts, then the four decayed scores
+  __shared__ __align__(16) uint16_t sUF[8 * kTile];  // U's and F's three parts, then the four decayed scores' two
   __shared__ __align__(16) double sL[64];
   __shared__ __align__(16) float s_rate[64], s_kn[64], s_qn[64], s_step[64], s_grow[64], s_left[64];
   __shared__ float s_row[4][64], s_col[4][64], s_diag[64], s_in[WAVES][64], s_out[WAVES][64], s_dot[WAVES];
   uint16_t *sU = sUF, *sF = sUF + 3 * kTile;
-  uint16_t *sZk = sUF, *sZq = sUF + kTile, *sNj = sUF + 2 * kTile, *sNi = sUF + 3 * kTile;
+  uint16_t *sZk = sUF, *sZq = sUF + 2 * kTile, *sNj = sUF + 4 * kTile, *sNi = sUF + 6 * kTile;
   const DeltaArgs& d = b.d;
   const ScanArgs& a = d.s;
   int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
@@ -254,12 +283,16 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
   }
   const int rows = (int)(pc.r1 - pc.r0);
   const int64_t gn = (int64_t)grp * a.N;
+  // the signs of the stored states and adjoints
+  const float sign_s = sign_at((pc.r0 >> 6) - (pc.s >> 6) + pc.seq, false);
+  const float sign_t = sign_at(((pc.e - 1) >> 6) - (pc.r0 >> 6) + pc.seq, true);
+  const float sign = sign_s * sign_t;
   {
     TileRegs<NT, T> tk, tq;
     load_tile<VEC>(tk, Rows(a.B + pc.r0 * a.B_ld + gn, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
     load_tile<VEC>(tq, Rows(a.C + pc.r0 * a.C_ld + gn, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
-    store_tile<16>(sK, tk);
-    store_tile<16>(sQ, tq);
+    store_tile<PAD>(sK, tk);
+    store_tile<PAD>(sQ, tq);
     auto norms = [&](const TileRegs<NT, T>& t, float* to) {
 #pragma unroll
       for (int k = 0; k < NT * 8 / T; ++k) {
@@ -289,9 +322,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
     if (w + WAVES * t < 10) {
 #pragma unroll
       for (int ks = 0; ks < NT / 32; ++ks) {
-        const bf16x8 kj = op_straight<NT, 16>(sK, 16 * jb, 32 * ks, lane);
-        kk[t] = mma(kj, op_straight<NT, 16>(sK, 16 * ib, 32 * ks, lane), kk[t]);
-        qk[t] = mma(kj, op_straight<NT, 16>(sQ, 16 * ib, 32 * ks, lane), qk[t]);
+        const bf16x8 kj = op_straight<NT, PAD>(sK, 16 * jb, 32 * ks, lane);
+        kk[t] = mma(kj, op_straight<NT, PAD>(sK, 16 * ib, 32 * ks, lane), kk[t]);
+        qk[t] = mma(kj, op_straight<NT, PAD>(sQ, 16 * ib, 32 * ks, lane), qk[t]);
       }
     }
   }
@@ -345,7 +378,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
         __syncthreads();  // the last tile's or head's reads are done; this head's factors are there
         store_tile(sY, ty);
         const Rows dv(b.dv + pc.r0 * b.dv_ld + col, b.dv_ld, rows, pn, 2);
-        const float rate = s_rate[row];
+        const float rate = sign_t * s_rate[row];
 #pragma unroll
         for (int e = 0; e < PER / 4; ++e) {
           const f32x4 o = f[e] * rate;
@@ -409,13 +442,13 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
 #pragma unroll
     for (int ib = 0; ib < 4; ++ib) {
       const int row = 16 * ib + i;
-      const float gq = d.scale * s_grow[row], gf = -s_rate[row] * s_grow[row], gu = s_left[row];
+      const float gq = sign_s * d.scale * s_grow[row], gf = -sign * s_rate[row] * s_grow[row], gu = sign * s_left[row];
       float in_q = 0.f, in_k = 0.f, out = 0.f;
 #pragma unroll
       for (int nb = 0; nb < NBW; ++nb) {
         const int n = 16 * (w * NBW + nb) + 4 * g;
-        const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + at_<NT, 16>(row, n));
-        const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + at_<NT, 16>(row, n));
+        const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + at_<NT, PAD>(row, n));
+        const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + at_<NT, PAD>(row, n));
         const f32x4 q4 = {bf_lo(qv.x), bf_hi(qv.x), bf_lo(qv.y), bf_hi(qv.y)};
         const f32x4 k4 = {bf_lo(kv.x), bf_hi(kv.x), bf_lo(kv.y), bf_hi(kv.y)};
         const f32x4 vq = aQ[nb][ib] * gq, vf = aF[nb][ib] * gf, vu = aU[nb][ib] * gu;
@@ -450,23 +483,23 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
         for (int r = 0; r < 4; ++r) {
           const bool under = col + r < row, here = col + r == row;
           const float m = under || here ? ex2((float)(Li - sL[col + r])) : 0.f;
-          const float z = m * W[t][r], n = under ? -(m * ri) * Y[t][r] : 0.f;
+          const float z = m * (sign_s * W[t][r]), y = sign * Y[t][r], n = under ? -(m * ri) * y : 0.f;
           zk[r] = z * (d.scale * knj[r]);
           zq[r] = z * qni;
           nj[r] = n * knj[r];
           ni[r] = n * kni;
           // P W - X Y below the diagonal
           const float x = under ? qk[t][r] * zq[r] * knj[r] + kk[t][r] * nj[r] * kni : 0.f;
-          diag = here ? Y[t][r] : diag;
+          diag = here ? y : diag;
           const float from = row16_suffix(x);  // rows >= i of column j
           if (i == 0) s_col[ib][col + r] = from;
           sum += ib != jb ? x : (4 * g + r < i ? from : 0.f);
         }
         const int o = at_<64>(row, col);
-        *reinterpret_cast<u32x2*>(sZk + o) = u32x2{pk_bf16(zk[0], zk[1]), pk_bf16(zk[2], zk[3])};
-        *reinterpret_cast<u32x2*>(sZq + o) = u32x2{pk_bf16(zq[0], zq[1]), pk_bf16(zq[2], zq[3])};
-        *reinterpret_cast<u32x2*>(sNj + o) = u32x2{pk_bf16(nj[0], nj[1]), pk_bf16(nj[2], nj[3])};
-        *reinterpret_cast<u32x2*>(sNi + o) = u32x2{pk_bf16(ni[0], ni[1]), pk_bf16(ni[2], ni[3])};
+        store_parts(sZk + o, zk);
+        store_parts(sZq + o, zq);
+        store_parts(sNj + o, nj);
+        store_parts(sNi + o, ni);
         sum = across16(sum);
         if (g == 0) s_row[jb][row] = sum;
         if (ib == jb && (i >> 2) == g) s_diag[row] = diag;
@@ -475,11 +508,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
     // blocks (0, 1), (2, 3): products over 32 rows or columns read them
     if (w < 2) {
       const int o = at_<64>(32 * w + i, 32 * w + 16 + 4 * g);
-      const u32x2 none = {0u, 0u};
-      *reinterpret_cast<u32x2*>(sZk + o) = none;
-      *reinterpret_cast<u32x2*>(sZq + o) = none;
-      *reinterpret_cast<u32x2*>(sNj + o) = none;
-      *reinterpret_cast<u32x2*>(sNi + o) = none;
+      store_parts(sZk + o, zero);
+      store_parts(sZq + o, zero);
+      store_parts(sNj + o, zero);
+      store_parts(sNi + o, zero);
     }
     __syncthreads();
     if (w == 0) {  // lane = row
@@ -507,7 +539,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
       const float inside = rows_on + on + columns + (m == 1 ? corner1 : m == 2 ? corner2 : 0.f);
       const float suffix = __shfl(wave_prefix(__shfl(in, 63 - lane)), 63 - lane);  // rows >= this one
       const float before = dpp0<0x138, 0xf>(wave_prefix(out));                     // rows < this one
-      const float dl = s_grow[63] * dots + suffix + inside + before;
+      const float dl = sign * s_grow[63] * dots + suffix + inside + before;
       const float step = s_step[lane], rate = s_rate[lane];
       const float dstep = A_h * dl, ddt = a.softplus ? dstep * -expm1f(-step) : dstep;
       const float db = s_diag[lane] * (1.f - rate / d.beta_max);
@@ -534,16 +566,19 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const int n = 16 * (w * NBW + nb);
-        const bf16x8 k = op_cols<NT, 16>(sK, 32 * ks, n, lane), q = op_cols<NT, 16>(sQ, 32 * ks, n, lane);
+        const bf16x8 k = op_cols<NT, PAD>(sK, 32 * ks, n, lane), q = op_cols<NT, PAD>(sQ, 32 * ks, n, lane);
 #pragma unroll
         for (int ib = 0; ib < 4; ++ib) {
-          if (ks <= ib / 2) {  // contracted columns j of row block ib
-            dQ[nb][ib] = mma(k, op_split<64>(sZk, 16 * ib, 32 * ks, lane), dQ[nb][ib]);
-            dK[nb][ib] = mma(k, op_split<64>(sNj, 16 * ib, 32 * ks, lane), dK[nb][ib]);
-          }
-          if (ks >= ib / 2) {  // contracted rows i of column block ib
-            dK[nb][ib] = mma(q, op_cols<64>(sZq, 32 * ks, 16 * ib, lane), dK[nb][ib]);
-            dK[nb][ib] = mma(k, op_cols<64>(sNi, 32 * ks, 16 * ib, lane), dK[nb][ib]);
+#pragma unroll
+          for (int p = 1; p >= 0; --p) {
+            if (ks <= ib / 2) {  // contracted columns j of row block ib
+              dQ[nb][ib] = mma(k, op_split<64>(sZk + p * kTile, 16 * ib, 32 * ks, lane), dQ[nb][ib]);
+              dK[nb][ib] = mma(k, op_split<64>(sNj + p * kTile, 16 * ib, 32 * ks, lane), dK[nb][ib]);
+            }
+            if (ks >= ib / 2) {  // contracted rows i of column block ib
+              dK[nb][ib] = mma(q, op_cols<64>(sZq + p * kTile, 32 * ks, 16 * ib, lane), dK[nb][ib]);
+              dK[nb][ib] = mma(k, op_cols<64>(sNi + p * kTile, 32 * ks, 16 * ib, lane), dK[nb][ib]);
+            }
           }
         }
         phase();
@@ -559,8 +594,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
 #pragma unroll
       for (int nb = 0; nb < NBW; ++nb) {
         const int n = 16 * (w * NBW + nb) + 4 * g;
-        const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + at_<NT, 16>(row, n));
-        const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + at_<NT, 16>(row, n));
+        const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + at_<NT, PAD>(row, n));
+        const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + at_<NT, PAD>(row, n));
         const f32x4 x = dQ[nb][ib], y = dK[nb][ib];
         dq += x[0] * bf_lo(qv.x) + x[1] * bf_hi(qv.x) + x[2] * bf_lo(qv.y) + x[3] * bf_hi(qv.y);
         dk += y[0] * bf_lo(kv.x) + y[1] * bf_hi(kv.x) + y[2] * bf_lo(kv.y) + y[3] * bf_hi(kv.y);
@@ -591,8 +626,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
 #pragma unroll
     for (int nb = 0; nb < NBW; ++nb) {
       const int n = 16 * (w * NBW + nb) + 4 * g;
-      const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + at_<NT, 16>(row, n));
-      const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + at_<NT, 16>(row, n));
+      const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + at_<NT, PAD>(row, n));
+      const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + at_<NT, PAD>(row, n));
       const f32x4 x = dQ[nb][ib] * fq - f32x4{bf_lo(qv.x), bf_hi(qv.x), bf_lo(qv.y), bf_hi(qv.y)} * dq;
       const f32x4 y = dK[nb][ib] * fk - f32x4{bf_lo(kv.x), bf_hi(kv.x), bf_lo(kv.y), bf_hi(kv.y)} * dk;
       store4<VEC>(oq, (uint32_t)b.dq_ld, row, n, a.N, u32x2{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])});
