@@ -25,6 +25,10 @@ bool sizes_ok(const delta_shape* s, int64_t rows, int64_t nseq) {
          mul_ok(ceil_div(rows, kChunk) + nseq + 1, hp * 64 * kMaxState);
 }
 int64_t chunk_ids(int64_t rows, int64_t nseq) { return ceil_div(rows, kChunk) + nseq; }
+// the key heads' records, first in either workspace
+int64_t keys_bytes(const delta_shape* s, int64_t rows, int64_t nseq) {
+  return align_up(chunk_ids(rows, nseq) * s->G * 2 * key_tile(state_tile(s->N)));
+}
 bool launches_ok(const delta_shape* s, int64_t rows, int64_t nseq) {
   return unit_blocks(nseq, s->H, s->G, ceil_div(s->P, kPTile), 1) <= kMaxBlocks / 2 &&
          mul_ok(chunk_ids(rows, nseq), s->H) && chunk_ids(rows, nseq) * s->H <= kMaxBlocks;
@@ -57,13 +61,14 @@ int layer_check(int64_t rows, int64_t d, const void* w, const void* bias, int w_
 
 // Byte offsets into the backward's workspace.
 struct BwdPlan {
-  int64_t rec_rev, cs, ct, u, f, head, bytes;
+  int64_t rec, rec_rev, cs, ct, u, f, head, bytes;
 };
 BwdPlan plan_bwd(const delta_shape* s, int64_t rows, int64_t nseq) {
   BwdPlan p{};
   const int64_t ids = chunk_ids(rows, nseq), tiles = ids * s->H * ceil_div(s->P, kPTile);
   const int64_t state = align_up(tiles * 64 * state_tile(s->N) * 4), values = align_up(tiles * 64 * 64 * 4);
-  int64_t at = align_up(ids * s->H * kRecFwd);
+  int64_t at = keys_bytes(s, rows, nseq);
+  p.rec = at, at += align_up(ids * s->H * kRecFwd);
   p.rec_rev = at, at += align_up(ids * s->H * kRecRev);
   p.cs = at, at += state;
   p.ct = at, at += state;
@@ -80,7 +85,7 @@ extern "C" {
 
 size_t delta_scan_fwd_workspace_bytes(const delta_shape* shape, int64_t rows, int64_t nseq) {
   if (!shape_ok(shape) || rows <= 0 || nseq <= 0 || !sizes_ok(shape, rows, nseq)) return 0;
-  return (size_t)align_up(chunk_ids(rows, nseq) * shape->H * kRecFwd);
+  return (size_t)(keys_bytes(shape, rows, nseq) + align_up(chunk_ids(rows, nseq) * shape->H * kRecFwd));
 }
 
 int delta_scan_fwd(const delta_shape* shape, int64_t rows, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
@@ -111,7 +116,8 @@ int delta_scan_fwd(const delta_shape* shape, int64_t rows, const void* q, int64_
   fill(&d, shape, rows, q, q_ld, k, k_ld, v, v_ld, dt, dt_ld, b, b_ld, A, dt_bias, seq, nseq);
   d.s.y = static_cast<uint16_t*>(y);
   d.s.y_ld = y_ld;
-  d.rec = static_cast<char*>(ws);
+  d.keys = static_cast<char*>(ws);
+  d.rec = d.keys + keys_bytes(shape, rows, nseq);
   return launch_delta_fwd(d, vec_ok(shape), stream) == hipSuccess ? CONV1D_OK : CONV1D_EHIP;
 }
 
@@ -158,7 +164,8 @@ int delta_scan_bwd(const delta_shape* shape, int64_t rows, const void* dy, int64
     g.d.s.init = initial_state;
     g.d.s.slots = nseq;
     g.d.s.s_slot = hp * shape->N;
-    g.d.rec = w;
+    g.d.keys = w;
+    g.d.rec = w + p.rec;
     g.dy = static_cast<const uint16_t*>(dy), g.dy_ld = dy_ld;
     g.dfin = dfinal_state, g.dinit = dinitial_state;
     g.dq = static_cast<uint16_t*>(dq), g.dq_ld = dq_ld;

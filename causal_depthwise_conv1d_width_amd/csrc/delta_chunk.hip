@@ -2,30 +2,42 @@
 //
 // With L the prefix sums of the log decays, r the rates, k and q unit or as they are, inside one chunk and head
 //   X_ij = r_i e^{L_i - L_j} k_i . k_j  (i > j),   T = (I + X)^-1,   P_ij = scale e^{L_i - L_j} q_i . k_j  (i >= j)
-// the walk needs U = T (r (V - e^L K S)) and P U.  A block takes one chunk and key head: the products K K^T and Q K^T of
-// the raw bf16 rows are made once, and each of its value heads decays them; row norms, steps and rates are FP32 factors
-// beside the products, so nothing is rounded before T is complete.
+// the walk needs U = T (r (V - e^L K S)) and P U.  A block takes one chunk and key head.  Rows of k and q go into fp16 tiles,
+// times a power of two that is exact; the products K K^T and Q K^T are made once, and each of the value heads decays
+// them.  Norms, steps and rates are FP32 factors beside the products, so nothing is rounded before T is complete.
 // T: the four 16 x 16 blocks on the diagonal by substitution, a column a lane; then pairs of them, then pairs of pairs,
-// [T1 0; -T2 X21 T1, T2], by FP32 matrix instructions.  The rates of the columns are taken into T, whose FP32 values are
-// stored as three bf16 parts, P's as two (forward).
+// [T1 0; -T2 X21 T1, T2], by FP32 matrix instructions.
 // A row of k, dt or b that is not finite makes the head's state and all later rows so; zeros times it would reach earlier
-// rows of the chunk.  Such rows are left out here, and the record names the first.
+// rows of the chunk.  Forward, such rows are left out here, and the record names the first.
 #include "delta_device.h"
 
 namespace cssm {
 
+// the largest of 8 bf16 magnitudes, as bf16 bits (an infinity or NaN is larger than all numbers)
+__device__ __forceinline__ uint32_t max_bits(u32x4 v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t lo = v[e] & 0x7fffu, hi = v[e] >> 16 & 0x7fffu;
+    m = m > lo ? m : lo;
+    m = m > hi ? m : hi;
+  }
+  return m;
+}
+
 template <int NT, bool VEC, bool BWD>
-__global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs d, char* rec_rev) {
+__global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_chunk_kernel(DeltaArgs d, char* rec_rev) {
   constexpr int LD = 68;  // rows of 64 FP32 values, 16 bytes further apart
-  __shared__ __align__(16) uint16_t sK[64 * kLd<NT>];
-  __shared__ __align__(16) uint16_t sQ[64 * kLd<NT>];
+  __shared__ __align__(16) uint16_t sK[key_tile(NT) / 2];
+  __shared__ __align__(16) uint16_t sQ[key_tile(NT) / 2];
   __shared__ __align__(16) float sX[64 * LD];
   __shared__ __align__(16) float sT[64 * LD];
   __shared__ __align__(16) double sL[64];
-  __shared__ __align__(16) float s_rate[64], s_kn[64], s_qn[64];
+  __shared__ __align__(16) float s_rate[64], s_kn[64], s_qn[64], s_max[4];
   __shared__ int s_bad;
   const ScanArgs& a = d.s;
-  const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15, w = wave_id();
+  int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+  const int w = wave_id();
   const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
   const int grp = blk % (uint32_t)a.G;
   const int64_t id = blk / (uint32_t)a.G;
@@ -37,31 +49,43 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs d, char* rec
     TileRegs<NT, 256> tk, tq;
     load_tile<VEC>(tk, Rows(a.B + pc.r0 * a.B_ld + gn, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
     load_tile<VEC>(tq, Rows(a.C + pc.r0 * a.C_ld + gn, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
-    store_tile(sK, tk);
-    store_tile(sQ, tq);
-    auto norms = [&](const TileRegs<NT, 256>& t, float* to, float factor) {
+    char* keys = d.keys + (id * a.G + grp) * 2 * key_tile(NT);
+    auto convert = [&](const TileRegs<NT, 256>& t, uint16_t* lds, char* to, float* norm, float factor) {
 #pragma unroll
       for (int k = 0; k < NT / 32; ++k) {
-        const int row = (threadIdx.x + 256 * k) / (NT / 8);
-        float s = 0.f;
+        const int q = threadIdx.x + 256 * k, row = q / (NT / 8), c = q % (NT / 8) * 8;
+        uint32_t m = max_bits(t.v[k]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float lo = bf_lo(t.v[k][e]), hi = bf_hi(t.v[k][e]);
+        for (int x = NT / 16; x > 0; x >>= 1) {
+          const uint32_t o = __shfl_xor(m, x);
+          m = m > o ? m : o;
+        }
+        uint32_t e = m >> 7;  // the largest one's exponent
+        e = e < 1 ? 1 : (e > 253 ? 253 : e);
+        const float up = __uint_as_float((254 - e) << 23), down = __uint_as_float(e << 23);
+        float s = 0.f;
+        u32x4 h;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float lo = bf_lo(t.v[k][x]) * up, hi = bf_hi(t.v[k][x]) * up;
           s = __builtin_fmaf(lo, lo, s);
           s = __builtin_fmaf(hi, hi, s);
+          h[x] = pk_f16(lo, hi);
         }
 #pragma unroll
-        for (int m = NT / 16; m > 0; m >>= 1) s += __shfl_xor(s, m);
+        for (int x = NT / 16; x > 0; x >>= 1) s += __shfl_xor(s, x);
+        *reinterpret_cast<u32x4*>(lds + key_at<NT>(row, c)) = h;
+        *reinterpret_cast<u32x4*>(to + key_at<NT>(row, c) * 2) = h;
         // s - s: a NaN where the row is not finite
-        const float f = (d.qk_norm ? rsqrtf(s + d.norm_eps) : 1.f) + (s - s);
-        if (threadIdx.x % (NT / 8) == 0) to[row] = row < rows ? f * factor : 0.f;
+        const float f = (d.qk_norm ? rsqrtf(s + (d.norm_eps > 0.f ? d.norm_eps * up * up : 0.f)) : down) + (s - s);
+        if (c == 0) norm[row] = row < rows ? f * factor : 0.f;
       }
     };
-    norms(tk, s_kn, 1.f);
-    norms(tq, s_qn, d.scale);
+    convert(tk, sK, keys, s_kn, 1.f);
+    convert(tq, sQ, keys + key_tile(NT), s_qn, d.scale);
   }
   __syncthreads();
-  // score blocks (ib, jb) of this wave: rows i in the lanes, columns j in the registers
+  // score blocks (ib, jb) of this wave: rows i in the lanes, columns j in the registers (qkt: the other way round)
   f32x4 kk[3], qk[3];
 #pragma unroll
   for (int t = 0; t < 3; ++t) {
@@ -71,36 +95,24 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs d, char* rec
     if (w + 4 * t < 10) {
 #pragma unroll
       for (int ks = 0; ks < NT / 32; ++ks) {
-        const bf16x8 kj = op_straight<NT>(sK, 16 * jb, 32 * ks, lane);
-        kk[t] = mma(kj, op_straight<NT>(sK, 16 * ib, 32 * ks, lane), kk[t]);
-        qk[t] = mma(kj, op_straight<NT>(sQ, 16 * ib, 32 * ks, lane), qk[t]);
-      }
-    }
-  }
-  f32x4 qkt[3];  // rows in the registers
-  if constexpr (BWD) {
-#pragma unroll
-    for (int t = 0; t < 3; ++t) {
-      int ib, jb;
-      lower_block(w + 4 * t, ib, jb);
-      qkt[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (w + 4 * t < 10) {
-#pragma unroll
-        for (int ks = 0; ks < NT / 32; ++ks)
-          qkt[t] = mma(op_straight<NT>(sQ, 16 * ib, 32 * ks, lane), op_straight<NT>(sK, 16 * jb, 32 * ks, lane), qkt[t]);
+        const f16x8 kj = key_rows<NT>(sK, 16 * jb, 32 * ks, lane);
+        const f16x8 qi = key_rows<NT>(sQ, 16 * ib, 32 * ks, lane);
+        kk[t] = mmah(kj, key_rows<NT>(sK, 16 * ib, 32 * ks, lane), kk[t]);
+        qk[t] = BWD ? mmah(qi, kj, qk[t]) : mmah(kj, qi, qk[t]);
       }
     }
   }
 
   for (int hh = 0; hh < hg; ++hh) {
+    lane = fresh(lane);
+    g = lane >> 4, i = lane & 15;
     const int h = grp * hg + hh;
     char* rec = d.rec + (id * a.H + h) * kRecFwd;
     char* rev = BWD ? rec_rev + (id * a.H + h) * kRecRev : nullptr;
     if (w == 0) {  // lane = row
       const Rate rate(a, h);
       const float step = rate.step(raw_step(a, pc.r0, rows, lane, h), lane < rows);
-      const int64_t at = (pc.r0 + lane) * d.b_ld + h;
-      const float b = lane < rows ? load_num(d.b, at, a.dt_f32) : 0.f;
+      const float b = lane < rows ? load_num(d.b, (pc.r0 + lane) * d.b_ld + h, a.dt_f32) : 0.f;
       float r = lane < rows ? d.beta_max / (1.f + ex2(-kLog2e * b)) : 0.f;
       float kn = s_kn[lane], qn = s_qn[lane];
       double l = rate.exponent(step);
@@ -113,13 +125,13 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs d, char* rec
       sL[lane] = L;
       s_rate[lane] = r;
       if (lane == 0) s_bad = bad;
-      const float grown = ex2((float)L), left = ex2((float)(end - L));
+      const float up = ex2((float)L), left = ex2((float)(end - L));
       auto factors = [&](char* to) {
         Factors* f = reinterpret_cast<Factors*>(to);
-        f->f[0][lane] = grown * kn;
-        f->f[1][lane] = grown * qn;
-        f->f[2][lane] = left * kn;
-        f->f[3][lane] = r;
+        f->in[lane] = up * kn;
+        f->read[lane] = up * qn;
+        f->out[lane] = left * kn;
+        f->rate[lane] = r;
         if (lane == 0) {
           f->decay = ex2((float)end);
           f->bad = bad;
@@ -143,23 +155,20 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs d, char* rec
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float m = ex2((float)(Li - sL[col + r])) * knj[r];
-          const bool in = row < bad;  // and so is every column up to the diagonal
-          x[r] = in && col + r < row ? kk[t][r] * (m * kni) : 0.f;
-          p[r] = in && col + r <= row ? qk[t][r] * (m * qni) : 0.f;
+          x[r] = row < bad && col + r < row ? kk[t][r] * (m * kni) : 0.f;
+          p[r] = row < bad && col + r <= row ? qk[t][r] * (m * qni) : 0.f;
         }
         *reinterpret_cast<f32x4*>(sX + row * LD + col) = x;
         if constexpr (!BWD) {
           store_tri<2>(rec + kRecT, tri_block(ib, jb), p, lane);
         } else {  // column 16 jb + i in the lanes, rows in the registers
           const int c = 16 * jb + i, r0 = 16 * ib + 4 * g;
+          const double Lc = sL[c];
           const float knc = s_kn[c];
-          f32x4 pt;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float m = ex2((float)(sL[r0 + r] - sL[c])) * knc * s_qn[r0 + r];
-            pt[r] = r0 + r < bad && c <= r0 + r ? qkt[t][r] * m : 0.f;
-          }
-          store_tri<3>(rev + kRecT, tri_block(ib, jb), pt, lane);
+          for (int r = 0; r < 4; ++r)
+            p[r] = c <= r0 + r ? qk[t][r] * (ex2((float)(sL[r0 + r] - Lc)) * knc * s_qn[r0 + r]) : 0.f;
+          store_tri<3>(rev + kRecT, tri_block(ib, jb), p, lane);
         }
       }
     }
@@ -206,19 +215,29 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs d, char* rec
         sum = mma_f32(y, t_rows(ib, m), sum);
       }
       *reinterpret_cast<f32x4*>(sT + (16 * ib + i) * LD + 16 * jb + 4 * g) = -sum;
+      // the largest of T: its blocks of level two are here, the others in shared memory
+      float m = max4(max4(0.f, sum), t_rows(w, w));
+      if (w < 2) m = max4(m, t_rows(2 * w + 1, 2 * w));
+      m = max_across16(m);
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, x));
+      if (lane == 0) s_max[w] = m;
     }
     __syncthreads();
+    const Pow2 scale = bring_to<10>(__builtin_fmaxf(__builtin_fmaxf(s_max[0], s_max[1]), __builtin_fmaxf(s_max[2], s_max[3])));
+    if (threadIdx.x == 0) {
+      reinterpret_cast<Factors*>(rec + kRecFwd - kRecVec)->t_scale = scale.down;
+      if constexpr (BWD) reinterpret_cast<Factors*>(rev + kRecRev - kRecVec)->t_scale = scale.down;
+    }
 #pragma unroll
     for (int t = 0; t < 3; ++t) {
       int ib, jb;
       lower_block(w + 4 * t, ib, jb);
       if (w + 4 * t < 10) {
-        const f32x4 rate = *reinterpret_cast<const f32x4*>(s_rate + 16 * jb + 4 * g);
-        store_tri<3>(rec, tri_block(ib, jb), t_rows(ib, jb) * rate, lane);
-        if constexpr (BWD) store_tri<3>(rev, tri_block(ib, jb), t_cols(ib, jb), lane);
+        store_halves(rec, tri_block(ib, jb), t_rows(ib, jb) * scale.up, lane);
+        if constexpr (BWD) store_halves(rev, tri_block(ib, jb), t_cols(ib, jb) * scale.up, lane);
       }
     }
-    __syncthreads();
   }
 }
 

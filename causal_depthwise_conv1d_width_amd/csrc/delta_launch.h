@@ -6,14 +6,18 @@
 
 namespace cssm {
 
-// A chunk's record for one head, written by the chunk kernel and copied to shared memory by the walks.  Lower triangles of
-// 64 x 64 in 16 x 16 blocks, block (ib, jb) at ib (ib + 1) / 2 + jb: lane l holds row l % 16 and the four columns from
-// 4 (l / 16) on (transposed for the reverse walk: column l % 16, four rows), each bf16 part 512 bytes.
+// What the chunk kernel leaves for the walks, which copy it to shared memory as it is.
+// A key head's record of a chunk: the tiles of k and of q, [64 places][NT + 8 columns] of fp16, each row times a power of two.
+constexpr int64_t key_tile(int NT) { return 64 * (NT + 8) * 2; }
+// A head's record: lower triangles of 64 x 64 in 16 x 16 blocks, block (ib, jb) at ib (ib + 1) / 2 + jb: lane l holds row
+// l % 16 and the four columns from 4 (l / 16) on (for the reverse walk: column l % 16, four rows), each 16-bit part 512 bytes.
+// First the triangular system's inverse T in two fp16 parts, then the scores P (in two bf16 parts forward, in three in
+// reverse), then factors.
 constexpr int kTriBlocks = 10, kTriPart = 512;
-constexpr int kRecT = kTriBlocks * 3 * kTriPart;  // the triangular system's inverse, three parts
-constexpr int kRecVec = 4 * 64 * 4 + 64;          // four factors a row, then: decay of the chunk, first row not finite
-constexpr int kRecFwd = kRecT + 2 * kTriBlocks * kTriPart + kRecVec;  // the scores in two parts
-constexpr int kRecRev = 2 * kRecT + kRecVec;                      // the reverse walk's, in three
+constexpr int kRecT = kTriBlocks * 2 * kTriPart;
+constexpr int kRecVec = 4 * 64 * 4 + 64;
+constexpr int kRecFwd = kRecT + kTriBlocks * 2 * kTriPart + kRecVec;
+constexpr int kRecRev = kRecT + kTriBlocks * 3 * kTriPart + kRecVec;
 
 // s: x = v, B = k, C = q, init, fin and slots as in the scan; y
 struct DeltaArgs {
@@ -23,7 +27,8 @@ struct DeltaArgs {
   float scale, beta_max, norm_eps;
   int qk_norm;
   int64_t n_chunk_slots;  // chunk id = row / kChunk, or n_chunk_slots + seq for a sequence's first
-  char* rec;              // [chunk id, H] records of kRecFwd bytes
+  char* keys;             // [chunk id, G] key heads' records of 2 key_tile(NT) bytes
+  char* rec;              // [chunk id, H] heads' records of kRecFwd bytes
 };
 
 struct DeltaBwdArgs {

@@ -1,25 +1,25 @@
 // delta_scan.hip -- forward gated delta rule over packed rows: the walk of the states.
 //
 // A block walks one sequence for 64 columns of one head, a chunk of 64 rows at a time (delta_chunk.hip: L, r, T, P):
-//   R = V - e^L K S^T,   U = T r R,   Y = scale e^L Q S^T + P U,   S' = e^{L_Q} S + U^T (e^{L_Q - L} K)
+//   R = r (V - e^L K S^T),   U = T R,   Y = scale e^L Q S^T + P U,   S' = e^{L_Q} S + U^T (e^{L_Q - L} K)
 // Each of its 4 waves owns 16 columns p of V, U, Y and S, which depend on no other column: nothing passes between waves.
 // The state's accumulators (registers n, lanes p) are, unmoved, the operand that K S^T and Q S^T contract over n, and R's
 // and U's the ones that T, P and K contract over rows.  Shared memory holds K, Q, V and the chunk's record for all waves;
 // the next chunk's are loaded over the current one's products.
-// FP32 operands enter as three bf16 parts (K S^T, S') or, both being FP32, six products (T R), so that states keep
-// FP32's precision; y takes the state, the scores and U in two: with one of the state and the scores it was up to
-// 2.7e-3 off where its terms cancel (its own rounding: 1.66e-3), PCT faster.
+// FP32 operands enter as two fp16 parts (delta_device.h), T R with three products, so that states keep 22 bits of their
+// column's largest value; y takes the first part of S alone (2^-12 of a term).  P U is of bf16 parts, two of each: the
+// scores and new values of a chunk's rows may lie far apart, and each row of y is to keep its own precision.
 #include "delta_device.h"
 
 namespace cssm {
 
 template <int NT, bool VEC>
 __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_kernel(DeltaArgs d) {
-  constexpr int T = 256, NB = NT / 16;
-  __shared__ __align__(16) uint16_t sK[64 * kLd<NT, 16>];
-  __shared__ __align__(16) uint16_t sQ[64 * kLd<NT>];
+  constexpr int T = 256, NB = NT / 16, kKeys = 2 * (int)key_tile(NT);
+  __shared__ __align__(16) uint16_t sKQ[kKeys / 2];
   __shared__ __align__(16) uint16_t sV[64 * kLd<64, 16>];
   __shared__ __align__(16) char sR[kRecFwd];
+  const uint16_t *sK = sKQ, *sQ = sKQ + kKeys / 4;
   const ScanArgs& a = d.s;
   const Units<1> us(a, blockIdx.x);
   if (!us.ok) return;
@@ -47,16 +47,22 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_kernel(
   }
   f32x4 S[NB];
   load_state(S, from && p_in < pn ? a.init + slot * a.s_slot + state_at + (int64_t)p_in * a.N : nullptr, a.N, g);
+  float s_down = 1.f;  // the state is s_down S
+  {
+    const Pow2 scale = state_scale<1>(state_max(S));
+    s_down = scale.down;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) S[nb] *= scale.up;
+  }
 
-  const int64_t gn = (int64_t)us.group * a.N;
-  TileRegs<NT, T> tK, tQ;
+  CopyRegs<kKeys, T> tK;
   TileRegs<64, T> tV;
-  RecordRegs<kRecFwd, T> tR;
+  CopyRegs<kRecFwd, T> tR;
   auto load = [&](const Chunks<false>& c, int rows) {
-    load_tile<VEC>(tK, Rows(a.B + c.c0 * a.B_ld + gn, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
-    load_tile<VEC>(tQ, Rows(a.C + c.c0 * a.C_ld + gn, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
+    const int64_t id = chunk_id(pc, c.c0, d.n_chunk_slots);
+    load_bytes(tK, d.keys + (id * a.G + us.group) * kKeys, rows > 0);
+    load_bytes(tR, d.rec + (id * a.H + me.h) * kRecFwd, rows > 0);
     load_tile<VEC>(tV, Rows(a.x + c.c0 * a.x_ld + me.col, a.x_ld, rows, pn, 2), (uint32_t)a.x_ld, pn);
-    load_record(tR, d.rec + (chunk_id(pc, c.c0, d.n_chunk_slots) * a.H + me.h) * kRecFwd, rows > 0);
   };
   Chunks<false> c(pc.s, pc.e);
   int rows = c.rows();
@@ -64,13 +70,13 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_kernel(
   const char* sT = sR;
   const char* sP = sR + kRecT;
   const Factors& fac = *reinterpret_cast<const Factors*>(sR + kRecFwd - kRecVec);
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   for (;;) {
     lane = fresh(lane);
     g = lane >> 4, i = lane & 15;
-    store_tile<16>(sK, tK);
-    store_tile(sQ, tQ);
+    store_bytes(sKQ, tK);
+    store_bytes(sR, tR);
     store_tile<16>(sV, tV);
-    store_record(sR, tR);
     __syncthreads();
     const Rows out(yb + c.c0 * a.y_ld, a.y_ld, rows, pn, 2);
     c = step_chunk(c, rows);  // rows == 0: that was the last one
@@ -78,30 +84,33 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_kernel(
     phase();
     f32x4 r[4], y[4];  // rows in the registers, columns p in the lanes; y the other way round
 #pragma unroll
-    for (int ib = 0; ib < 4; ++ib) r[ib] = y[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int ib = 0; ib < 4; ++ib) r[ib] = y[ib] = zero;
 #pragma unroll
     for (int ks = 0; ks < NT / 32; ++ks) {
-      const Parts s = split(S[2 * ks], S[2 * ks + 1]);
+      const Halves s = halves(S[2 * ks], S[2 * ks + 1]);
 #pragma unroll
       for (int ib = 0; ib < 4; ++ib) {
-        r[ib] = mma3(op_split<NT, 16>(sK, 16 * ib, 32 * ks, lane), s, r[ib]);
-        const bf16x8 q = op_split<NT>(sQ, 16 * ib, 32 * ks, lane);
-        y[ib] = mma(s.p[1], q, y[ib]);
-        y[ib] = mma(s.p[0], q, y[ib]);
+        r[ib] = mma2(key_rows<NT>(sK, 16 * ib, 32 * ks, lane), s, r[ib]);
+        y[ib] = mmah(s.hi, key_rows<NT>(sQ, 16 * ib, 32 * ks, lane), y[ib]);
       }
-      phase();
     }
+    const float s_max = state_max(S);
+    {
+      f32x4 sd;  // the columns' scales, where columns are in the registers
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sd[e] = __shfl(s_down, 4 * g + e);
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) y[ib] *= sd * fac.read[16 * ib + i];
+    }
+    float r_max = 0.f;
     bool fine = true;
 #pragma unroll
     for (int ib = 0; ib < 4; ++ib) {
-      const f32x4 f = *reinterpret_cast<const f32x4*>(fac.f[0] + 16 * ib + 4 * g);
-      const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_s16x4*)(sV + at<64, 16>(16 * ib + 4 * g + (i >> 2), 16 * w + 4 * (i & 3))));
-      const u32x2 v = __builtin_bit_cast(u32x2, t);
-      r[ib] = f32x4{bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y)} - f * r[ib];
+      const f32x4 f = *reinterpret_cast<const f32x4*>(fac.in + 16 * ib + 4 * g) * s_down;
+      r[ib] = (column4(sV, 16 * ib, 16 * w, g, i) - f * r[ib]) * *reinterpret_cast<const f32x4*>(fac.rate + 16 * ib + 4 * g);
 #pragma unroll
       for (int e = 0; e < 4; ++e) fine = fine && __builtin_isfinite(r[ib][e]);
-      y[ib] *= fac.f[1][16 * ib + i];
+      r_max = max4(r_max, r[ib]);
     }
     // The first row of this lane's column that is not finite: it and the later ones are left out of the products, whose
     // zeros would spread them, and put in at the end
@@ -117,49 +126,59 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_kernel(
         }
       bad = min(bad, __shfl_xor(bad, 16));
       bad = min(bad, __shfl_xor(bad, 32));
+      r_max = 0.f;
 #pragma unroll
-      for (int ib = 0; ib < 4; ++ib)
+      for (int ib = 0; ib < 4; ++ib) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (16 * ib + 4 * g + e >= bad) r[ib][e] = 0.f;
+        r_max = max4(r_max, r[ib]);
+      }
     }
-    phase();
+    const Pow2 rs = bring_to<10>(max_across16(r_max));
     f32x4 u[4];
     {
-      const Parts rp[2] = {split(r[0], r[1]), split(r[2], r[3])};
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) r[ib] *= rs.up;
+      const Halves rp[2] = {halves(r[0], r[1]), halves(r[2], r[3])};
+      const float u_down = rs.down * fac.t_scale;
 #pragma unroll
       for (int ib = 0; ib < 4; ++ib) {
-        u[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
+        u[ib] = zero;
 #pragma unroll
-        for (int ks = 0; ks <= ib / 2; ++ks) {
-          const Parts t = {{tri_rows<3>(sT, ib, ks, 0, lane), tri_rows<3>(sT, ib, ks, 1, lane), tri_rows<3>(sT, ib, ks, 2, lane)}};
-          u[ib] = mma6(t, rp[ks], u[ib]);
-        }
-        phase();
+        for (int ks = 0; ks <= ib / 2; ++ks)
+          u[ib] = mma3(t_rows(sT, ib, ks, lane), rp[ks], u[ib]);
       }
-    }
-    const float decay = fac.decay;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) S[nb] *= decay;
+      for (int ib = 0; ib < 4; ++ib) u[ib] *= u_down;
+    }
+    // what goes into the state and its scale
+    f32x4 o[4];
+    float o_max = 0.f;
+#pragma unroll
+    for (int ib = 0; ib < 4; ++ib) {
+      o[ib] = u[ib] * *reinterpret_cast<const f32x4*>(fac.out + 16 * ib + 4 * g);
+      o_max = max4(o_max, o[ib]);
+    }
+    const float grown = fac.decay * s_down;
+    const Pow2 ss = state_scale<1>(__builtin_fmaxf(max_across16(o_max), s_max * grown));
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) S[nb] *= grown * ss.up;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      {
-        const Parts up = split(u[2 * ks], u[2 * ks + 1]);
+      const Halves op = halves(o[2 * ks] * ss.up, o[2 * ks + 1] * ss.up);
 #pragma unroll
-        for (int ib = 2 * ks; ib < 4; ++ib) {
-          const bf16x8 p = tri_rows<2>(sP, ib, ks, 0, lane);
-          y[ib] = mma(up.p[0], tri_rows<2>(sP, ib, ks, 1, lane), y[ib]);
-          y[ib] = mma(up.p[1], p, y[ib]);
-          y[ib] = mma(up.p[0], p, y[ib]);
-        }
+      for (int nb = 0; nb < NB; ++nb) S[nb] = mma2(key_cols<NT>(sK, 32 * ks, 16 * nb, lane), op, S[nb]);
+      const Parts up = split(u[2 * ks], u[2 * ks + 1]);
+#pragma unroll
+      for (int ib = 2 * ks; ib < 4; ++ib) {
+        const bf16x8 p = __builtin_bit_cast(bf16x8, tri_rows<2>(sP, ib, ks, 0, lane));
+        y[ib] = mma(up.p[0], __builtin_bit_cast(bf16x8, tri_rows<2>(sP, ib, ks, 1, lane)), y[ib]);
+        y[ib] = mma(up.p[1], p, y[ib]);
+        y[ib] = mma(up.p[0], p, y[ib]);
       }
-      const f32x4 wa = *reinterpret_cast<const f32x4*>(fac.f[2] + 32 * ks + 4 * g);
-      const f32x4 wb = *reinterpret_cast<const f32x4*>(fac.f[2] + 32 * ks + 16 + 4 * g);
-      const Parts us_ = split(u[2 * ks] * wa, u[2 * ks + 1] * wb);
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) S[nb] = mma3(op_cols<NT, 16>(sK, 32 * ks, 16 * nb, lane), us_, S[nb]);
-      phase();
     }
+    s_down = ss.down;
     if (__builtin_expect(any_bad, 0)) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -181,7 +200,11 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_kernel(
     if (rows == 0) break;
     __syncthreads();
   }
-  if (a.fin && p_in < pn) store_state(S, a.fin + slot * a.s_slot + state_at + (int64_t)p_in * a.N, a.N, lane >> 4);
+  if (a.fin && p_in < pn) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) S[nb] *= s_down;
+    store_state(S, a.fin + slot * a.s_slot + state_at + (int64_t)p_in * a.N, a.N, lane >> 4);
+  }
 }
 
 template <int NT>

@@ -16,7 +16,8 @@
 //          + sum_{j < t} k_j . e^{L_Q - L_j} D^T U_j + sum_{i >= t > j} (P_ij W_ij - X_ij Y_ij)
 //   d(dt_t) = A dl_t softplus',  and through the norms of q and k at the end.
 // All of dl's terms are sums of what decays over row t, by blocks of 16 rows: no differences of longer sums.
-// dl, db, dA and the initial states' gradient are FP32 results: S, D, U and F enter their products as three bf16 parts.
+// dl, db, dA and the initial states' gradient are FP32 results: S, D, U and F enter their products as two fp16 parts
+// (delta_device.h), dY as it is.
 // The decayed scores that go into dq and dk alone enter as two: with one these were up to 2.7e-3 off where terms cancel (their own
 // rounding: 1.66e-3).
 #include "delta_device.h"
@@ -40,16 +41,16 @@ __device__ __forceinline__ int at_(int row, int col) {
 
 // 16 x 16 FP32 blocks of a state (registers n, lanes p) to its place
 template <int NB>
-__device__ __forceinline__ void store_blocks(float* to, const f32x4 (&S)[NB], int w, int lane, bool in) {
-  const Rows r(to + w * NB * 256, NB * 256, 1, in ? NB * 256 : 0, 4);
+__device__ __forceinline__ void store_blocks(float* to, const f32x4 (&S)[NB], float scale, int w, int lane) {
+  const Rows r(to + w * NB * 256, NB * 256, 1, NB * 256, 4);
   const int at = ((lane & 15) * 16 + (lane >> 4) * 4) * 4;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[nb]), r.r, nb * 1024 + at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[nb] * scale), r.r, nb * 1024 + at, 0, 0);
 }
 // 64 rows of 64 columns (registers rows, lanes columns), this wave's 16 columns
-__device__ __forceinline__ void store_rows(float* to, const f32x4 (&v)[4], int w, int lane, bool in) {
-  const Rows r(to, 4096, 1, in ? 4096 : 0, 4);
+__device__ __forceinline__ void store_rows(float* to, const f32x4 (&v)[4], int w, int lane) {
+  const Rows r(to, 4096, 1, 4096, 4);
 #pragma unroll
   for (int ib = 0; ib < 4; ++ib)
 #pragma unroll
@@ -60,8 +61,7 @@ __device__ __forceinline__ void store_rows(float* to, const f32x4 (&v)[4], int w
 
 template <int NT>
 struct WalkShared {
-  __align__(16) uint16_t k[64 * kLd<NT, 16>];
-  __align__(16) uint16_t q[64 * kLd<NT, 16>];
+  __align__(16) uint16_t kq[key_tile(NT)];  // both tiles' bytes
   __align__(16) uint16_t v[64 * kLd<64, 16>];
   __align__(16) char rec[kRecRev];
 };
@@ -69,6 +69,7 @@ struct WalkShared {
 template <int NT, bool VEC, bool REV>
 __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>& sh) {
   constexpr int T = kWalkThreads, NB = NT / 16, kBytes = REV ? kRecRev : kRecFwd;
+  constexpr int kKeys = (REV ? 2 : 1) * (int)key_tile(NT);  // the forward walk reads k alone
   const DeltaArgs& d = b.d;
   const ScanArgs& a = d.s;
   const Units<1> us(a, blockIdx.x);
@@ -89,79 +90,66 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
   }
   f32x4 S[NB];
   load_state(S, start && p_in < pn ? start + state_at + (int64_t)p_in * a.N : nullptr, a.N, g);
+  int64_t walked = pc.seq;  // sequences of few chunks do not all begin with the same signs
+  float turn = sign_at(walked, REV);  // the state's sign in the chunk
+  float s_down;  // the state is turn s_down S
+  {
+    const Pow2 scale = state_scale<REV ? 2 : 1>(state_max(S));
+    s_down = scale.down;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) S[nb] *= turn * scale.up;
+  }
 
-  const int64_t gn = (int64_t)us.group * a.N;
   const uint16_t* vb = REV ? b.dy : a.x;
   const int64_t v_ld = REV ? b.dy_ld : a.x_ld;
   const char* recs = REV ? b.rec_rev : d.rec;
-  TileRegs<NT, T> tK, tQ;
+  CopyRegs<kKeys, T> tK;
   TileRegs<64, T> tV;
-  RecordRegs<kBytes, T> tR;
+  CopyRegs<kBytes, T> tR;
   auto load = [&](const Chunks<REV>& c, int rows) {
-    load_tile<VEC>(tK, Rows(a.B + c.c0 * a.B_ld + gn, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
-    if constexpr (REV) load_tile<VEC>(tQ, Rows(a.C + c.c0 * a.C_ld + gn, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
+    const int64_t id = chunk_id(pc, c.c0, d.n_chunk_slots);
+    load_bytes(tK, d.keys + (id * a.G + us.group) * 2 * key_tile(NT), rows > 0);
+    load_bytes(tR, recs + (id * a.H + me.h) * kBytes, rows > 0);
     load_tile<VEC>(tV, Rows(vb + c.c0 * v_ld + me.col, v_ld, rows, pn, 2), (uint32_t)v_ld, pn);
-    load_record(tR, recs + (chunk_id(pc, c.c0, d.n_chunk_slots) * a.H + me.h) * kBytes, rows > 0);
   };
   Chunks<REV> c(pc.s, pc.e);
   int rows = c.rows();
   load(c, rows);
-  int64_t walked = pc.seq;  // sequences of few chunks do not all begin with the same signs
-  float turn = sign_at(walked, REV);  // the state's sign in the chunk
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) S[nb] *= turn;
+  const uint16_t *sK = sh.kq, *sQ = sh.kq + key_tile(NT) / 2;
   const char *sT = sh.rec, *sP = sh.rec + kRecT;
   const Factors& fac = *reinterpret_cast<const Factors*>(sh.rec + kBytes - kRecVec);
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   for (;;) {
     lane = fresh(lane);
     g = lane >> 4, i = lane & 15;
-    store_tile<16>(sh.k, tK);
-    if constexpr (REV) store_tile<16>(sh.q, tQ);
+    store_bytes(sh.kq, tK);
+    store_bytes(sh.rec, tR);
     store_tile<16>(sh.v, tV);
-    store_record(sh.rec, tR);
     __syncthreads();
     const int64_t at = (chunk_id(pc, c.c0, d.n_chunk_slots) * a.H + me.h) * a.ptiles + (me.p_first / kPTile);
     c = step_chunk(c, rows);  // rows == 0: that was the last one
     load(c, rows);
-    store_blocks((REV ? b.ct : b.cs) + at * (64 * NT), S, w, lane, true);
+    store_blocks((REV ? b.ct : b.cs) + at * (64 * NT), S, s_down, w, lane);
     phase();
     f32x4 r[4];  // K S: rows in the registers, columns p in the lanes
 #pragma unroll
-    for (int ib = 0; ib < 4; ++ib) r[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int ib = 0; ib < 4; ++ib) r[ib] = zero;
 #pragma unroll
     for (int ks = 0; ks < NT / 32; ++ks) {
-      const Parts s = split(S[2 * ks], S[2 * ks + 1]);
+      const Halves s = halves(S[2 * ks], S[2 * ks + 1]);
 #pragma unroll
-      for (int ib = 0; ib < 4; ++ib) r[ib] = mma3(op_split<NT, 16>(sh.k, 16 * ib, 32 * ks, lane), s, r[ib]);
-      phase();
+      for (int ib = 0; ib < 4; ++ib) r[ib] = mma2(key_rows<NT>(sK, 16 * ib, 32 * ks, lane), s, r[ib]);
     }
-    const float next = sign_at(++walked, REV), change = turn * next;
-    const float decay = change * fac.decay;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) S[nb] *= decay;
-    f32x4 u[4];
+    const float s_max = state_max(S);
+    bf16x8 y[2];
     if constexpr (!REV) {
 #pragma unroll
       for (int ib = 0; ib < 4; ++ib) {
-        const f32x4 f = *reinterpret_cast<const f32x4*>(fac.f[0] + 16 * ib + 4 * g);
-        const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_s16x4*)(sh.v + at_<64, 16>(16 * ib + 4 * g + (i >> 2), 16 * w + 4 * (i & 3))));
-        const u32x2 v = __builtin_bit_cast(u32x2, t);
-        r[ib] = f32x4{bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y)} * turn - f * r[ib];
+        const f32x4 f = *reinterpret_cast<const f32x4*>(fac.in + 16 * ib + 4 * g) * s_down;
+        r[ib] = (column4(sh.v, 16 * ib, 16 * w, g, i) * turn - f * r[ib]) *
+                *reinterpret_cast<const f32x4*>(fac.rate + 16 * ib + 4 * g);
       }
-      const Parts rp[2] = {split(r[0], r[1]), split(r[2], r[3])};
-#pragma unroll
-      for (int ib = 0; ib < 4; ++ib) {
-        u[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks <= ib / 2; ++ks)
-          u[ib] = mma6(Parts{{tri_rows<3>(sT, ib, ks, 0, lane), tri_rows<3>(sT, ib, ks, 1, lane), tri_rows<3>(sT, ib, ks, 2, lane)}},
-                       rp[ks], u[ib]);
-        phase();
-      }
-      store_rows(b.u + at * 4096, u, w, lane, true);
     } else {
-      bf16x8 y[2];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         u32x4 v = __builtin_bit_cast(u32x4, op_cols<64, 16>(sh.v, 32 * ks, 16 * w, lane));
@@ -170,56 +158,79 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
       }
 #pragma unroll
       for (int jb = 0; jb < 4; ++jb) {
-        r[jb] *= *reinterpret_cast<const f32x4*>(fac.f[2] + 16 * jb + 4 * g);
+        r[jb] *= *reinterpret_cast<const f32x4*>(fac.out + 16 * jb + 4 * g) * s_down;
 #pragma unroll
         for (int ks = jb / 2; ks < 2; ++ks)
-          r[jb] = mma3(Parts{{tri_cols<3>(sP, jb, ks, 0, lane), tri_cols<3>(sP, jb, ks, 1, lane), tri_cols<3>(sP, jb, ks, 2, lane)}},
-                       y[ks], r[jb]);
-        phase();
-      }
-      const Parts rp[2] = {split(r[0], r[1]), split(r[2], r[3])};
 #pragma unroll
-      for (int jb = 0; jb < 4; ++jb) {
-        u[jb] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = jb / 2; ks < 2; ++ks)
-          u[jb] = mma6(Parts{{tri_cols<3>(sT, jb, ks, 0, lane), tri_cols<3>(sT, jb, ks, 1, lane), tri_cols<3>(sT, jb, ks, 2, lane)}},
-                       rp[ks], u[jb]);
-        phase();
-      }
-      store_rows(b.f + at * 4096, u, w, lane, true);
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const f32x4 wa = *reinterpret_cast<const f32x4*>(fac.f[1] + 32 * ks + 4 * g);
-        const f32x4 wb = *reinterpret_cast<const f32x4*>(fac.f[1] + 32 * ks + 16 + 4 * g);
-        const Parts yp = split_scaled(y[ks], wa * change, wb * change);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) S[nb] = mma3(op_cols<NT, 16>(sh.q, 32 * ks, 16 * nb, lane), yp, S[nb]);
-        phase();
+          for (int p = 2; p >= 0; --p)
+            r[jb] = mma(__builtin_bit_cast(bf16x8, tri_cols<3>(sP, jb, ks, p, lane)), y[ks], r[jb]);
       }
     }
+    float r_max = 0.f;
+#pragma unroll
+    for (int ib = 0; ib < 4; ++ib) r_max = max4(r_max, r[ib]);
+    const Pow2 rs = bring_to<10>(max_across16(r_max));
+    f32x4 u[4];
+    {
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) r[ib] *= rs.up;
+      const Halves rp[2] = {halves(r[0], r[1]), halves(r[2], r[3])};
+      const float u_down = rs.down * fac.t_scale;
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) {
+        u[ib] = zero;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          if (REV ? ks >= ib / 2 : ks <= ib / 2)
+            u[ib] = mma3(REV ? t_cols(sT, ib, ks, lane) : t_rows(sT, ib, ks, lane), rp[ks], u[ib]);
+      }
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) u[ib] *= u_down;
+    }
+    store_rows((REV ? b.f : b.u) + at * 4096, u, w, lane);
+    // what goes into the state and its scale
+    f32x4 yo[4];
+    float o_max = 0.f;
+#pragma unroll
+    for (int ib = 0; ib < 4; ++ib) {
+      const int row = 16 * ib + 4 * g;
+      if constexpr (REV) {
+        const u32x4 v = __builtin_bit_cast(u32x4, y[ib / 2]);
+        const uint32_t v0 = v[2 * (ib & 1)], v1 = v[2 * (ib & 1) + 1];
+        yo[ib] = f32x4{bf_lo(v0), bf_hi(v0), bf_lo(v1), bf_hi(v1)} * *reinterpret_cast<const f32x4*>(fac.read + row);
+        o_max = max4(o_max, yo[ib]);
+        u[ib] *= -*reinterpret_cast<const f32x4*>(fac.in + row) * *reinterpret_cast<const f32x4*>(fac.rate + row);
+      } else {
+        u[ib] *= *reinterpret_cast<const f32x4*>(fac.out + row);
+      }
+      o_max = max4(o_max, u[ib]);
+    }
+    const float next = sign_at(++walked, REV), change = turn * next, kept = fac.decay * s_down;
+    const Pow2 ss = state_scale<REV ? 2 : 1>(__builtin_fmaxf(max_across16(o_max), s_max * kept));
+    const float up = change * ss.up;
+    s_down = ss.down;
+    turn = next;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) S[nb] *= kept * up;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      f32x4 wt[2];
+      const Halves o = halves(u[2 * ks] * up, u[2 * ks + 1] * up);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int row = 32 * ks + 16 * q + 4 * g;
-        if constexpr (REV)
-          wt[q] = *reinterpret_cast<const f32x4*>(fac.f[0] + row) * *reinterpret_cast<const f32x4*>(fac.f[3] + row) * -change;
-        else wt[q] = *reinterpret_cast<const f32x4*>(fac.f[2] + row) * change;
+      for (int nb = 0; nb < NB; ++nb) S[nb] = mma2(key_cols<NT>(sK, 32 * ks, 16 * nb, lane), o, S[nb]);
+      if constexpr (REV) {
+        const Halves q = halves(yo[2 * ks] * up, yo[2 * ks + 1] * up);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) S[nb] = mma2(key_cols<NT>(sQ, 32 * ks, 16 * nb, lane), q, S[nb]);
       }
-      const Parts up = split(u[2 * ks] * wt[0], u[2 * ks + 1] * wt[1]);
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) S[nb] = mma3(op_cols<NT, 16>(sh.k, 32 * ks, 16 * nb, lane), up, S[nb]);
-      phase();
     }
-    turn = next;
     if (rows == 0) break;
     __syncthreads();
   }
+  if (REV && b.dinit && p_in < pn) {
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) S[nb] *= turn;
-  if (REV && b.dinit && p_in < pn) store_state(S, b.dinit + state_at + (int64_t)p_in * a.N, a.N, lane >> 4);
+    for (int nb = 0; nb < NB; ++nb) S[nb] *= turn * s_down;
+    store_state(S, b.dinit + state_at + (int64_t)p_in * a.N, a.N, lane >> 4);
+  }
 }
 
 template <int NT, bool VEC>
@@ -229,22 +240,22 @@ __global__ __launch_bounds__(kWalkThreads, NT <= 128 ? 2 : 1) void delta_walks_k
   else delta_walk<NT, VEC, false>(b, sh);
 }
 
-// sum over the four rows of 16 lanes, in every lane
-__device__ __forceinline__ float across16(float v) {
-  const uint32_t u = __float_as_uint(v);
-  const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  const uint32_t x = __float_as_uint(__uint_as_float(p[0]) + __uint_as_float(p[1]));
-  const auto q = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+// the largest of 8 and of 64 neighbouring lanes, in every one of them (v >= 0)
+__device__ __forceinline__ float max8_lanes(float v) {
+  v = __builtin_fmaxf(v, dpp0<0xb1, 0xf>(v));
+  v = __builtin_fmaxf(v, dpp0<0x4e, 0xf>(v));
+  return __builtin_fmaxf(v, dpp0<0x141, 0xf>(v));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = max8_lanes(v);
+  return max_across16(__builtin_fmaxf(v, dpp0<0x140, 0xf>(v)));
 }
 
-// 64 x 64 FP32 values as three bf16 tiles
+// 64 x 64 values as two fp16 tiles
 constexpr int kTile = 64 * kLd<64>;
-__device__ __forceinline__ Parts tile_parts(const uint16_t* tiles, int row0, int k0, int l) {
-  return Parts{{op_split<64>(tiles, row0, k0, l), op_split<64>(tiles + kTile, row0, k0, l),
-                op_split<64>(tiles + 2 * kTile, row0, k0, l)}};
+__device__ __forceinline__ Halves tile_halves(const uint16_t* tiles, int row0, int k0, int l) {
+  return Halves{as_f16(op_split<64>(tiles, row0, k0, l)), as_f16(op_split<64>(tiles + kTile, row0, k0, l))};
 }
-
 // four values of a row as two parts
 __device__ __forceinline__ void store_parts(uint16_t* tiles, f32x4 v) {
   const u32x2 u = {pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
@@ -257,16 +268,17 @@ __device__ __forceinline__ void store_parts(uint16_t* tiles, f32x4 v) {
 // dq and dk and one or two of the ten score blocks.
 template <int NT, int WAVES, bool VEC>
 __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(DeltaBwdArgs b) {
-  constexpr int T = 64 * WAVES, NBW = NT / 16 / WAVES, SB = (10 + WAVES - 1) / WAVES, PER = 64 * 64 / T;
+  constexpr int T = 64 * WAVES, NBW = NT / 16 / WAVES, SB = (10 + WAVES - 1) / WAVES, KT = 512 / T;
   constexpr int PAD = NT > 128 ? 8 : 16;  // 256 columns leave no room for more
   __shared__ __align__(16) uint16_t sK[64 * kLd<NT, PAD>];
   __shared__ __align__(16) uint16_t sQ[64 * kLd<NT, PAD>];
   __shared__ __align__(16) uint16_t sY[kTile];
-  __shared__ __align__(16) uint16_t sUF[8 * kTile];  // U's and F's three parts, then the four decayed scores' two
+  __shared__ __align__(16) uint16_t sUF[8 * kTile];  // U's and F's parts, then the four decayed scores' two
   __shared__ __align__(16) double sL[64];
   __shared__ __align__(16) float s_rate[64], s_kn[64], s_qn[64], s_step[64], s_grow[64], s_left[64];
+  __shared__ __align__(16) float s_u[64], s_f[64], s_y[64];  // the tiles' rows are these times their values
   __shared__ float s_row[4][64], s_col[4][64], s_diag[64], s_in[WAVES][64], s_out[WAVES][64], s_dot[WAVES];
-  uint16_t *sU = sUF, *sF = sUF + 3 * kTile;
+  uint16_t *sU = sUF, *sF = sUF + 2 * kTile;
   uint16_t *sZk = sUF, *sZq = sUF + 2 * kTile, *sNj = sUF + 4 * kTile, *sNi = sUF + 6 * kTile;
   const DeltaArgs& d = b.d;
   const ScanArgs& a = d.s;
@@ -335,6 +347,27 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
 #pragma unroll
     for (int ib = 0; ib < 4; ++ib) dQ[nb][ib] = dK[nb][ib] = zero;
 
+  // rows of U, F and dY, 8 values a thread and step, loaded a tile ahead
+  f32x4 lu[KT][2], lf[KT][2];
+  TileRegs<64, T> ly;
+  const int tiles = hg * a.ptiles;
+  auto load_values = [&](int t) {
+    const int h = grp * hg + (uint32_t)t / (uint32_t)a.ptiles, pt = (uint32_t)t % (uint32_t)a.ptiles, p_first = pt * kPTile;
+    const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile, n = t < tiles ? 4096 : 0;
+    const int64_t at = (id * a.H + h) * a.ptiles + pt;
+    const Rows ru(b.u + at * 4096, 4096, 1, n, 4), rf(b.f + at * 4096, 4096, 1, n, 4);
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int o = (threadIdx.x + T * k) * 32 + 16 * e;
+        lu[k][e] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ru.r, o, 0, 0));
+        lf[k][e] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rf.r, o, 0, 0));
+      }
+    load_tile<VEC>(ly, Rows(b.dy + pc.r0 * b.dy_ld + (int64_t)h * a.P + p_first, b.dy_ld, n ? rows : 0, pn, 2),
+                   (uint32_t)b.dy_ld, pn);
+  };
+  load_values(0);
   for (int hh = 0; hh < hg; ++hh) {
     lane = fresh(lane);
     g = lane >> 4, i = lane & 15;
@@ -364,76 +397,107 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
     for (int pt = 0; pt < a.ptiles; ++pt) {
       const int p_first = pt * kPTile, pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
       const int64_t col = (int64_t)h * a.P + p_first, at = (id * a.H + h) * a.ptiles + pt;
+      // the state and the adjoint: this wave's columns n in the lanes, contracted rows p in the registers
+      f32x4 s[NBW][2][2], t[NBW][2][2];
       {
-        const int row = threadIdx.x / (64 / PER), c = threadIdx.x % (64 / PER) * PER;
-        f32x4 u[PER / 4], f[PER / 4];
-        const float *pu = b.u + at * 4096 + row * 64 + c, *pf = b.f + at * 4096 + row * 64 + c;
+        const Rows rs(b.cs + at * (64 * NT), 64 * NT, 1, 64 * NT, 4), rt(b.ct + at * (64 * NT), 64 * NT, 1, 64 * NT, 4);
 #pragma unroll
-        for (int e = 0; e < PER / 4; ++e) {
-          u[e] = *reinterpret_cast<const f32x4*>(pu + 4 * e);
-          f[e] = *reinterpret_cast<const f32x4*>(pf + 4 * e);
-        }
-        TileRegs<64, T> ty;
-        load_tile<VEC>(ty, Rows(b.dy + pc.r0 * b.dy_ld + col, b.dy_ld, rows, pn, 2), (uint32_t)b.dy_ld, pn);
-        __syncthreads();  // the last tile's or head's reads are done; this head's factors are there
-        store_tile(sY, ty);
+        for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int o = (((2 * ks + q) * (NT / 16) + w * NBW + nb) * 256 + (4 * g + e) * 16 + i) * 4;
+                s[nb][ks][q][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs.r, o, 0, 0));
+                t[nb][ks][q][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rt.r, o, 0, 0));
+              }
+      }
+      __syncthreads();  // the last tile's or head's reads are done; this head's factors are there
+      {
         const Rows dv(b.dv + pc.r0 * b.dv_ld + col, b.dv_ld, rows, pn, 2);
-        const float rate = sign_t * s_rate[row];
 #pragma unroll
-        for (int e = 0; e < PER / 4; ++e) {
-          const f32x4 o = f[e] * rate;
-          store4<VEC>(dv, (uint32_t)b.dv_ld, row, c + 4 * e, pn, u32x2{pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3])});
-#pragma unroll
-          for (int p = 0; p < 3; ++p) {
-            const u32x2 x = {pk_bf16(u[e][0], u[e][1]), pk_bf16(u[e][2], u[e][3])};
-            const u32x2 z = {pk_bf16(f[e][0], f[e][1]), pk_bf16(f[e][2], f[e][3])};
-            *reinterpret_cast<u32x2*>(sU + p * kTile + at_<64>(row, c + 4 * e)) = x;
-            *reinterpret_cast<u32x2*>(sF + p * kTile + at_<64>(row, c + 4 * e)) = z;
-            u[e] -= f32x4{bf_lo(x.x), bf_hi(x.x), bf_lo(x.y), bf_hi(x.y)};
-            f[e] -= f32x4{bf_lo(z.x), bf_hi(z.x), bf_lo(z.y), bf_hi(z.y)};
+        for (int k = 0; k < KT; ++k) {
+          const int row = (threadIdx.x + T * k) / 8, c = (threadIdx.x + T * k) % 8 * 8, o = at_<64>(row, c);
+          const u32x4 yv = ly.v[k];
+          f32x4 y0 = {bf_lo(yv.x), bf_hi(yv.x), bf_lo(yv.y), bf_hi(yv.y)}, y1 = {bf_lo(yv.z), bf_hi(yv.z), bf_lo(yv.w), bf_hi(yv.w)};
+          const Pow2 us = bring_to<10>(max8_lanes(max4(max4(0.f, lu[k][0]), lu[k][1])));
+          const Pow2 fs = bring_to<10>(max8_lanes(max4(max4(0.f, lf[k][0]), lf[k][1])));
+          const Pow2 ys = bring_to<10>(max8_lanes(max4(max4(0.f, y0), y1)));
+          const Halves hu = halves(lu[k][0] * us.up, lu[k][1] * us.up), hf = halves(lf[k][0] * fs.up, lf[k][1] * fs.up);
+          *reinterpret_cast<f16x8*>(sU + o) = hu.hi;
+          *reinterpret_cast<f16x8*>(sU + kTile + o) = hu.lo;
+          *reinterpret_cast<f16x8*>(sF + o) = hf.hi;
+          *reinterpret_cast<f16x8*>(sF + kTile + o) = hf.lo;
+          *reinterpret_cast<f16x8*>(sY + o) = halves_hi(y0 * ys.up, y1 * ys.up);
+          if (c == 0) {
+            s_u[row] = us.down;
+            s_f[row] = fs.down;
+            s_y[row] = ys.down;
           }
+          const float rate = sign_t * s_rate[row];
+          const f32x4 v0 = lf[k][0] * rate, v1 = lf[k][1] * rate;
+          store4<VEC>(dv, (uint32_t)b.dv_ld, row, c, pn, u32x2{pk_bf16(v0[0], v0[1]), pk_bf16(v0[2], v0[3])});
+          store4<VEC>(dv, (uint32_t)b.dv_ld, row, c + 4, pn, u32x2{pk_bf16(v1[0], v1[1]), pk_bf16(v1[2], v1[3])});
         }
       }
       __syncthreads();
-      // the state and the adjoint as operands: this wave's columns n in the lanes, contracted rows p in the registers
-      const float *ps = b.cs + at * (64 * NT), *pd = b.ct + at * (64 * NT);
+      phase();
 #pragma unroll
-      for (int nb = 0; nb < NBW; ++nb)
+      for (int nb = 0; nb < NBW; ++nb) {
+        float ms = 0.f, mt = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          f32x4 s[2], t[2];
+        for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const int64_t o = ((2 * ks + q) * (NT / 16) + w * NBW + nb) * 256 + 4 * g * 16 + i;
+            ms = max4(ms, s[nb][ks][q]);
+            mt = max4(mt, t[nb][ks][q]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s[q][e] = ps[o + 16 * e];
-              t[q][e] = pd[o + 16 * e];
-              dot = __builtin_fmaf(s[q][e], t[q][e], dot);
-            }
+            for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(s[nb][ks][q][e], t[nb][ks][q][e], dot);
           }
-          const Parts sp = split(s[0], s[1]), tp = split(t[0], t[1]);
+        const Pow2 ss = bring_to<10>(wave_max(ms)), ts = bring_to<10>(wave_max(mt));
+        f32x4 q4[4], f4[4], u4[4];
+#pragma unroll
+        for (int ib = 0; ib < 4; ++ib) q4[ib] = f4[ib] = u4[ib] = zero;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const Halves sp = halves(s[nb][ks][0] * ss.up, s[nb][ks][1] * ss.up);
+          const Halves tp = halves(t[nb][ks][0] * ts.up, t[nb][ks][1] * ts.up);
 #pragma unroll
           for (int ib = 0; ib < 4; ++ib) {
-            aQ[nb][ib] = mma3(sp, op_split<64>(sY, 16 * ib, 32 * ks, lane), aQ[nb][ib]);
-            aF[nb][ib] = mma6(sp, tile_parts(sF, 16 * ib, 32 * ks, lane), aF[nb][ib]);
-            aU[nb][ib] = mma6(tp, tile_parts(sU, 16 * ib, 32 * ks, lane), aU[nb][ib]);
-            phase();
+            q4[ib] = mma2(sp, as_f16(op_split<64>(sY, 16 * ib, 32 * ks, lane)), q4[ib]);
+            f4[ib] = mma3(sp, tile_halves(sF, 16 * ib, 32 * ks, lane), f4[ib]);
+            u4[ib] = mma3(tp, tile_halves(sU, 16 * ib, 32 * ks, lane), u4[ib]);
           }
         }
+#pragma unroll
+        for (int ib = 0; ib < 4; ++ib) {
+          const int row = 16 * ib + i;
+          aQ[nb][ib] += q4[ib] * (ss.down * s_y[row]);
+          aF[nb][ib] += f4[ib] * (ss.down * s_f[row]);
+          aU[nb][ib] += u4[ib] * (ts.down * s_u[row]);
+        }
+        phase();
+      }
+      load_values(hh * a.ptiles + pt + 1);
+      phase();
 #pragma unroll
       for (int t = 0; t < SB; ++t) {
         int ib, jb;
         lower_block(w + WAVES * t, ib, jb);
         if (w + WAVES * t < 10) {
+          f32x4 w4 = zero, y4 = zero;
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) {
-            const Parts u = tile_parts(sU, 16 * jb, 32 * ks, lane);
-            W[t] = mma3(u, op_split<64>(sY, 16 * ib, 32 * ks, lane), W[t]);
-            Y[t] = mma6(u, tile_parts(sF, 16 * ib, 32 * ks, lane), Y[t]);
+            const Halves u = tile_halves(sU, 16 * jb, 32 * ks, lane);
+            w4 = mma2(u, as_f16(op_split<64>(sY, 16 * ib, 32 * ks, lane)), w4);
+            y4 = mma3(u, tile_halves(sF, 16 * ib, 32 * ks, lane), y4);
           }
+          const f32x4 uj = *reinterpret_cast<const f32x4*>(s_u + 16 * jb + 4 * g);
+          W[t] += w4 * (uj * s_y[16 * ib + i]);
+          Y[t] += y4 * (uj * s_f[16 * ib + i]);
         }
-        phase();
       }
     }
     dot = wave_sum(dot);
@@ -461,7 +525,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
         dQ[nb][ib] += vq;
         dK[nb][ib] += vf + vu;
       }
-      const float in = across16(in_q * s_qn[row] + in_k * s_kn[row]), o = across16(out * s_kn[row]);
+      const float in = sum_across16(in_q * s_qn[row] + in_k * s_kn[row]), o = sum_across16(out * s_kn[row]);
       if (g == 0) {
         s_in[w][row] = in;
         s_out[w][row] = o;
@@ -500,7 +564,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
         store_parts(sZq + o, zq);
         store_parts(sNj + o, nj);
         store_parts(sNi + o, ni);
-        sum = across16(sum);
+        sum = sum_across16(sum);
         if (g == 0) s_row[jb][row] = sum;
         if (ib == jb && (i >> 2) == g) s_diag[row] = diag;
       }
@@ -600,7 +664,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
         dq += x[0] * bf_lo(qv.x) + x[1] * bf_hi(qv.x) + x[2] * bf_lo(qv.y) + x[3] * bf_hi(qv.y);
         dk += y[0] * bf_lo(kv.x) + y[1] * bf_hi(kv.x) + y[2] * bf_lo(kv.y) + y[3] * bf_hi(kv.y);
       }
-      dq = across16(dq), dk = across16(dk);
+      dq = sum_across16(dq), dk = sum_across16(dk);
       if (g == 0) {
         s_in[w][row] = dq;
         s_out[w][row] = dk;
