@@ -61,19 +61,15 @@ int layer_check(int64_t rows, int64_t d, const void* w, const void* bias, int w_
 
 // Byte offsets into the backward's workspace.
 struct BwdPlan {
-  int64_t rec, rec_rev, cs, ct, u, f, head, bytes;
+  int64_t rec, rec_rev, tiles, head, bytes;
 };
 BwdPlan plan_bwd(const delta_shape* s, int64_t rows, int64_t nseq) {
   BwdPlan p{};
-  const int64_t ids = chunk_ids(rows, nseq), tiles = ids * s->H * ceil_div(s->P, kPTile);
-  const int64_t state = align_up(tiles * 64 * state_tile(s->N) * 4), values = align_up(tiles * 64 * 64 * 4);
+  const int64_t ids = chunk_ids(rows, nseq);
   int64_t at = keys_bytes(s, rows, nseq);
   p.rec = at, at += align_up(ids * s->H * kRecFwd);
   p.rec_rev = at, at += align_up(ids * s->H * kRecRev);
-  p.cs = at, at += state;
-  p.ct = at, at += state;
-  p.u = at, at += values;
-  p.f = at, at += values;
+  p.tiles = at, at += align_up(ids * s->H * ceil_div(s->P, kPTile) * tile_floats(state_tile(s->N)) * 4);
   p.head = at, at += align_up(ids * s->H * 2 * 4);
   p.bytes = at;
   return p;
@@ -173,8 +169,7 @@ int delta_scan_bwd(const delta_shape* shape, int64_t rows, const void* dy, int64
     g.dv = static_cast<uint16_t*>(dv), g.dv_ld = dv_ld;
     g.ddt = ddt, g.ddt_ld = ddt_ld, g.db = db, g.db_ld = db_ld;
     g.rec_rev = w + p.rec_rev;
-    g.cs = reinterpret_cast<float*>(w + p.cs), g.ct = reinterpret_cast<float*>(w + p.ct);
-    g.u = reinterpret_cast<float*>(w + p.u), g.f = reinterpret_cast<float*>(w + p.f);
+    g.tiles = reinterpret_cast<float*>(w + p.tiles);
     g.head_part = reinterpret_cast<float*>(w + p.head);
   }
   return launch_delta_bwd(g, vec_ok(shape), stream) == hipSuccess ? CONV1D_OK : CONV1D_EHIP;

@@ -46,6 +46,11 @@ __device__ __forceinline__ f32x4 mma3(const Halves& a, const Halves& b, f32x4 c)
   return mmah(a.hi, b.hi, mmah(a.hi, b.lo, mmah(a.lo, b.hi, c)));
 }
 
+// Has a value computed here: sums that only the next pass needs otherwise move behind the following branches, and what they are
+// made of stays in registers until then.
+__device__ __forceinline__ void here(float& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void here(f32x4& v) { asm volatile("" : "+v"(v)); }
+
 // The power of two that brings m > 0 to [2^TO, 2^(TO + 1)), and its inverse.  Any m: of zeros and the smallest values the
 // largest possible one, of an infinity or NaN a small one.
 struct Pow2 {

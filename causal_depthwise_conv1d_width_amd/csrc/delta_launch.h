@@ -19,6 +19,16 @@ constexpr int kRecVec = 4 * 64 * 4 + 64;
 constexpr int kRecFwd = kRecT + kTriBlocks * 2 * kTriPart + kRecVec;
 constexpr int kRecRev = kRecT + kTriBlocks * 3 * kTriPart + kRecVec;
 
+// What the backward's walks leave of a chunk and 64 columns of a head, FP32: the state before (S) and the adjoint after the
+// chunk (D) as [4 blocks of 16 rows, NT / 16 blocks of 16 columns, 16 rows, 16 columns]; the new values (U) and what reaches
+// them (F) as [64 rows, 64 columns]; the largest of S by blocks of 16 rows, and of D.
+constexpr int tile_s(int) { return 0; }
+constexpr int tile_d(int NT) { return 64 * NT; }
+constexpr int tile_u(int NT) { return 2 * 64 * NT; }
+constexpr int tile_f(int NT) { return tile_u(NT) + 4096; }
+constexpr int tile_tops(int NT) { return tile_f(NT) + 4096; }
+constexpr int tile_floats(int NT) { return tile_tops(NT) + 32; }
+
 // s: x = v, B = k, C = q, init, fin and slots as in the scan; y
 struct DeltaArgs {
   ScanArgs s;
@@ -42,10 +52,7 @@ struct DeltaBwdArgs {
   int64_t dq_ld, dk_ld, dv_ld, ddt_ld, db_ld;
   float *dA, *dbias;         // [H]; dbias may be nullptr
   char* rec_rev;             // [chunk id, H] records of kRecRev bytes
-  // states before and adjoints after every chunk, [chunk id, H, ptiles, 4 blocks of 16 rows, NT / 16 blocks of 16 columns,
-  // 16 rows, 16 columns]
-  float *cs, *ct;
-  float *u, *f;              // new values and what reaches them: [chunk id, H, ptiles, 64 rows, 64 columns]
+  float* tiles;              // [chunk id, H, ptiles] records of tile_floats(NT)
   float* head_part;          // [chunk id, H, 2]: sums for dA, d(dt_bias)
 };
 

@@ -39,24 +39,49 @@ __device__ __forceinline__ int at_(int row, int col) {
   return at<W, PAD>(row, col);
 }
 
-// 16 x 16 FP32 blocks of a state (registers n, lanes p) to its place
+// A tile's record as a buffer (past the last one, with nothing in it)
+template <int NT>
+__device__ __forceinline__ Rows tile_record(const DeltaBwdArgs& b, int64_t tile, bool in) {
+  return Rows(b.tiles + tile * tile_floats(NT), tile_floats(NT), 1, in ? tile_floats(NT) : 0, 4);
+}
+// 16 x 16 blocks of a state (registers n, lanes p)
 template <int NB>
-__device__ __forceinline__ void store_blocks(float* to, const f32x4 (&S)[NB], float scale, int w, int lane) {
-  const Rows r(to + w * NB * 256, NB * 256, 1, NB * 256, 4);
-  const int at = ((lane & 15) * 16 + (lane >> 4) * 4) * 4;
+__device__ __forceinline__ void store_blocks(const Rows& to, int at, const f32x4 (&S)[NB], float scale, int w, int lane) {
+  const int o = (at + w * NB * 256 + (lane & 15) * 16 + (lane >> 4) * 4) * 4;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[nb] * scale), r.r, nb * 1024 + at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[nb] * scale), to.r, o + nb * 1024, 0, 0);
 }
 // 64 rows of 64 columns (registers rows, lanes columns), this wave's 16 columns
-__device__ __forceinline__ void store_rows(float* to, const f32x4 (&v)[4], int w, int lane) {
-  const Rows r(to, 4096, 1, 4096, 4);
+__device__ __forceinline__ void store_rows(const Rows& to, int at, const f32x4 (&v)[4], int w, int lane) {
+  const int o = (at + 4 * (lane >> 4) * 64 + 16 * w + (lane & 15)) * 4;
 #pragma unroll
   for (int ib = 0; ib < 4; ++ib)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[ib][e]), r.r,
-                                            ((16 * ib + 4 * (lane >> 4) + e) * 64 + 16 * w + (lane & 15)) * 4, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[ib][e]), to.r, o + (16 * ib + e) * 256, 0, 0);
+}
+
+// the largest of 8 and of 64 neighbouring lanes, in every one of them (v >= 0)
+__device__ __forceinline__ float max8_lanes(float v) {
+  v = __builtin_fmaxf(v, dpp0<0xb1, 0xf>(v));
+  v = __builtin_fmaxf(v, dpp0<0x4e, 0xf>(v));
+  return __builtin_fmaxf(v, dpp0<0x141, 0xf>(v));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = max8_lanes(v);
+  return max_across16(__builtin_fmaxf(v, dpp0<0x140, 0xf>(v)));
+}
+
+__device__ __forceinline__ float max16_lanes(float v) {
+  v = max8_lanes(v);
+  return __builtin_fmaxf(v, dpp0<0x140, 0xf>(v));
+}
+// four values to two fp16 tiles `other` elements apart
+__device__ __forceinline__ void store_half4(uint16_t* to, int other, f32x4 v) {
+  const u32x2 u = {pk_f16(v[0], v[1]), pk_f16(v[2], v[3])};
+  *reinterpret_cast<u32x2*>(to) = u;
+  *reinterpret_cast<u32x2*>(to + other) = u32x2{rest_f16(v[0], v[1], u.x), rest_f16(v[2], v[3], u.y)};
 }
 
 template <int NT>
@@ -126,10 +151,10 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
     store_bytes(sh.rec, tR);
     store_tile<16>(sh.v, tV);
     __syncthreads();
-    const int64_t at = (chunk_id(pc, c.c0, d.n_chunk_slots) * a.H + me.h) * a.ptiles + (me.p_first / kPTile);
+    const Rows to = tile_record<NT>(b, (chunk_id(pc, c.c0, d.n_chunk_slots) * a.H + me.h) * a.ptiles + me.p_first / kPTile, true);
     c = step_chunk(c, rows);  // rows == 0: that was the last one
     load(c, rows);
-    store_blocks((REV ? b.ct : b.cs) + at * (64 * NT), S, s_down, w, lane);
+    store_blocks(to, REV ? tile_d(NT) : tile_s(NT), S, s_down, w, lane);
     phase();
     f32x4 r[4];  // K S: rows in the registers, columns p in the lanes
 #pragma unroll
@@ -141,6 +166,11 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
       for (int ib = 0; ib < 4; ++ib) r[ib] = mma2(key_rows<NT>(sK, 16 * ib, 32 * ks, lane), s, r[ib]);
     }
     const float s_max = state_max(S);
+    {
+      const float top = max16_lanes(s_max * s_down);
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(top), to.r,
+                                            (int)(lane == 0 ? (tile_tops(NT) + (REV ? 4 : 0) + w) * 4 : kOutside), 0, 0);
+    }
     bf16x8 y[2];
     if constexpr (!REV) {
 #pragma unroll
@@ -187,7 +217,7 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
 #pragma unroll
       for (int ib = 0; ib < 4; ++ib) u[ib] *= u_down;
     }
-    store_rows((REV ? b.f : b.u) + at * 4096, u, w, lane);
+    store_rows(to, REV ? tile_f(NT) : tile_u(NT), u, w, lane);
     // what goes into the state and its scale
     f32x4 yo[4];
     float o_max = 0.f;
@@ -240,22 +270,25 @@ __global__ __launch_bounds__(kWalkThreads, NT <= 128 ? 2 : 1) void delta_walks_k
   else delta_walk<NT, VEC, false>(b, sh);
 }
 
-// the largest of 8 and of 64 neighbouring lanes, in every one of them (v >= 0)
-__device__ __forceinline__ float max8_lanes(float v) {
-  v = __builtin_fmaxf(v, dpp0<0xb1, 0xf>(v));
-  v = __builtin_fmaxf(v, dpp0<0x4e, 0xf>(v));
-  return __builtin_fmaxf(v, dpp0<0x141, 0xf>(v));
-}
-__device__ __forceinline__ float wave_max(float v) {
-  v = max8_lanes(v);
-  return max_across16(__builtin_fmaxf(v, dpp0<0x140, 0xf>(v)));
-}
-
 // 64 x 64 values as two fp16 tiles
 constexpr int kTile = 64 * kLd<64>;
 __device__ __forceinline__ Halves tile_halves(const uint16_t* tiles, int row0, int k0, int l) {
   return Halves{as_f16(op_split<64>(tiles, row0, k0, l)), as_f16(op_split<64>(tiles + kTile, row0, k0, l))};
 }
+template <int NT>
+__device__ __forceinline__ bf16x8 key_bf16(const uint16_t* tile, int row0, int k0, int l) {
+  return __builtin_bit_cast(bf16x8, key_rows<NT>(tile, row0, k0, l));
+}
+
+// four bf16 values of a row times four FP32 ones
+__device__ __forceinline__ float row_dot(const uint16_t* at, f32x4 v) {
+  const u32x2 u = *reinterpret_cast<const u32x2*>(at);
+  float s = bf_lo(u.x) * v[0];
+  s = __builtin_fmaf(bf_hi(u.x), v[1], s);
+  s = __builtin_fmaf(bf_lo(u.y), v[2], s);
+  return __builtin_fmaf(bf_hi(u.y), v[3], s);
+}
+
 // four values of a row as two parts
 __device__ __forceinline__ void store_parts(uint16_t* tiles, f32x4 v) {
   const u32x2 u = {pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
@@ -264,14 +297,429 @@ __device__ __forceinline__ void store_parts(uint16_t* tiles, f32x4 v) {
   *reinterpret_cast<u32x2*>(tiles + kTile) = u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
 }
 
-// A block takes a chunk and a key head and walks the 64-column tiles of its value heads.  A wave owns 16 NBW columns n of
-// dq and dk and one or two of the ten score blocks.
+// The sum of the chunk's dl terms and the gradients made of it, one lane a row (a wave): `in`, `out` and `dots` are the rows'
+// products with the state, with the adjoint, and the product of both; s_row and s_col the sums by blocks of 16 rows and
+// columns of P W - X Y below the diagonal (s_row's diagonal blocks: row r's of all i >= r > j); `diag` is F . U.
+struct RowSums {
+  float in, out, dots, diag, step, rate, grow_end;
+};
+__device__ __forceinline__ void finish_rows(const DeltaBwdArgs& b, const RowSums& x, const float (&s_row)[4][64],
+                                            const float (&s_col)[4][64], int64_t id, int h, int64_t r0, int rows, int lane) {
+  const ScanArgs& a = b.d.s;
+  const int m = lane >> 4;
+  float left = 0.f, below = 0.f, on = 0.f, corner[2] = {0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float r = k <= m ? s_row[k][lane] : 0.f, c = k >= m ? s_col[k][lane] : 0.f;
+    left += k < m ? r : 0.f;
+    below += k > m ? c : 0.f;
+    on += k == m ? r : 0.f;
+    if (k == 0) corner[0] = m >= 2 ? r : 0.f;
+    if (k <= 1) corner[1] += m == 3 ? r : 0.f;
+  }
+  const float corner1 = wave_sum(corner[0]), corner2 = wave_sum(corner[1]);
+  const float rows_on = row16_suffix(left);  // rows >= this one
+  const float columns = dpp0<0x111, 0xf>(row16_sum(below));
+  const float inside = rows_on + on + columns + (m == 1 ? corner1 : m == 2 ? corner2 : 0.f);
+  const float suffix = __shfl(wave_prefix(__shfl(x.in, 63 - lane)), 63 - lane);  // rows >= this one
+  const float before = dpp0<0x138, 0xf>(wave_prefix(x.out));                     // rows < this one
+  const float dl = x.grow_end * x.dots + suffix + inside + before;
+  const float dstep = a.A[h] * dl, ddt = a.softplus ? dstep * -expm1f(-x.step) : dstep;
+  const float db = x.diag * (1.f - x.rate / b.d.beta_max);
+  const int size = a.dt_f32 ? 4 : 2;
+  const Rows to(static_cast<char*>(b.ddt) + (r0 * b.ddt_ld + h) * size, b.ddt_ld, rows, 1, size);
+  const Rows tb(static_cast<char*>(b.db) + (r0 * b.db_ld + h) * size, b.db_ld, rows, 1, size);
+  const int o = (int)((uint32_t)lane * (uint32_t)b.ddt_ld * size), ob = (int)((uint32_t)lane * (uint32_t)b.db_ld * size);
+  if (a.dt_f32) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(ddt), to.r, o, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(db), tb.r, ob, 0, 0);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b16(to_bf16(ddt), to.r, o, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b16(to_bf16(db), tb.r, ob, 0, 0);
+  }
+  const float sum_A = wave_sum(lane < rows ? x.step * dl : 0.f), sum_b = wave_sum(lane < rows ? ddt : 0.f);
+  if (lane == 0) {
+    b.head_part[(id * a.H + h) * 2] = sum_A;
+    b.head_part[(id * a.H + h) * 2 + 1] = sum_b;
+  }
+}
+
+// A block takes a chunk and a key head and walks the 64-column tiles of its value heads: U, F, dY, S and D of a tile go
+// to shared memory as fp16 parts while the next tile's are loaded.  A wave owns 16 columns n of dq and dk and 32 of the 64
+// rows, and one of the ten score blocks: 16 waves (N > 64) in 128 registers, four a SIMD, to cover what each of them
+// waits for.  (8 waves of 256 registers that held their parts of S and D spilled, and took TIMES.)
+template <int NT, int WR, bool VEC>
+__global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArgs b) {
+  constexpr int T = 4 * NT * WR, NB = NT / 16, QR = 4 / WR;  // threads, blocks of columns n, of rows a wave
+  constexpr int KV = 1024 / T, KS = 64 * NT / 4 / T;  // pieces of four values of U (F, dY), of S (D) a thread
+  constexpr int SB = (10 + T / 64 - 1) / (T / 64);    // score blocks a wave
+  constexpr int kState = (int)key_tile(NT) / 2;    // elements of one part of S
+  // K and Q, bf16; then Y, U's and F's parts and S's and D's, or the four decayed scores' two parts
+  __shared__ __align__(16) uint16_t sKQ[2 * kState];
+  __shared__ __align__(16) uint16_t sAll[5 * kTile + 4 * kState > 8 * kTile ? 5 * kTile + 4 * kState : 8 * kTile];
+  __shared__ __align__(16) double sL[64];
+  __shared__ __align__(16) float s_rate[64], s_kn[64], s_qn[64], s_step[64], s_grow[64], s_left[64];
+  __shared__ __align__(16) float s_u[64], s_f[64], s_y[64];  // the tiles' rows are these times their values
+  __shared__ float s_row[4][64], s_col[4][64], s_diag[64], s_in[NB][64], s_out[NB][64], s_dot[T / 64];
+  uint16_t *sK = sKQ, *sQ = sKQ + kState;
+  uint16_t *sY = sAll, *sU = sAll + kTile, *sF = sU + 2 * kTile, *sS = sF + 2 * kTile, *sD = sS + 2 * kState;
+  uint16_t *sZk = sAll, *sZq = sAll + 2 * kTile, *sNj = sAll + 4 * kTile, *sNi = sAll + 6 * kTile;
+  const DeltaArgs& d = b.d;
+  const ScanArgs& a = d.s;
+  int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+  const int w = wave_id(), nb = w % NB, rh = w / NB;  // columns n from 16 nb on, rows from 16 QR rh on
+  const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
+  const int grp = blk % (uint32_t)a.G;
+  const int64_t id = blk / (uint32_t)a.G;
+  const int hg = a.H / a.G;
+  const Piece pc = find_chunk(a.q, id, d.n_chunk_slots);
+  if (!pc.ok) {
+    for (int e = threadIdx.x; e < hg * 2; e += T) b.head_part[(id * a.H + grp * hg) * 2 + e] = 0.f;
+    return;
+  }
+  const int rows = (int)(pc.r1 - pc.r0), tiles = hg * a.ptiles;
+  const int64_t gn = (int64_t)grp * a.N;
+  // the signs of the stored states and adjoints
+  const float sign_s = sign_at((pc.r0 >> 6) - (pc.s >> 6) + pc.seq, false);
+  const float sign_t = sign_at(((pc.e - 1) >> 6) - (pc.r0 >> 6) + pc.seq, true);
+  const float sign = sign_s * sign_t;
+  // four values a thread and piece, a tile ahead; the tile's scales beside them
+  f32x4 lu[KV], lf[KV], ls[KS], lt[KS];
+  u32x2 ly[KV];
+  float lm[2];
+  auto load_all = [&](int t) {
+    const int tid = fresh((int)threadIdx.x);
+    const int64_t at = (id * a.H + grp * hg) * a.ptiles + t;
+    const int h = grp * hg + (uint32_t)t / (uint32_t)a.ptiles, p_first = (uint32_t)t % (uint32_t)a.ptiles * kPTile;
+    const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
+    const bool in = t < tiles;
+    const Rows rt = tile_record<NT>(b, at, in);
+    const Rows ry(b.dy + pc.r0 * b.dy_ld + (int64_t)h * a.P + p_first, b.dy_ld, in ? rows : 0, pn, 2);
+    lm[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rt.r, (tile_tops(NT) + (tid & 3)) * 4, 0, 0));
+    lm[1] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rt.r, (tile_tops(NT) + (tid & 3)) * 4 + 16, 0, 0));
+#pragma unroll
+    for (int k = 0; k < KV; ++k) {
+      const int o = tid + T * k, row = o / 16, c = o % 16 * 4;
+      lu[k] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rt.r, o * 16 + tile_u(NT) * 4, 0, 0));
+      lf[k] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rt.r, o * 16 + tile_f(NT) * 4, 0, 0));
+      const uint32_t at_y = (row * (uint32_t)b.dy_ld + c) * 2;
+      if constexpr (VEC) {
+        ly[k] = __builtin_amdgcn_raw_buffer_load_b64(ry.r, (int)(c < pn ? at_y : kOutside), 0, 0);
+      } else {
+        ly[k] = u32x2{0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t v = __builtin_amdgcn_raw_buffer_load_b16(ry.r, (int)(c + e < pn ? at_y + 2 * e : kOutside), 0, 0);
+          ly[k][e >> 1] |= v << (16 * (e & 1));
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      ls[k] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rt.r, (tid + T * k) * 16, 0, 0));
+      lt[k] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rt.r, (tid + T * k) * 16 + tile_d(NT) * 4, 0, 0));
+    }
+  };
+  load_all(0);
+  {
+    TileRegs<NT, T> tk, tq;
+    load_tile<VEC>(tk, Rows(a.B + pc.r0 * a.B_ld + gn, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
+    load_tile<VEC>(tq, Rows(a.C + pc.r0 * a.C_ld + gn, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
+    auto place = [&](const TileRegs<NT, T>& t, uint16_t* tile, float* to) {
+#pragma unroll
+      for (int k = 0; k < NT * 8 / T; ++k) {
+        const int q = threadIdx.x + T * k, row = q / (NT / 8);
+        *reinterpret_cast<u32x4*>(tile + key_at<NT>(row, q % (NT / 8) * 8)) = t.v[k];
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float lo = bf_lo(t.v[k][e]), hi = bf_hi(t.v[k][e]);
+          s = __builtin_fmaf(lo, lo, s);
+          s = __builtin_fmaf(hi, hi, s);
+        }
+#pragma unroll
+        for (int m = NT / 16; m > 0; m >>= 1) s += __shfl_xor(s, m);
+        if (q % (NT / 8) == 0) to[row] = row < rows ? (d.qk_norm ? rsqrtf(s + d.norm_eps) : 1.f) + (s - s) : 0.f;
+      }
+    };
+    place(tk, sK, s_kn);
+    place(tq, sQ, s_qn);
+  }
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  f32x4 dQ[QR], dK[QR];  // registers n, lanes rows; summed over the heads
+#pragma unroll
+  for (int q = 0; q < QR; ++q) dQ[q] = dK[q] = zero;
+
+  for (int hh = 0; hh < hg; ++hh) {
+    const int h = grp * hg + hh;
+    if (w == T / 64 - 1) {  // lane = row
+      const Rate rate(a, h);
+      const float step = rate.step(raw_step(a, pc.r0, rows, lane, h), lane < rows);
+      const float bv = lane < rows ? load_num(d.b, (pc.r0 + lane) * d.b_ld + h, a.dt_f32) : 0.f;
+      const double L = wave_prefix(rate.exponent(step));
+      const double end = __shfl(L, 63);
+      sL[lane] = L;
+      s_step[lane] = step;
+      s_rate[lane] = lane < rows ? d.beta_max / (1.f + ex2(-kLog2e * bv)) : 0.f;
+      s_grow[lane] = ex2((float)L);
+      s_left[lane] = ex2((float)(end - L));
+    }
+    f32x4 W[SB], Y[SB];  // score blocks: columns j in the registers, rows i in the lanes
+#pragma unroll
+    for (int t = 0; t < SB; ++t) W[t] = Y[t] = zero;
+    float in[QR] = {}, out[QR] = {};  // the rows' products with the state and the adjoint
+    float dot = 0.f;
+    for (int pt = 0; pt < a.ptiles; ++pt) {
+      lane = fresh(lane);
+      g = lane >> 4, i = lane & 15;
+      const int p_first = pt * kPTile, pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
+      const float ms = __builtin_fmaxf(lm[0], dpp0<0xb1, 0xf>(lm[0])), mt = __builtin_fmaxf(lm[1], dpp0<0xb1, 0xf>(lm[1]));
+      const Pow2 ss = bring_to<10>(uniform(__builtin_fmaxf(ms, dpp0<0x4e, 0xf>(ms))));
+      const Pow2 ts = bring_to<10>(uniform(__builtin_fmaxf(mt, dpp0<0x4e, 0xf>(mt))));
+      __syncthreads();  // the last tile's or head's reads are done; this head's factors are there
+      const int tid = fresh((int)threadIdx.x);
+      const Rows dv(b.dv + pc.r0 * b.dv_ld + (int64_t)h * a.P + p_first, b.dv_ld, rows, pn, 2);
+#pragma unroll
+      for (int k = 0; k < KV; ++k) {
+        const int q = tid + T * k, row = q / 16, c = q % 16 * 4, o = at_<64>(row, c);
+        const f32x4 y = {bf_lo(ly[k].x), bf_hi(ly[k].x), bf_lo(ly[k].y), bf_hi(ly[k].y)};
+        const Pow2 us = bring_to<10>(max16_lanes(max4(0.f, lu[k])));
+        const Pow2 fs = bring_to<10>(max16_lanes(max4(0.f, lf[k])));
+        const Pow2 ys = bring_to<10>(max16_lanes(max4(0.f, y)));
+        store_half4(sU + o, kTile, lu[k] * us.up);
+        store_half4(sF + o, kTile, lf[k] * fs.up);
+        const f32x4 yv = y * ys.up;
+        *reinterpret_cast<u32x2*>(sY + o) = u32x2{pk_f16(yv[0], yv[1]), pk_f16(yv[2], yv[3])};
+        if (c == 0) {
+          s_u[row] = us.down;
+          s_f[row] = fs.down;
+          s_y[row] = ys.down;
+        }
+        const f32x4 v = lf[k] * (sign_t * s_rate[row]);
+        store4<VEC>(dv, (uint32_t)b.dv_ld, row, c, pn, u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])});
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {  // 16 x 16 blocks, [p block][n block][16 p][16 n]
+        const int q = tid + T * k, p = q / (4 * NT) * 16 + q / 4 % 16, n = q / 64 % NB * 16 + q % 4 * 4;
+        store_half4(sS + key_at<NT>(p, n), kState, ls[k] * ss.up);
+        store_half4(sD + key_at<NT>(p, n), kState, lt[k] * ts.up);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(ls[k][e], lt[k][e], dot);
+      }
+      here(dot);
+      load_all(hh * a.ptiles + pt + 1);
+      phase();
+      __syncthreads();
+      lane = fresh(lane);
+      g = lane >> 4, i = lane & 15;
+      {
+        Halves sp[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          sp[ks] = Halves{key_cols<NT>(sS, 32 * ks, 16 * nb, lane), key_cols<NT>(sS + kState, 32 * ks, 16 * nb, lane)};
+#pragma unroll
+        for (int q = 0; q < QR; ++q) {
+          const int row0 = 16 * (QR * rh + q), row = row0 + i, n = 16 * nb + 4 * g;
+          f32x4 q4 = zero, f4 = zero;
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            q4 = mma2(sp[ks], as_f16(op_split<64>(sY, row0, 32 * ks, lane)), q4);
+            f4 = mma3(sp[ks], tile_halves(sF, row0, 32 * ks, lane), f4);
+          }
+          const f32x4 vq = q4 * (sign_s * d.scale * s_grow[row] * s_y[row] * ss.down);
+          const f32x4 vf = f4 * (-sign * s_rate[row] * s_grow[row] * s_f[row] * ss.down);
+          in[q] += row_dot(sQ + key_at<NT>(row, n), vq) * s_qn[row] + row_dot(sK + key_at<NT>(row, n), vf) * s_kn[row];
+          dQ[q] += vq;
+          dK[q] += vf;
+          here(in[q]), here(dQ[q]), here(dK[q]);
+          phase();
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          sp[ks] = Halves{key_cols<NT>(sD, 32 * ks, 16 * nb, lane), key_cols<NT>(sD + kState, 32 * ks, 16 * nb, lane)};
+#pragma unroll
+        for (int q = 0; q < QR; ++q) {
+          const int row0 = 16 * (QR * rh + q), row = row0 + i, n = 16 * nb + 4 * g;
+          f32x4 u4 = zero;
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) u4 = mma3(sp[ks], tile_halves(sU, row0, 32 * ks, lane), u4);
+          const f32x4 vu = u4 * (sign * s_left[row] * s_u[row] * ts.down);
+          out[q] += row_dot(sK + key_at<NT>(row, n), vu) * s_kn[row];
+          dK[q] += vu;
+          here(out[q]), here(dK[q]);
+          phase();
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < SB; ++s) {
+        int ib, jb;
+        lower_block(w + T / 64 * s, ib, jb);
+        if (w + T / 64 * s >= 10) continue;
+        f32x4 w4 = zero, y4 = zero;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const Halves u = tile_halves(sU, 16 * jb, 32 * ks, lane);
+          w4 = mma2(u, as_f16(op_split<64>(sY, 16 * ib, 32 * ks, lane)), w4);
+          y4 = mma3(u, tile_halves(sF, 16 * ib, 32 * ks, lane), y4);
+        }
+        const f32x4 uj = *reinterpret_cast<const f32x4*>(s_u + 16 * jb + 4 * g);
+        W[s] += w4 * (uj * s_y[16 * ib + i]);
+        Y[s] += y4 * (uj * s_f[16 * ib + i]);
+        here(W[s]), here(Y[s]);
+      }
+      phase();
+    }
+    dot = wave_sum(dot);
+    if (lane == 0) s_dot[w] = dot;
+#pragma unroll
+    for (int q = 0; q < QR; ++q) {
+      const float x = sum_across16(in[q]), o = sum_across16(out[q]);
+      if (g == 0) {
+        s_in[nb][16 * (QR * rh + q) + i] = x;
+        s_out[nb][16 * (QR * rh + q) + i] = o;
+      }
+    }
+    __syncthreads();  // the tile is read
+    lane = fresh(lane);
+    g = lane >> 4, i = lane & 15;
+#pragma unroll
+    for (int s = 0; s < SB; ++s) {
+      int ib, jb;
+      lower_block(w + T / 64 * s, ib, jb);
+      if (w + T / 64 * s >= 10) continue;
+      const int row = 16 * ib + i, col = 16 * jb + 4 * g;
+      f32x4 kk = zero, qk = zero;
+#pragma unroll
+      for (int ks = 0; ks < NT / 32; ++ks) {
+        const bf16x8 kj = key_bf16<NT>(sK, 16 * jb, 32 * ks, lane);
+        kk = mma(kj, key_bf16<NT>(sK, 16 * ib, 32 * ks, lane), kk);
+        qk = mma(kj, key_bf16<NT>(sQ, 16 * ib, 32 * ks, lane), qk);
+      }
+      const double Li = sL[row];
+      const float ri = s_rate[row], kni = s_kn[row], qni = d.scale * s_qn[row];
+      const f32x4 knj = *reinterpret_cast<const f32x4*>(s_kn + col);
+      f32x4 zk, zq, nj, ni;
+      float sum = 0.f, diag = 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool under = col + r < row, here = col + r == row;
+        const float m = under || here ? ex2((float)(Li - sL[col + r])) : 0.f;
+        const float z = m * (sign_s * W[s][r]), y = sign * Y[s][r], n = under ? -(m * ri) * y : 0.f;
+        zk[r] = z * (d.scale * knj[r]);
+        zq[r] = z * qni;
+        nj[r] = n * knj[r];
+        ni[r] = n * kni;
+        // P W - X Y below the diagonal
+        const float x = under ? qk[r] * zq[r] * knj[r] + kk[r] * nj[r] * kni : 0.f;
+        diag = here ? y : diag;
+        const float from = row16_suffix(x);  // rows >= i of column j
+        if (i == 0) s_col[ib][col + r] = from;
+        sum += ib != jb ? x : (4 * g + r < i ? from : 0.f);
+      }
+      const int o = at_<64>(row, col);
+      store_parts(sZk + o, zk);
+      store_parts(sZq + o, zq);
+      store_parts(sNj + o, nj);
+      store_parts(sNi + o, ni);
+      sum = sum_across16(sum);
+      if (g == 0) s_row[jb][row] = sum;
+      if (ib == jb && (i >> 2) == g) s_diag[row] = diag;
+    }
+    // blocks (0, 1), (2, 3): products over 32 rows or columns read them
+    if (w < 2) {
+      const int o = at_<64>(32 * w + i, 32 * w + 16 + 4 * g);
+      store_parts(sZk + o, zero);
+      store_parts(sZq + o, zero);
+      store_parts(sNj + o, zero);
+      store_parts(sNi + o, zero);
+    }
+    __syncthreads();
+    if (w == T / 64 - 1) {  // lane = row
+      RowSums x{0.f, 0.f, 0.f, s_diag[lane], s_step[lane], s_rate[lane], sign * s_grow[63]};
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        x.in += s_in[k][lane];
+        x.out += s_out[k][lane];
+      }
+#pragma unroll
+      for (int k = 0; k < T / 64; ++k) x.dots += s_dot[k];
+      finish_rows(b, x, s_row, s_col, id, h, pc.r0, rows, lane);
+    }
+    phase();
+    lane = fresh(lane);
+    g = lane >> 4, i = lane & 15;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const bf16x8 k = __builtin_bit_cast(bf16x8, key_cols<NT>(sK, 32 * ks, 16 * nb, lane));
+      const bf16x8 qq = __builtin_bit_cast(bf16x8, key_cols<NT>(sQ, 32 * ks, 16 * nb, lane));
+#pragma unroll
+      for (int q = 0; q < QR; ++q) {
+        const int row0 = 16 * (QR * rh + q);
+        if (ks <= (QR * rh + q) / 2) {  // contracted columns j of these rows
+#pragma unroll
+          for (int p = 1; p >= 0; --p) {
+            dQ[q] = mma(k, op_split<64>(sZk + p * kTile, row0, 32 * ks, lane), dQ[q]);
+            dK[q] = mma(k, op_split<64>(sNj + p * kTile, row0, 32 * ks, lane), dK[q]);
+          }
+        }
+        if (ks >= (QR * rh + q) / 2) {  // contracted rows i of these columns
+#pragma unroll
+          for (int p = 1; p >= 0; --p) {
+            dK[q] = mma(qq, op_cols<64>(sZq + p * kTile, 32 * ks, row0, lane), dK[q]);
+            dK[q] = mma(k, op_cols<64>(sNi + p * kTile, 32 * ks, row0, lane), dK[q]);
+          }
+        }
+      }
+      phase();
+    }
+  }
+  // through the norms: x = f y, f = (|y|^2 + eps)^(-1/2):  dy = f dx - f^3 y (y . dx)
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < QR; ++q) {
+    const int row = 16 * (QR * rh + q) + i, n = 16 * nb + 4 * g;
+    const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + key_at<NT>(row, n));
+    const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + key_at<NT>(row, n));
+    const f32x4 x = dQ[q], y = dK[q];
+    const float dq = sum_across16(x[0] * bf_lo(qv.x) + x[1] * bf_hi(qv.x) + x[2] * bf_lo(qv.y) + x[3] * bf_hi(qv.y));
+    const float dk = sum_across16(y[0] * bf_lo(kv.x) + y[1] * bf_hi(kv.x) + y[2] * bf_lo(kv.y) + y[3] * bf_hi(kv.y));
+    if (g == 0) {
+      s_in[nb][row] = dq;
+      s_out[nb][row] = dk;
+    }
+  }
+  __syncthreads();
+  const Rows oq(b.dq + pc.r0 * b.dq_ld + gn, b.dq_ld, rows, a.N, 2), ok(b.dk + pc.r0 * b.dk_ld + gn, b.dk_ld, rows, a.N, 2);
+#pragma unroll
+  for (int q = 0; q < QR; ++q) {
+    const int row = 16 * (QR * rh + q) + i, n = 16 * nb + 4 * g;
+    const float fq = s_qn[row], fk = s_kn[row];
+    float dq = 0.f, dk = 0.f;
+    if (d.qk_norm) {
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        dq += s_in[k][row];
+        dk += s_out[k][row];
+      }
+      dq *= fq * fq * fq;
+      dk *= fk * fk * fk;
+    }
+    const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + key_at<NT>(row, n));
+    const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + key_at<NT>(row, n));
+    const f32x4 x = dQ[q] * fq - f32x4{bf_lo(qv.x), bf_hi(qv.x), bf_lo(qv.y), bf_hi(qv.y)} * dq;
+    const f32x4 y = dK[q] * fk - f32x4{bf_lo(kv.x), bf_hi(kv.x), bf_lo(kv.y), bf_hi(kv.y)} * dk;
+    store4<VEC>(oq, (uint32_t)b.dq_ld, row, n, a.N, u32x2{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])});
+    store4<VEC>(ok, (uint32_t)b.dk_ld, row, n, a.N, u32x2{pk_bf16(y[0], y[1]), pk_bf16(y[2], y[3])});
+  }
+}
+
+// The same for states of more than 128 columns, whose tiles shared memory does not hold: a wave keeps its columns' part of S and
+// D in registers.  It owns 16 NBW columns n of dq and dk and one or two of the ten score blocks.
 template <int NT, int WAVES, bool VEC>
-__global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(DeltaBwdArgs b) {
+__global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_wide_kernel(DeltaBwdArgs b) {
   constexpr int T = 64 * WAVES, NBW = NT / 16 / WAVES, SB = (10 + WAVES - 1) / WAVES, KT = 512 / T;
-  constexpr int PAD = NT > 128 ? 8 : 16;  // 256 columns leave no room for more
-  __shared__ __align__(16) uint16_t sK[64 * kLd<NT, PAD>];
-  __shared__ __align__(16) uint16_t sQ[64 * kLd<NT, PAD>];
+  __shared__ __align__(16) uint16_t sK[key_tile(NT) / 2];  // bf16, in the places of the walks' tiles
+  __shared__ __align__(16) uint16_t sQ[key_tile(NT) / 2];
   __shared__ __align__(16) uint16_t sY[kTile];
   __shared__ __align__(16) uint16_t sUF[8 * kTile];  // U's and F's parts, then the four decayed scores' two
   __shared__ __align__(16) double sL[64];
@@ -303,8 +751,12 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
     TileRegs<NT, T> tk, tq;
     load_tile<VEC>(tk, Rows(a.B + pc.r0 * a.B_ld + gn, a.B_ld, rows, a.N, 2), (uint32_t)a.B_ld, a.N);
     load_tile<VEC>(tq, Rows(a.C + pc.r0 * a.C_ld + gn, a.C_ld, rows, a.N, 2), (uint32_t)a.C_ld, a.N);
-    store_tile<PAD>(sK, tk);
-    store_tile<PAD>(sQ, tq);
+#pragma unroll
+    for (int k = 0; k < NT * 8 / T; ++k) {
+      const int q = threadIdx.x + T * k, o = key_at<NT>(q / (NT / 8), q % (NT / 8) * 8);
+      *reinterpret_cast<u32x4*>(sK + o) = tk.v[k];
+      *reinterpret_cast<u32x4*>(sQ + o) = tq.v[k];
+    }
     auto norms = [&](const TileRegs<NT, T>& t, float* to) {
 #pragma unroll
       for (int k = 0; k < NT * 8 / T; ++k) {
@@ -325,21 +777,6 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
     norms(tq, s_qn);
   }
   __syncthreads();
-  f32x4 kk[SB], qk[SB];  // score blocks (ib, jb): columns j in the registers, rows i in the lanes
-#pragma unroll
-  for (int t = 0; t < SB; ++t) {
-    int ib, jb;
-    lower_block(w + WAVES * t, ib, jb);
-    kk[t] = qk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (w + WAVES * t < 10) {
-#pragma unroll
-      for (int ks = 0; ks < NT / 32; ++ks) {
-        const bf16x8 kj = op_straight<NT, PAD>(sK, 16 * jb, 32 * ks, lane);
-        kk[t] = mma(kj, op_straight<NT, PAD>(sK, 16 * ib, 32 * ks, lane), kk[t]);
-        qk[t] = mma(kj, op_straight<NT, PAD>(sQ, 16 * ib, 32 * ks, lane), qk[t]);
-      }
-    }
-  }
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   f32x4 dQ[NBW][4], dK[NBW][4];  // registers n, lanes rows; summed over the heads
 #pragma unroll
@@ -355,24 +792,42 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
     const int h = grp * hg + (uint32_t)t / (uint32_t)a.ptiles, pt = (uint32_t)t % (uint32_t)a.ptiles, p_first = pt * kPTile;
     const int pn = a.P - p_first < kPTile ? a.P - p_first : kPTile, n = t < tiles ? 4096 : 0;
     const int64_t at = (id * a.H + h) * a.ptiles + pt;
-    const Rows ru(b.u + at * 4096, 4096, 1, n, 4), rf(b.f + at * 4096, 4096, 1, n, 4);
+    const Rows rt = tile_record<NT>(b, at, n > 0);
 #pragma unroll
     for (int k = 0; k < KT; ++k)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int o = (threadIdx.x + T * k) * 32 + 16 * e;
-        lu[k][e] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ru.r, o, 0, 0));
-        lf[k][e] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rf.r, o, 0, 0));
+        lu[k][e] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rt.r, o + tile_u(NT) * 4, 0, 0));
+        lf[k][e] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rt.r, o + tile_f(NT) * 4, 0, 0));
       }
     load_tile<VEC>(ly, Rows(b.dy + pc.r0 * b.dy_ld + (int64_t)h * a.P + p_first, b.dy_ld, n ? rows : 0, pn, 2),
                    (uint32_t)b.dy_ld, pn);
   };
+  // the state and the adjoint: this wave's columns n in the lanes, contracted rows p in the registers
+  f32x4 ls[NBW][2][2], lt[NBW][2][2];
+  auto load_states = [&](int t) {
+    const int64_t at = (id * a.H + grp * hg) * a.ptiles + t;
+    const Rows rt = tile_record<NT>(b, at, t < tiles);
+#pragma unroll
+    for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int o = (((2 * ks + q) * (NT / 16) + w * NBW + nb) * 256 + (4 * g + e) * 16 + i) * 4;
+            ls[nb][ks][q][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rt.r, o, 0, 0));
+            lt[nb][ks][q][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rt.r, o + tile_d(NT) * 4, 0, 0));
+          }
+  };
   load_values(0);
+  load_states(0);
   for (int hh = 0; hh < hg; ++hh) {
     lane = fresh(lane);
     g = lane >> 4, i = lane & 15;
     const int h = grp * hg + hh;
-    float A_h = 0.f;
     if (w == 0) {  // lane = row
       const Rate rate(a, h);
       const float step = rate.step(raw_step(a, pc.r0, rows, lane, h), lane < rows);
@@ -384,36 +839,17 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
       s_rate[lane] = lane < rows ? d.beta_max / (1.f + ex2(-kLog2e * bv)) : 0.f;
       s_grow[lane] = ex2((float)L);
       s_left[lane] = ex2((float)(end - L));
-      A_h = a.A[h];
     }
-    f32x4 aQ[NBW][4], aF[NBW][4], aU[NBW][4], W[SB], Y[SB];
-#pragma unroll
-    for (int nb = 0; nb < NBW; ++nb)
-#pragma unroll
-      for (int ib = 0; ib < 4; ++ib) aQ[nb][ib] = aF[nb][ib] = aU[nb][ib] = zero;
+    f32x4 W[SB], Y[SB];
+    float in[4] = {0.f, 0.f, 0.f, 0.f}, out[4] = {0.f, 0.f, 0.f, 0.f};  // the rows' products with the state and the adjoint
 #pragma unroll
     for (int t = 0; t < SB; ++t) W[t] = Y[t] = zero;
     float dot = 0.f;
     for (int pt = 0; pt < a.ptiles; ++pt) {
+      lane = fresh(lane);
+      g = lane >> 4, i = lane & 15;
       const int p_first = pt * kPTile, pn = a.P - p_first < kPTile ? a.P - p_first : kPTile;
-      const int64_t col = (int64_t)h * a.P + p_first, at = (id * a.H + h) * a.ptiles + pt;
-      // the state and the adjoint: this wave's columns n in the lanes, contracted rows p in the registers
-      f32x4 s[NBW][2][2], t[NBW][2][2];
-      {
-        const Rows rs(b.cs + at * (64 * NT), 64 * NT, 1, 64 * NT, 4), rt(b.ct + at * (64 * NT), 64 * NT, 1, 64 * NT, 4);
-#pragma unroll
-        for (int nb = 0; nb < NBW; ++nb)
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int o = (((2 * ks + q) * (NT / 16) + w * NBW + nb) * 256 + (4 * g + e) * 16 + i) * 4;
-                s[nb][ks][q][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs.r, o, 0, 0));
-                t[nb][ks][q][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rt.r, o, 0, 0));
-              }
-      }
+      const int64_t col = (int64_t)h * a.P + p_first;
       __syncthreads();  // the last tile's or head's reads are done; this head's factors are there
       {
         const Rows dv(b.dv + pc.r0 * b.dv_ld + col, b.dv_ld, rows, pn, 2);
@@ -442,8 +878,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
           store4<VEC>(dv, (uint32_t)b.dv_ld, row, c + 4, pn, u32x2{pk_bf16(v1[0], v1[1]), pk_bf16(v1[2], v1[3])});
         }
       }
-      __syncthreads();
-      phase();
+      Halves sp[NBW][2], tp[NBW][2];
+      float s_dn[NBW], t_dn[NBW];
 #pragma unroll
       for (int nb = 0; nb < NBW; ++nb) {
         float ms = 0.f, mt = 0.f;
@@ -451,37 +887,69 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            ms = max4(ms, s[nb][ks][q]);
-            mt = max4(mt, t[nb][ks][q]);
+            ms = max4(ms, ls[nb][ks][q]);
+            mt = max4(mt, lt[nb][ks][q]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(s[nb][ks][q][e], t[nb][ks][q][e], dot);
+            for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(ls[nb][ks][q][e], lt[nb][ks][q][e], dot);
           }
+        here(dot);
         const Pow2 ss = bring_to<10>(wave_max(ms)), ts = bring_to<10>(wave_max(mt));
-        f32x4 q4[4], f4[4], u4[4];
-#pragma unroll
-        for (int ib = 0; ib < 4; ++ib) q4[ib] = f4[ib] = u4[ib] = zero;
+        s_dn[nb] = ss.down, t_dn[nb] = ts.down;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          const Halves sp = halves(s[nb][ks][0] * ss.up, s[nb][ks][1] * ss.up);
-          const Halves tp = halves(t[nb][ks][0] * ts.up, t[nb][ks][1] * ts.up);
+          sp[nb][ks] = halves(ls[nb][ks][0] * ss.up, ls[nb][ks][1] * ss.up);
+          tp[nb][ks] = halves(lt[nb][ks][0] * ts.up, lt[nb][ks][1] * ts.up);
+        }
+      }
+      phase();
+      load_values(hh * a.ptiles + pt + 1);
+      load_states(hh * a.ptiles + pt + 1);
+      phase();
+      __syncthreads();
+      lane = fresh(lane);
+      g = lane >> 4, i = lane & 15;
 #pragma unroll
-          for (int ib = 0; ib < 4; ++ib) {
-            q4[ib] = mma2(sp, as_f16(op_split<64>(sY, 16 * ib, 32 * ks, lane)), q4[ib]);
-            f4[ib] = mma3(sp, tile_halves(sF, 16 * ib, 32 * ks, lane), f4[ib]);
-            u4[ib] = mma3(tp, tile_halves(sU, 16 * ib, 32 * ks, lane), u4[ib]);
+      for (int ib = 0; ib < 4; ++ib) {
+        const int row = 16 * ib + i;
+        f32x4 q4[NBW], f4[NBW], u4[NBW];
+#pragma unroll
+        for (int nb = 0; nb < NBW; ++nb) q4[nb] = f4[nb] = u4[nb] = zero;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const f16x8 y = as_f16(op_split<64>(sY, 16 * ib, 32 * ks, lane));
+          const Halves f = tile_halves(sF, 16 * ib, 32 * ks, lane), u = tile_halves(sU, 16 * ib, 32 * ks, lane);
+#pragma unroll
+          for (int nb = 0; nb < NBW; ++nb) {
+            q4[nb] = mma2(sp[nb][ks], y, q4[nb]);
+            f4[nb] = mma3(sp[nb][ks], f, f4[nb]);
+            u4[nb] = mma3(tp[nb][ks], u, u4[nb]);
           }
         }
+        const float gq = sign_s * d.scale * s_grow[row] * s_y[row], gf = -sign * s_rate[row] * s_grow[row] * s_f[row];
+        const float gu = sign * s_left[row] * s_u[row];
+        float in_q = 0.f, in_k = 0.f, ou = 0.f;
 #pragma unroll
-        for (int ib = 0; ib < 4; ++ib) {
-          const int row = 16 * ib + i;
-          aQ[nb][ib] += q4[ib] * (ss.down * s_y[row]);
-          aF[nb][ib] += f4[ib] * (ss.down * s_f[row]);
-          aU[nb][ib] += u4[ib] * (ts.down * s_u[row]);
+        for (int nb = 0; nb < NBW; ++nb) {
+          const int n = 16 * (w * NBW + nb) + 4 * g;
+          const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + key_at<NT>(row, n));
+          const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + key_at<NT>(row, n));
+          const f32x4 qr = {bf_lo(qv.x), bf_hi(qv.x), bf_lo(qv.y), bf_hi(qv.y)};
+          const f32x4 kr = {bf_lo(kv.x), bf_hi(kv.x), bf_lo(kv.y), bf_hi(kv.y)};
+          const f32x4 vq = q4[nb] * (gq * s_dn[nb]), vf = f4[nb] * (gf * s_dn[nb]), vu = u4[nb] * (gu * t_dn[nb]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            in_q = __builtin_fmaf(qr[e], vq[e], in_q);
+            in_k = __builtin_fmaf(kr[e], vf[e], in_k);
+            ou = __builtin_fmaf(kr[e], vu[e], ou);
+          }
+          dQ[nb][ib] += vq;
+          dK[nb][ib] += vf + vu;
+          here(dQ[nb][ib]), here(dK[nb][ib]);
         }
+        in[ib] += in_q * s_qn[row] + in_k * s_kn[row];
+        out[ib] += ou * s_kn[row];
         phase();
       }
-      load_values(hh * a.ptiles + pt + 1);
-      phase();
 #pragma unroll
       for (int t = 0; t < SB; ++t) {
         int ib, jb;
@@ -502,42 +970,31 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
     }
     dot = wave_sum(dot);
     if (lane == 0) s_dot[w] = dot;
-    // the rows' sums with the state and the adjoint, and dQ's and dK's terms of them
 #pragma unroll
     for (int ib = 0; ib < 4; ++ib) {
-      const int row = 16 * ib + i;
-      const float gq = sign_s * d.scale * s_grow[row], gf = -sign * s_rate[row] * s_grow[row], gu = sign * s_left[row];
-      float in_q = 0.f, in_k = 0.f, out = 0.f;
-#pragma unroll
-      for (int nb = 0; nb < NBW; ++nb) {
-        const int n = 16 * (w * NBW + nb) + 4 * g;
-        const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + at_<NT, PAD>(row, n));
-        const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + at_<NT, PAD>(row, n));
-        const f32x4 q4 = {bf_lo(qv.x), bf_hi(qv.x), bf_lo(qv.y), bf_hi(qv.y)};
-        const f32x4 k4 = {bf_lo(kv.x), bf_hi(kv.x), bf_lo(kv.y), bf_hi(kv.y)};
-        const f32x4 vq = aQ[nb][ib] * gq, vf = aF[nb][ib] * gf, vu = aU[nb][ib] * gu;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          in_q = __builtin_fmaf(q4[e], vq[e], in_q);
-          in_k = __builtin_fmaf(k4[e], vf[e], in_k);
-          out = __builtin_fmaf(k4[e], vu[e], out);
-        }
-        dQ[nb][ib] += vq;
-        dK[nb][ib] += vf + vu;
-      }
-      const float in = sum_across16(in_q * s_qn[row] + in_k * s_kn[row]), o = sum_across16(out * s_kn[row]);
+      const float x = sum_across16(in[ib]), o = sum_across16(out[ib]);
       if (g == 0) {
-        s_in[w][row] = in;
-        s_out[w][row] = o;
+        s_in[w][16 * ib + i] = x;
+        s_out[w][16 * ib + i] = o;
       }
     }
     __syncthreads();  // U's and F's parts are read
+    lane = fresh(lane);
+    g = lane >> 4, i = lane & 15;
 #pragma unroll
     for (int t = 0; t < SB; ++t) {
       int ib, jb;
       lower_block(w + WAVES * t, ib, jb);
       if (w + WAVES * t < 10) {
         const int row = 16 * ib + i, col = 16 * jb + 4 * g;
+        // the products again for every head: kept, their registers spill
+        f32x4 kk = zero, qk = zero;
+#pragma unroll
+        for (int ks = 0; ks < NT / 32; ++ks) {
+          const bf16x8 kj = key_bf16<NT>(sK, 16 * jb, 32 * ks, lane);
+          kk = mma(kj, key_bf16<NT>(sK, 16 * ib, 32 * ks, lane), kk);
+          qk = mma(kj, key_bf16<NT>(sQ, 16 * ib, 32 * ks, lane), qk);
+        }
         const double Li = sL[row];
         const float ri = s_rate[row], kni = s_kn[row], qni = d.scale * s_qn[row];
         const f32x4 knj = *reinterpret_cast<const f32x4*>(s_kn + col);
@@ -553,7 +1010,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
           nj[r] = n * knj[r];
           ni[r] = n * kni;
           // P W - X Y below the diagonal
-          const float x = under ? qk[t][r] * zq[r] * knj[r] + kk[t][r] * nj[r] * kni : 0.f;
+          const float x = under ? qk[r] * zq[r] * knj[r] + kk[r] * nj[r] * kni : 0.f;
           diag = here ? y : diag;
           const float from = row16_suffix(x);  // rows >= i of column j
           if (i == 0) s_col[ib][col + r] = from;
@@ -567,6 +1024,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
         sum = sum_across16(sum);
         if (g == 0) s_row[jb][row] = sum;
         if (ib == jb && (i >> 2) == g) s_diag[row] = diag;
+        phase();
       }
     }
     // blocks (0, 1), (2, 3): products over 32 rows or columns read them
@@ -579,58 +1037,25 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
     }
     __syncthreads();
     if (w == 0) {  // lane = row
-      float in = 0.f, out = 0.f, dots = 0.f;
+      RowSums x{0.f, 0.f, 0.f, s_diag[lane], s_step[lane], s_rate[lane], sign * s_grow[63]};
 #pragma unroll
       for (int k = 0; k < WAVES; ++k) {
-        in += s_in[k][lane];
-        out += s_out[k][lane];
-        dots += s_dot[k];
+        x.in += s_in[k][lane];
+        x.out += s_out[k][lane];
+        x.dots += s_dot[k];
       }
-      const int m = lane >> 4;
-      float left = 0.f, below = 0.f, on = 0.f, corner[2] = {0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float r = k <= m ? s_row[k][lane] : 0.f, cl = k >= m ? s_col[k][lane] : 0.f;
-        left += k < m ? r : 0.f;
-        below += k > m ? cl : 0.f;
-        on += k == m ? r : 0.f;
-        if (k == 0) corner[0] = m >= 2 ? r : 0.f;
-        if (k <= 1) corner[1] += m == 3 ? r : 0.f;
-      }
-      const float corner1 = wave_sum(corner[0]), corner2 = wave_sum(corner[1]);
-      const float rows_on = row16_suffix(left);  // rows >= this one
-      const float columns = dpp0<0x111, 0xf>(row16_sum(below));
-      const float inside = rows_on + on + columns + (m == 1 ? corner1 : m == 2 ? corner2 : 0.f);
-      const float suffix = __shfl(wave_prefix(__shfl(in, 63 - lane)), 63 - lane);  // rows >= this one
-      const float before = dpp0<0x138, 0xf>(wave_prefix(out));                     // rows < this one
-      const float dl = sign * s_grow[63] * dots + suffix + inside + before;
-      const float step = s_step[lane], rate = s_rate[lane];
-      const float dstep = A_h * dl, ddt = a.softplus ? dstep * -expm1f(-step) : dstep;
-      const float db = s_diag[lane] * (1.f - rate / d.beta_max);
-      const int size = a.dt_f32 ? 4 : 2;
-      const Rows to(static_cast<char*>(b.ddt) + (pc.r0 * b.ddt_ld + h) * size, b.ddt_ld, rows, 1, size);
-      const Rows tb(static_cast<char*>(b.db) + (pc.r0 * b.db_ld + h) * size, b.db_ld, rows, 1, size);
-      const int o = (int)((uint32_t)lane * (uint32_t)b.ddt_ld * size), ob = (int)((uint32_t)lane * (uint32_t)b.db_ld * size);
-      if (a.dt_f32) {
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(ddt), to.r, o, 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(db), tb.r, ob, 0, 0);
-      } else {
-        __builtin_amdgcn_raw_buffer_store_b16(to_bf16(ddt), to.r, o, 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b16(to_bf16(db), tb.r, ob, 0, 0);
-      }
-      const float sum_A = wave_sum(lane < rows ? step * dl : 0.f), sum_b = wave_sum(lane < rows ? ddt : 0.f);
-      if (lane == 0) {
-        b.head_part[(id * a.H + h) * 2] = sum_A;
-        b.head_part[(id * a.H + h) * 2 + 1] = sum_b;
-      }
+      finish_rows(b, x, s_row, s_col, id, h, pc.r0, rows, lane);
     }
     phase();
+    lane = fresh(lane);
+    g = lane >> 4, i = lane & 15;
 #pragma unroll
     for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const int n = 16 * (w * NBW + nb);
-        const bf16x8 k = op_cols<NT, PAD>(sK, 32 * ks, n, lane), q = op_cols<NT, PAD>(sQ, 32 * ks, n, lane);
+        const bf16x8 k = __builtin_bit_cast(bf16x8, key_cols<NT>(sK, 32 * ks, n, lane));
+        const bf16x8 q = __builtin_bit_cast(bf16x8, key_cols<NT>(sQ, 32 * ks, n, lane));
 #pragma unroll
         for (int ib = 0; ib < 4; ++ib) {
 #pragma unroll
@@ -658,8 +1083,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
 #pragma unroll
       for (int nb = 0; nb < NBW; ++nb) {
         const int n = 16 * (w * NBW + nb) + 4 * g;
-        const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + at_<NT, PAD>(row, n));
-        const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + at_<NT, PAD>(row, n));
+        const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + key_at<NT>(row, n));
+        const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + key_at<NT>(row, n));
         const f32x4 x = dQ[nb][ib], y = dK[nb][ib];
         dq += x[0] * bf_lo(qv.x) + x[1] * bf_hi(qv.x) + x[2] * bf_lo(qv.y) + x[3] * bf_hi(qv.y);
         dk += y[0] * bf_lo(kv.x) + y[1] * bf_hi(kv.x) + y[2] * bf_lo(kv.y) + y[3] * bf_hi(kv.y);
@@ -690,8 +1115,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void delta_scan_bwd_kernel(D
 #pragma unroll
     for (int nb = 0; nb < NBW; ++nb) {
       const int n = 16 * (w * NBW + nb) + 4 * g;
-      const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + at_<NT, PAD>(row, n));
-      const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + at_<NT, PAD>(row, n));
+      const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + key_at<NT>(row, n));
+      const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + key_at<NT>(row, n));
       const f32x4 x = dQ[nb][ib] * fq - f32x4{bf_lo(qv.x), bf_hi(qv.x), bf_lo(qv.y), bf_hi(qv.y)} * dq;
       const f32x4 y = dK[nb][ib] * fk - f32x4{bf_lo(kv.x), bf_hi(kv.x), bf_lo(kv.y), bf_hi(kv.y)} * dk;
       store4<VEC>(oq, (uint32_t)b.dq_ld, row, n, a.N, u32x2{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])});
@@ -723,13 +1148,16 @@ __global__ __launch_bounds__(256) void delta_head_reduce_kernel(DeltaBwdArgs b, 
   }
 }
 
-template <int NT, int WAVES, bool VEC>
+template <int NT, bool VEC>
 static hipError_t launch(const DeltaBwdArgs& b, hipStream_t s) {
   const ScanArgs& a = b.d.s;
   const int64_t ids = b.d.n_chunk_slots + a.q.nseq;
+  const dim3 blocks((uint32_t)(ids * a.G));
   delta_walks_kernel<NT, VEC><<<dim3((uint32_t)unit_blocks(a.q.nseq, a.H, a.G, a.ptiles, 1), 2), kWalkThreads, 0, s>>>(b);
-  if (a.q.rows > 0)
-    delta_scan_bwd_kernel<NT, WAVES, VEC><<<dim3((uint32_t)(ids * a.G)), 64 * WAVES, 0, s>>>(b);
+  if (a.q.rows > 0) {
+    if constexpr (NT > 128) delta_scan_bwd_wide_kernel<NT, 8, VEC><<<blocks, 512, 0, s>>>(b);
+    else delta_scan_bwd_kernel<NT, 2, VEC><<<blocks, 8 * NT, 0, s>>>(b);
+  }
   delta_head_reduce_kernel<<<dim3((uint32_t)a.H), 256, 0, s>>>(b, a.q.rows > 0 ? ids : 0);
   return hipGetLastError();
 }
@@ -744,9 +1172,9 @@ hipError_t launch_delta_bwd(const DeltaBwdArgs& b, bool vec, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   switch (state_tile(b.d.s.N)) {
-    case 64: return vec ? launch<64, 4, true>(b, s) : launch<64, 4, false>(b, s);
-    case 128: return vec ? launch<128, 8, true>(b, s) : launch<128, 8, false>(b, s);
-    default: return vec ? launch<256, 8, true>(b, s) : launch<256, 8, false>(b, s);
+    case 64: return vec ? launch<64, true>(b, s) : launch<64, false>(b, s);
+    case 128: return vec ? launch<128, true>(b, s) : launch<128, false>(b, s);
+    default: return vec ? launch<256, true>(b, s) : launch<256, false>(b, s);
   }
 }
 
