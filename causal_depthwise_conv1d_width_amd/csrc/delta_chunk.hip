@@ -26,15 +26,16 @@ __device__ __forceinline__ uint32_t max_bits(u32x4 v) {
 }
 
 template <int NT, bool VEC, bool BWD>
-__global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_chunk_kernel(DeltaArgs d, char* rec_rev) {
+__global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs d, char* rec_rev) {
   constexpr int LD = 68;  // rows of 64 FP32 values, 16 bytes further apart
-  __shared__ __align__(16) uint16_t sK[key_tile(NT) / 2];
-  __shared__ __align__(16) uint16_t sQ[key_tile(NT) / 2];
-  __shared__ __align__(16) float sX[64 * LD];
-  __shared__ __align__(16) float sT[64 * LD];
-  __shared__ __align__(16) double sL[64];
-  __shared__ __align__(16) float s_rate[64], s_kn[64], s_qn[64], s_max[4];
-  __shared__ int s_bad;
+  // the tiles of k and q until their products are made, then X and T
+  constexpr int kTiles = 2 * (int)key_tile(NT), kSystems = 2 * 64 * LD * 4;
+  __shared__ __align__(16) char sAll[kTiles > kSystems ? kTiles : kSystems];
+  uint16_t *sK = reinterpret_cast<uint16_t*>(sAll), *sQ = sK + key_tile(NT) / 2;
+  float *sX = reinterpret_cast<float*>(sAll), *sT = sX + 64 * LD;
+  __shared__ __align__(16) double sL_[4][64];  // of four heads
+  __shared__ __align__(16) float s_rate_[4][64], s_kn[64], s_qn[64], s_max[4];
+  __shared__ int s_bad_[4];
   const ScanArgs& a = d.s;
   int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
   const int w = wave_id();
@@ -55,11 +56,7 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_chunk_kernel(Del
       for (int k = 0; k < NT / 32; ++k) {
         const int q = threadIdx.x + 256 * k, row = q / (NT / 8), c = q % (NT / 8) * 8;
         uint32_t m = max_bits(t.v[k]);
-#pragma unroll
-        for (int x = NT / 16; x > 0; x >>= 1) {
-          const uint32_t o = __shfl_xor(m, x);
-          m = m > o ? m : o;
-        }
+        m = row_lanes<NT / 8>(m, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
         uint32_t e = m >> 7;  // the largest one's exponent
         e = e < 1 ? 1 : (e > 253 ? 253 : e);
         const float up = __uint_as_float((254 - e) << 23), down = __uint_as_float(e << 23);
@@ -72,8 +69,9 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_chunk_kernel(Del
           s = __builtin_fmaf(hi, hi, s);
           h[x] = pk_f16(lo, hi);
         }
-#pragma unroll
-        for (int x = NT / 16; x > 0; x >>= 1) s += __shfl_xor(s, x);
+        s = __uint_as_float(row_lanes<NT / 8>(__float_as_uint(s), [](uint32_t a, uint32_t b) {
+          return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+        }));
         *reinterpret_cast<u32x4*>(lds + key_at<NT>(row, c)) = h;
         *reinterpret_cast<u32x4*>(to + key_at<NT>(row, c) * 2) = h;
         // s - s: a NaN where the row is not finite
@@ -106,42 +104,48 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_chunk_kernel(Del
   for (int hh = 0; hh < hg; ++hh) {
     lane = fresh(lane);
     g = lane >> 4, i = lane & 15;
-    const int h = grp * hg + hh;
+    const int h = grp * hg + hh, at4 = hh & 3;
     char* rec = d.rec + (id * a.H + h) * kRecFwd;
     char* rev = BWD ? rec_rev + (id * a.H + h) * kRecRev : nullptr;
-    if (w == 0) {  // lane = row
-      const Rate rate(a, h);
-      const float step = rate.step(raw_step(a, pc.r0, rows, lane, h), lane < rows);
-      const float b = lane < rows ? load_num(d.b, (pc.r0 + lane) * d.b_ld + h, a.dt_f32) : 0.f;
-      float r = lane < rows ? d.beta_max / (1.f + ex2(-kLog2e * b)) : 0.f;
-      float kn = s_kn[lane], qn = s_qn[lane];
-      double l = rate.exponent(step);
-      const bool fine = __builtin_isfinite((float)l) && __builtin_isfinite(r) && __builtin_isfinite(kn);
-      const uint64_t not_fine = __ballot(!fine);
-      const int bad = not_fine && !BWD ? __builtin_ctzll(not_fine) : 64;  // backward, they may reach every row
-      if (lane >= bad) l = 0.0, r = kn = qn = 0.f;
-      const double L = wave_prefix(l);
-      const double end = __shfl(L, 63);
-      sL[lane] = L;
-      s_rate[lane] = r;
-      if (lane == 0) s_bad = bad;
-      const float up = ex2((float)L), left = ex2((float)(end - L));
-      auto factors = [&](char* to) {
-        Factors* f = reinterpret_cast<Factors*>(to);
-        f->in[lane] = up * kn;
-        f->read[lane] = up * qn;
-        f->out[lane] = left * kn;
-        f->rate[lane] = r;
-        if (lane == 0) {
-          f->decay = ex2((float)end);
-          f->bad = bad;
-        }
-      };
-      factors(rec + kRecFwd - kRecVec);
-      if constexpr (BWD) factors(rev + kRecRev - kRecVec);
+    if (at4 == 0) {  // the gates of the next four heads, one a wave; lane = row
+      if (hh > 0) __syncthreads();  // the last four are read
+      if (hh + w < hg) {
+        const int hw = h + w;
+        const Rate rate(a, hw);
+        const float step = rate.step(raw_step(a, pc.r0, rows, lane, hw), lane < rows);
+        const float b = lane < rows ? load_num(d.b, (pc.r0 + lane) * d.b_ld + hw, a.dt_f32) : 0.f;
+        float r = lane < rows ? d.beta_max / (1.f + ex2(-kLog2e * b)) : 0.f;
+        float kn = s_kn[lane], qn = s_qn[lane];
+        double l = rate.exponent(step);
+        const bool fine = __builtin_isfinite((float)l) && __builtin_isfinite(r) && __builtin_isfinite(kn);
+        const uint64_t not_fine = __ballot(!fine);
+        const int bad = not_fine && !BWD ? __builtin_ctzll(not_fine) : 64;  // backward, they may reach every row
+        if (lane >= bad) l = 0.0, r = kn = qn = 0.f;
+        const double L = wave_prefix(l);
+        const double end = __shfl(L, 63);
+        sL_[w][lane] = L;
+        s_rate_[w][lane] = r;
+        if (lane == 0) s_bad_[w] = bad;
+        const float up = ex2((float)L), left = ex2((float)(end - L));
+        auto factors = [&](char* to) {
+          Factors* f = reinterpret_cast<Factors*>(to);
+          f->in[lane] = up * kn;
+          f->read[lane] = up * qn;
+          f->out[lane] = left * kn;
+          f->rate[lane] = r;
+          if (lane == 0) {
+            f->decay = ex2((float)end);
+            f->bad = bad;
+          }
+        };
+        factors(rec + w * kRecFwd + kRecFwd - kRecVec);
+        if constexpr (BWD) factors(rev + w * kRecRev + kRecRev - kRecVec);
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    const int bad = s_bad;
+    const double* sL = sL_[at4];
+    const float* s_rate = s_rate_[at4];
+    const int bad = s_bad_[at4];
 #pragma unroll
     for (int t = 0; t < 3; ++t) {
       int ib, jb;

@@ -81,6 +81,25 @@ __device__ __forceinline__ float sum_across16(float v) {
   const auto q = __builtin_amdgcn_permlane32_swap(x, x, false, false);
   return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
+// an associative, commutative operation over LANES (8, 16 or 32) neighbouring lanes, in every one of them: neighbours, pairs of
+// them, mirrored halves of rows and rows of 16 lanes, then rows of 16
+template <int CTRL>
+__device__ __forceinline__ uint32_t lane_bits(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+template <int LANES, typename Op>
+__device__ __forceinline__ uint32_t row_lanes(uint32_t v, Op op) {
+  v = op(v, lane_bits<0xb1>(v));
+  v = op(v, lane_bits<0x4e>(v));
+  v = op(v, lane_bits<0x141>(v));
+  if constexpr (LANES > 8) v = op(v, lane_bits<0x140>(v));
+  if constexpr (LANES > 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = op(p[0], p[1]);
+  }
+  return v;
+}
+
 // 16 x 16 x 16 in FP32 by the FP32 matrix instructions: each operand holds index l % 16 and the contracted positions
 // 4 (l / 16) + r, which is how results come
 __device__ __forceinline__ f32x4 mma_f32(f32x4 a, f32x4 b, f32x4 c) {
