@@ -192,25 +192,49 @@ __device__ __forceinline__ int64_t chunk_id(const Piece& pc, int64_t c0, int64_t
   return c0 == pc.s ? n_chunk_slots + pc.seq : c0 >> 6;
 }
 
-// Consecutive bytes that T threads copy to shared memory, 16 a thread and step
+// Consecutive bytes that T threads (thread numbers `tid`) copy to shared memory, 16 a thread and step
 template <int BYTES, int T>
 struct CopyRegs {
   u32x4 v[(BYTES / 16 + T - 1) / T];
 };
 template <int BYTES, int T>
-__device__ __forceinline__ void load_bytes(CopyRegs<BYTES, T>& t, const char* from, bool in) {
+__device__ __forceinline__ void load_bytes(CopyRegs<BYTES, T>& t, const char* from, bool in, int tid) {
   const Rows r(from, BYTES, 1, in ? BYTES : 0, 1);
 #pragma unroll
   for (int k = 0; k < (BYTES / 16 + T - 1) / T; ++k)
-    t.v[k] = __builtin_amdgcn_raw_buffer_load_b128(r.r, (int)((threadIdx.x + T * k) * 16), 0, 0);
+    t.v[k] = __builtin_amdgcn_raw_buffer_load_b128(r.r, (tid + T * k) * 16, 0, 0);
 }
 template <int BYTES, int T>
-__device__ __forceinline__ void store_bytes(void* lds, const CopyRegs<BYTES, T>& t) {
+__device__ __forceinline__ void store_bytes(void* lds, const CopyRegs<BYTES, T>& t, int tid) {
 #pragma unroll
   for (int k = 0; k < (BYTES / 16 + T - 1) / T; ++k) {
-    const int at = (threadIdx.x + T * k) * 16;
+    const int at = (tid + T * k) * 16;
     if (at < BYTES) *reinterpret_cast<u32x4*>(static_cast<char*>(lds) + at) = t.v[k];
   }
+}
+
+// 64 rows of 64 columns by 256 threads (thread numbers `tid`), as load_tile and store_tile by all of a block's
+template <bool VEC>
+__device__ __forceinline__ void load_rows64(u32x4 (&v)[2], const Rows& rows, uint32_t ld, int ncols, int tid) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int row = tid / 8 + 32 * k, c = tid % 8 * 8;
+    const uint32_t off = (row * ld + c) * 2;
+    if constexpr (VEC) {
+      v[k] = __builtin_amdgcn_raw_buffer_load_b128(rows.r, (int)(c < ncols ? off : kOutside), 0, 0);
+    } else {
+      v[k] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u = __builtin_amdgcn_raw_buffer_load_b16(rows.r, (int)(c + e < ncols ? off + 2 * e : kOutside), 0, 0);
+        v[k][e >> 1] |= u << (16 * (e & 1));
+      }
+    }
+  }
+}
+__device__ __forceinline__ void store_rows64(uint16_t* lds, const u32x4 (&v)[2], int tid) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) *reinterpret_cast<u32x4*>(lds + at<64, 16>(tid / 8 + 32 * k, tid % 8 * 8)) = v[k];
 }
 
 // four rows of this lane's column of a bf16 tile: rows row0 + 4 g .., column c0 + i

@@ -13,8 +13,283 @@
 
 namespace cssm {
 
+// What shared memory holds of a chunk for the waves that walk the state: the chunk's and the next one's
+template <int NT>
+struct ChainShared {
+  __align__(16) uint16_t k[key_tile(NT) / 2];
+  __align__(16) char t[kRecT];
+  Factors fac;
+  __align__(16) uint16_t v[64 * kLd<64, 16>];
+};
+// and for the waves that make y, with what the others hand them: S's first parts, U, the columns' scales and first rows that
+// are not finite
+template <int NT>
+struct OutputShared {
+  __align__(16) uint16_t q[key_tile(NT) / 2];
+  __align__(16) char p[kTriBlocks * 2 * kTriPart];
+  f16x8 s[4][NT / 32][64];
+  f32x4 u[4][4][64];
+  __align__(16) float down[4][16];
+  __align__(16) int bad[4][16];
+};
+
+// Waves 0 to 3 walk the state and make U, a chain of products that each wait for the last; waves 4 to 7 make y of what the
+// first ones leave in shared memory, a half chunk behind, and bring the next chunks' tiles there.  Two barriers a chunk:
+// after S's parts (1) and after U (2) are there.  Before (1) of a chunk its K, T, V and factors and Q are in place; the
+// next chunk's K, T, V and factors come between (1) and (2), with this chunk's P, the next Q after (2).
 template <int NT, bool VEC>
-__global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_kernel(DeltaArgs d) {
+__global__ __launch_bounds__(512, 2) void delta_scan_fwd_kernel(DeltaArgs d) {
+  constexpr int NB = NT / 16;
+  __shared__ ChainShared<NT> chain[2];
+  __shared__ OutputShared<NT> outp;
+  const ScanArgs& a = d.s;
+  const Units<1> us(a, blockIdx.x);
+  if (!us.ok) return;
+  const Unit me(a, us, 0);
+  const int w = wave_id() & 3, pn = me.pn;
+  const bool walks = wave_id() < 4;
+  Piece pc;
+  pc.seq = us.item;
+  seq_bounds(a.q, pc.seq, pc.s, pc.e);
+  int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+  const int64_t state_at = ((int64_t)me.h * a.P + me.p_first) * a.N;
+  int64_t slot = 0;
+  const bool has_slot = state_slot(a, pc.seq, slot), from = has_slot && starts_from_state(a, pc.seq);
+  if (pc.e <= pc.s) {  // an empty sequence: a separate final state array still gets the start state
+    if (a.fin && a.fin != a.init && has_slot)
+      for (int e = threadIdx.x; e < pn * a.N; e += 512)
+        a.fin[slot * a.s_slot + state_at + e] = from ? a.init[slot * a.s_slot + state_at + e] : 0.f;
+    return;
+  }
+  uint16_t* yb = a.y + me.col;
+  if (!has_slot) {  // zero rows, no state access
+    for (int64_t r = pc.s + wave_id(); r < pc.e; r += 8)
+      if (lane < pn) yb[r * a.y_ld + lane] = 0;
+    return;
+  }
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  Chunks<false> c(pc.s, pc.e);
+  int rows = c.rows();
+
+  if (!walks) {
+    const int tid = threadIdx.x - 256;
+    CopyRegs<(int)key_tile(NT), 256> tK, tQ;
+    CopyRegs<kRecT, 256> tT, tP;
+    CopyRegs<kRecVec, 256> tF;
+    u32x4 tV[2];
+    auto load_chain = [&](const Chunks<false>& n, int left) {
+      const int64_t id = chunk_id(pc, n.c0, d.n_chunk_slots);
+      const char* rec = d.rec + (id * a.H + me.h) * kRecFwd;
+      load_bytes(tK, d.keys + (id * a.G + us.group) * 2 * key_tile(NT), left > 0, tid);
+      load_bytes(tT, rec, left > 0, tid);
+      load_bytes(tF, rec + kRecFwd - kRecVec, left > 0, tid);
+      load_rows64<VEC>(tV, Rows(a.x + n.c0 * a.x_ld + me.col, a.x_ld, left, pn, 2), (uint32_t)a.x_ld, pn, tid);
+    };
+    auto store_chain = [&](ChainShared<NT>& to) {
+      store_bytes(to.k, tK, tid);
+      store_bytes(to.t, tT, tid);
+      store_bytes(&to.fac, tF, tid);
+      store_rows64(to.v, tV, tid);
+    };
+    auto load_q = [&](const Chunks<false>& n, int left) {
+      load_bytes(tQ, d.keys + ((chunk_id(pc, n.c0, d.n_chunk_slots) * a.G + us.group) * 2 + 1) * key_tile(NT), left > 0, tid);
+    };
+    auto load_p = [&](const Chunks<false>& n, int left) {
+      load_bytes(tP, d.rec + (chunk_id(pc, n.c0, d.n_chunk_slots) * a.H + me.h) * kRecFwd + kRecT, left > 0, tid);
+    };
+    load_chain(c, rows);
+    load_q(c, rows);
+    load_p(c, rows);
+    Chunks<false> next = c, after = c;
+    int next_rows = rows, after_rows = rows;
+    next = step_chunk(next, next_rows);
+    store_chain(chain[0]);
+    store_bytes(outp.q, tQ, tid);
+    load_chain(next, next_rows);
+    load_q(next, next_rows);
+    __syncthreads();
+    for (int buf = 0;; buf ^= 1) {
+      lane = fresh(lane);
+      g = lane >> 4, i = lane & 15;
+      after = next, after_rows = next_rows;
+      after = step_chunk(after, after_rows);
+      __syncthreads();  // (1)
+      store_bytes(outp.p, tP, tid);
+      store_chain(chain[buf ^ 1]);
+      load_p(next, next_rows);
+      load_chain(after, after_rows);
+      phase();
+      f32x4 y[4];  // columns p in the registers, rows in the lanes
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) y[ib] = zero;
+#pragma unroll
+      for (int ks = 0; ks < NT / 32; ++ks) {
+        const f16x8 s = outp.s[w][ks][lane];
+#pragma unroll
+        for (int ib = 0; ib < 4; ++ib) y[ib] = mmah(s, key_rows<NT>(outp.q, 16 * ib, 32 * ks, lane), y[ib]);
+      }
+      const f32x4 down = *reinterpret_cast<const f32x4*>(&outp.down[w][4 * g]);
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) y[ib] *= down * chain[buf].fac.read[16 * ib + i];
+      phase();
+      __syncthreads();  // (2)
+      store_bytes(outp.q, tQ, tid);
+      load_q(after, after_rows);
+      phase();
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const Parts up = split(outp.u[w][2 * ks][lane], outp.u[w][2 * ks + 1][lane]);
+#pragma unroll
+        for (int ib = 2 * ks; ib < 4; ++ib) {
+          const bf16x8 p = __builtin_bit_cast(bf16x8, tri_rows<2>(outp.p, ib, ks, 0, lane));
+          y[ib] = mma(up.p[0], __builtin_bit_cast(bf16x8, tri_rows<2>(outp.p, ib, ks, 1, lane)), y[ib]);
+          y[ib] = mma(up.p[1], p, y[ib]);
+          y[ib] = mma(up.p[0], p, y[ib]);
+        }
+      }
+      typedef int i32x4 __attribute__((ext_vector_type(4)));
+      const i32x4 bad = *reinterpret_cast<const i32x4*>(&outp.bad[w][4 * g]);
+      if (__builtin_expect(__ballot(min(min(bad[0], bad[1]), min(bad[2], bad[3])) < 64) != 0, 0)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int ib = 0; ib < 4; ++ib)
+            if (16 * ib + i >= bad[e]) y[ib][e] = __builtin_nanf("");
+      }
+      const Rows out(yb + c.c0 * a.y_ld, a.y_ld, rows, pn, 2);
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) {
+        const f32x4 v = y[ib];
+        store4<VEC>(out, (uint32_t)a.y_ld, 16 * ib + i, 16 * w + 4 * g, pn, u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])});
+      }
+      if (next_rows == 0) return;
+      c = next, rows = next_rows;
+      next = after, next_rows = after_rows;
+    }
+  }
+
+  const int p_in = 16 * w + i;  // this lane's state row
+  f32x4 S[NB];
+  load_state(S, from && p_in < pn ? a.init + slot * a.s_slot + state_at + (int64_t)p_in * a.N : nullptr, a.N, g);
+  float s_down = 1.f;  // the state is s_down S
+  {
+    const Pow2 scale = state_scale<1>(state_max(S));
+    s_down = scale.down;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) S[nb] *= scale.up;
+  }
+  __syncthreads();
+  for (int buf = 0;; buf ^= 1) {
+    lane = fresh(lane);
+    g = lane >> 4, i = lane & 15;
+    const ChainShared<NT>& sh = chain[buf];
+    const Factors& fac = sh.fac;
+    f32x4 r[4];  // rows in the registers, columns p in the lanes
+#pragma unroll
+    for (int ib = 0; ib < 4; ++ib) r[ib] = zero;
+    if (g == 0) outp.down[w][i] = s_down;
+    Halves s[NT / 32];
+#pragma unroll
+    for (int ks = 0; ks < NT / 32; ++ks) {
+      s[ks] = halves(S[2 * ks], S[2 * ks + 1]);
+      outp.s[w][ks][lane] = s[ks].hi;
+    }
+    __syncthreads();  // (1)
+#pragma unroll
+    for (int ks = 0; ks < NT / 32; ++ks)
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) r[ib] = mma2(key_rows<NT>(sh.k, 16 * ib, 32 * ks, lane), s[ks], r[ib]);
+    const float s_max = state_max(S);
+    float r_max = 0.f;
+    bool fine = true;
+#pragma unroll
+    for (int ib = 0; ib < 4; ++ib) {
+      const f32x4 f = *reinterpret_cast<const f32x4*>(fac.in + 16 * ib + 4 * g) * s_down;
+      r[ib] = (column4(sh.v, 16 * ib, 16 * w, g, i) - f * r[ib]) * *reinterpret_cast<const f32x4*>(fac.rate + 16 * ib + 4 * g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) fine = fine && __builtin_isfinite(r[ib][e]);
+      r_max = max4(r_max, r[ib]);
+    }
+    // The first row of this lane's column that is not finite: it and the later ones are left out of the products, whose
+    // zeros would spread them, and put in at the end
+    int bad = __builtin_amdgcn_readfirstlane(fac.bad);
+    const bool any_bad = bad < 64 || __ballot(!fine) != 0;
+    if (__builtin_expect(any_bad, 0)) {
+#pragma unroll
+      for (int ib = 3; ib >= 0; --ib)
+#pragma unroll
+        for (int e = 3; e >= 0; --e) {
+          const int row = 16 * ib + 4 * g + e;
+          if (!__builtin_isfinite(r[ib][e]) && row < bad) bad = row;
+        }
+      bad = min(bad, __shfl_xor(bad, 16));
+      bad = min(bad, __shfl_xor(bad, 32));
+      r_max = 0.f;
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (16 * ib + 4 * g + e >= bad) r[ib][e] = 0.f;
+        r_max = max4(r_max, r[ib]);
+      }
+    }
+    const Pow2 rs = bring_to<10>(max_across16(r_max));
+    f32x4 u[4];
+    {
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) r[ib] *= rs.up;
+      const Halves rp[2] = {halves(r[0], r[1]), halves(r[2], r[3])};
+      const float u_down = rs.down * fac.t_scale;
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) {
+        u[ib] = zero;
+#pragma unroll
+        for (int ks = 0; ks <= ib / 2; ++ks) u[ib] = mma3(t_rows(sh.t, ib, ks, lane), rp[ks], u[ib]);
+      }
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) {
+        u[ib] *= u_down;
+        outp.u[w][ib][lane] = u[ib];
+      }
+      if (g == 0) outp.bad[w][i] = bad;
+    }
+    __syncthreads();  // (2)
+    // what goes into the state and its scale
+    float o_max = 0.f;
+#pragma unroll
+    for (int ib = 0; ib < 4; ++ib) {
+      u[ib] *= *reinterpret_cast<const f32x4*>(fac.out + 16 * ib + 4 * g);
+      o_max = max4(o_max, u[ib]);
+    }
+    const float grown = fac.decay * s_down;
+    const Pow2 ss = state_scale<1>(__builtin_fmaxf(max_across16(o_max), s_max * grown));
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) S[nb] *= grown * ss.up;
+    s_down = ss.down;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const Halves o = halves(u[2 * ks] * ss.up, u[2 * ks + 1] * ss.up);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) S[nb] = mma2(key_cols<NT>(sh.k, 32 * ks, 16 * nb, lane), o, S[nb]);
+    }
+    if (__builtin_expect(any_bad, 0)) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        if (bad < 64) S[nb] = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
+    }
+    c = step_chunk(c, rows);
+    if (rows == 0) break;
+  }
+  if (a.fin && p_in < pn) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) S[nb] *= s_down;
+    store_state(S, a.fin + slot * a.s_slot + state_at + (int64_t)p_in * a.N, a.N, lane >> 4);
+  }
+}
+
+// The same for states of more than 128 columns, whose tiles shared memory does not hold twice: four waves that walk and make y.
+template <int NT, bool VEC>
+__global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_wide_kernel(DeltaArgs d) {
   constexpr int T = 256, NB = NT / 16, kKeys = 2 * (int)key_tile(NT);
   __shared__ __align__(16) uint16_t sKQ[kKeys / 2];
   __shared__ __align__(16) uint16_t sV[64 * kLd<64, 16>];
@@ -60,8 +335,8 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_kernel(
   CopyRegs<kRecFwd, T> tR;
   auto load = [&](const Chunks<false>& c, int rows) {
     const int64_t id = chunk_id(pc, c.c0, d.n_chunk_slots);
-    load_bytes(tK, d.keys + (id * a.G + us.group) * kKeys, rows > 0);
-    load_bytes(tR, d.rec + (id * a.H + me.h) * kRecFwd, rows > 0);
+    load_bytes(tK, d.keys + (id * a.G + us.group) * kKeys, rows > 0, threadIdx.x);
+    load_bytes(tR, d.rec + (id * a.H + me.h) * kRecFwd, rows > 0, threadIdx.x);
     load_tile<VEC>(tV, Rows(a.x + c.c0 * a.x_ld + me.col, a.x_ld, rows, pn, 2), (uint32_t)a.x_ld, pn);
   };
   Chunks<false> c(pc.s, pc.e);
@@ -74,8 +349,8 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_kernel(
   for (;;) {
     lane = fresh(lane);
     g = lane >> 4, i = lane & 15;
-    store_bytes(sKQ, tK);
-    store_bytes(sR, tR);
+    store_bytes(sKQ, tK, threadIdx.x);
+    store_bytes(sR, tR, threadIdx.x);
     store_tile<16>(sV, tV);
     __syncthreads();
     const Rows out(yb + c.c0 * a.y_ld, a.y_ld, rows, pn, 2);
@@ -210,8 +485,13 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_kernel(
 template <int NT>
 static void launch(const DeltaArgs& a, bool vec, hipStream_t s) {
   const dim3 grid((uint32_t)unit_blocks(a.s.q.nseq, a.s.H, a.s.G, a.s.ptiles, 1));
-  if (vec) delta_scan_fwd_kernel<NT, true><<<grid, 256, 0, s>>>(a);
-  else delta_scan_fwd_kernel<NT, false><<<grid, 256, 0, s>>>(a);
+  if constexpr (NT > 128) {
+    if (vec) delta_scan_fwd_wide_kernel<NT, true><<<grid, 256, 0, s>>>(a);
+    else delta_scan_fwd_wide_kernel<NT, false><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (vec) delta_scan_fwd_kernel<NT, true><<<grid, 512, 0, s>>>(a);
+    else delta_scan_fwd_kernel<NT, false><<<grid, 512, 0, s>>>(a);
+  }
 }
 
 hipError_t launch_delta_fwd(const DeltaArgs& a, bool vec, hipStream_t s) {

@@ -133,8 +133,8 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
   CopyRegs<kBytes, T> tR;
   auto load = [&](const Chunks<REV>& c, int rows) {
     const int64_t id = chunk_id(pc, c.c0, d.n_chunk_slots);
-    load_bytes(tK, d.keys + (id * a.G + us.group) * 2 * key_tile(NT), rows > 0);
-    load_bytes(tR, recs + (id * a.H + me.h) * kBytes, rows > 0);
+    load_bytes(tK, d.keys + (id * a.G + us.group) * 2 * key_tile(NT), rows > 0, threadIdx.x);
+    load_bytes(tR, recs + (id * a.H + me.h) * kBytes, rows > 0, threadIdx.x);
     load_tile<VEC>(tV, Rows(vb + c.c0 * v_ld + me.col, v_ld, rows, pn, 2), (uint32_t)v_ld, pn);
   };
   Chunks<REV> c(pc.s, pc.e);
@@ -147,8 +147,8 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
   for (;;) {
     lane = fresh(lane);
     g = lane >> 4, i = lane & 15;
-    store_bytes(sh.kq, tK);
-    store_bytes(sh.rec, tR);
+    store_bytes(sh.kq, tK, threadIdx.x);
+    store_bytes(sh.rec, tR, threadIdx.x);
     store_tile<16>(sh.v, tV);
     __syncthreads();
     const Rows to = tile_record<NT>(b, (chunk_id(pc, c.c0, d.n_chunk_slots) * a.H + me.h) * a.ptiles + me.p_first / kPTile, true);
