@@ -25,13 +25,18 @@ bool sizes_ok(const delta_shape* s, int64_t rows, int64_t nseq) {
          mul_ok(ceil_div(rows, kChunk) + nseq + 1, hp * 64 * kMaxState);
 }
 int64_t chunk_ids(int64_t rows, int64_t nseq) { return ceil_div(rows, kChunk) + nseq; }
-// the key heads' records, first in either workspace
+// the key heads' records, first in either workspace, and then the sequences' order
 int64_t keys_bytes(const delta_shape* s, int64_t rows, int64_t nseq) {
   return align_up(chunk_ids(rows, nseq) * s->G * 2 * key_tile(state_tile(s->N)));
 }
+int64_t order_bytes(int64_t nseq) { return align_up(nseq * 4); }
 bool launches_ok(const delta_shape* s, int64_t rows, int64_t nseq) {
   return unit_blocks(nseq, s->H, s->G, ceil_div(s->P, kPTile), 1) <= kMaxBlocks / 2 &&
-         mul_ok(chunk_ids(rows, nseq), s->H) && chunk_ids(rows, nseq) * s->H <= kMaxBlocks;
+         mul_ok(chunk_ids(rows, nseq), s->H) && chunk_ids(rows, nseq) * s->H < kMaxBlocks;
+}
+// sequences of unknown lengths, the chunk kernel being run
+void set_order(DeltaArgs* d, const delta_shape* s, int64_t rows, int64_t nseq) {
+  if (d->s.q.cu && nseq > 1 && rows > 0) d->order = reinterpret_cast<int32_t*>(d->keys + keys_bytes(s, rows, nseq));
 }
 bool vec_ok(const delta_shape* s) { return s->P % 8 == 0 && s->N % 8 == 0; }
 
@@ -67,6 +72,7 @@ BwdPlan plan_bwd(const delta_shape* s, int64_t rows, int64_t nseq) {
   BwdPlan p{};
   const int64_t ids = chunk_ids(rows, nseq);
   int64_t at = keys_bytes(s, rows, nseq);
+  at += order_bytes(nseq);
   p.rec = at, at += align_up(ids * s->H * kRecFwd);
   p.rec_rev = at, at += align_up(ids * s->H * kRecRev);
   p.tiles = at, at += align_up(ids * s->H * ceil_div(s->P, kPTile) * tile_floats(state_tile(s->N)) * 4);
@@ -81,7 +87,7 @@ extern "C" {
 
 size_t delta_scan_fwd_workspace_bytes(const delta_shape* shape, int64_t rows, int64_t nseq) {
   if (!shape_ok(shape) || rows <= 0 || nseq <= 0 || !sizes_ok(shape, rows, nseq)) return 0;
-  return (size_t)(keys_bytes(shape, rows, nseq) + align_up(chunk_ids(rows, nseq) * shape->H * kRecFwd));
+  return (size_t)(keys_bytes(shape, rows, nseq) + order_bytes(nseq) + align_up(chunk_ids(rows, nseq) * shape->H * kRecFwd));
 }
 
 int delta_scan_fwd(const delta_shape* shape, int64_t rows, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
@@ -113,7 +119,8 @@ int delta_scan_fwd(const delta_shape* shape, int64_t rows, const void* q, int64_
   d.s.y = static_cast<uint16_t*>(y);
   d.s.y_ld = y_ld;
   d.keys = static_cast<char*>(ws);
-  d.rec = d.keys + keys_bytes(shape, rows, nseq);
+  d.rec = d.keys + keys_bytes(shape, rows, nseq) + order_bytes(nseq);
+  set_order(&d, shape, rows, nseq);
   return launch_delta_fwd(d, vec_ok(shape), stream) == hipSuccess ? CONV1D_OK : CONV1D_EHIP;
 }
 
@@ -162,6 +169,7 @@ int delta_scan_bwd(const delta_shape* shape, int64_t rows, const void* dy, int64
     g.d.s.s_slot = hp * shape->N;
     g.d.keys = w;
     g.d.rec = w + p.rec;
+    set_order(&g.d, shape, rows, nseq);
     g.dy = static_cast<const uint16_t*>(dy), g.dy_ld = dy_ld;
     g.dfin = dfinal_state, g.dinit = dinitial_state;
     g.dq = static_cast<uint16_t*>(dq), g.dq_ld = dq_ld;

@@ -25,8 +25,31 @@ __device__ __forceinline__ uint32_t max_bits(u32x4 v) {
   return m;
 }
 
+// The sequences from long to short (by chunks, 255 and more alike; which of equal ones comes first makes no difference to
+// any result): a walk lasts as long as its sequence, and one that began last would keep the others waiting.  64 mixed
+// prompts (longest 4000 of 32512 rows): ORDER.
+__device__ __forceinline__ void order_sequences(const Seqs& q, int32_t* order) {
+  __shared__ uint32_t s_at[256];
+  s_at[threadIdx.x] = 0;
+  __syncthreads();
+  auto key = [&](int64_t i) {
+    int64_t s = q.cu[i], e = q.cu[i + 1];
+    s = s < 0 ? 0 : s, e = e > q.rows ? q.rows : e;
+    const int64_t chunks = e > s ? (e - s + kChunk - 1) / kChunk : 0;
+    return 255 - (int)(chunks < 255 ? chunks : 255);
+  };
+  for (int64_t i = threadIdx.x; i < q.nseq; i += 256) atomicAdd(&s_at[key(i)], 1u);
+  __syncthreads();
+  uint32_t before = 0;
+  for (int k = 0; k < (int)threadIdx.x; ++k) before += s_at[k];
+  __syncthreads();
+  s_at[threadIdx.x] = before;
+  __syncthreads();
+  for (int64_t i = threadIdx.x; i < q.nseq; i += 256) order[atomicAdd(&s_at[key(i)], 1u)] = (int32_t)i;
+}
+
 template <int NT, bool VEC, bool BWD>
-__global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs d, char* rec_rev) {
+__global__ __launch_bounds__(256, NT <= 128 ? 3 : 2) void delta_chunk_kernel(DeltaArgs d, char* rec_rev) {
   constexpr int LD = 68;  // rows of 64 FP32 values, 16 bytes further apart
   // the tiles of k and q until their products are made, then X and T
   constexpr int kTiles = 2 * (int)key_tile(NT), kSystems = 2 * 64 * LD * 4;
@@ -39,7 +62,11 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs d, char* 
   const ScanArgs& a = d.s;
   int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
   const int w = wave_id();
-  const uint32_t blk = xcd_block(blockIdx.x, gridDim.x);
+  if (blockIdx.x + 1 == gridDim.x) {
+    if (d.order) order_sequences(a.q, d.order);
+    return;
+  }
+  const uint32_t blk = xcd_block(blockIdx.x, gridDim.x - 1);
   const int grp = blk % (uint32_t)a.G;
   const int64_t id = blk / (uint32_t)a.G;
   const Piece pc = find_chunk(a.q, id, d.n_chunk_slots);
@@ -54,7 +81,7 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs d, char* 
     auto convert = [&](const TileRegs<NT, 256>& t, uint16_t* lds, char* to, float* norm, float factor) {
 #pragma unroll
       for (int k = 0; k < NT / 32; ++k) {
-        const int q = threadIdx.x + 256 * k, row = q / (NT / 8), c = q % (NT / 8) * 8;
+        const int q = fresh((int)threadIdx.x) + 256 * k, row = q / (NT / 8), c = q % (NT / 8) * 8;
         uint32_t m = max_bits(t.v[k]);
         m = row_lanes<NT / 8>(m, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
         uint32_t e = m >> 7;  // the largest one's exponent
@@ -77,6 +104,7 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs d, char* 
         // s - s: a NaN where the row is not finite
         const float f = (d.qk_norm ? rsqrtf(s + (d.norm_eps > 0.f ? d.norm_eps * up * up : 0.f)) : down) + (s - s);
         if (c == 0) norm[row] = row < rows ? f * factor : 0.f;
+        phase();
       }
     };
     convert(tk, sK, keys, s_kn, 1.f);
@@ -97,6 +125,7 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs d, char* 
         const f16x8 qi = key_rows<NT>(sQ, 16 * ib, 32 * ks, lane);
         kk[t] = mmah(kj, key_rows<NT>(sK, 16 * ib, 32 * ks, lane), kk[t]);
         qk[t] = BWD ? mmah(qi, kj, qk[t]) : mmah(kj, qi, qk[t]);
+        phase();
       }
     }
   }
@@ -148,6 +177,8 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs d, char* 
     const int bad = s_bad_[at4];
 #pragma unroll
     for (int t = 0; t < 3; ++t) {
+        lane = fresh(lane);
+      g = lane >> 4, i = lane & 15;
       int ib, jb;
       lower_block(w + 4 * t, ib, jb);
       if (w + 4 * t < 10) {
@@ -177,26 +208,31 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs d, char* 
       }
     }
     __syncthreads();
+    lane = fresh(lane);
+    g = lane >> 4, i = lane & 15;
     {  // diagonal block w: column i of its inverse; the four groups of lanes do the same
       const float* X = sX + 16 * w * LD + 16 * w;
       float t[16];
+      f32x4 x[2][4];  // a row of X, and the next one on its way
+      x[1][0] = *reinterpret_cast<const f32x4*>(X + LD);
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
+#pragma unroll
+        for (int m4 = 0; m4 <= r; m4 += 4)
+          if (r < 15) x[(r + 1) & 1][m4 / 4] = *reinterpret_cast<const f32x4*>(X + (r + 1) * LD + m4);
         float v = r == i ? 1.f : 0.f;
 #pragma unroll
-        for (int m4 = 0; m4 < r; m4 += 4) {
-          const f32x4 x = *reinterpret_cast<const f32x4*>(X + r * LD + m4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (m4 + e < r) v = __builtin_fmaf(-x[e], t[m4 + e], v);
-        }
+        for (int m = 0; m < r; ++m) v = __builtin_fmaf(-x[r & 1][m / 4][m % 4], t[m], v);
         t[r] = v;
+        phase();
       }
 #pragma unroll
       for (int r = 0; r < 16; ++r)
         if ((r >> 2) == g) sT[(16 * w + r) * LD + 16 * w + i] = t[r];
     }
     __syncthreads();
+    lane = fresh(lane);
+    g = lane >> 4, i = lane & 15;
     auto x_rows = [&](int ib, int jb) { return *reinterpret_cast<const f32x4*>(sX + (16 * ib + i) * LD + 16 * jb + 4 * g); };
     auto t_rows = [&](int ib, int jb) { return *reinterpret_cast<const f32x4*>(sT + (16 * ib + i) * LD + 16 * jb + 4 * g); };
     auto t_cols = [&](int ib, int jb) {  // column i in the lanes, rows in the registers
@@ -233,6 +269,8 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs d, char* 
       reinterpret_cast<Factors*>(rec + kRecFwd - kRecVec)->t_scale = scale.down;
       if constexpr (BWD) reinterpret_cast<Factors*>(rev + kRecRev - kRecVec)->t_scale = scale.down;
     }
+    lane = fresh(lane);
+    g = lane >> 4, i = lane & 15;
 #pragma unroll
     for (int t = 0; t < 3; ++t) {
       int ib, jb;
@@ -247,7 +285,7 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs d, char* 
 
 template <int NT>
 static void launch(const DeltaArgs& a, char* rec_rev, bool vec, hipStream_t s) {
-  const dim3 grid((uint32_t)((a.n_chunk_slots + a.s.q.nseq) * a.s.G));
+  const dim3 grid((uint32_t)((a.n_chunk_slots + a.s.q.nseq) * a.s.G + 1));  // the last block orders the sequences
   if (rec_rev) {
     if (vec) delta_chunk_kernel<NT, true, true><<<grid, 256, 0, s>>>(a, rec_rev);
     else delta_chunk_kernel<NT, false, true><<<grid, 256, 0, s>>>(a, rec_rev);

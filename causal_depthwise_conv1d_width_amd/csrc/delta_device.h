@@ -192,6 +192,11 @@ __device__ __forceinline__ int64_t chunk_id(const Piece& pc, int64_t c0, int64_t
   return c0 == pc.s ? n_chunk_slots + pc.seq : c0 >> 6;
 }
 
+// the sequence that the item-th walk takes
+__device__ __forceinline__ int64_t walk_sequence(const DeltaArgs& d, int64_t item) {
+  return d.order ? __builtin_amdgcn_readfirstlane(d.order[item]) : item;
+}
+
 // Consecutive bytes that T threads (thread numbers `tid`) copy to shared memory, 16 a thread and step
 template <int BYTES, int T>
 struct CopyRegs {

@@ -39,6 +39,7 @@ struct DeltaArgs {
   int64_t n_chunk_slots;  // chunk id = row / kChunk, or n_chunk_slots + seq for a sequence's first
   char* keys;             // [chunk id, G] key heads' records of 2 key_tile(NT) bytes
   char* rec;              // [chunk id, H] heads' records of kRecFwd bytes
+  int32_t* order;         // with offsets: the sequences from long to short, for the walks
 };
 
 struct DeltaBwdArgs {

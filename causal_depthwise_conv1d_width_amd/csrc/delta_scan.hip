@@ -49,7 +49,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan_fwd_kernel(DeltaArgs d) {
   const int w = wave_id() & 3, pn = me.pn;
   const bool walks = wave_id() < 4;
   Piece pc;
-  pc.seq = us.item;
+  pc.seq = walk_sequence(d, us.item);
   seq_bounds(a.q, pc.seq, pc.s, pc.e);
   int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
   const int64_t state_at = ((int64_t)me.h * a.P + me.p_first) * a.N;
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_wide_ke
   const Unit me(a, us, 0);
   const int w = wave_id(), pn = me.pn;
   Piece pc;
-  pc.seq = us.item;
+  pc.seq = walk_sequence(d, us.item);
   seq_bounds(a.q, pc.seq, pc.s, pc.e);
   int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
   const int p_in = 16 * w + i;  // this lane's state row

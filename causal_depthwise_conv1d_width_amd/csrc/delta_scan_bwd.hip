@@ -102,7 +102,7 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
   const Unit me(a, us, 0);
   const int w = wave_id(), pn = me.pn;
   Piece pc;
-  pc.seq = us.item;
+  pc.seq = walk_sequence(d, us.item);
   seq_bounds(a.q, pc.seq, pc.s, pc.e);
   int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
   const int p_in = 16 * w + i;
@@ -275,6 +275,16 @@ constexpr int kTile = 64 * kLd<64>;
 __device__ __forceinline__ Halves tile_halves(const uint16_t* tiles, int row0, int k0, int l) {
   return Halves{as_f16(op_split<64>(tiles, row0, k0, l)), as_f16(op_split<64>(tiles + kTile, row0, k0, l))};
 }
+// the same of tiles whose rows are in key_at's places
+__device__ __forceinline__ bf16x8 tile_rows(const uint16_t* tile, int row0, int k0, int l) {
+  return __builtin_bit_cast(bf16x8, key_rows<64>(tile, row0, k0, l));
+}
+__device__ __forceinline__ bf16x8 tile_cols(const uint16_t* tile, int k0, int c0, int l) {
+  return __builtin_bit_cast(bf16x8, key_cols<64>(tile, k0, c0, l));
+}
+__device__ __forceinline__ Halves placed_halves(const uint16_t* tiles, int row0, int k0, int l) {
+  return Halves{key_rows<64>(tiles, row0, k0, l), key_rows<64>(tiles + kTile, row0, k0, l)};
+}
 template <int NT>
 __device__ __forceinline__ bf16x8 key_bf16(const uint16_t* tile, int row0, int k0, int l) {
   return __builtin_bit_cast(bf16x8, key_rows<NT>(tile, row0, k0, l));
@@ -358,7 +368,8 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
   __shared__ __align__(16) uint16_t sKQ[2 * kState];
   __shared__ __align__(16) uint16_t sAll[5 * kTile + 4 * kState > 8 * kTile ? 5 * kTile + 4 * kState : 8 * kTile];
   __shared__ __align__(16) double sL[64];
-  __shared__ __align__(16) float s_rate[64], s_kn[64], s_qn[64], s_step[64], s_grow[64], s_left[64];
+  __shared__ __align__(16) float s_rate[64], s_kn[64], s_qn[64], s_step[64], s_grow;
+  __shared__ __align__(16) float s_read[64], s_in_f[64], s_out_f[64], s_dv[64];  // signed factors of S^T dY, S^T F, D^T U, F
   __shared__ __align__(16) float s_u[64], s_f[64], s_y[64];  // the tiles' rows are these times their values
   __shared__ float s_row[4][64], s_col[4][64], s_diag[64], s_in[NB][64], s_out[NB][64], s_dot[T / 64];
   uint16_t *sK = sKQ, *sQ = sKQ + kState;
@@ -461,8 +472,12 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
       sL[lane] = L;
       s_step[lane] = step;
       s_rate[lane] = lane < rows ? d.beta_max / (1.f + ex2(-kLog2e * bv)) : 0.f;
-      s_grow[lane] = ex2((float)L);
-      s_left[lane] = ex2((float)(end - L));
+      const float grow = ex2((float)L);
+      if (lane == 63) s_grow = sign * grow;
+      s_read[lane] = sign_s * d.scale * grow;
+      s_in_f[lane] = -sign * s_rate[lane] * grow;
+      s_out_f[lane] = sign * ex2((float)(end - L));
+      s_dv[lane] = sign_t * s_rate[lane];
     }
     f32x4 W[SB], Y[SB];  // score blocks: columns j in the registers, rows i in the lanes
 #pragma unroll
@@ -481,7 +496,7 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
       const Rows dv(b.dv + pc.r0 * b.dv_ld + (int64_t)h * a.P + p_first, b.dv_ld, rows, pn, 2);
 #pragma unroll
       for (int k = 0; k < KV; ++k) {
-        const int q = tid + T * k, row = q / 16, c = q % 16 * 4, o = at_<64>(row, c);
+        const int q = tid + T * k, row = q / 16, c = q % 16 * 4, o = key_at<64>(row, c);
         const f32x4 y = {bf_lo(ly[k].x), bf_hi(ly[k].x), bf_lo(ly[k].y), bf_hi(ly[k].y)};
         const Pow2 us = bring_to<10>(max16_lanes(max4(0.f, lu[k])));
         const Pow2 fs = bring_to<10>(max16_lanes(max4(0.f, lf[k])));
@@ -495,7 +510,7 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
           s_f[row] = fs.down;
           s_y[row] = ys.down;
         }
-        const f32x4 v = lf[k] * (sign_t * s_rate[row]);
+        const f32x4 v = lf[k] * s_dv[row];
         store4<VEC>(dv, (uint32_t)b.dv_ld, row, c, pn, u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])});
       }
 #pragma unroll
@@ -523,11 +538,11 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
           f32x4 q4 = zero, f4 = zero;
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) {
-            q4 = mma2(sp[ks], as_f16(op_split<64>(sY, row0, 32 * ks, lane)), q4);
-            f4 = mma3(sp[ks], tile_halves(sF, row0, 32 * ks, lane), f4);
+            q4 = mma2(sp[ks], as_f16(tile_rows(sY, row0, 32 * ks, lane)), q4);
+            f4 = mma3(sp[ks], placed_halves(sF, row0, 32 * ks, lane), f4);
           }
-          const f32x4 vq = q4 * (sign_s * d.scale * s_grow[row] * s_y[row] * ss.down);
-          const f32x4 vf = f4 * (-sign * s_rate[row] * s_grow[row] * s_f[row] * ss.down);
+          const f32x4 vq = q4 * (s_read[row] * s_y[row] * ss.down);
+          const f32x4 vf = f4 * (s_in_f[row] * s_f[row] * ss.down);
           in[q] += row_dot(sQ + key_at<NT>(row, n), vq) * s_qn[row] + row_dot(sK + key_at<NT>(row, n), vf) * s_kn[row];
           dQ[q] += vq;
           dK[q] += vf;
@@ -542,8 +557,8 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
           const int row0 = 16 * (QR * rh + q), row = row0 + i, n = 16 * nb + 4 * g;
           f32x4 u4 = zero;
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) u4 = mma3(sp[ks], tile_halves(sU, row0, 32 * ks, lane), u4);
-          const f32x4 vu = u4 * (sign * s_left[row] * s_u[row] * ts.down);
+          for (int ks = 0; ks < 2; ++ks) u4 = mma3(sp[ks], placed_halves(sU, row0, 32 * ks, lane), u4);
+          const f32x4 vu = u4 * (s_out_f[row] * s_u[row] * ts.down);
           out[q] += row_dot(sK + key_at<NT>(row, n), vu) * s_kn[row];
           dK[q] += vu;
           here(out[q]), here(dK[q]);
@@ -558,9 +573,9 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
         f32x4 w4 = zero, y4 = zero;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          const Halves u = tile_halves(sU, 16 * jb, 32 * ks, lane);
-          w4 = mma2(u, as_f16(op_split<64>(sY, 16 * ib, 32 * ks, lane)), w4);
-          y4 = mma3(u, tile_halves(sF, 16 * ib, 32 * ks, lane), y4);
+          const Halves u = placed_halves(sU, 16 * jb, 32 * ks, lane);
+          w4 = mma2(u, as_f16(tile_rows(sY, 16 * ib, 32 * ks, lane)), w4);
+          y4 = mma3(u, placed_halves(sF, 16 * ib, 32 * ks, lane), y4);
         }
         const f32x4 uj = *reinterpret_cast<const f32x4*>(s_u + 16 * jb + 4 * g);
         W[s] += w4 * (uj * s_y[16 * ib + i]);
@@ -616,7 +631,7 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
         if (i == 0) s_col[ib][col + r] = from;
         sum += ib != jb ? x : (4 * g + r < i ? from : 0.f);
       }
-      const int o = at_<64>(row, col);
+      const int o = key_at<64>(row, col);
       store_parts(sZk + o, zk);
       store_parts(sZq + o, zq);
       store_parts(sNj + o, nj);
@@ -627,7 +642,7 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
     }
     // blocks (0, 1), (2, 3): products over 32 rows or columns read them
     if (w < 2) {
-      const int o = at_<64>(32 * w + i, 32 * w + 16 + 4 * g);
+      const int o = key_at<64>(32 * w + i, 32 * w + 16 + 4 * g);
       store_parts(sZk + o, zero);
       store_parts(sZq + o, zero);
       store_parts(sNj + o, zero);
@@ -635,7 +650,7 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
     }
     __syncthreads();
     if (w == T / 64 - 1) {  // lane = row
-      RowSums x{0.f, 0.f, 0.f, s_diag[lane], s_step[lane], s_rate[lane], sign * s_grow[63]};
+      RowSums x{0.f, 0.f, 0.f, s_diag[lane], s_step[lane], s_rate[lane], s_grow};
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         x.in += s_in[k][lane];
@@ -658,15 +673,15 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
         if (ks <= (QR * rh + q) / 2) {  // contracted columns j of these rows
 #pragma unroll
           for (int p = 1; p >= 0; --p) {
-            dQ[q] = mma(k, op_split<64>(sZk + p * kTile, row0, 32 * ks, lane), dQ[q]);
-            dK[q] = mma(k, op_split<64>(sNj + p * kTile, row0, 32 * ks, lane), dK[q]);
+            dQ[q] = mma(k, tile_rows(sZk + p * kTile, row0, 32 * ks, lane), dQ[q]);
+            dK[q] = mma(k, tile_rows(sNj + p * kTile, row0, 32 * ks, lane), dK[q]);
           }
         }
         if (ks >= (QR * rh + q) / 2) {  // contracted rows i of these columns
 #pragma unroll
           for (int p = 1; p >= 0; --p) {
-            dK[q] = mma(qq, op_cols<64>(sZq + p * kTile, 32 * ks, row0, lane), dK[q]);
-            dK[q] = mma(k, op_cols<64>(sNi + p * kTile, 32 * ks, row0, lane), dK[q]);
+            dK[q] = mma(qq, tile_cols(sZq + p * kTile, 32 * ks, row0, lane), dK[q]);
+            dK[q] = mma(k, tile_cols(sNi + p * kTile, 32 * ks, row0, lane), dK[q]);
           }
         }
       }
