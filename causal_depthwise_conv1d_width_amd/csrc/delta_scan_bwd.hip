@@ -275,15 +275,28 @@ constexpr int kTile = 64 * kLd<64>;
 __device__ __forceinline__ Halves tile_halves(const uint16_t* tiles, int row0, int k0, int l) {
   return Halves{as_f16(op_split<64>(tiles, row0, k0, l)), as_f16(op_split<64>(tiles + kTile, row0, k0, l))};
 }
-// the same of tiles whose rows are in key_at's places
-__device__ __forceinline__ bf16x8 tile_rows(const uint16_t* tile, int row0, int k0, int l) {
-  return __builtin_bit_cast(bf16x8, key_rows<64>(tile, row0, k0, l));
+// The chunk kernel's tiles, of NT + 8 columns: of 16 rows, 0 to 3 and 8 to 11 in the even places, the others in the odd ones.
+// Places are 4 or 36 banks apart (mod 64): the 16 bytes that 16 rows hold of 8 columns fall on different banks, and so do the
+// transposing reads' 8 rows of 32 bytes, which contract rows in the same order, 8 (l / 16) on.
+template <int NT>
+__device__ __forceinline__ int spot_at(int row, int col) {
+  return ((row & ~15) + 2 * ((row & 3) + (row >> 1 & 4)) + (row >> 2 & 1)) * (NT + 8) + col;
 }
-__device__ __forceinline__ bf16x8 tile_cols(const uint16_t* tile, int k0, int c0, int l) {
-  return __builtin_bit_cast(bf16x8, key_cols<64>(tile, k0, c0, l));
+// rows row0 .. row0 + 15 (a multiple of 16), contracted columns k0 .. k0 + 31
+template <int NT>
+__device__ __forceinline__ bf16x8 spot_rows(const uint16_t* tile, int row0, int k0, int l) {
+  return *reinterpret_cast<const bf16x8*>(tile + spot_at<NT>(l & 15, (l >> 4) * 8) + row0 * (NT + 8) + k0);
 }
-__device__ __forceinline__ Halves placed_halves(const uint16_t* tiles, int row0, int k0, int l) {
-  return Halves{key_rows<64>(tiles, row0, k0, l), key_rows<64>(tiles + kTile, row0, k0, l)};
+// columns c0 .. c0 + 15, contracted rows k0 .. k0 + 31
+template <int NT>
+__device__ __forceinline__ bf16x8 spot_cols(const uint16_t* tile, int k0, int c0, int l) {
+  const uint16_t* p = tile + spot_at<NT>((l >> 4) * 8 + ((l & 15) >> 2), (l & 3) * 4) + k0 * (NT + 8) + c0;
+  const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
+  const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + NT + 8)));
+  return __builtin_bit_cast(bf16x8, u32x4{a.x, a.y, b.x, b.y});
+}
+__device__ __forceinline__ Halves spot_halves(const uint16_t* tiles, int row0, int k0, int l) {
+  return Halves{as_f16(spot_rows<64>(tiles, row0, k0, l)), as_f16(spot_rows<64>(tiles + kTile, row0, k0, l))};
 }
 template <int NT>
 __device__ __forceinline__ bf16x8 key_bf16(const uint16_t* tile, int row0, int k0, int l) {
@@ -364,7 +377,7 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
   constexpr int KV = 1024 / T, KS = 64 * NT / 4 / T;  // pieces of four values of U (F, dY), of S (D) a thread
   constexpr int SB = (10 + T / 64 - 1) / (T / 64);    // score blocks a wave
   constexpr int kState = (int)key_tile(NT) / 2;    // elements of one part of S
-  // K and Q, bf16; then Y, U's and F's parts and S's and D's, or the four decayed scores' two parts
+  // all in spot_at's places: K and Q, bf16; then Y, U's and F's parts and S's and D's, or the four decayed scores' two parts
   __shared__ __align__(16) uint16_t sKQ[2 * kState];
   __shared__ __align__(16) uint16_t sAll[5 * kTile + 4 * kState > 8 * kTile ? 5 * kTile + 4 * kState : 8 * kTile];
   __shared__ __align__(16) double sL[64];
@@ -440,7 +453,7 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
 #pragma unroll
       for (int k = 0; k < NT * 8 / T; ++k) {
         const int q = threadIdx.x + T * k, row = q / (NT / 8);
-        *reinterpret_cast<u32x4*>(tile + key_at<NT>(row, q % (NT / 8) * 8)) = t.v[k];
+        *reinterpret_cast<u32x4*>(tile + spot_at<NT>(row, q % (NT / 8) * 8)) = t.v[k];
         float s = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -496,7 +509,7 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
       const Rows dv(b.dv + pc.r0 * b.dv_ld + (int64_t)h * a.P + p_first, b.dv_ld, rows, pn, 2);
 #pragma unroll
       for (int k = 0; k < KV; ++k) {
-        const int q = tid + T * k, row = q / 16, c = q % 16 * 4, o = key_at<64>(row, c);
+        const int q = tid + T * k, row = q / 16, c = q % 16 * 4, o = spot_at<64>(row, c);
         const f32x4 y = {bf_lo(ly[k].x), bf_hi(ly[k].x), bf_lo(ly[k].y), bf_hi(ly[k].y)};
         const Pow2 us = bring_to<10>(max16_lanes(max4(0.f, lu[k])));
         const Pow2 fs = bring_to<10>(max16_lanes(max4(0.f, lf[k])));
@@ -516,8 +529,8 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
 #pragma unroll
       for (int k = 0; k < KS; ++k) {  // 16 x 16 blocks, [p block][n block][16 p][16 n]
         const int q = tid + T * k, p = q / (4 * NT) * 16 + q / 4 % 16, n = q / 64 % NB * 16 + q % 4 * 4;
-        store_half4(sS + key_at<NT>(p, n), kState, ls[k] * ss.up);
-        store_half4(sD + key_at<NT>(p, n), kState, lt[k] * ts.up);
+        store_half4(sS + spot_at<NT>(p, n), kState, ls[k] * ss.up);
+        store_half4(sD + spot_at<NT>(p, n), kState, lt[k] * ts.up);
 #pragma unroll
         for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(ls[k][e], lt[k][e], dot);
       }
@@ -531,19 +544,19 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
         Halves sp[2];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
-          sp[ks] = Halves{key_cols<NT>(sS, 32 * ks, 16 * nb, lane), key_cols<NT>(sS + kState, 32 * ks, 16 * nb, lane)};
+          sp[ks] = Halves{as_f16(spot_cols<NT>(sS, 32 * ks, 16 * nb, lane)), as_f16(spot_cols<NT>(sS + kState, 32 * ks, 16 * nb, lane))};
 #pragma unroll
         for (int q = 0; q < QR; ++q) {
           const int row0 = 16 * (QR * rh + q), row = row0 + i, n = 16 * nb + 4 * g;
           f32x4 q4 = zero, f4 = zero;
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) {
-            q4 = mma2(sp[ks], as_f16(tile_rows(sY, row0, 32 * ks, lane)), q4);
-            f4 = mma3(sp[ks], placed_halves(sF, row0, 32 * ks, lane), f4);
+            q4 = mma2(sp[ks], as_f16(spot_rows<64>(sY, row0, 32 * ks, lane)), q4);
+            f4 = mma3(sp[ks], spot_halves(sF, row0, 32 * ks, lane), f4);
           }
           const f32x4 vq = q4 * (s_read[row] * s_y[row] * ss.down);
           const f32x4 vf = f4 * (s_in_f[row] * s_f[row] * ss.down);
-          in[q] += row_dot(sQ + key_at<NT>(row, n), vq) * s_qn[row] + row_dot(sK + key_at<NT>(row, n), vf) * s_kn[row];
+          in[q] += row_dot(sQ + spot_at<NT>(row, n), vq) * s_qn[row] + row_dot(sK + spot_at<NT>(row, n), vf) * s_kn[row];
           dQ[q] += vq;
           dK[q] += vf;
           here(in[q]), here(dQ[q]), here(dK[q]);
@@ -551,15 +564,15 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
         }
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
-          sp[ks] = Halves{key_cols<NT>(sD, 32 * ks, 16 * nb, lane), key_cols<NT>(sD + kState, 32 * ks, 16 * nb, lane)};
+          sp[ks] = Halves{as_f16(spot_cols<NT>(sD, 32 * ks, 16 * nb, lane)), as_f16(spot_cols<NT>(sD + kState, 32 * ks, 16 * nb, lane))};
 #pragma unroll
         for (int q = 0; q < QR; ++q) {
           const int row0 = 16 * (QR * rh + q), row = row0 + i, n = 16 * nb + 4 * g;
           f32x4 u4 = zero;
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) u4 = mma3(sp[ks], placed_halves(sU, row0, 32 * ks, lane), u4);
+          for (int ks = 0; ks < 2; ++ks) u4 = mma3(sp[ks], spot_halves(sU, row0, 32 * ks, lane), u4);
           const f32x4 vu = u4 * (s_out_f[row] * s_u[row] * ts.down);
-          out[q] += row_dot(sK + key_at<NT>(row, n), vu) * s_kn[row];
+          out[q] += row_dot(sK + spot_at<NT>(row, n), vu) * s_kn[row];
           dK[q] += vu;
           here(out[q]), here(dK[q]);
           phase();
@@ -573,9 +586,9 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
         f32x4 w4 = zero, y4 = zero;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          const Halves u = placed_halves(sU, 16 * jb, 32 * ks, lane);
-          w4 = mma2(u, as_f16(tile_rows(sY, 16 * ib, 32 * ks, lane)), w4);
-          y4 = mma3(u, placed_halves(sF, 16 * ib, 32 * ks, lane), y4);
+          const Halves u = spot_halves(sU, 16 * jb, 32 * ks, lane);
+          w4 = mma2(u, as_f16(spot_rows<64>(sY, 16 * ib, 32 * ks, lane)), w4);
+          y4 = mma3(u, spot_halves(sF, 16 * ib, 32 * ks, lane), y4);
         }
         const f32x4 uj = *reinterpret_cast<const f32x4*>(s_u + 16 * jb + 4 * g);
         W[s] += w4 * (uj * s_y[16 * ib + i]);
@@ -606,9 +619,9 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
       f32x4 kk = zero, qk = zero;
 #pragma unroll
       for (int ks = 0; ks < NT / 32; ++ks) {
-        const bf16x8 kj = key_bf16<NT>(sK, 16 * jb, 32 * ks, lane);
-        kk = mma(kj, key_bf16<NT>(sK, 16 * ib, 32 * ks, lane), kk);
-        qk = mma(kj, key_bf16<NT>(sQ, 16 * ib, 32 * ks, lane), qk);
+        const bf16x8 kj = spot_rows<NT>(sK, 16 * jb, 32 * ks, lane);
+        kk = mma(kj, spot_rows<NT>(sK, 16 * ib, 32 * ks, lane), kk);
+        qk = mma(kj, spot_rows<NT>(sQ, 16 * ib, 32 * ks, lane), qk);
       }
       const double Li = sL[row];
       const float ri = s_rate[row], kni = s_kn[row], qni = d.scale * s_qn[row];
@@ -631,7 +644,7 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
         if (i == 0) s_col[ib][col + r] = from;
         sum += ib != jb ? x : (4 * g + r < i ? from : 0.f);
       }
-      const int o = key_at<64>(row, col);
+      const int o = spot_at<64>(row, col);
       store_parts(sZk + o, zk);
       store_parts(sZq + o, zq);
       store_parts(sNj + o, nj);
@@ -642,7 +655,7 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
     }
     // blocks (0, 1), (2, 3): products over 32 rows or columns read them
     if (w < 2) {
-      const int o = key_at<64>(32 * w + i, 32 * w + 16 + 4 * g);
+      const int o = spot_at<64>(32 * w + i, 32 * w + 16 + 4 * g);
       store_parts(sZk + o, zero);
       store_parts(sZq + o, zero);
       store_parts(sNj + o, zero);
@@ -665,23 +678,23 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
     g = lane >> 4, i = lane & 15;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      const bf16x8 k = __builtin_bit_cast(bf16x8, key_cols<NT>(sK, 32 * ks, 16 * nb, lane));
-      const bf16x8 qq = __builtin_bit_cast(bf16x8, key_cols<NT>(sQ, 32 * ks, 16 * nb, lane));
+      const bf16x8 k = spot_cols<NT>(sK, 32 * ks, 16 * nb, lane);
+      const bf16x8 qq = spot_cols<NT>(sQ, 32 * ks, 16 * nb, lane);
 #pragma unroll
       for (int q = 0; q < QR; ++q) {
         const int row0 = 16 * (QR * rh + q);
         if (ks <= (QR * rh + q) / 2) {  // contracted columns j of these rows
 #pragma unroll
           for (int p = 1; p >= 0; --p) {
-            dQ[q] = mma(k, tile_rows(sZk + p * kTile, row0, 32 * ks, lane), dQ[q]);
-            dK[q] = mma(k, tile_rows(sNj + p * kTile, row0, 32 * ks, lane), dK[q]);
+            dQ[q] = mma(k, spot_rows<64>(sZk + p * kTile, row0, 32 * ks, lane), dQ[q]);
+            dK[q] = mma(k, spot_rows<64>(sNj + p * kTile, row0, 32 * ks, lane), dK[q]);
           }
         }
         if (ks >= (QR * rh + q) / 2) {  // contracted rows i of these columns
 #pragma unroll
           for (int p = 1; p >= 0; --p) {
-            dK[q] = mma(qq, tile_cols(sZq + p * kTile, 32 * ks, row0, lane), dK[q]);
-            dK[q] = mma(k, tile_cols(sNi + p * kTile, 32 * ks, row0, lane), dK[q]);
+            dK[q] = mma(qq, spot_cols<64>(sZq + p * kTile, 32 * ks, row0, lane), dK[q]);
+            dK[q] = mma(k, spot_cols<64>(sNi + p * kTile, 32 * ks, row0, lane), dK[q]);
           }
         }
       }
@@ -693,8 +706,8 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
 #pragma unroll
   for (int q = 0; q < QR; ++q) {
     const int row = 16 * (QR * rh + q) + i, n = 16 * nb + 4 * g;
-    const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + key_at<NT>(row, n));
-    const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + key_at<NT>(row, n));
+    const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + spot_at<NT>(row, n));
+    const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + spot_at<NT>(row, n));
     const f32x4 x = dQ[q], y = dK[q];
     const float dq = sum_across16(x[0] * bf_lo(qv.x) + x[1] * bf_hi(qv.x) + x[2] * bf_lo(qv.y) + x[3] * bf_hi(qv.y));
     const float dk = sum_across16(y[0] * bf_lo(kv.x) + y[1] * bf_hi(kv.x) + y[2] * bf_lo(kv.y) + y[3] * bf_hi(kv.y));
@@ -719,8 +732,8 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
       dq *= fq * fq * fq;
       dk *= fk * fk * fk;
     }
-    const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + key_at<NT>(row, n));
-    const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + key_at<NT>(row, n));
+    const u32x2 qv = *reinterpret_cast<const u32x2*>(sQ + spot_at<NT>(row, n));
+    const u32x2 kv = *reinterpret_cast<const u32x2*>(sK + spot_at<NT>(row, n));
     const f32x4 x = dQ[q] * fq - f32x4{bf_lo(qv.x), bf_hi(qv.x), bf_lo(qv.y), bf_hi(qv.y)} * dq;
     const f32x4 y = dK[q] * fk - f32x4{bf_lo(kv.x), bf_hi(kv.x), bf_lo(kv.y), bf_hi(kv.y)} * dk;
     store4<VEC>(oq, (uint32_t)b.dq_ld, row, n, a.N, u32x2{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])});
