@@ -12,10 +12,13 @@ using namespace cssm;
 
 namespace {
 
+constexpr float kMaxFloat = 3.40282347e38f;
+
 bool shape_ok(const delta_shape* s) {
   return s && s->H >= 1 && s->P >= 1 && s->G >= 1 && s->N >= 1 && s->N <= kMaxState && s->H % s->G == 0 &&
          s->H <= (1 << 20) && s->P <= (1 << 20) && dtype_ok(s->gate_dtype) && (s->dt_softplus == 0 || s->dt_softplus == 1) &&
-         (s->qk_norm == 0 || s->qk_norm == 1) && s->norm_eps >= 0.f && s->beta_max == s->beta_max && s->scale == s->scale;
+         (s->qk_norm == 0 || s->qk_norm == 1) && s->norm_eps >= 0.f && s->norm_eps <= kMaxFloat && s->beta_max > 0.f &&
+         s->beta_max <= kMaxFloat && s->scale >= -kMaxFloat && s->scale <= kMaxFloat;
 }
 
 // every extent of the workspace and every launch, bounded by one chunk a row and sequence

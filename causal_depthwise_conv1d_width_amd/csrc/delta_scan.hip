@@ -37,6 +37,9 @@ struct OutputShared {
 // first ones leave in shared memory, a half chunk behind, and bring the next chunks' tiles there.  Two barriers a chunk:
 // after S's parts (1) and after U (2) are there.  Before (1) of a chunk its K, T, V and factors and Q are in place; the
 // next chunk's K, T, V and factors come between (1) and (2), with this chunk's P, the next Q after (2).
+// What bounds it is the chain: R needs S, U needs R and the next S needs U, 3.3 us a chunk at 128 x 128, in which a SIMD's
+// matrix instructions are busy for 0.8.  4 x 4096 rows of 32 heads of 128 x 128: 335 us with the chunk kernel's 125; with all of it in
+// four waves, which waited for y's products and for the tiles between the chain's, 454.  One prompt of 2048 rows: 130 (174).
 template <int NT, bool VEC>
 __global__ __launch_bounds__(512, 2) void delta_scan_fwd_kernel(DeltaArgs d) {
   constexpr int NB = NT / 16;
@@ -287,7 +290,8 @@ __global__ __launch_bounds__(512, 2) void delta_scan_fwd_kernel(DeltaArgs d) {
   }
 }
 
-// The same for states of more than 128 columns, whose tiles shared memory does not hold twice: four waves that walk and make y.
+// The same for states of more than 128 columns, whose tiles shared memory does not hold twice: four waves that walk and make y,
+// a wave's 16 x 256 values of the state in 64 registers a lane.  Shared memory is filled between the chunks.
 template <int NT, bool VEC>
 __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_wide_kernel(DeltaArgs d) {
   constexpr int T = 256, NB = NT / 16, kKeys = 2 * (int)key_tile(NT);

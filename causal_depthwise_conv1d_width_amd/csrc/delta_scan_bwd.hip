@@ -29,7 +29,7 @@ constexpr int kWalkThreads = 256;
 // The walks hold their state, and with it U or F, with a sign that changes from chunk to chunk.  What matrix instructions add up
 // comes out a little low, whatever its sign; dl's terms are sums of both signs, and over all the rows of dA and d(dt_bias)
 // such offsets add up: 2.8e-6 of dA over 16384 rows, 8e-6 with rates up to two.  With the signs they cancel:
-// ERR.  The forward walk's change at every chunk, the reverse walk's at every second, so that their products'
+// 2.3e-7.  The forward walk's change at every chunk, the reverse walk's at every second, so that their products'
 // change as well.
 __device__ __forceinline__ float sign_at(int64_t chunk, bool rev) { return (rev ? chunk >> 1 : chunk) & 1 ? -1.f : 1.f; }
 
@@ -370,13 +370,15 @@ __device__ __forceinline__ void finish_rows(const DeltaBwdArgs& b, const RowSums
 // A block takes a chunk and a key head and walks the 64-column tiles of its value heads: U, F, dY, S and D of a tile go
 // to shared memory as fp16 parts while the next tile's are loaded.  A wave owns 16 columns n of dq and dk and 32 of the 64
 // rows, and one of the ten score blocks: 16 waves (N > 64) in 128 registers, four a SIMD, to cover what each of them
-// waits for.  (8 waves of 256 registers that held their parts of S and D spilled, and took TIMES.)
+// waits for.  (8 waves of 256 registers that held their parts of S and D spilled: the whole backward took
+// 1794 us at 4 x 4096 rows, with these 1510.)  Reading the tiles by 16 bytes from places without bank conflicts made that 1410,
+// of which this kernel takes 750: it reads 1.6 GB of tiles, and one block a CU hides little of what its passes wait for.
 template <int NT, int WR, bool VEC>
 __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArgs b) {
   constexpr int T = 4 * NT * WR, NB = NT / 16, QR = 4 / WR;  // threads, blocks of columns n, of rows a wave
   constexpr int KV = 1024 / T, KS = 64 * NT / 4 / T;  // pieces of four values of U (F, dY), of S (D) a thread
   constexpr int SB = (10 + T / 64 - 1) / (T / 64);    // score blocks a wave
-  constexpr int kState = (int)key_tile(NT) / 2;    // elements of one part of S
+  constexpr int kState = 64 * (NT + 8);               // elements of one part of S
   // all in spot_at's places: K and Q, bf16; then Y, U's and F's parts and S's and D's, or the four decayed scores' two parts
   __shared__ __align__(16) uint16_t sKQ[2 * kState];
   __shared__ __align__(16) uint16_t sAll[5 * kTile + 4 * kState > 8 * kTile ? 5 * kTile + 4 * kState : 8 * kTile];

@@ -1,7 +1,8 @@
 // delta_step.hip -- the gated delta rule for one token a sequence against the slot pool of FP32 states.
 //
 //   u = r (v - a S k),   S' = a S + u k^T,   y = scale S' q = scale (a S q + u (k q))
-// A stream over the states (read and written once): 8 bytes for 7 operations, bound by memory.  A lane holds four
+// A stream over the states (read and written once): 8 bytes for 7 operations, bound by memory: 64 sequences of 32 heads of
+// 128 x 128 in 52 us, 5.2 TB/s (a large copy: 4.9).  One sequence takes 14 us, which is its launch.  A lane holds four
 // columns n of a row p; LN lanes (a power of two, up to 64) share a row, and a wave keeps kRowsHeld rows a lane in flight.
 // Both of a row's products come from the state as it was read, so that their sums over the lanes run side by side.
 #include "delta_launch.h"
@@ -72,7 +73,9 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepArgs a) {
     kq = __builtin_fmaf(kv[e], qv[e], kq);
   }
   kk = lanes_sum<LN>(kk), qq = lanes_sum<LN>(qq), kq = lanes_sum<LN>(kq);
-  const float kn = a.qk_norm ? rsqrtf(kk + a.norm_eps) : 1.f, qn = (a.qk_norm ? rsqrtf(qq + a.norm_eps) : 1.f) * a.scale;
+  // kk - kk: a NaN where the sum is not finite
+  const float kn = a.qk_norm ? rsqrtf(kk + a.norm_eps) + (kk - kk) : 1.f;
+  const float qn = (a.qk_norm ? rsqrtf(qq + a.norm_eps) + (qq - qq) : 1.f) * a.scale;
   float sk[kRowsHeld], sq[kRowsHeld];
 #pragma unroll
   for (int k = 0; k < kRowsHeld; ++k) {

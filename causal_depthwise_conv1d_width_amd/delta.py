@@ -28,10 +28,15 @@ def _shape(q, k, v, dt, b, dt_softplus, qk_norm, scale, beta_max, norm_eps):
         raise ValueError("k, v: need heads divisible by groups and 1 <= state <= 256")
     scale = N ** -0.5 if scale is None else float(scale)
     norm_eps = float(norm_eps)
-    if not norm_eps >= 0:
-        raise ValueError("norm_eps: must not be negative")
+    beta_max = float(beta_max)
+    if not 0 <= norm_eps < float("inf"):
+        raise ValueError(f"norm_eps: must be finite and not negative (got {norm_eps})")
+    if not 0 < beta_max < float("inf"):
+        raise ValueError(f"beta_max: must be finite and positive (got {beta_max})")
+    if not abs(scale) < float("inf"):
+        raise ValueError(f"scale: must be finite (got {scale})")
     return _lib.DeltaShape(H, P, G, N, _lib.F32 if dt.dtype is _F32 else _lib.BF16, int(bool(dt_softplus)),
-                           int(bool(qk_norm)), scale, float(beta_max), norm_eps)
+                           int(bool(qk_norm)), scale, beta_max, norm_eps)
 
 
 def _inputs(q, k, v, dt, b, A, dt_bias):
@@ -190,14 +195,13 @@ def layer_norm_fwd(x, weight, bias=None, *, residual=None, scale=1.0, eps=1e-5, 
         if bias.dtype is not weight.dtype:
             raise ValueError(f"bias: need weight's dtype {weight.dtype} (got {bias.dtype})")
         bp = _weight(bias, d)[0]
+    if residual is None and (residual_out is not None or scale != 1.0):
+        raise ValueError("residual_out, scale: need a residual")
     dev = _on(x, (residual, "residual"), (weight, "weight"), (bias, "bias"), (out, "out"), (residual_out, "residual_out"))
     if out is None:
         out = _result(x, (rows, d), _BF16, stream)
     rr, rt, ro = (None, 0), _lib.BF16, (None, 0)
-    if residual is None:
-        if residual_out is not None or scale != 1.0:
-            raise ValueError("residual_out, scale: need a residual")
-    else:
+    if residual is not None:
         rt, rr = _res_dtype(residual, "residual"), _rows(residual, "residual", (rows, d), residual.dtype)
         if residual_out is None:
             residual_out = _result(residual, (rows, d), residual.dtype, stream)

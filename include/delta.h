@@ -17,10 +17,15 @@
  * `stream`.  q, k, v, y and their gradients: bf16; dt, b, ddt, db: FP32 or bf16 (`gate_dtype`); A, dt_bias, states and
  * the parameters' gradients: FP32.  1 <= N <= SSM_MAX_STATE, G divides H, any P >= 1.
  *   - States, decays, norms, the chunks' triangular systems and every reduction are FP32 or better.  Matrix instructions
- *     take q, k, v and dy as they are and what is FP32 as three bf16 parts, its 24 bits; the normalisation is a row's
- *     FP32 factor beside the product.  What enters y, dq and dk alone is rounded further: in y the state and the decayed
- *     scores to bf16 (2^-9 of a term), in dq and dk the decayed scores.
- *   - No atomics: equal calls give equal bits, whatever the workspace holds.
+ *     take FP32 operands as two fp16 parts, which hold 22 bits of the largest value of a state's column, of a row of new
+ *     values or of a tile and an absolute 2^-25 of it below; the walked state therefore keeps 22 bits of its column's
+ *     largest.  Norms and rates are FP32 factors beside the products.  What enters y, dq and dk alone is rounded further: in
+ *     y the state that comes into a chunk to its first part (2^-12 of a term), new values and decayed scores to two bf16
+ *     parts (2^-17); in dq and dk the decayed scores to two.
+ *   - scale is finite, beta_max finite and positive, norm_eps finite and not negative.  The squares of a row of q or k are
+ *     summed in FP32 in the step and the backward: a row whose sum overflows counts as not finite there.  norm_eps = 0 gives
+ *     a row of zeros no direction, NaN.
+ *   - Equal calls give equal bits, whatever the workspace holds.
  */
 #ifndef DELTA_H
 #define DELTA_H
