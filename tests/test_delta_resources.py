@@ -3,8 +3,8 @@ their blocks into a CU's 160 KB of shared memory.
 
 A spill in the walks waits for every load before it, so that the next chunk's tiles stop being ahead.  Not meant: the chunk
 kernel, whose blocks run three to a CU with a few of its addresses spilled outside its inner products; the backward's chunk
-kernel of states past 128 columns, which holds two tiles' gradients in registers; and the layer norm's backward above 16384
-channels (4 pieces of 8 channels a thread in 128 registers).  CPU only: hipcc cross-compiles for gfx950.
+kernel of states past 128 columns, which holds two tiles' gradients in registers; and the layer norm's backward above 8192
+channels (2 or 4 pieces of 8 channels a thread, with both parameters' sums, in 128 registers).  CPU only: hipcc cross-compiles for gfx950.
 """
 import os
 import re
@@ -40,7 +40,7 @@ def test_no_scratch_and_blocks_fit(tmp_path):
             kernel = re.search(r"(delta|layer|slots)_\w*?kernel", name).group(0)
             seen.add(kernel)
             spills = kernel in ("delta_chunk_kernel", "delta_scan_bwd_wide_kernel") or (
-                kernel == "layer_norm_bwd_kernel" and ints[:2] == [1024, 4])
+                kernel == "layer_norm_bwd_kernel" and ints[0] == 1024 and ints[1] > 1)
             wide = ints and ints[0] > 128
             if (scratch and not spills) or lds * (1 if wide else BLOCKS.get(kernel, 1)) > LDS:
                 bad[name] = (lds, scratch)
