@@ -25,7 +25,9 @@ __device__ __forceinline__ uint32_t pk_f16(float a, float b) {
 // what the two halves of u leave of a and b
 __device__ __forceinline__ uint32_t rest_f16(float a, float b, uint32_t u) {
   const f16x2 h = __builtin_bit_cast(f16x2, u);
-  return pk_f16(a - (float)h.x, b - (float)h.y);
+  float minus = -1.f;
+  asm("" : "+s"(minus));  // a factor the compiler does not know: an fma takes h's halves as they are, a difference converts them
+  return pk_f16(__builtin_fmaf((float)h.x, minus, a), __builtin_fmaf((float)h.y, minus, b));
 }
 __device__ __forceinline__ f16x8 as_f16(u32x4 v) { return __builtin_bit_cast(f16x8, v); }
 __device__ __forceinline__ f16x8 as_f16(bf16x8 v) { return __builtin_bit_cast(f16x8, v); }  // the bits of an operand read
@@ -65,6 +67,13 @@ __device__ __forceinline__ float max4(float m, f32x4 v) {
   m = __builtin_fmaxf(__builtin_fmaxf(m, __builtin_fabsf(v[0])), __builtin_fabsf(v[1]));
   return __builtin_fmaxf(__builtin_fmaxf(m, __builtin_fabsf(v[2])), __builtin_fabsf(v[3]));
 }
+// the same, but a NaN where one of them is
+__device__ __forceinline__ float max4_nan(float m, f32x4 v) {
+  m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, __builtin_fabsf(v[0])), __builtin_fabsf(v[1]));
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, __builtin_fabsf(v[2])), __builtin_fabsf(v[3]));
+}
+// a b + c
+__device__ __forceinline__ f32x4 fma4(f32x4 a, f32x4 b, f32x4 c) { return __builtin_elementwise_fma(a, b, c); }
 // over the four rows of 16 lanes, in every lane: swapping the odd rows of a copy with the even rows of another puts the
 // rows' neighbours side by side, and the same for halves
 __device__ __forceinline__ float max_across16(float v) {
@@ -218,12 +227,12 @@ __device__ __forceinline__ void store_bytes(void* lds, const CopyRegs<BYTES, T>&
   }
 }
 
-// 64 rows of 64 columns by 256 threads (thread numbers `tid`), as load_tile and store_tile by all of a block's
-template <bool VEC>
-__device__ __forceinline__ void load_rows64(u32x4 (&v)[2], const Rows& rows, uint32_t ld, int ncols, int tid) {
+// 64 rows of COLS columns by 4 COLS threads (thread numbers `tid`), as load_tile and store_tile by all of a block's
+template <int COLS, bool VEC>
+__device__ __forceinline__ void load_rows(u32x4 (&v)[2], const Rows& rows, uint32_t ld, int ncols, int tid) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int row = tid / 8 + 32 * k, c = tid % 8 * 8;
+    const int row = tid / (COLS / 8) + 32 * k, c = tid % (COLS / 8) * 8;
     const uint32_t off = (row * ld + c) * 2;
     if constexpr (VEC) {
       v[k] = __builtin_amdgcn_raw_buffer_load_b128(rows.r, (int)(c < ncols ? off : kOutside), 0, 0);
@@ -237,15 +246,18 @@ __device__ __forceinline__ void load_rows64(u32x4 (&v)[2], const Rows& rows, uin
     }
   }
 }
-__device__ __forceinline__ void store_rows64(uint16_t* lds, const u32x4 (&v)[2], int tid) {
+template <int COLS>
+__device__ __forceinline__ void store_rows(uint16_t* lds, const u32x4 (&v)[2], int tid) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) *reinterpret_cast<u32x4*>(lds + at<64, 16>(tid / 8 + 32 * k, tid % 8 * 8)) = v[k];
+  for (int k = 0; k < 2; ++k)
+    *reinterpret_cast<u32x4*>(lds + at<COLS, 16>(tid / (COLS / 8) + 32 * k, tid % (COLS / 8) * 8)) = v[k];
 }
 
-// four rows of this lane's column of a bf16 tile: rows row0 + 4 g .., column c0 + i
+// four rows of this lane's column of a bf16 tile of COLS columns: rows row0 + 4 g .., column c0 + i
+template <int COLS = 64>
 __device__ __forceinline__ f32x4 column4(const uint16_t* tile, int row0, int c0, int g, int i) {
   const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (lds_s16x4*)(tile + at<64, 16>(row0 + 4 * g + (i >> 2), c0 + 4 * (i & 3))));
+      (lds_s16x4*)(tile + at<COLS, 16>(row0 + 4 * g + (i >> 2), c0 + 4 * (i & 3))));
   const u32x2 v = __builtin_bit_cast(u32x2, t);
   return f32x4{bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y)};
 }

@@ -13,61 +13,63 @@
 
 namespace cssm {
 
-// What shared memory holds of a chunk for the waves that walk the state: the chunk's and the next one's
-template <int NT>
+// What shared memory holds of a chunk for the waves that walk the state, 16 W columns: the chunk's and the next one's
+template <int NT, int W>
 struct ChainShared {
   __align__(16) uint16_t k[key_tile(NT) / 2];
   __align__(16) char t[kRecT];
   Factors fac;
-  __align__(16) uint16_t v[64 * kLd<64, 16>];
+  __align__(16) uint16_t v[64 * kLd<16 * W, 16>];
 };
 // and for the waves that make y, with what the others hand them: S's first parts, U, the columns' scales and first rows that
 // are not finite
-template <int NT>
+template <int NT, int W>
 struct OutputShared {
   __align__(16) uint16_t q[key_tile(NT) / 2];
   __align__(16) char p[kTriBlocks * 2 * kTriPart];
-  f16x8 s[4][NT / 32][64];
-  f32x4 u[4][4][64];
-  __align__(16) float down[4][16];
-  __align__(16) int bad[4][16];
+  f16x8 s[W][NT / 32][64];
+  f32x4 u[W][4][64];
+  __align__(16) float down[W][16];
+  __align__(16) int bad[W][16];
 };
 
-// Waves 0 to 3 walk the state and make U, a chain of products that each wait for the last; waves 4 to 7 make y of what the
+// Waves 0 to W - 1 walk the state and make U, a chain of products that each wait for the last; the other W make y of what the
 // first ones leave in shared memory, a half chunk behind, and bring the next chunks' tiles there.  Two barriers a chunk:
 // after S's parts (1) and after U (2) are there.  Before (1) of a chunk its K, T, V and factors and Q are in place; the
 // next chunk's K, T, V and factors come between (1) and (2), with this chunk's P, the next Q after (2).
 // What bounds it is the chain: R needs S, U needs R and the next S needs U, 3.3 us a chunk at 128 x 128, in which a SIMD's
 // matrix instructions are busy for 0.8.  4 x 4096 rows of 32 heads of 128 x 128: 335 us with the chunk kernel's 125; with all of it in
 // four waves, which waited for y's products and for the tiles between the chain's, 454.  One prompt of 2048 rows: 130 (174).
-template <int NT, bool VEC>
-__global__ __launch_bounds__(512, 2) void delta_scan_fwd_kernel(DeltaArgs d) {
-  constexpr int NB = NT / 16;
-  __shared__ ChainShared<NT> chain[2];
-  __shared__ OutputShared<NT> outp;
-  const ScanArgs& a = d.s;
+template <int NT, int W, bool VEC>
+__global__ __launch_bounds__(128 * W) void delta_scan_fwd_kernel(DeltaArgs d) {
+  constexpr int NB = NT / 16, TH = 64 * W, COLS = 16 * W;
+  __shared__ ChainShared<NT, W> chain[2];
+  __shared__ OutputShared<NT, W> outp;
+  const ScanArgs& a = d.s;  // its ptiles are of COLS columns
   const Units<1> us(a, blockIdx.x);
   if (!us.ok) return;
-  const Unit me(a, us, 0);
-  const int w = wave_id() & 3, pn = me.pn;
-  const bool walks = wave_id() < 4;
+  const int tile = us.group * us.units + us.first, h = (uint32_t)tile / (uint32_t)a.ptiles, p_first = (tile - h * a.ptiles) * COLS;
+  const int pn = a.P - p_first < COLS ? a.P - p_first : COLS;
+  const uint32_t col = (uint32_t)h * a.P + p_first;
+  const int w = wave_id() & (W - 1);
+  const bool walks = wave_id() < W;
   Piece pc;
   pc.seq = walk_sequence(d, us.item);
   seq_bounds(a.q, pc.seq, pc.s, pc.e);
   int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
-  const int64_t state_at = ((int64_t)me.h * a.P + me.p_first) * a.N;
+  const int64_t state_at = ((int64_t)h * a.P + p_first) * a.N;
   int64_t slot = 0;
   const bool has_slot = state_slot(a, pc.seq, slot), from = has_slot && starts_from_state(a, pc.seq);
   if (pc.e <= pc.s) {  // an empty sequence: a separate final state array still gets the start state
     if (a.fin && a.fin != a.init && has_slot)
-      for (int e = threadIdx.x; e < pn * a.N; e += 512)
+      for (int e = threadIdx.x; e < pn * a.N; e += 2 * TH)
         a.fin[slot * a.s_slot + state_at + e] = from ? a.init[slot * a.s_slot + state_at + e] : 0.f;
     return;
   }
-  uint16_t* yb = a.y + me.col;
+  uint16_t* yb = a.y + col;
   if (!has_slot) {  // zero rows, no state access
-    for (int64_t r = pc.s + wave_id(); r < pc.e; r += 8)
-      if (lane < pn) yb[r * a.y_ld + lane] = 0;
+    for (int64_t r = pc.s + wave_id(); r < pc.e; r += 2 * W)
+      for (int c = lane; c < pn; c += 64) yb[r * a.y_ld + c] = 0;
     return;
   }
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -75,30 +77,31 @@ __global__ __launch_bounds__(512, 2) void delta_scan_fwd_kernel(DeltaArgs d) {
   int rows = c.rows();
 
   if (!walks) {
-    const int tid = threadIdx.x - 256;
-    CopyRegs<(int)key_tile(NT), 256> tK, tQ;
-    CopyRegs<kRecT, 256> tT, tP;
-    CopyRegs<kRecVec, 256> tF;
+    const int tid = threadIdx.x - TH;
+    CopyRegs<(int)key_tile(NT), TH> tK, tQ;
+    CopyRegs<kRecT, TH> tT, tP;
+    CopyRegs<kRecVec, TH> tF;
     u32x4 tV[2];
+    auto id_of = [&](const Chunks<false>& n) { return chunk_id(pc, n.c0, d.n_chunk_slots); };
     auto load_chain = [&](const Chunks<false>& n, int left) {
-      const int64_t id = chunk_id(pc, n.c0, d.n_chunk_slots);
-      const char* rec = d.rec + (id * a.H + me.h) * kRecFwd;
+      const int64_t id = id_of(n);
+      const char* rec = d.rec + (id * a.H + h) * kRecFwd;
       load_bytes(tK, d.keys + (id * a.G + us.group) * 2 * key_tile(NT), left > 0, tid);
       load_bytes(tT, rec, left > 0, tid);
       load_bytes(tF, rec + kRecFwd - kRecVec, left > 0, tid);
-      load_rows64<VEC>(tV, Rows(a.x + n.c0 * a.x_ld + me.col, a.x_ld, left, pn, 2), (uint32_t)a.x_ld, pn, tid);
+      load_rows<COLS, VEC>(tV, Rows(a.x + n.c0 * a.x_ld + col, a.x_ld, left, pn, 2), (uint32_t)a.x_ld, pn, tid);
     };
-    auto store_chain = [&](ChainShared<NT>& to) {
+    auto store_chain = [&](ChainShared<NT, W>& to) {
       store_bytes(to.k, tK, tid);
       store_bytes(to.t, tT, tid);
       store_bytes(&to.fac, tF, tid);
-      store_rows64(to.v, tV, tid);
+      store_rows<COLS>(to.v, tV, tid);
     };
     auto load_q = [&](const Chunks<false>& n, int left) {
-      load_bytes(tQ, d.keys + ((chunk_id(pc, n.c0, d.n_chunk_slots) * a.G + us.group) * 2 + 1) * key_tile(NT), left > 0, tid);
+      load_bytes(tQ, d.keys + ((id_of(n) * a.G + us.group) * 2 + 1) * key_tile(NT), left > 0, tid);
     };
     auto load_p = [&](const Chunks<false>& n, int left) {
-      load_bytes(tP, d.rec + (chunk_id(pc, n.c0, d.n_chunk_slots) * a.H + me.h) * kRecFwd + kRecT, left > 0, tid);
+      load_bytes(tP, d.rec + (id_of(n) * a.H + h) * kRecFwd + kRecT, left > 0, tid);
     };
     load_chain(c, rows);
     load_q(c, rows);
@@ -185,7 +188,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan_fwd_kernel(DeltaArgs d) {
   for (int buf = 0;; buf ^= 1) {
     lane = fresh(lane);
     g = lane >> 4, i = lane & 15;
-    const ChainShared<NT>& sh = chain[buf];
+    const ChainShared<NT, W>& sh = chain[buf];
     const Factors& fac = sh.fac;
     f32x4 r[4];  // rows in the registers, columns p in the lanes
 #pragma unroll
@@ -204,19 +207,16 @@ __global__ __launch_bounds__(512, 2) void delta_scan_fwd_kernel(DeltaArgs d) {
       for (int ib = 0; ib < 4; ++ib) r[ib] = mma2(key_rows<NT>(sh.k, 16 * ib, 32 * ks, lane), s[ks], r[ib]);
     const float s_max = state_max(S);
     float r_max = 0.f;
-    bool fine = true;
 #pragma unroll
     for (int ib = 0; ib < 4; ++ib) {
       const f32x4 f = *reinterpret_cast<const f32x4*>(fac.in + 16 * ib + 4 * g) * s_down;
-      r[ib] = (column4(sh.v, 16 * ib, 16 * w, g, i) - f * r[ib]) * *reinterpret_cast<const f32x4*>(fac.rate + 16 * ib + 4 * g);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) fine = fine && __builtin_isfinite(r[ib][e]);
-      r_max = max4(r_max, r[ib]);
+      r[ib] = fma4(-f, r[ib], column4<COLS>(sh.v, 16 * ib, 16 * w, g, i)) * *reinterpret_cast<const f32x4*>(fac.rate + 16 * ib + 4 * g);
+      r_max = max4_nan(r_max, r[ib]);
     }
     // The first row of this lane's column that is not finite: it and the later ones are left out of the products, whose
     // zeros would spread them, and put in at the end
     int bad = __builtin_amdgcn_readfirstlane(fac.bad);
-    const bool any_bad = bad < 64 || __ballot(!fine) != 0;
+    const bool any_bad = bad < 64 || __ballot(!__builtin_isfinite(r_max)) != 0;
     if (__builtin_expect(any_bad, 0)) {
 #pragma unroll
       for (int ib = 3; ib >= 0; --ib)
@@ -382,19 +382,16 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_wide_ke
       for (int ib = 0; ib < 4; ++ib) y[ib] *= sd * fac.read[16 * ib + i];
     }
     float r_max = 0.f;
-    bool fine = true;
 #pragma unroll
     for (int ib = 0; ib < 4; ++ib) {
       const f32x4 f = *reinterpret_cast<const f32x4*>(fac.in + 16 * ib + 4 * g) * s_down;
-      r[ib] = (column4(sV, 16 * ib, 16 * w, g, i) - f * r[ib]) * *reinterpret_cast<const f32x4*>(fac.rate + 16 * ib + 4 * g);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) fine = fine && __builtin_isfinite(r[ib][e]);
-      r_max = max4(r_max, r[ib]);
+      r[ib] = fma4(-f, r[ib], column4(sV, 16 * ib, 16 * w, g, i)) * *reinterpret_cast<const f32x4*>(fac.rate + 16 * ib + 4 * g);
+      r_max = max4_nan(r_max, r[ib]);
     }
     // The first row of this lane's column that is not finite: it and the later ones are left out of the products, whose
     // zeros would spread them, and put in at the end
     int bad = __builtin_amdgcn_readfirstlane(fac.bad);
-    const bool any_bad = bad < 64 || __ballot(!fine) != 0;
+    const bool any_bad = bad < 64 || __ballot(!__builtin_isfinite(r_max)) != 0;
     if (__builtin_expect(any_bad, 0)) {
 #pragma unroll
       for (int ib = 3; ib >= 0; --ib)
@@ -486,15 +483,27 @@ __global__ __launch_bounds__(256, NT <= 128 ? 2 : 1) void delta_scan_fwd_wide_ke
   }
 }
 
+// 64 columns a block, or 32 if there is a CU for every such block: a wave that walks then has its SIMD for itself.  One prompt of
+// 2048 rows, 32 heads of 128: 122 us with 32, 129 with 64 (110 since the instructions of a chunk became fewer); 4 x 4096 rows, which
+// fill the card with 64: 495 and 328.  (128 columns,
+// 16 waves of 128 registers: 490, and 64 mixed prompts 990 for 800.)
+template <int NT, int W>
+static void walk(DeltaArgs a, bool vec, hipStream_t s) {
+  a.s.ptiles = (a.s.P + 16 * W - 1) / (16 * W);
+  const dim3 grid((uint32_t)unit_blocks(a.s.q.nseq, a.s.H, a.s.G, a.s.ptiles, 1));
+  if (vec) delta_scan_fwd_kernel<NT, W, true><<<grid, 128 * W, 0, s>>>(a);
+  else delta_scan_fwd_kernel<NT, W, false><<<grid, 128 * W, 0, s>>>(a);
+}
+
 template <int NT>
 static void launch(const DeltaArgs& a, bool vec, hipStream_t s) {
-  const dim3 grid((uint32_t)unit_blocks(a.s.q.nseq, a.s.H, a.s.G, a.s.ptiles, 1));
   if constexpr (NT > 128) {
+    const dim3 grid((uint32_t)unit_blocks(a.s.q.nseq, a.s.H, a.s.G, a.s.ptiles, 1));
     if (vec) delta_scan_fwd_wide_kernel<NT, true><<<grid, 256, 0, s>>>(a);
     else delta_scan_fwd_wide_kernel<NT, false><<<grid, 256, 0, s>>>(a);
   } else {
-    if (vec) delta_scan_fwd_kernel<NT, true><<<grid, 512, 0, s>>>(a);
-    else delta_scan_fwd_kernel<NT, false><<<grid, 512, 0, s>>>(a);
+    if (a.s.q.nseq * a.s.H * ((a.s.P + 31) / 32) <= 256) walk<NT, 2>(a, vec, s);
+    else walk<NT, 4>(a, vec, s);
   }
 }
 

@@ -176,7 +176,7 @@ __device__ __forceinline__ void delta_walk(const DeltaBwdArgs& b, WalkShared<NT>
 #pragma unroll
       for (int ib = 0; ib < 4; ++ib) {
         const f32x4 f = *reinterpret_cast<const f32x4*>(fac.in + 16 * ib + 4 * g) * s_down;
-        r[ib] = (column4(sh.v, 16 * ib, 16 * w, g, i) * turn - f * r[ib]) *
+        r[ib] = fma4(-f, r[ib], column4(sh.v, 16 * ib, 16 * w, g, i) * turn) *
                 *reinterpret_cast<const f32x4*>(fac.rate + 16 * ib + 4 * g);
       }
     } else {
@@ -593,8 +593,8 @@ __global__ __launch_bounds__(4 * NT * WR) void delta_scan_bwd_kernel(DeltaBwdArg
           y4 = mma3(u, spot_halves(sF, 16 * ib, 32 * ks, lane), y4);
         }
         const f32x4 uj = *reinterpret_cast<const f32x4*>(s_u + 16 * jb + 4 * g);
-        W[s] += w4 * (uj * s_y[16 * ib + i]);
-        Y[s] += y4 * (uj * s_f[16 * ib + i]);
+        W[s] = fma4(w4, uj * s_y[16 * ib + i], W[s]);
+        Y[s] = fma4(y4, uj * s_f[16 * ib + i], Y[s]);
         here(W[s]), here(Y[s]);
       }
       phase();
