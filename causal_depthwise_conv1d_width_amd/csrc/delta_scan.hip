@@ -1,8 +1,8 @@
 // delta_scan.hip -- forward gated delta rule over packed rows: the walk of the states.
 //
-// A block walks one sequence for 64 columns of one head, a chunk of 64 rows at a time (delta_chunk.hip: L, r, T, P):
+// A block walks one sequence for 64 (or 32) columns of one head, a chunk of 64 rows at a time (delta_chunk.hip: L, r, T, P):
 //   R = r (V - e^L K S^T),   U = T R,   Y = scale e^L Q S^T + P U,   S' = e^{L_Q} S + U^T (e^{L_Q - L} K)
-// Each of its 4 waves owns 16 columns p of V, U, Y and S, which depend on no other column: nothing passes between waves.
+// Each of its waves owns 16 columns p of V, U, Y and S, which depend on no other column: nothing passes between waves.
 // The state's accumulators (registers n, lanes p) are, unmoved, the operand that K S^T and Q S^T contract over n, and R's
 // and U's the ones that T, P and K contract over rows.  Shared memory holds K, Q, V and the chunk's record for all waves;
 // the next chunk's are loaded over the current one's products.
@@ -37,9 +37,11 @@ struct OutputShared {
 // first ones leave in shared memory, a half chunk behind, and bring the next chunks' tiles there.  Two barriers a chunk:
 // after S's parts (1) and after U (2) are there.  Before (1) of a chunk its K, T, V and factors and Q are in place; the
 // next chunk's K, T, V and factors come between (1) and (2), with this chunk's P, the next Q after (2).
-// What bounds it is the chain: R needs S, U needs R and the next S needs U, 3.3 us a chunk at 128 x 128, in which a SIMD's
-// matrix instructions are busy for 0.8.  4 x 4096 rows of 32 heads of 128 x 128: 335 us with the chunk kernel's 125; with all of it in
-// four waves, which waited for y's products and for the tiles between the chain's, 454.  One prompt of 2048 rows: 130 (174).
+// What bounds it: R needs S, U needs R and the next S needs U, and y's products share the SIMDs: a chunk takes 3.1 us at 128 x 128
+// columns (2.7 with 32 columns a block), in which a SIMD's matrix instructions are busy for 0.8.  Without y's products or without
+// the walk's it would be a seventh less, without either (copies, barriers, scalings) a third; two chunks' tiles on their way instead
+// of one change nothing.  4 x 4096 rows of 32 heads of 128 x 128: 322 us with the chunk kernel's 125; with all of it in
+// four waves, which waited for y's products and for the tiles between the chain's, 454.
 template <int NT, int W, bool VEC>
 __global__ __launch_bounds__(128 * W) void delta_scan_fwd_kernel(DeltaArgs d) {
   constexpr int NB = NT / 16, TH = 64 * W, COLS = 16 * W;
