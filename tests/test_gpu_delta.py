@@ -1,7 +1,8 @@
 """GPU: the gated delta rule and its step against float64 (delta_reference.py).
 
 Tolerances count roundings.  bf16 rounds by at most 2^-8 of a value.  y: the result, and each term's operand (the state
-or the decayed score) once: 2^-8 |y| + 2^-8 (1 + 2^-6) times the sum of the terms' magnitudes.  A state's rounding errors
+or the decayed score) once: 2^-8 |y| + 2^-8 (1 + 2^-6) times the sum of the terms' magnitudes (for operands of one bf16
+part; the kernels' have 2^-12 and 2^-17).  A state's rounding errors
 are those of FP32 sums: in a chunk at most 40 roundings (12 accumulations of K S, 12 of T R, 6 of K^T U, decays and
 splits) of 2^-24 of a column's largest sum of magnitudes, over at most 8 chunks, none grown by a later chunk (decays and
 I - r k k^T have norms of at most one for |k|^2 r <= 2): 8 * 40 * 2^-24 < 2^-15.  The step is FP32 throughout: sums of 256

@@ -1,9 +1,10 @@
 """GPU: the gated delta rule's backward against float64 (delta_reference.py).
 
 Tolerances count roundings.  A bf16 result: 2^-8 of its value.  dq and dk: the decayed scores of their terms between two
-rows once more, 2^-8 (1 + 2^-6) of these terms' magnitudes.  Everything else is FP32 arithmetic on operands of 24 bits: with
-at most 40 roundings of 2^-24 a chunk in a state or an adjoint, as many in the other and in the products of both, over at
-most 8 chunks, 2^-14 of the largest sum of magnitudes in the head (ddt, db, the initial states' gradient); of dA and
+rows once more, 2^-8 (1 + 2^-6) of these terms' magnitudes.  Everything else is FP32 arithmetic on operands of two fp16
+parts, off by at most 2^-23 of their column's, row's or tile's largest (two roundings of 2^-24; at most eight such operands
+a chunk): with at most 40 roundings of 2^-24 a chunk in a state or an adjoint, as many in the other and in the products of
+both, over at most 8 chunks, 2^-14 of the largest sum of magnitudes in the head (ddt, db, the initial states' gradient); of dA and
 d(dt_bias) of their sum over rows; the same share of the largest |adjoint| |key| or |state| |key| stays in dq, dk, dv.
 """
 import pytest
