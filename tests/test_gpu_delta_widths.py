@@ -76,3 +76,17 @@ def test_many_short_sequences():
                 assert float((a - b).abs().max()) <= 2.0 ** -7 * float(b.abs().max()), (name, i)
         else:
             assert torch.equal(g.dinitial_state[i], p.dS[i])
+
+
+def test_rows_whose_squares_pass_fp32():
+    """Unit keys do not depend on their length.  The forward brings rows to one size first; the step, which sums the squares
+    as they are, gives no number rather than a wrong one."""
+    p = Problem([70], 2, 32, 1, 64, seed=8, norm_eps=0.0)
+    want = cc.delta_scan_fwd(*p.args(), cu_seqlens=p.cu, **p.kw)
+    p.k.mul_(2.0 ** 70)
+    assert bool(torch.isfinite(p.k).all())
+    assert torch.equal(cc.delta_scan_fwd(*p.args(), cu_seqlens=p.cu, **p.kw), want)
+    pool = torch.zeros(3, 2, 32, 64, device="cuda")
+    slots = torch.tensor([1], dtype=torch.int32, device="cuda")
+    y = cc.delta_state_update(*(t[:1] for t in p.args()[:5]), p.A, p.bias, state_pool=pool, cache_indices=slots, **p.kw)
+    assert bool(torch.isnan(y).all()) and bool(torch.isnan(pool[1]).all()) and float(pool[[0, 2]].abs().max()) == 0
